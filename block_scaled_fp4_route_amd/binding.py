@@ -19,13 +19,16 @@ MOE_OK, MOE_ERR_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_HIP, MOE_ERR_WORKSPACE = 0, -1
 MOE_MODE_ROUTE, MOE_MODE_DECODE, MOE_MODE_PREFILL = 0, 1, 2
 MOE_OUT_F32, MOE_OUT_BF16 = 0, 1
 MOE_NOALLOC_SCRATCH_BYTES = 1 << 20
+MOE_ACC_DX, MOE_ACC_DWR = 1, 2
+MOE_ACT_F32, MOE_ACT_BF16, MOE_ACT_F16 = 0, 1, 2
 FORMATS = {"nvfp4": MOE_FMT_NVFP4, "mxfp4": MOE_FMT_MXFP4}
 
 # every symbol declared in include/moe_fp4.h
 EXPORTS = ("moe_block_bytes", "moe_block_layout", "moe_workspace_bytes", "moe_route", "moe_expert_decode",
            "moe_layer_decode", "moe_layer_decode_noalloc", "moe_expert_prefill", "moe_dequant_block", "moe_act_quant_fp8", "moe_gemv_fp8",
            "moe_prefetch_sink_bytes", "moe_expert_prefetch", "moe_tier_create", "moe_tier_destroy", "moe_tier_update", "moe_tier_get_stats", "moe_tier_slot_of",
-           "moe_status_string", "moe_last_error")
+           "moe_balance_workspace_bytes", "moe_balance_loss", "moe_route_backward_workspace_bytes", "moe_route_backward",
+           "moe_lora_workspace_bytes", "moe_lora_apply", "moe_lora_backward", "moe_status_string", "moe_last_error")
 
 
 class MoeError(RuntimeError):
@@ -51,6 +54,10 @@ class moe_prefill_debug(C.Structure):
 class moe_tier_stats(C.Structure):
     _fields_ = [("resident", C.c_int64), ("pending", C.c_int64), ("hits", C.c_int64), ("misses", C.c_int64),
                 ("promotions", C.c_int64), ("evictions", C.c_int64)]
+
+
+class moe_lora_desc(C.Structure):
+    _fields_ = [("K", C.c_int32), ("N", C.c_int32), ("n", C.c_int32), ("max_rank", C.c_int32), ("dtype", C.c_int32)]
 
 
 def _load():
@@ -88,6 +95,18 @@ def _load():
     L.moe_tier_update.restype = C.c_int; L.moe_tier_update.argtypes = [P, P, I32, P]
     L.moe_tier_get_stats.restype = C.c_int; L.moe_tier_get_stats.argtypes = [P, C.POINTER(moe_tier_stats)]
     L.moe_tier_slot_of.restype = I32; L.moe_tier_slot_of.argtypes = [P, I32, I32]
+    F32, I64, LD = C.c_float, C.c_int64, C.POINTER(moe_lora_desc)
+    L.moe_balance_workspace_bytes.restype = SZ; L.moe_balance_workspace_bytes.argtypes = [D, I32, I32]
+    L.moe_balance_loss.restype = C.c_int
+    L.moe_balance_loss.argtypes = [D, P, I32, P, P, P, I32, F32, F32, P, P, P, P, P, P, SZ, P]
+    L.moe_route_backward_workspace_bytes.restype = SZ; L.moe_route_backward_workspace_bytes.argtypes = [D, I32]
+    L.moe_route_backward.restype = C.c_int
+    L.moe_route_backward.argtypes = [D, P, I32, P, P, P, P, P, P, P, P, P, I32, P, SZ, P]
+    L.moe_lora_workspace_bytes.restype = SZ; L.moe_lora_workspace_bytes.argtypes = [LD, I32, I32]
+    L.moe_lora_apply.restype = C.c_int
+    L.moe_lora_apply.argtypes = [LD, P, I64, I32, P, P, P, P, P, P, I64, P, I64, P, SZ, P]
+    L.moe_lora_backward.restype = C.c_int
+    L.moe_lora_backward.argtypes = [LD, P, I64, P, I64, I32, P, P, P, P, P, P, I64, P, I64, P, P, I32, P, SZ, P]
     L.moe_status_string.restype = C.c_char_p; L.moe_status_string.argtypes = [C.c_int]
     L.moe_last_error.restype = C.c_char_p; L.moe_last_error.argtypes = []
     return L
@@ -264,3 +283,80 @@ def moe_prefetch_sink_bytes(d: moe_desc, n: int) -> int:
 def moe_expert_prefetch(d, expert_ptrs, idx, n, sink, stream=None):
     _check(lib.moe_expert_prefetch(C.byref(d), _ptr(expert_ptrs), _ptr(idx), n, _ptr(sink),
                                    sink.numel() * sink.element_size(), _stream(stream)))
+
+
+# --- training the router, low-rank adapters ---------------------------------
+
+def _run(fn, head, stream, tensors, *args):
+    """fn(head, *args, stream) with the device of the tensors current (they
+    may lie on another one than the caller's) and, without a stream, on that
+    device's current stream."""
+    import torch
+    dev = None
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            continue
+        if not t.is_cuda:
+            raise MoeError(MOE_ERR_ARG, "a tensor is not on the GPU")
+        if dev is None:
+            dev = t.get_device()
+        elif t.get_device() != dev:
+            raise MoeError(MOE_ERR_ARG, "tensors on different devices")
+    if dev is None or dev == torch.cuda.current_device():
+        _check(fn(C.byref(head), *args, _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(C.byref(head), *args, _stream(stream)))
+
+
+def _ws_bytes(ws, ws_bytes):
+    return ws.numel() * ws.element_size() if ws_bytes is None and ws is not None else (ws_bytes or 0)
+
+
+def moe_balance_workspace_bytes(d, T: int, S: int = 1) -> int:
+    return int(lib.moe_balance_workspace_bytes(C.byref(d), T, S))
+
+
+def moe_balance_loss(d, logits, T, idx, mask, seq_off, S, balance_coef, z_coef, dloss, loss, counts, probs, dlogits,
+                     ws, ws_bytes=None, stream=None):
+    _run(lib.moe_balance_loss, d, stream, (loss, logits, idx, mask, seq_off, dloss, counts, probs, dlogits, ws),
+         _ptr(logits), T, _ptr(idx), _ptr(mask), _ptr(seq_off), S, balance_coef, z_coef, _ptr(dloss), _ptr(loss),
+         _ptr(counts), _ptr(probs), _ptr(dlogits), _ptr(ws), _ws_bytes(ws, ws_bytes))
+
+
+def moe_route_backward_workspace_bytes(d, T: int) -> int:
+    return int(lib.moe_route_backward_workspace_bytes(C.byref(d), T))
+
+
+def moe_route_backward(d, x, T, Wr, idx, w, dw, mask, dlogits_in, dlogits_out, dx, dWr, accumulate, ws, ws_bytes=None,
+                       stream=None):
+    _run(lib.moe_route_backward, d, stream, (x, Wr, idx, w, dw, mask, dlogits_in, dlogits_out, dx, dWr, ws),
+         _ptr(x), T, _ptr(Wr), _ptr(idx), _ptr(w), _ptr(dw), _ptr(mask), _ptr(dlogits_in), _ptr(dlogits_out), _ptr(dx),
+         _ptr(dWr), accumulate, _ptr(ws), _ws_bytes(ws, ws_bytes))
+
+
+def lora_desc(K: int, N: int, n: int, max_rank: int, dtype) -> moe_lora_desc:
+    """dtype: the activations' torch dtype (float32, bfloat16, float16) or MOE_ACT_*."""
+    if not isinstance(dtype, int):
+        import torch
+        dtype = {torch.float32: MOE_ACT_F32, torch.bfloat16: MOE_ACT_BF16, torch.float16: MOE_ACT_F16}[dtype]
+    return moe_lora_desc(K, N, n, max_rank, dtype)
+
+
+def moe_lora_workspace_bytes(l, T: int, backward) -> int:
+    return int(lib.moe_lora_workspace_bytes(C.byref(l), T, 1 if backward else 0))
+
+
+def moe_lora_apply(l, x, ldx, T, ids, a_ptrs, b_ptrs, ranks, scales, base, ldbase, y, ldy, ws, ws_bytes=None,
+                   stream=None):
+    _run(lib.moe_lora_apply, l, stream, (y, x, ids, a_ptrs, b_ptrs, ranks, scales, base, ws),
+         _ptr(x), ldx, T, _ptr(ids), _ptr(a_ptrs), _ptr(b_ptrs), _ptr(ranks), _ptr(scales), _ptr(base), ldbase,
+         _ptr(y), ldy, _ptr(ws), _ws_bytes(ws, ws_bytes))
+
+
+def moe_lora_backward(l, x, ldx, dy, lddy, T, ids, a_ptrs, b_ptrs, ranks, scales, dx_base, lddx_base, dx, lddx,
+                      da_ptrs, db_ptrs, accumulate, ws, ws_bytes=None, stream=None):
+    _run(lib.moe_lora_backward, l, stream, (x, dy, ids, a_ptrs, b_ptrs, ranks, scales, dx_base, dx, da_ptrs, db_ptrs, ws),
+         _ptr(x), ldx, _ptr(dy), lddy, T, _ptr(ids), _ptr(a_ptrs), _ptr(b_ptrs), _ptr(ranks), _ptr(scales),
+         _ptr(dx_base), lddx_base, _ptr(dx), lddx, _ptr(da_ptrs), _ptr(db_ptrs), accumulate, _ptr(ws),
+         _ws_bytes(ws, ws_bytes))

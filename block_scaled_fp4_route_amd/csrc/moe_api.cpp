@@ -6,11 +6,13 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
 
 #include "moe_internal.h"
+#include "moe_learn.h"
 
 namespace {
 
@@ -319,6 +321,175 @@ int moe_gemv_fp8(const uint8_t* W, const float* row_scale, const float* x, int32
         (r = check_ptr(y, 4, "y")))
         return r;
     return hip_status(moe::launch_gemv_fp8(W, row_scale, x, y, rows, cols, (hipStream_t)stream), "gemv_fp8 launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+int balance_checks(const moe_desc* d, int32_t T, int32_t S) {
+    int r;
+    if ((r = check_desc(d))) return r;
+    if (T < 0) return fail(MOE_ERR_ARG, "T=%d is negative", T);
+    if (S < 1) return fail(MOE_ERR_ARG, "S=%d must be >= 1", S);
+    if (d->E > moe::kMaxE || d->k > moe::kMaxK || S > 65535 || T > (1 << 24))
+        return fail(MOE_ERR_UNSUPPORTED, "balance loss needs E <= %d, k <= %d, S <= 65535, T <= 2^24 (E=%d k=%d S=%d T=%d)",
+                    moe::kMaxE, moe::kMaxK, d->E, d->k, S, T);
+    return MOE_OK;
+}
+
+int route_backward_checks(const moe_desc* d, int32_t T) {
+    int r;
+    if ((r = check_desc(d))) return r;
+    if (T < 0) return fail(MOE_ERR_ARG, "T=%d is negative", T);
+    if (!moe::route_supported(d->H, d->E, d->k))
+        return fail(MOE_ERR_UNSUPPORTED, "router needs H %% 256 == 0, H <= 8192, E <= %d, k <= %d (H=%d E=%d k=%d)",
+                    moe::kMaxE, moe::kMaxK, d->H, d->E, d->k);
+    if (T > (1 << 20)) return fail(MOE_ERR_UNSUPPORTED, "T=%d exceeds 2^20", T);
+    return MOE_OK;
+}
+
+int lora_checks(const moe_lora_desc* l, int32_t T) {
+    if (!l) return fail(MOE_ERR_ARG, "lora desc is NULL");
+    if (l->dtype != MOE_ACT_F32 && l->dtype != MOE_ACT_BF16 && l->dtype != MOE_ACT_F16)
+        return fail(MOE_ERR_ARG, "unknown dtype %d", l->dtype);
+    if (l->K <= 0 || l->N <= 0 || l->n <= 0 || l->max_rank <= 0)
+        return fail(MOE_ERR_ARG, "K, N, n, max_rank must be positive (K=%d N=%d n=%d max_rank=%d)", l->K, l->N, l->n,
+                    l->max_rank);
+    if (l->K % 8 || l->N % 8) return fail(MOE_ERR_ARG, "K=%d and N=%d must be multiples of 8", l->K, l->N);
+    if (T < 0) return fail(MOE_ERR_ARG, "T=%d is negative", T);
+    if (l->K > moe::kLoraMaxDim || l->N > moe::kLoraMaxDim || l->n > moe::kLoraMaxN || l->max_rank > moe::kLoraMaxRank ||
+        T > moe::kLoraMaxT)
+        return fail(MOE_ERR_UNSUPPORTED, "adapters need K, N <= %d, n <= %d, max_rank <= %d, T <= %d (K=%d N=%d n=%d max_rank=%d T=%d)",
+                    moe::kLoraMaxDim, moe::kLoraMaxN, moe::kLoraMaxRank, moe::kLoraMaxT, l->K, l->N, l->n, l->max_rank, T);
+    return MOE_OK;
+}
+
+// A matrix of rows of `cols` elements with a stride.
+int check_rows(const void* p, int64_t ld, int32_t cols, const char* name) {
+    int r;
+    if ((r = check_ptr(p, 16, name))) return r;
+    if (ld < cols || ld % 8 || ld > ((int64_t)1 << 40))
+        return fail(MOE_ERR_ARG, "%s: stride %lld must be a multiple of 8 and at least %d", name, (long long)ld, cols);
+    return MOE_OK;
+}
+
+int lora_table_checks(const int32_t* ids, const void* const* a, const void* const* b, const int32_t* ranks,
+                      const float* scales) {
+    int r;
+    if ((r = check_ptr(ids, 4, "ids")) || (r = check_ptr(a, 8, "a_ptrs")) || (r = check_ptr(b, 8, "b_ptrs")) ||
+        (r = check_ptr(ranks, 4, "ranks")) || (r = check_ptr(scales, 4, "scales")))
+        return r;
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_balance_workspace_bytes(const moe_desc* d, int32_t T, int32_t S) {
+    return balance_checks(d, T, S) == MOE_OK ? moe::balance_ws_bytes(T, d->E, S) : 0;
+}
+
+int moe_balance_loss(const moe_desc* d, const float* logits, int32_t T, const int32_t* idx, const uint8_t* mask,
+                     const int32_t* seq_off, int32_t S, float balance_coef, float z_coef, const float* dloss,
+                     float* loss, int32_t* counts, float* probs, float* dlogits, void* ws, size_t ws_bytes,
+                     void* stream) {
+    int r;
+    if ((r = balance_checks(d, T, S))) return r;
+    if (T > 0 && ((r = check_ptr(logits, 16, "logits")) || (r = check_ptr(idx, 4, "idx")))) return r;
+    if (!seq_off && S != 1) return fail(MOE_ERR_ARG, "S=%d without seq_off", S);
+    if (seq_off && !aligned(seq_off, 4)) return fail(MOE_ERR_ARG, "seq_off is not 4-byte aligned");
+    if (dloss && !aligned(dloss, 4)) return fail(MOE_ERR_ARG, "dloss is not 4-byte aligned");
+    if (!std::isfinite(balance_coef) || !std::isfinite(z_coef)) return fail(MOE_ERR_ARG, "a coefficient is not finite");
+    if ((r = check_ptr(loss, 4, "loss"))) return r;
+    if (counts && !aligned(counts, 4)) return fail(MOE_ERR_ARG, "counts is not 4-byte aligned");
+    if (probs && !aligned(probs, 4)) return fail(MOE_ERR_ARG, "probs is not 4-byte aligned");
+    if (dlogits && !aligned(dlogits, 16)) return fail(MOE_ERR_ARG, "dlogits is not 16-byte aligned");
+    if (dlogits && T > 0 && dlogits == logits) return fail(MOE_ERR_ARG, "dlogits is logits");
+    if ((r = check_ws(ws, ws_bytes, moe::balance_ws_bytes(T, d->E, S)))) return r;
+    return hip_status(moe::launch_balance(d->E, d->k, logits, T, idx, mask, seq_off, S, balance_coef, z_coef, dloss,
+                                          loss, counts, probs, dlogits, ws, reinterpret_cast<hipStream_t>(stream)),
+                      "balance loss launch");
+}
+
+size_t moe_route_backward_workspace_bytes(const moe_desc* d, int32_t T) {
+    return route_backward_checks(d, T) == MOE_OK ? moe::route_backward_ws_bytes(d->H, d->E, T) : 0;
+}
+
+int moe_route_backward(const moe_desc* d, const float* x, int32_t T, const float* Wr, const int32_t* idx,
+                       const float* w, const float* dw, const uint8_t* mask, const float* dlogits_in,
+                       float* dlogits_out, float* dx, float* dWr, int32_t accumulate, void* ws, size_t ws_bytes,
+                       void* stream) {
+    int r;
+    if ((r = route_backward_checks(d, T))) return r;
+    if (accumulate & ~(MOE_ACC_DX | MOE_ACC_DWR)) return fail(MOE_ERR_ARG, "unknown accumulate bits %d", accumulate);
+    if (T > 0) {
+        if (!dw && !dlogits_in) return fail(MOE_ERR_ARG, "neither dw nor dlogits_in");
+        if (!dlogits_out && !dx && !dWr) return fail(MOE_ERR_ARG, "no output");
+        if (dw && ((r = check_ptr(idx, 4, "idx")) || (r = check_ptr(w, 4, "w")) || (r = check_ptr(dw, 4, "dw")))) return r;
+        if (dlogits_in && (r = check_ptr(dlogits_in, 4, "dlogits_in"))) return r;
+        if (dlogits_out && (r = check_ptr(dlogits_out, 4, "dlogits_out"))) return r;
+        if (dx && ((r = check_ptr(dx, 16, "dx")) || (r = check_ptr(Wr, 16, "Wr")))) return r;
+        if (dWr && (r = check_ptr(x, 16, "x"))) return r;
+    }
+    if (dWr && (r = check_ptr(dWr, 16, "dWr"))) return r;
+    if ((r = check_ws(ws, ws_bytes, moe::route_backward_ws_bytes(d->H, d->E, T)))) return r;
+    return hip_status(moe::launch_route_backward(d->H, d->E, d->k, x, T, Wr, idx, w, dw, mask, dlogits_in, dlogits_out,
+                                                 dx, dWr, accumulate, ws, reinterpret_cast<hipStream_t>(stream)),
+                      "routing gradient launch");
+}
+
+size_t moe_lora_workspace_bytes(const moe_lora_desc* l, int32_t T, int32_t backward) {
+    return lora_checks(l, T) == MOE_OK ? moe::lora_ws_bytes(l->K, l->N, l->n, l->max_rank, T, backward != 0) : 0;
+}
+
+int moe_lora_apply(const moe_lora_desc* l, const void* x, int64_t ldx, int32_t T, const int32_t* ids,
+                   const void* const* a_ptrs, const void* const* b_ptrs, const int32_t* ranks, const float* scales,
+                   const void* base, int64_t ldbase, void* y, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+    int r;
+    if ((r = lora_checks(l, T))) return r;
+    if (T == 0) return ok();
+    if ((r = check_rows(x, ldx, l->K, "x")) || (r = lora_table_checks(ids, a_ptrs, b_ptrs, ranks, scales)) ||
+        (r = check_rows(y, ldy, l->N, "y")) || (base && (r = check_rows(base, ldbase, l->N, "base"))))
+        return r;
+    if (base == y && ldbase != ldy) return fail(MOE_ERR_ARG, "base is y with another stride");
+    if (x == y) return fail(MOE_ERR_ARG, "y is x");
+    if ((r = check_ws(ws, ws_bytes, moe::lora_ws_bytes(l->K, l->N, l->n, l->max_rank, T, false)))) return r;
+    const moe::LoraTable tab = {ids, a_ptrs, b_ptrs, ranks, scales};
+    return hip_status(moe::launch_lora_apply(l->dtype, l->K, l->N, l->n, l->max_rank, x, (size_t)ldx, T, tab, base,
+                                             (size_t)ldbase, y, (size_t)ldy, ws, reinterpret_cast<hipStream_t>(stream)),
+                      "adapter launch");
+}
+
+int moe_lora_backward(const moe_lora_desc* l, const void* x, int64_t ldx, const void* dy, int64_t lddy, int32_t T,
+                      const int32_t* ids, const void* const* a_ptrs, const void* const* b_ptrs, const int32_t* ranks,
+                      const float* scales, const void* dx_base, int64_t lddx_base, void* dx, int64_t lddx,
+                      float* const* da_ptrs, float* const* db_ptrs, int32_t accumulate, void* ws, size_t ws_bytes,
+                      void* stream) {
+    int r;
+    if ((r = lora_checks(l, T))) return r;
+    if (T > 0 && !dx && !da_ptrs && !db_ptrs) return fail(MOE_ERR_ARG, "no output");
+    if (T == 0 && !da_ptrs && !db_ptrs) return ok();
+    if (da_ptrs && (r = check_ptr(da_ptrs, 8, "da_ptrs"))) return r;
+    if (db_ptrs && (r = check_ptr(db_ptrs, 8, "db_ptrs"))) return r;
+    if (T > 0) {
+        if ((r = check_rows(x, ldx, l->K, "x")) || (r = check_rows(dy, lddy, l->N, "dy")) ||
+            (r = lora_table_checks(ids, a_ptrs, b_ptrs, ranks, scales)))
+            return r;
+        if (dx && (r = check_rows(dx, lddx, l->K, "dx"))) return r;
+        if (dx && dx_base && (r = check_rows(dx_base, lddx_base, l->K, "dx_base"))) return r;
+        if (dx && dx_base == dx && lddx_base != lddx) return fail(MOE_ERR_ARG, "dx_base is dx with another stride");
+        if (dx && (dx == x || dx == dy)) return fail(MOE_ERR_ARG, "dx is an input");
+    } else if ((r = check_ptr(ranks, 4, "ranks"))) {
+        return r;
+    }
+    if ((r = check_ws(ws, ws_bytes, moe::lora_ws_bytes(l->K, l->N, l->n, l->max_rank, T, true)))) return r;
+    const moe::LoraTable tab = {ids, a_ptrs, b_ptrs, ranks, scales};
+    return hip_status(moe::launch_lora_backward(l->dtype, l->K, l->N, l->n, l->max_rank, x, (size_t)ldx, dy,
+                                                (size_t)lddy, T, tab, dx_base, (size_t)lddx_base, dx, (size_t)lddx,
+                                                da_ptrs, db_ptrs, accumulate, ws, reinterpret_cast<hipStream_t>(stream)),
+                      "adapter gradient launch");
 }
 
 size_t moe_prefetch_sink_bytes(const moe_desc* d, int32_t n) {

@@ -266,6 +266,147 @@ int moe_gemv_fp8(const uint8_t *W, const float *row_scale, const float *x, int32
                  void *stream);
 
 /* ---------------------------------------------------------------------- */
+/* Training the router                                                     */
+/* ---------------------------------------------------------------------- */
+
+/* The router's balance loss, its z loss, the per-expert counts and the
+ * gradient of the logits. A batch is T tokens in S sequences: sequence s
+ * holds the tokens seq_off[s] <= t < seq_off[s + 1] with mask[t] != 0 (its
+ * counted tokens, n_s of them); tokens before seq_off[0], behind seq_off[S]
+ * or with mask[t] == 0 are not counted, and nothing of them is read but the
+ * mask. With p_t = softmax(logits[t]) over all E, lse_t its log-sum-exp,
+ * live = the sequences with n_s > 0 and N = sum n_s:
+ *   counts[s][e] = #{(t, j): t counted in s, idx[t][j] = e}
+ *   probs[s][e]  = mean of p_t[e] over the counted tokens of s (0 if none)
+ *   balance = 1/live sum_s E sum_e counts[s][e] / (n_s k) * probs[s][e]
+ *   z       = 1/N sum_t lse_t^2
+ *   loss    = { balance_coef * balance + z_coef * z, balance, z }
+ *   dlogits = dloss[0] * d loss[0] / d logits, the counts taken as constants;
+ *             0 in the rows of tokens that are not counted
+ * A term whose coefficient is 0 does not enter loss[0] or dlogits. A counted
+ * token whose logits are all -inf has p = 0 and lse = 0. A batch without
+ * counted tokens has the loss 0. Softmax and sums in fp32, in a fixed order:
+ * results are bit-identical from run to run.
+ *   logits  [T][E] fp32, 16-B aligned (e.g. logits_out of moe_route)
+ *   idx     [T][k] int32 (the routing)
+ *   mask    [T] uint8, or NULL: every token counts
+ *   seq_off [S + 1] int32, not decreasing, in [0, T]; or NULL: one sequence
+ *           of T tokens (S must be 1)
+ *   dloss   [1] fp32, or NULL: 1
+ *   loss    [3] fp32 (out)
+ *   counts  [S][E] int32 (out) or NULL;  probs [S][E] fp32 (out) or NULL
+ *   dlogits [T][E] fp32 (out), 16-B aligned, or NULL; not logits itself
+ * If seq_off decreases or leaves [0, T], or a counted token names an expert
+ * outside [0, E), every fp32 output is NaN and every count -1. T = 0 gives
+ * the loss 0 (logits, idx and dlogits are not used). Workspace:
+ * moe_balance_workspace_bytes(d, T, S). Errors: MOE_ERR_ARG (descriptor,
+ * pointers, T < 0, S < 1, coefficients that are not finite);
+ * MOE_ERR_UNSUPPORTED unless E <= 1024, k <= 32, S <= 65535 and T <= 2^24;
+ * MOE_ERR_WORKSPACE. d->H, d->I and d->format only have to be valid. */
+size_t moe_balance_workspace_bytes(const moe_desc *d, int32_t T, int32_t S);
+int moe_balance_loss(const moe_desc *d, const float *logits, int32_t T, const int32_t *idx, const uint8_t *mask,
+                     const int32_t *seq_off, int32_t S, float balance_coef, float z_coef, const float *dloss,
+                     float *loss, int32_t *counts, float *probs, float *dlogits, void *ws, size_t ws_bytes,
+                     void *stream);
+
+#define MOE_ACC_DX 1  /* add to dx instead of writing it */
+#define MOE_ACC_DWR 2 /* add to dWr instead of writing it */
+
+/* The backward pass of moe_route: from dw, the loss's gradient at the
+ * routing weights w, and dlogits_in, a gradient that reaches the logits
+ * directly (moe_balance_loss), to the logits, the layer input and the router.
+ *   ds[t][j] = w[t][j] * (dw[t][j] - sum_i w[t][i] dw[t][i])
+ *   G[t][e]  = dlogits_in[t][e] + sum_{j: idx[t][j] = e} ds[t][j]
+ *   dx = G Wr ([T][H]),  dWr = G^T x ([E][H])
+ * Tokens with mask[t] == 0 have G = 0, and nothing of them is read but the
+ * mask. A token with an index outside [0, E) (dw given) has G = NaN in its
+ * whole row. fp32 operands, products and sums; results are bit-identical
+ * from run to run.
+ *   x [T][H], Wr [E][H] fp32, 16-B aligned (x may be NULL without dWr, Wr
+ *   without dx);  idx [T][k] int32, w [T][k], dw [T][k] fp32 (dw NULL: only
+ *   dlogits_in; idx and w are then not used);  mask [T] uint8 or NULL;
+ *   dlogits_in [T][E] fp32 or NULL (one of dw and dlogits_in is needed);
+ *   dlogits_out [T][E] fp32 (out): G, or NULL; may be dlogits_in;
+ *   dx [T][H], dWr [E][H] fp32 (out), 16-B aligned, or NULL
+ *   accumulate  a sum of MOE_ACC_*
+ * T = 0 writes zeros to dWr (unless it accumulates). Workspace:
+ * moe_route_backward_workspace_bytes(d, T). Errors: MOE_ERR_ARG;
+ * MOE_ERR_UNSUPPORTED unless moe_route supports the descriptor and
+ * T <= 2^20; MOE_ERR_WORKSPACE. */
+size_t moe_route_backward_workspace_bytes(const moe_desc *d, int32_t T);
+int moe_route_backward(const moe_desc *d, const float *x, int32_t T, const float *Wr, const int32_t *idx,
+                       const float *w, const float *dw, const uint8_t *mask, const float *dlogits_in,
+                       float *dlogits_out, float *dx, float *dWr, int32_t accumulate, void *ws, size_t ws_bytes,
+                       void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* Low-rank adapters beside a shared projection                            */
+/* ---------------------------------------------------------------------- */
+
+/* Types of activations (x, base, y and their gradients) and of the factors:
+ * F32: fp32 activations, bf16 factors; BF16: both bf16; F16: both fp16. */
+#define MOE_ACT_F32 0
+#define MOE_ACT_BF16 1
+#define MOE_ACT_F16 2
+
+/* K = input size, N = output size of the projection, n = adapters in the
+ * tables, max_rank = the largest rank among them, dtype = MOE_ACT_*. */
+typedef struct moe_lora_desc {
+    int32_t K, N, n, max_rank, dtype;
+} moe_lora_desc;
+
+/* Many requests share one projection (moe_gemv_fp8, a shared expert's
+ * matrix, any other), each with a low-rank adapter of its own: with
+ * a = ids[t],
+ *   y[t] = base[t] + scales[a] * B_a^T (A_a x[t])        (a < 0: y[t] = base[t])
+ * where base is the projection's output. y may be base (the same rows and
+ * stride). Products and sums in fp32 (16-bit operands multiply exactly, fp32
+ * activations enter with all their bits); the intermediate A_a x stays fp32;
+ * y is rounded once. Results are bit-identical from run to run.
+ *   x     [T] rows of K, stride ldx elements;  base (or NULL: zeros) and y
+ *         [T] rows of N, strides ldbase and ldy. 16-B aligned, strides
+ *         multiples of 8 and at least the row.
+ *   ids   [T] int32: the token's adapter; negative: none
+ *   a_ptrs, b_ptrs  DEVICE arrays of n pointers, 16-B-aligned each: A_a
+ *         [r_a][K] and B_a [r_a][N] (rank-major: B_a is the transpose of the
+ *         usual [N][r]), dense
+ *   ranks [n] int32, 0 .. max_rank;  scales [n] fp32
+ * A token whose id is n or more, or whose adapter's rank is not in
+ * 0 .. max_rank, gets NaN in its row. Only rows of x whose tokens have an
+ * adapter are read. T = 0 enqueues nothing. Workspace:
+ * moe_lora_workspace_bytes(l, T, 0). Errors: MOE_ERR_ARG (descriptor: sizes
+ * not positive, K or N not a multiple of 8, unknown dtype; pointers, strides,
+ * T < 0); MOE_ERR_UNSUPPORTED unless K, N <= 65536, n <= 1024,
+ * max_rank <= 128 and T <= 2^20; MOE_ERR_WORKSPACE. */
+size_t moe_lora_workspace_bytes(const moe_lora_desc *l, int32_t T, int32_t backward);
+int moe_lora_apply(const moe_lora_desc *l, const void *x, int64_t ldx, int32_t T, const int32_t *ids,
+                   const void *const *a_ptrs, const void *const *b_ptrs, const int32_t *ranks, const float *scales,
+                   const void *base, int64_t ldbase, void *y, int64_t ldy, void *ws, size_t ws_bytes, void *stream);
+
+/* The backward pass of moe_lora_apply: with v_t = scales[a] * B_a dy[t] and
+ * u_t = scales[a] * A_a x[t],
+ *   dx[t] = dx_base[t] + A_a^T v_t     (dx_base: the projection's own
+ *           gradient of x, or NULL: zeros; dx may be dx_base; dx may be NULL)
+ *   dA_a  = sum_{t: ids[t] = a} v_t x[t]^T   ([r_a][K] fp32)
+ *   dB_a  = sum_{t: ids[t] = a} u_t dy[t]^T  ([r_a][N] fp32)
+ * Tables, types, alignment and strides as for moe_lora_apply; dy [T] rows of
+ * N. da_ptrs and db_ptrs are DEVICE arrays of n pointers to fp32 memory (16-B
+ * aligned each, no two the same), or NULL; an entry that is NULL skips that
+ * adapter's factor (an adapter that is served but not trained). An adapter
+ * without tokens gets zeros. accumulate != 0 adds to dA and dB instead of
+ * writing them. A token whose id is n or more, or whose adapter's rank is
+ * not in 0 .. max_rank, gets NaN in its row of dx and enters no gradient; the
+ * gradients of an adapter with such a rank are left as they are. Sums over
+ * tokens run in a fixed order: results are bit-identical from run to run.
+ * Workspace: moe_lora_workspace_bytes(l, T, 1). Errors as for
+ * moe_lora_apply. */
+int moe_lora_backward(const moe_lora_desc *l, const void *x, int64_t ldx, const void *dy, int64_t lddy, int32_t T,
+                      const int32_t *ids, const void *const *a_ptrs, const void *const *b_ptrs, const int32_t *ranks,
+                      const float *scales, const void *dx_base, int64_t lddx_base, void *dx, int64_t lddx,
+                      float *const *da_ptrs, float *const *db_ptrs, int32_t accumulate, void *ws, size_t ws_bytes,
+                      void *stream);
+
+/* ---------------------------------------------------------------------- */
 /* Speculative expert prefetch                                             */
 /* ---------------------------------------------------------------------- */
 

@@ -1,0 +1,356 @@
+"""Low-rank adapters on the GPU, forward and backward, against their formulas
+in 64 bits (tests/learn_ref.py) and against differences, over types, ranks,
+orders of tokens and strides; bad ids and ranks; untrained adapters;
+accumulation; no tokens; streams and graphs."""
+import pytest
+import torch
+
+import learn_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module")
+def m():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    import block_scaled_fp4_route_amd as m
+    return m
+
+
+def ptrs(ts):
+    return torch.tensor([0 if t is None else t.data_ptr() for t in ts], dtype=torch.int64, device="cuda")
+
+
+def strided(t, pad):
+    """The same rows with `pad` elements of junk behind each."""
+    if t is None or not pad:
+        return t
+    wide = torch.full((t.shape[0], t.shape[1] + pad), 3.0, dtype=t.dtype, device=t.device)
+    wide[:, :t.shape[1]] = t
+    return wide
+
+
+class Case:
+    def __init__(self, m, dt, T, K, N, ranks, order="mixed", R=None, seed=0):
+        g = torch.Generator().manual_seed(31 * T + K + N + len(ranks) + seed)
+        self.m, self.T, self.K, self.N, self.n, self.dt = m, T, K, N, len(ranks), DT[dt]
+        self.R = R or max(max(ranks), 1)
+        wt = torch.float16 if dt == "f16" else torch.bfloat16
+        rnd = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+        self.A = [(rnd(r, K) * K ** -0.5).to(wt).cuda() for r in ranks]
+        self.B = [(rnd(r, N) * 0.1).to(wt).cuda() for r in ranks]
+        self.ranks = torch.tensor(ranks, dtype=torch.int32).cuda()
+        self.scales = torch.tensor([0.5 + 0.25 * a for a in range(self.n)]).cuda()
+        if order == "mixed":
+            ids = torch.randint(-1, self.n, (T,), generator=g)
+        elif order == "runs":
+            ids = torch.sort(torch.randint(-1, self.n, (T,), generator=g)).values.flip(0)
+        else:  # one adapter for all
+            ids = torch.zeros(T, dtype=torch.int64)
+        self.ids = ids.to(torch.int32).cuda()
+        self.x, self.dy = rnd(T, K).to(self.dt).cuda(), rnd(T, N).to(self.dt).cuda()
+        self.base, self.dxb = rnd(T, N).to(self.dt).cuda(), rnd(T, K).to(self.dt).cuda()
+        self.l = m.lora_desc(K, N, self.n, self.R, self.dt)
+        self.tabs = None
+
+    def table(self):
+        if self.tabs is None:
+            self.tabs = (ptrs(self.A), ptrs(self.B))
+        return (self.ids, *self.tabs, self.ranks, self.scales)
+
+    def ws(self, back):
+        return torch.full((self.m.moe_lora_workspace_bytes(self.l, self.T, back),), 0xA5, dtype=torch.uint8, device="cuda")
+
+    def apply(self, base="own", inplace=False, pads=(0, 0, 0), stream=None, ws=None):
+        T, K, N = self.T, self.K, self.N
+        x, b = strided(self.x, pads[0]), None if base is None else strided(self.base.clone(), pads[1])
+        y = b if inplace else torch.full((T, N + pads[2]), 7.0, dtype=self.dt, device="cuda")
+        self.args = (self.l, x, K + pads[0], T, *self.table(), b, N + pads[1], y, y.shape[1] if T else N,
+                     self.ws(False) if ws is None else ws)
+        torch.cuda.synchronize()
+        self.m.moe_lora_apply(*self.args, stream=stream)
+        torch.cuda.synchronize()
+        if y.shape[1] > N:
+            junk = 3.0 if inplace else 7.0
+            assert (y[:, N:] == junk).all()  # nothing behind the rows is written
+        return y[:, :N]
+
+    def want(self, base="own"):
+        return ref.lora(self.x, self.ids, self.A, self.B, self.scales, None if base is None else self.base, self.dt, self.n)
+
+    def backward(self, dx=True, base=True, grads=True, acc=0, old=None, skip=(), pads=(0, 0, 0), inplace=False, ws=None):
+        T, K, N = self.T, self.K, self.N
+        x, dy = strided(self.x, pads[0]), strided(self.dy, pads[1])
+        b = strided(self.dxb.clone(), pads[2]) if base else None
+        o = b if inplace else torch.full((T, K + pads[2]), 7.0, dtype=self.dt, device="cuda")
+        self.dA = [torch.full(a.shape, 7.0, device="cuda") if old is None else old[0][i].clone() for i, a in enumerate(self.A)]
+        self.dB = [torch.full(a.shape, 7.0, device="cuda") if old is None else old[1][i].clone() for i, a in enumerate(self.B)]
+        self.gp = (ptrs([None if ("A", i) in skip else t for i, t in enumerate(self.dA)]),
+                   ptrs([None if ("B", i) in skip else t for i, t in enumerate(self.dB)]))
+        self.args = (self.l, x, K + pads[0], dy, N + pads[1], T, *self.table(), b, K + pads[2], o if dx else None, K + pads[2],
+                     *(self.gp if grads else (None, None)), acc, self.ws(True) if ws is None else ws)
+        torch.cuda.synchronize()
+        self.m.moe_lora_backward(*self.args)
+        torch.cuda.synchronize()
+        return o[:, :K] if dx else None
+
+    def check_backward(self, dx, base=True):
+        if dx is not None:
+            v = ref.lora(self.dy, self.ids, self.B, self.A, self.scales, self.dxb if base else None, self.dt, self.n)
+            ref.close(dx, *v, "dx")
+        for a, (wa, wb) in enumerate(ref.lora_grads(self.x, self.dy, self.ids, self.A, self.B, self.scales, self.n)):
+            ref.close(self.dA[a], *wa, ("dA", a))
+            ref.close(self.dB[a], *wb, ("dB", a))
+
+
+SHAPES = [(1, 8, 8, [1], "one"), (1, 2560, 8192, [16, 8], "one"), (2, 16, 2560, [3, 1, 0], "mixed"),
+          (17, 264, 40, [5, 16, 7], "mixed"), (64, 2560, 640, [16] * 8, "mixed"), (65, 2560, 640, [16] * 8, "mixed"),
+          (65, 8, 8, [128], "one"), (130, 520, 1032, [33, 64, 1, 17], "mixed"), (300, 640, 2560, [8, 3], "runs"),
+          (257, 1000, 264, [128, 100], "mixed"), (700, 256, 512, [20, 31, 48], "runs"), (1500, 136, 24, [2] * 40, "mixed")]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,K,N,ranks,order", SHAPES)
+def test_apply(m, dt, T, K, N, ranks, order):
+    c = Case(m, dt, T, K, N, ranks, order)
+    ref.close(c.apply(), *c.want(), "y")
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,K,N,ranks,order", SHAPES)
+def test_backward(m, dt, T, K, N, ranks, order):
+    c = Case(m, dt, T, K, N, ranks, order)
+    c.check_backward(c.backward())
+
+
+@pytest.mark.parametrize("T", [5, 200])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_bases_places_and_strides(m, dt, T):
+    c = Case(m, dt, T, 264, 520, [16, 5, 9])
+    y = c.apply()
+    assert torch.equal(y, c.apply(inplace=True))
+    assert torch.equal(y, c.apply(pads=(8, 16, 24)))
+    assert torch.equal(y, c.apply(pads=(24, 8, 8), inplace=True))
+    ref.close(c.apply(base=None), *c.want(base=None), "y")
+    rows = c.ids < 0
+    assert torch.equal(y[rows], c.base[rows]) and rows.any()
+    dx = c.backward()
+    first = [t.clone() for t in c.dA + c.dB]
+    for kw in ({"inplace": True}, {"pads": (8, 16, 24)}, {"pads": (16, 8, 8), "inplace": True}):
+        assert torch.equal(dx, c.backward(**kw))
+        assert all(torch.equal(a, b) for a, b in zip(first, c.dA + c.dB))
+    c.check_backward(c.backward(base=False), base=False)
+    assert c.backward(dx=False) is None
+    assert all(torch.equal(a, b) for a, b in zip(first, c.dA + c.dB))
+    assert torch.equal(dx, c.backward(grads=False))
+
+
+@pytest.mark.parametrize("T", [40, 400])
+def test_max_rank_above_the_ranks(m, T):
+    """The tables' largest rank only sizes the workspace; results agree with the tight one to the bound."""
+    for R in (16, 30, 40, 128):
+        c = Case(m, "bf16", T, 264, 520, [16, 5, 9], R=R)
+        ref.close(c.apply(), *c.want(), "y")
+        c.check_backward(c.backward())
+
+
+@pytest.mark.parametrize("T", [6, 90])
+def test_no_adapter_at_all(m, T):
+    c = Case(m, "bf16", T, 264, 520, [16, 5])
+    c.ids.fill_(-3)
+    c.x.fill_(float("nan"))  # rows without an adapter are not read
+    assert torch.equal(c.apply(), c.base) and torch.equal(c.apply(inplace=True), c.base)
+    assert not c.apply(base=None).any()
+    dx = c.backward()
+    assert torch.equal(dx, c.dxb) and all(not t.any() for t in c.dA + c.dB)
+
+
+@pytest.mark.parametrize("T", [8, 150])
+def test_bad_ids(m, T):
+    c = Case(m, "f32", T, 64, 72, [4, 4])
+    c.ids[3], c.ids[T - 1] = 2, 1 << 30
+    ref.close(c.apply(), *c.want(), "y")
+    assert torch.isnan(c.apply()[3]).all()
+    c.check_backward(c.backward())
+
+
+@pytest.mark.parametrize("T", [8, 150])
+@pytest.mark.parametrize("bad", [-1, 17, 1 << 30])
+def test_bad_rank(m, T, bad):
+    c = Case(m, "f32", T, 64, 72, [16, 4, 16])
+    c.ids[:4] = 1
+    y, v = c.apply(), c.want()
+    dx = c.backward()
+    good = [t.clone() for t in c.dA + c.dB]
+    c.ranks[1] = bad
+    y2, rows = c.apply(), c.ids == 1
+    assert torch.isnan(y2[rows]).all() and torch.equal(y2[~rows], y[~rows])
+    dx2 = c.backward()
+    assert torch.isnan(dx2[rows]).all() and torch.equal(dx2[~rows], dx[~rows])
+    for i, (a, b) in enumerate(zip(good, c.dA + c.dB)):
+        assert (b == 7.0).all() if i % 3 == 1 else torch.equal(a, b)
+    ref.close(y, *v, "y")
+
+
+@pytest.mark.parametrize("T", [20, 900])
+def test_accumulate_and_untrained(m, T):
+    c = Case(m, "bf16", T, 264, 136, [8, 3, 5, 2])
+    c.ids[c.ids == 3] = 0  # adapter 3 has no token
+    c.check_backward(c.backward())
+    assert not c.dA[3].any() and not c.dB[3].any()
+    g = torch.Generator().manual_seed(2)
+    old = ([torch.randn(a.shape, generator=g).cuda() for a in c.A], [torch.randn(b.shape, generator=g).cuda() for b in c.B])
+    c.backward(acc=1, old=old, skip={("A", 1), ("B", 2)})
+    want = ref.lora_grads(c.x, c.dy, c.ids, c.A, c.B, c.scales, c.n)
+    for a in range(4):
+        for name, got, o, (v, e) in (("A", c.dA[a], old[0][a], want[a][0]), ("B", c.dB[a], old[1][a], want[a][1])):
+            if (name, a) in {("A", 1), ("B", 2)}:
+                assert torch.equal(got, o)
+            else:
+                ref.close(got, v + o.cpu().double(), e + 2 * ref.EPS * (v.abs() + o.cpu().double().abs()), (name, a))
+    assert torch.equal(c.dA[3], old[0][3])
+
+
+def test_one_side_only(m):
+    c = Case(m, "f16", 100, 64, 72, [4, 8])
+    c.backward()
+    dA, dB = [t.clone() for t in c.dA], [t.clone() for t in c.dB]
+    args = list(c.args)
+    for t in c.dA + c.dB:
+        t.fill_(7.0)
+    m.moe_lora_backward(*args[:15], c.gp[0], None, 0, args[-1])
+    assert all(torch.equal(a, b) for a, b in zip(dA, c.dA)) and all((t == 7).all() for t in c.dB)
+    m.moe_lora_backward(*args[:15], None, c.gp[1], 0, args[-1])
+    assert all(torch.equal(a, b) for a, b in zip(dB, c.dB))
+
+
+def test_no_tokens(m):
+    c = Case(m, "bf16", 0, 64, 72, [4, 8])
+    c.apply()
+    c.backward()
+    assert all(not t.any() for t in c.dA + c.dB)
+    old = ([torch.ones_like(t) for t in c.dA], [torch.ones_like(t) for t in c.dB])
+    c.backward(acc=1, old=old)
+    assert all((t == 1).all() for t in c.dA + c.dB)
+
+
+def test_infinite_activations(m):
+    """An infinity reaches its own row as fp32 arithmetic has it, and no other row."""
+    for dt in DT:
+        for T in (9, 100):
+            c = Case(m, dt, T, 64, 72, [4], "one")
+            y = c.apply()
+            c.x[2, 5], c.x[4, 9] = float("inf"), float("nan")
+            z = c.apply()
+            rest = [t for t in range(T) if t not in (2, 4)]
+            assert torch.equal(y[rest], z[rest])
+            assert not torch.isfinite(z[2]).any() and torch.isnan(z[4]).all()
+
+
+def test_fp32_activations_keep_all_bits(m):
+    """x = 1 + 2^-23 against a factor row that cancels the ones: what is left
+    is the last bit, which a rounded activation would lose."""
+    for T in (3, 70):
+        c = Case(m, "f32", T, 16, 8, [1], "one")
+        c.x[:] = 1.0 + 2.0 ** -23
+        c.x[:, 8:] = 1.0
+        c.A[0][0, :8], c.A[0][0, 8:] = 1.0, -1.0
+        c.B[0][:] = 1.0
+        c.scales[:] = 1.0
+        y = c.apply(base=None)
+        assert (y == 8 * 2.0 ** -23).all()
+
+
+def test_strides_past_32_bits(m):
+    """Rows 2^31 and more elements apart."""
+    c = Case(m, "bf16", 3, 64, 72, [4], "one")
+    y, dx = c.apply(), None
+    ld = (1 << 30) + 64
+    wide = torch.empty(2 * ld + 128, dtype=torch.bfloat16, device="cuda")
+    xw = wide.as_strided((3, 64), (ld, 1))
+    xw.copy_(c.x)
+    out = torch.empty(2 * ld + 128, dtype=torch.bfloat16, device="cuda")
+    m.moe_lora_apply(c.l, wide, ld, 3, *c.table(), c.base, 72, out, ld, c.ws(False))
+    assert torch.equal(out.as_strided((3, 72), (ld, 1)), y)
+    dx = c.backward()
+    m.moe_lora_backward(c.l, wide, ld, c.dy, 72, 3, *c.table(), c.dxb, 64, out, ld, None, None, 0, c.ws(True))
+    assert torch.equal(out.as_strided((3, 64), (ld, 1)), dx)
+    # and through the grouped kernels
+    T = 70
+    c = Case(m, "bf16", T, 64, 72, [4], "one")
+    y = c.apply()
+    ld = (1 << 31) // 64 + 64
+    wide = torch.empty((T - 1) * ld + 128, dtype=torch.bfloat16, device="cuda")
+    wide.as_strided((T, 64), (ld, 1)).copy_(c.x)
+    out = torch.empty((T - 1) * ld + 128, dtype=torch.bfloat16, device="cuda")
+    m.moe_lora_apply(c.l, wide, ld, T, *c.table(), c.base, 72, out, ld, c.ws(False))
+    assert torch.equal(out.as_strided((T, 72), (ld, 1)), y)
+
+
+def test_gradients_against_differences(m):
+    """y is linear in each factor, so the difference of the framework's own
+    fp32 forward over a step h of one element is exact up to its rounding:
+    off by at most sum|dy| times y's bound over h, beside the gradient's own bound."""
+    c = Case(m, "f32", 70, 24, 16, [3, 2])
+    c.backward(dx=False)
+    dA, dB = [t.clone() for t in c.dA], [t.clone() for t in c.dB]
+    h = 0.5
+    bounds = ref.lora_grads(c.x, c.dy, c.ids, c.A, c.B, c.scales, c.n)
+    for side, (facs, grads) in enumerate(((c.A, dA), (c.B, dB))):
+        for a in range(2):
+            for (i, j) in ((0, 0), (1, 7), (facs[a].shape[0] - 1, 15)):
+                old = facs[a][i, j].item()
+                ys, steps, off = [], [], 0.0
+                for sign in (1, -1):
+                    facs[a][i, j] = old + sign * h  # rounded to bf16; the step taken is what counts
+                    steps.append(facs[a][i, j].item())
+                    ys.append((c.apply().double() * c.dy.double()).sum().item())
+                    off += (c.want()[1] * c.dy.cpu().double().abs()).sum().item()
+                facs[a][i, j] = old
+                diff = (ys[0] - ys[1]) / (steps[0] - steps[1])
+                assert abs(diff - grads[a][i, j].item()) \
+                    <= off / abs(steps[0] - steps[1]) + bounds[a][side][1][i, j].item()
+
+
+def test_repeats_streams_and_graphs(m):
+    cases = [Case(m, "bf16", 300, 264, 520, [16, 5, 9]), Case(m, "f16", 40, 520, 264, [8, 30]), Case(m, "f32", 90, 64, 72, [128])]
+    need = max(m.moe_lora_workspace_bytes(c.l, c.T, True) for c in cases)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    runs = []
+    for c in cases:
+        want = c.apply(), c.backward(), [t.clone() for t in c.dA + c.dB]
+        y = c.apply(ws=ws)
+        fwd = c.args
+        dx = c.backward(ws=ws)
+        bwd = c.args
+        assert torch.equal(y, want[0]) and torch.equal(dx, want[1])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            m.moe_lora_apply(*fwd)
+            m.moe_lora_backward(*bwd)
+        runs.append((c, y, dx, list(c.dA + c.dB), want, g, fwd, bwd))
+    for turn in range(3):
+        for c, y, dx, gr, want, g, fwd, bwd in runs:
+            for t in (y, dx, *gr):
+                t.fill_(9)
+        for r in (runs if turn % 2 else runs[::-1]):
+            r[5].replay()
+        torch.randn(1000, device="cuda").sum()
+        torch.cuda.synchronize()
+        for c, y, dx, gr, want, g, fwd, bwd in runs:
+            assert torch.equal(y, want[0]) and torch.equal(dx, want[1]) and all(torch.equal(a, b) for a, b in zip(gr, want[2]))
+        m.moe_lora_apply(*runs[0][6])
+    # two at once, each with its own workspace, on streams of their own
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    a, b = runs[0], runs[1]
+    for r in (a, b):
+        r[1].fill_(9)
+    wa, wb = a[0].ws(False), b[0].ws(False)
+    torch.cuda.synchronize()
+    m.moe_lora_apply(*a[6][:-1], wa, stream=sa)
+    m.moe_lora_apply(*b[6][:-1], wb, stream=sb)
+    torch.cuda.synchronize()
+    assert torch.equal(a[1], a[4][0]) and torch.equal(b[1], b[4][0])

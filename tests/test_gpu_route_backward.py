@@ -1,0 +1,242 @@
+"""The routing's gradient on the GPU against its formulas in 64 bits
+(tests/learn_ref.py), against torch's autograd of the routing, and on its
+edges: masks, duplicate and bad experts, accumulation, no tokens, graphs."""
+import pytest
+import torch
+
+import learn_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    import block_scaled_fp4_route_amd as m
+    return m
+
+
+class Case:
+    def __init__(self, m, T, E, k, H, masked=0.0, seed=0):
+        g = torch.Generator().manual_seed(7000 * T + 10 * E + k + H + seed)
+        self.m, self.T, self.E, self.k, self.H = m, T, E, k, H
+        rnd = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+        self.x, self.Wr, self.dw, self.din = rnd(T, H), rnd(E, H) * 0.02, rnd(T, k) * 0.1, rnd(T, E) * 1e-3
+        top = torch.topk(rnd(T, E), k, dim=1)
+        self.idx, self.w = top.indices.to(torch.int32), torch.softmax(top.values, 1)
+        self.mask = (torch.rand(T, generator=g) >= masked) if masked else None
+
+    def run(self, dw=True, din=True, dx=True, dWr=True, acc=0, before=None, inplace=False, ws=None):
+        m, T, E, H, dev = self.m, self.T, self.E, self.H, "cuda"
+        self.d = m.desc(H, 64, E, self.k, "nvfp4")
+        up = lambda t: t.to(dev).contiguous()  # noqa: E731
+        self.dev = [up(t) for t in (self.x, self.Wr, self.idx, self.w, self.dw, self.din)]
+        x, Wr, idx, w, dwd, dind = self.dev
+        md = None if self.mask is None else self.mask.to(torch.uint8).to(dev)
+        before = before or {}
+        out = {"dlogits": dind if inplace else torch.full((T, E), 7.0, device=dev),
+               "dx": up(before["dx"]) if "dx" in before else torch.full((T, H), 7.0, device=dev),
+               "dWr": up(before["dWr"]) if "dWr" in before else torch.full((E, H), 7.0, device=dev)}
+        n = m.moe_route_backward_workspace_bytes(self.d, T)
+        ws = torch.full((n,), 0xA5, dtype=torch.uint8, device=dev) if ws is None else ws
+        self.args = (self.d, x, T, Wr, idx, w, dwd if dw else None, md, dind if din else None, out["dlogits"],
+                     out["dx"] if dx else None, out["dWr"] if dWr else None, acc, ws)
+        m.moe_route_backward(*self.args)
+        torch.cuda.synchronize()
+        return {"dlogits": out["dlogits"], "dx": out["dx"] if dx else None, "dWr": out["dWr"] if dWr else None}
+
+    def want(self, dw=True, din=True):
+        return ref.route_backward(self.x, self.Wr, self.idx, self.w, self.dw if dw else None, self.mask,
+                                  self.din if din else None, self.T, self.E, self.k)
+
+    def check(self, out, dw=True, din=True):
+        want = self.want(dw, din)
+        for name, v in out.items():
+            if v is not None:
+                ref.close(v, *want[name], name)
+
+
+@pytest.mark.parametrize("T,E,k,H", [(1, 1, 1, 256), (1, 512, 10, 2560), (2, 5, 5, 256), (17, 384, 6, 4096), (33, 33, 3, 512),
+                                     (64, 64, 8, 768), (127, 129, 2, 256), (129, 130, 32, 1280), (311, 384, 6, 512),
+                                     (600, 512, 10, 256), (70, 1023, 7, 256), (40, 1024, 32, 8192), (5000, 9, 2, 256)])
+def test_shapes(m, T, E, k, H):
+    c = Case(m, T, E, k, H)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("dw,din,dx,dWr", [(True, False, True, True), (False, True, True, True), (True, True, False, True),
+                                           (True, True, True, False), (True, True, False, False)])
+def test_parts_left_out(m, dw, din, dx, dWr):
+    c = Case(m, 90, 60, 4, 512, 0.2)
+    c.check(c.run(dw, din, dx, dWr), dw, din)
+
+
+def test_norm_of_the_error(m):
+    """Beside the elementwise worst case: roundings of both signs add up like
+    a random walk, sqrt(K) EPS / sqrt(3) of the products' norm; four times
+    that is allowed, plus 4 EPS for the operands."""
+    c = Case(m, 2451, 512, 10, 2560)
+    out, want = c.run(), c.want()
+    for name, K, a, b in (("dx", 512, want["dlogits"][0], c.Wr.double()), ("dWr", 2451, want["dlogits"][0].t(), c.x.double())):
+        size = torch.sqrt((a ** 2) @ (b ** 2))  # root of the sum of squared products
+        off = (out[name].cpu().double() - want[name][0]).norm() / size.norm()
+        assert off <= 4 * (K ** 0.5) * ref.EPS / 3 ** 0.5 + 4 * ref.EPS, (name, off)
+
+
+def test_masked_rows_hold_anything(m):
+    a, b = Case(m, 200, 96, 5, 512, 0.4), Case(m, 200, 96, 5, 512, 0.4)
+    off = (~b.mask).nonzero()[:, 0]
+    b.x[off] = float("nan")
+    b.dw[off] = float("inf")
+    b.din[off[::2]] = float("nan")
+    b.din[off[1::2]] = -float("inf")
+    b.idx[off] = -7
+    x, y = a.run(), b.run()
+    for name in x:
+        assert torch.equal(x[name], y[name]), name
+    a.check(x)
+    assert not x["dx"][off.cuda()].any()
+
+
+def test_all_masked(m):
+    c = Case(m, 30, 24, 3, 256)
+    c.mask = torch.zeros(30, dtype=torch.bool)
+    out = c.run()
+    assert all(not v.any() for v in out.values())
+
+
+def test_an_expert_named_twice(m):
+    c = Case(m, 50, 40, 4, 256)
+    c.idx[:, 2] = c.idx[:, 0]
+    c.idx[::2, 3] = c.idx[::2, 0]
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("bad", [-1, 40, 1 << 30])
+def test_bad_expert(m, bad):
+    c = Case(m, 50, 40, 4, 256)
+    c.idx[20, 2] = bad
+    out = c.run()
+    assert torch.isnan(out["dlogits"][20]).all() and torch.isnan(out["dx"][20]).all() and torch.isnan(out["dWr"]).all()
+    rest = [t for t in range(50) if t != 20]
+    c.idx[20, 2] = 0
+    want = c.want()
+    for name in ("dlogits", "dx"):
+        ref.close(out[name][rest], want[name][0][rest], want[name][1][rest], name)
+    # without dw the experts are not looked at
+    c.idx[20, 2] = bad
+    c.check(c.run(dw=False), dw=False)
+
+
+@pytest.mark.parametrize("T", [30, 700])
+def test_accumulate(m, T):
+    c = Case(m, T, 40, 4, 256)
+    g = torch.Generator().manual_seed(1)
+    old = {"dx": torch.randn((T, 256), generator=g), "dWr": torch.randn((40, 256), generator=g)}
+    want = c.want()
+    for acc in (1, 2, 3):
+        out = c.run(acc=acc, before=old)
+        for bit, name in ((1, "dx"), (2, "dWr")):
+            v, e = want[name]
+            if acc & bit:
+                v, e = v + old[name].double(), e + ref.EPS * (v.abs() + old[name].double().abs()) * 2
+            ref.close(out[name], v, e, name)
+
+
+def test_in_place_on_dlogits(m):
+    c = Case(m, 90, 60, 4, 512, 0.2)
+    a, b = c.run(), c.run(inplace=True)
+    for name in a:
+        assert torch.equal(a[name], b[name]), name
+
+
+def test_no_tokens(m):
+    c = Case(m, 0, 40, 4, 256)
+    out = c.run()
+    assert not out["dWr"].any()
+    old = torch.randn(40, 256)
+    assert torch.equal(c.run(acc=2, before={"dWr": old})["dWr"].cpu(), old)
+
+
+def test_against_autograd(m):
+    """The gradient of sum(dw * w(logits)) + sum(din * logits) by torch's autograd in 64 bits."""
+    c = Case(m, 60, 48, 5, 256)
+    x, Wr = c.x.double().requires_grad_(), c.Wr.double().requires_grad_()
+    logits = x @ Wr.t()
+    logits.retain_grad()
+    idx = torch.topk(logits, 5, dim=1).indices
+    w = torch.softmax(logits.gather(1, idx), 1)
+    ((w * c.dw.double()).sum() + (logits * c.din.double()).sum()).backward()
+    c.idx, c.w = idx.to(torch.int32), w.detach().float()
+    out, want = c.run(), c.want()
+    for name, g in (("dlogits", logits.grad), ("dx", x.grad), ("dWr", Wr.grad)):
+        # w is rounded to fp32 before the call: one EPS of it more in ds, through both products
+        more = (4 * ref.EPS * g.abs() + 4 * ref.EPS * g.abs().max())
+        ref.close(out[name], g, want[name][1] + more, name)
+
+
+def test_large_and_small_values(m):
+    """Rows, columns and tokens of very unlike sizes keep fp32's relative accuracy."""
+    c = Case(m, 150, 96, 5, 512)
+    g = torch.Generator().manual_seed(5)
+    c.din *= 2.0 ** torch.randint(-30, 30, (150, 1), generator=g)
+    c.Wr *= 2.0 ** torch.randint(-30, 30, (1, 512), generator=g)
+    c.check(c.run(dw=False, dWr=False), dw=False)
+    c = Case(m, 150, 96, 5, 512)
+    c.din *= 2.0 ** torch.randint(-30, 30, (1, 96), generator=g)
+    c.x *= 2.0 ** torch.randint(-30, 30, (1, 512), generator=g)
+    c.check(c.run(dw=False, dx=False), dw=False)
+
+
+def test_infinite_and_nan_values(m):
+    c = Case(m, 40, 33, 3, 256)
+    c.din[5, 3] = float("inf")
+    c.din[9, 8] = float("nan")
+    c.Wr[3, 17] = 0.0
+    out, want = c.run(dw=False), c.want(dw=False)
+    ok = [t for t in range(40) if t not in (5, 9)]
+    ref.close(out["dx"][ok], want["dx"][0][ok], want["dx"][1][ok], "dx")
+    assert not torch.isfinite(out["dx"][5]).any() and torch.isnan(out["dx"][9]).all()
+    ok = [e for e in range(33) if e not in (3, 8)]
+    ref.close(out["dWr"][ok], want["dWr"][0][ok], want["dWr"][1][ok], "dWr")
+    assert not torch.isfinite(out["dWr"][3]).any() and torch.isnan(out["dWr"][8]).all()
+
+
+def test_repeats_streams_and_graphs(m):
+    a, b = Case(m, 700, 130, 6, 512, 0.1), Case(m, 300, 256, 8, 256)
+    want = []
+    graphs = []
+    ws = torch.zeros(max(m.moe_route_backward_workspace_bytes(m.desc(c.H, 64, c.E, c.k, "nvfp4"), c.T) for c in (a, b)),
+                     dtype=torch.uint8, device="cuda")
+    for c in (a, b):
+        first = c.run()
+        again = c.run(ws=ws)
+        for name in first:
+            assert torch.equal(first[name], again[name]), name
+        c.out = again
+        want.append(first)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            m.moe_route_backward(*c.args)
+        graphs.append(g)
+    for turn in range(3):
+        for c in (a, b):
+            for v in c.out.values():
+                v.fill_(9)
+        for g in (graphs if turn % 2 else graphs[::-1]):
+            g.replay()
+        torch.randn(1000, device="cuda").sum()
+        torch.cuda.synchronize()
+        for c, w in zip((a, b), want):
+            for k, v in c.out.items():
+                assert torch.equal(v, w[k]), (turn, k)
+        m.moe_route_backward(*a.args)
+    s = torch.cuda.Stream()
+    for v in a.out.values():
+        v.fill_(9)
+    torch.cuda.synchronize()
+    m.moe_route_backward(*a.args, stream=s)
+    s.synchronize()
+    for k, v in a.out.items():
+        assert torch.equal(v, want[0][k])
