@@ -31,9 +31,12 @@ namespace {
 
 constexpr int kBadSeq = -1;  // n_s of a sequence with a bad offset or a bad expert index
 
+constexpr int kSelfCount = 8192;  // T * k up to which k_bal_main counts by itself
+
 // Workspace regions (all 256-byte aligned).
 struct BalWs {
     int J;           // parts per sequence of the counting launch
+    int JM;          // parts that k_bal_main finds (1 behind k_bal_merge)
     int TB;          // tokens per chunk of the main launch
     int chunks;
     size_t part, cnt, n, ticket, psum, zsum, q, total;
@@ -41,10 +44,14 @@ struct BalWs {
 
 BalWs bal_ws(int T, int E, int S) {
     BalWs b;
-    // about 512 tokens per counting workgroup, 64 parts at most
+    // about 1024 tokens per counting workgroup, 64 parts at most; several
+    // sequences, which may be of unlike lengths, get 4 parts where that still
+    // leaves 128 tokens each; the main launch adds up to 4 parts itself
     const int64_t per = ((int64_t)T + S - 1) / S;
-    b.J = (int)((per + 511) / 512);
+    b.J = (int)((per + 1023) / 1024);
+    if (S > 1 && b.J < 4) b.J = (int)(per / 128 < 4 ? per / 128 : 4);
     b.J = b.J < 1 ? 1 : (b.J > 64 ? 64 : b.J);
+    b.JM = b.J <= 4 ? b.J : 1;
     // about 1024 chunks (four workgroups per compute unit) of whole rounds of
     // the four waves
     b.TB = (int)(((int64_t)T + 1023) / 1024);
@@ -58,9 +65,9 @@ BalWs bal_ws(int T, int E, int S) {
         return at;
     };
     const size_t row = (size_t)E * 4;
-    b.part = take(b.J > 1 ? (size_t)S * b.J * (row + 4) : 0);
-    b.cnt = take((size_t)S * row);
-    b.n = take((size_t)S * 4);
+    b.part = take(b.J > b.JM ? (size_t)S * b.J * (row + 4) : 0);
+    b.cnt = take((size_t)S * b.JM * row);
+    b.n = take((size_t)S * b.JM * 4);
     b.ticket = take(4);
     b.psum = take(((size_t)b.chunks + S) * row);
     b.zsum = take(((size_t)b.chunks + S) * 4);
@@ -76,42 +83,66 @@ __device__ __forceinline__ bool seq_bounds(const int32_t* __restrict__ off, int 
     return lo >= 0 && lo <= hi && hi <= T;
 }
 
-// grid (J, S), 256 threads: counts of the tokens of part j of sequence s.
-__global__ __launch_bounds__(256) void k_bal_count(const int32_t* __restrict__ idx, const uint8_t* __restrict__ mask,
-                                                   const int32_t* __restrict__ off, int T, int E, int k, int J,
-                                                   int32_t* __restrict__ cnt, int32_t* __restrict__ n,
-                                                   uint32_t* __restrict__ ticket) {
+// Adds the routing of tokens a .. b - 1 to hist (LDS) by NT threads, eight
+// loads in flight each; returns whether this thread saw a bad index, and its
+// share of the counted tokens in `mine`.
+template <int NT>
+__device__ __forceinline__ bool bal_hist(const int32_t* __restrict__ idx, const uint8_t* __restrict__ mask, int a,
+                                         int b, int E, int k, int* hist, int& mine) {
+    constexpr int U = 8;
+    const int64_t i1 = (int64_t)b * k;
+    bool bad = false;
+    mine = 0;
+    if (mask)
+        for (int t = a + (int)threadIdx.x; t < b; t += NT) mine += mask[t] != 0;
+    else if (threadIdx.x == 0)
+        mine = b - a;
+    for (int64_t i = (int64_t)a * k + threadIdx.x; i < i1; i += U * NT) {
+        int e[U];
+        bool on[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int64_t q = i + u * NT;
+            on[u] = q < i1;
+            e[u] = on[u] ? idx[q] : 0;
+            if (mask && on[u]) on[u] = mask[(uint32_t)q / (uint32_t)k] != 0;  // T * k < 2^30
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const bool in = (unsigned)e[u] < (unsigned)E;
+            if (on[u] && in) atomicAdd(&hist[e[u]], 1);
+            bad |= on[u] && !in;
+        }
+    }
+    return bad;
+}
+
+// grid (J, S), 1024 threads: counts of the tokens of part j of sequence s.
+__global__ __launch_bounds__(1024) void k_bal_count(const int32_t* __restrict__ idx, const uint8_t* __restrict__ mask,
+                                                    const int32_t* __restrict__ off, int T, int E, int k, int J,
+                                                    int32_t* __restrict__ cnt, int32_t* __restrict__ n,
+                                                    uint32_t* __restrict__ ticket) {
     __shared__ int hist[kMaxE];
     __shared__ int tot[2];
     const int j = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
-    for (int e = tid; e < E; e += 256) hist[e] = 0;
+    if (tid < E) hist[tid] = 0;
     if (tid < 2) tot[tid] = 0;
     if (tid == 0 && j == 0 && s == 0) *ticket = 0;
-    __syncthreads();
     int lo, hi;
     const bool fine = seq_bounds(off, s, T, lo, hi);
-    int mine = 0, bad = fine ? 0 : 1;
+    __syncthreads();
+    int mine = 0;
+    bool bad = !fine;
     if (fine) {
         const int per = (hi - lo + J - 1) / J;
         const int a = (int)min((int64_t)hi, lo + (int64_t)j * per), b = (int)min((int64_t)hi, (int64_t)a + per);
-        for (int t = a + tid; t < b; t += 256) {
-            if (mask && !mask[t]) continue;
-            mine++;
-            const int32_t* it = idx + (size_t)t * k;
-            for (int i = 0; i < k; i++) {
-                const int e = it[i];
-                if ((unsigned)e < (unsigned)E)
-                    atomicAdd(&hist[e], 1);
-                else
-                    bad = 1;
-            }
-        }
+        bad = bal_hist<1024>(idx, mask, a, b, E, k, hist, mine);
     }
     if (mine) atomicAdd(&tot[0], mine);
     if (bad) atomicOr(&tot[1], 1);
     __syncthreads();
     const size_t p = (size_t)s * J + j;
-    for (int e = tid; e < E; e += 256) cnt[p * E + e] = hist[e];
+    if (tid < E) cnt[p * E + tid] = hist[tid];
     if (tid == 0) n[p] = tot[1] ? kBadSeq : tot[0];
 }
 
@@ -137,12 +168,24 @@ __global__ __launch_bounds__(256) void k_bal_merge(const int32_t* __restrict__ p
     }
 }
 
+// Counted tokens of sequence s from its parts; kBadSeq if one of them is bad.
+__device__ __forceinline__ int seq_n(const int32_t* __restrict__ n, int s, int J) {
+    int a = 0;
+    bool bad = false;
+    for (int j = 0; j < J; j++) {
+        const int v = n[(size_t)s * J + j];
+        bad |= v < 0;
+        a += v;
+    }
+    return bad ? kBadSeq : a;
+}
+
 // Live sequences and counted tokens over all S (every thread of a workgroup
 // of NT threads gets them); false if any sequence is bad.
 template <int NT>
-__device__ __forceinline__ bool bal_totals(const int32_t* __restrict__ n, int S, int& live, int& total) {
+__device__ __forceinline__ bool bal_totals(const int32_t* __restrict__ n, int S, int J, int& live, int& total) {
     if (S == 1) {
-        const int v = n[0];
+        const int v = seq_n(n, 0, J);
         live = v > 0;
         total = v;
         return v >= 0;
@@ -152,7 +195,7 @@ __device__ __forceinline__ bool bal_totals(const int32_t* __restrict__ n, int S,
     __syncthreads();
     int l = 0, t = 0, b = 0;
     for (int s = threadIdx.x; s < S; s += NT) {
-        const int v = n[s];
+        const int v = seq_n(n, s, J);
         l += v > 0;
         t += max(v, 0);
         b |= v < 0;
@@ -215,11 +258,15 @@ __device__ __forceinline__ void row_store(float* __restrict__ row, int E, int la
 // grid chunks, 256 threads. A chunk's tokens are cut at the sequences'
 // bounds; the piece of sequence s in chunk c writes its sums at row c + s
 // (pieces follow one another with c or s growing, so no two share a row).
-// Each wave takes every fourth token of a piece, a lane 64 NV / 64 columns.
-template <int NV, bool VEC>
+// Each wave takes every fourth token of a piece, a lane NV columns, the next
+// token's row in flight while one is worked on.
+// SELF (one sequence, few tokens): every workgroup counts the whole routing
+// itself, the first one also for k_bal_reduce, and no counting launch runs.
+template <int NV, bool VEC, bool SELF>
 __global__ __launch_bounds__(256) void k_bal_main(const float* __restrict__ logits, const uint8_t* __restrict__ mask,
                                                   const int32_t* __restrict__ off, int T, int E, int k, int S, int TB,
-                                                  const int32_t* __restrict__ cnt, const int32_t* __restrict__ n,
+                                                  const int32_t* __restrict__ idx, int J, int32_t* __restrict__ cnt,
+                                                  int32_t* __restrict__ n, uint32_t* __restrict__ ticket,
                                                   float cb, float cz, const float* __restrict__ dloss,
                                                   float* __restrict__ dlogits, float* __restrict__ psum,
                                                   float* __restrict__ zsum) {
@@ -228,7 +275,33 @@ __global__ __launch_bounds__(256) void k_bal_main(const float* __restrict__ logi
     const int lane = threadIdx.x & 63, wave = wave_id(), c = blockIdx.x;
     const int t0 = c * TB, t1 = min(T, t0 + TB);
     int live, total;
-    const bool fine = bal_totals<256>(n, S, live, total);
+    bool fine;
+    __shared__ int hist[SELF ? 64 * NV : 1];
+    __shared__ int tot[2];
+    if constexpr (SELF) {
+        const int tid = threadIdx.x;
+        for (int e = tid; e < E; e += 256) hist[e] = 0;
+        if (tid < 2) tot[tid] = 0;
+        int lo, hi, mine = 0;
+        bool bad = !seq_bounds(off, 0, T, lo, hi);
+        __syncthreads();
+        if (!bad) bad = bal_hist<256>(idx, mask, lo, hi, E, k, hist, mine);
+        if (mine) atomicAdd(&tot[0], mine);
+        if (bad) atomicOr(&tot[1], 1);
+        __syncthreads();
+        total = tot[0];
+        live = total > 0;
+        fine = tot[1] == 0;
+        if (c == 0) {
+            for (int e = tid; e < E; e += 256) cnt[e] = hist[e];
+            if (tid == 0) {
+                *n = fine ? total : kBadSeq;
+                *ticket = 0;
+            }
+        }
+    } else {
+        fine = bal_totals<256>(n, S, J, live, total);
+    }
     if (!fine) {
         if (dlogits) {
             float q[NV];
@@ -259,23 +332,40 @@ __global__ __launch_bounds__(256) void k_bal_main(const float* __restrict__ logi
         if (dlogits)
             for (int u = t + wave; u < a; u += 4) row_store<NV, VEC>(dlogits + (size_t)u * E, E, lane, zero);
         if (a < b) {
-            const int ns = n[s];
+            const int ns = SELF ? total : seq_n(n, s, J);
             const float cf = ns > 0 ? cb * (float)E / ((float)live * (float)k * (float)ns * (float)ns) : 0.0f;
             const float zf = cz != 0.0f && total > 0 ? cz * 2.0f / (float)total : 0.0f;
-            float co[NV], ps[NV], v[NV];
+            float co[NV], ps[NV], v[NV], nx[NV];
+            // the row of token u; masked (and missing) ones are not read
+            auto fetch = [&](int u, float (&to)[NV]) {
+                const bool on = u < b && (!mask || mask[u]);
+                if (on) row_load<NV, VEC>(logits + (size_t)u * E, E, lane, -INFINITY, to);
+                return on;
+            };
+            bool on = fetch(a + wave, nx);
 #pragma unroll
             for (int i = 0; i < NV; i++) {
                 const int e = bal_col<VEC>(lane, i);
-                co[i] = e < E ? cf * (float)cnt[(size_t)s * E + e] : 0.0f;
+                int h = 0;
+                if (e < E) {
+                    if constexpr (SELF)
+                        h = hist[e];
+                    else
+                        for (int j = 0; j < J; j++) h += cnt[((size_t)s * J + j) * E + e];
+                }
+                co[i] = cf * (float)h;
                 ps[i] = 0.0f;
             }
             float zs = 0.0f;
             for (int u = a + wave; u < b; u += 4) {
-                if (mask && !mask[u]) {
+                const bool mine = on;
+#pragma unroll
+                for (int i = 0; i < NV; i++) v[i] = nx[i];
+                on = fetch(u + 4, nx);
+                if (!mine) {
                     if (dlogits) row_store<NV, VEC>(dlogits + (size_t)u * E, E, lane, zero);
                     continue;
                 }
-                row_load<NV, VEC>(logits + (size_t)u * E, E, lane, -INFINITY, v);
                 float m = v[0];
 #pragma unroll
                 for (int i = 1; i < NV; i++) m = fmaxf(m, v[i]);
@@ -326,43 +416,46 @@ __global__ __launch_bounds__(256) void k_bal_main(const float* __restrict__ logi
     }
 }
 
-// grid (ceil(E / 16), S), 1024 threads: 16 columns x 64 row groups over the
+// grid (ceil(E / 16), S), 16 RG threads: 16 columns x RG row groups over the
 // pieces of sequence s; the last workgroup to finish adds the sequences up.
-__global__ __launch_bounds__(1024) void k_bal_reduce(const int32_t* __restrict__ off, int T, int E, int k, int S,
-                                                     int TB, const int32_t* __restrict__ cnt,
+template <int RG>
+__global__ __launch_bounds__(16 * RG) void k_bal_reduce(const int32_t* __restrict__ off, int T, int E, int k, int S,
+                                                     int TB, int J, const int32_t* __restrict__ cnt,
                                                      const int32_t* __restrict__ n, float cb, float cz,
                                                      const float* __restrict__ psum, const float* __restrict__ zsum,
                                                      float* __restrict__ q, uint32_t* __restrict__ ticket,
                                                      float* __restrict__ loss, int32_t* __restrict__ counts,
                                                      float* __restrict__ probs) {
-    __shared__ float red[64][17];
-    __shared__ float zr[16];
+    constexpr int NT = 16 * RG, NW = NT / 64;
+    __shared__ float red[RG][17];
+    __shared__ float zr[NW];
     __shared__ uint32_t last;
     const int tid = threadIdx.x, col = tid & 15, g = tid >> 4, s = blockIdx.y;
     const int EB = gridDim.x, e = blockIdx.x * 16 + col;
     int live, total;
-    const bool fine = bal_totals<1024>(n, S, live, total);
+    const bool fine = bal_totals<NT>(n, S, J, live, total);
     int lo = 0, hi = 0;
     if (fine) seq_bounds(off, s, T, lo, hi);
-    const int ns = n[s];
+    const int ns = seq_n(n, s, J);
     const bool any = fine && hi > lo;
     const int r0 = any ? lo / TB + s : 0, r1 = any ? (hi - 1) / TB + s + 1 : 0;
     float a = 0.0f;
     if (e < E)
 #pragma unroll 4
-        for (int r = r0 + g; r < r1; r += 64) a += psum[(size_t)r * E + e];
+        for (int r = r0 + g; r < r1; r += RG) a += psum[(size_t)r * E + e];
     red[g][col] = a;
     __syncthreads();
 #pragma unroll
-    for (int h = 32; h >= 1; h >>= 1) {
+    for (int h = RG / 2; h >= 1; h >>= 1) {
         if (g < h) red[g][col] += red[g + h][col];
         __syncthreads();
     }
     if (tid < 16) {
         float p = ns > 0 ? red[0][col] / (float)ns : 0.0f;
         if (!fine) p = __builtin_nanf("");
-        const int c = e < E ? cnt[(size_t)s * E + e] : 0;
+        int c = 0;
         if (e < E) {
+            for (int j = 0; j < J; j++) c += cnt[((size_t)s * J + j) * E + e];
             if (probs) probs[(size_t)s * E + e] = p;
             if (counts) counts[(size_t)s * E + e] = fine ? c : -1;
         }
@@ -374,29 +467,30 @@ __global__ __launch_bounds__(1024) void k_bal_reduce(const int32_t* __restrict__
     }
     if (blockIdx.x == 0) {  // this sequence's sum of lse^2
         float z = 0.0f;
-        for (int r = r0 + tid; r < r1; r += 1024) z += zsum[r];
+        for (int r = r0 + tid; r < r1; r += NT) z += zsum[r];
         z = wave_sum(z);
         if ((tid & 63) == 0) zr[tid >> 6] = z;
         __syncthreads();
         if (tid == 0) {
             z = 0.0f;
-            for (int i = 0; i < 16; i++) z += zr[i];
+            for (int i = 0; i < NW; i++) z += zr[i];
             __hip_atomic_store(&q[(size_t)s * (EB + 1) + EB], z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
     }
-    // the workgroup's stores are out before its ticket is taken
-    __syncthreads();
+    // Thread 0 made this workgroup's one or two stores of q itself, with
+    // device-coherent stores: it waits for them, then takes the ticket. (A
+    // release fence would write back the XCD's whole L2, here full of the
+    // gradient just written: 65 us against 7 at 32768 x 512 in 37 sequences.)
     if (tid == 0) {
-        __threadfence();
-        last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) + 1u ==
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u ==
                (uint32_t)EB * (uint32_t)S;
-        __threadfence();
     }
     __syncthreads();
     if (!last) return;
     float bal = 0.0f, z = 0.0f;
     const size_t cells = (size_t)S * (EB + 1);
-    for (size_t i = tid; i < cells; i += 1024) {
+    for (size_t i = tid; i < cells; i += NT) {
         const float v = __hip_atomic_load(&q[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         if (i % (EB + 1) == (size_t)EB) z += v; else bal += v;
     }
@@ -409,7 +503,7 @@ __global__ __launch_bounds__(1024) void k_bal_reduce(const int32_t* __restrict__
     __syncthreads();
     if (tid == 0) {
         bal = z = 0.0f;
-        for (int i = 0; i < 16; i++) {
+        for (int i = 0; i < NW; i++) {
             bal += red[i][0];
             z += red[i][1];
         }
@@ -423,14 +517,6 @@ __global__ __launch_bounds__(1024) void k_bal_reduce(const int32_t* __restrict__
     }
 }
 
-template <int NV, bool VEC>
-void bal_main(const float* logits, const uint8_t* mask, const int32_t* off, int T, int E, int k, int S, const BalWs& b,
-              const int32_t* cnt, const int32_t* n, float cb, float cz, const float* dloss, float* dlogits,
-              float* psum, float* zsum, hipStream_t s) {
-    hipLaunchKernelGGL((k_bal_main<NV, VEC>), dim3(b.chunks), dim3(256), 0, s, logits, mask, off, T, E, k, S, b.TB,
-                       cnt, n, cb, cz, dloss, dlogits, psum, zsum);
-}
-
 }  // namespace
 
 size_t balance_ws_bytes(int T, int E, int S) { return bal_ws(T, E, S).total; }
@@ -439,38 +525,48 @@ hipError_t launch_balance(int E, int k, const float* logits, int T, const int32_
                           const int32_t* seq_off, int S, float cb, float cz, const float* dloss, float* loss,
                           int32_t* counts, float* probs, float* dlogits, void* ws, hipStream_t s) {
     const BalWs b = bal_ws(T, E, S);
+    const bool self = S == 1 && T > 0 && (int64_t)T * k <= kSelfCount;
     char* base = reinterpret_cast<char*>(ws);
     int32_t* cnt = reinterpret_cast<int32_t*>(base + b.cnt);
     int32_t* n = reinterpret_cast<int32_t*>(base + b.n);
-    int32_t* pc = b.J > 1 ? reinterpret_cast<int32_t*>(base + b.part) : cnt;
-    int32_t* pn = b.J > 1 ? pc + (size_t)S * b.J * E : n;
     uint32_t* ticket = reinterpret_cast<uint32_t*>(base + b.ticket);
     float* psum = reinterpret_cast<float*>(base + b.psum);
     float* zsum = reinterpret_cast<float*>(base + b.zsum);
     float* q = reinterpret_cast<float*>(base + b.q);
-    hipLaunchKernelGGL(k_bal_count, dim3(b.J, S), dim3(256), 0, s, idx, mask, seq_off, T, E, k, b.J, pc, pn, ticket);
-    hipError_t r = hipGetLastError();
-    if (r != hipSuccess) return r;
-    if (b.J > 1) {
-        hipLaunchKernelGGL(k_bal_merge, dim3((E + 255) / 256, S), dim3(256), 0, s, pc, pn, E, b.J, cnt, n);
+    const int J = self ? 1 : b.JM;  // parts of each sequence in cnt and n
+    hipError_t r;
+    if (!self) {
+        int32_t* pc = b.J > b.JM ? reinterpret_cast<int32_t*>(base + b.part) : cnt;
+        int32_t* pn = b.J > b.JM ? pc + (size_t)S * b.J * E : n;
+        hipLaunchKernelGGL(k_bal_count, dim3(b.J, S), dim3(1024), 0, s, idx, mask, seq_off, T, E, k, b.J, pc, pn, ticket);
         if ((r = hipGetLastError()) != hipSuccess) return r;
+        if (b.J > b.JM) {
+            hipLaunchKernelGGL(k_bal_merge, dim3((E + 255) / 256, S), dim3(256), 0, s, pc, pn, E, b.J, cnt, n);
+            if ((r = hipGetLastError()) != hipSuccess) return r;
+        }
     }
     if (b.chunks > 0) {
         const bool vec = E % 4 == 0;
-#define BM(NV, VEC) \
-    bal_main<NV, VEC>(logits, mask, seq_off, T, E, k, S, b, cnt, n, cb, cz, dloss, dlogits, psum, zsum, s)
+#define BM(NV, VEC, SELF)                                                                                              hipLaunchKernelGGL((k_bal_main<NV, VEC, SELF>), dim3(b.chunks), dim3(256), 0, s, logits, mask, seq_off, T, E, k, S,                        b.TB, idx, J, cnt, n, ticket, cb, cz, dloss, dlogits, psum, zsum)
+#define BMV(NV)     if (vec) { if (self) BM(NV, true, true); else BM(NV, true, false); } else { if (self) BM(NV, false, true); else BM(NV, false, false); }
         if (E <= 256) {
-            if (vec) BM(4, true); else BM(4, false);
+            BMV(4)
         } else if (E <= 512) {
-            if (vec) BM(8, true); else BM(8, false);
+            BMV(8)
         } else {
-            if (vec) BM(16, true); else BM(16, false);
+            BMV(16)
         }
+#undef BMV
 #undef BM
         if ((r = hipGetLastError()) != hipSuccess) return r;
     }
-    hipLaunchKernelGGL(k_bal_reduce, dim3((E + 15) / 16, S), dim3(1024), 0, s, seq_off, T, E, k, S, b.TB, cnt, n, cb,
-                       cz, psum, zsum, q, ticket, loss, counts, probs);
+    // a row group per piece of an average sequence, about
+    const dim3 grid((E + 15) / 16, S);
+#define BR(RG)                                                                                                      \
+    hipLaunchKernelGGL((k_bal_reduce<RG>), grid, dim3(16 * RG), 0, s, seq_off, T, E, k, S, b.TB, J, cnt, n, cb, cz, psum, \
+                       zsum, q, ticket, loss, counts, probs)
+    if (b.chunks / S >= 64) BR(64); else BR(16);
+#undef BR
     return hipGetLastError();
 }
 

@@ -30,10 +30,22 @@ def close(got, ref, tol, what):
                            (d / tol)[bad].max().item())
 
 
-def mm(a, b, ea=None, eb=None):
-    """a @ b and what fp32 may be off by, with errors ea, eb already in the operands."""
+def mm(a, b, ea=None, eb=None, pairs=False):
+    """a @ b and what fp32 may be off by, with errors ea, eb already in the operands.
+
+    pairs: the operands are sums of two fp16 parts h + l, scaled so that the
+    largest of a row of a (a column of b) is in [2^14, 2^15). h rounds to
+    2^-11 of the value and l to 2^-11 of what is left, so h + l is off by at
+    most 2^-22 of it, or by half the smallest fp16 step, 2^-25, which is 2^-39
+    of the largest at most; the product of the two l, 2^-22 of the product, is
+    left out: 3 * 2^-22 of each product, and 2^-39 of the largest times the
+    other operand. A product of three sums has 3 K terms to add."""
     K = a.shape[1]
-    off = (K + 2) * EPS * (a.abs() @ b.abs())
+    off = ((3 * K if pairs else K) + 2) * EPS * (a.abs() @ b.abs())
+    if pairs:
+        off = off + 3 * 2.0 ** -22 * (a.abs() @ b.abs())
+        off = off + 2.0 ** -39 * (a.abs().amax(1, keepdim=True) * b.abs().sum(0, keepdim=True) +
+                                  a.abs().sum(1, keepdim=True) * b.abs().amax(0, keepdim=True))
     if ea is not None:
         off = off + ea @ b.abs()
     if eb is not None:
@@ -122,14 +134,15 @@ def route_backward(x, Wr, idx, w, dw, mask, din, T, E, k):
         off = ~mask
         G[off], eG[off] = 0.0, 0.0
     out = {"dlogits": (G, eG + 2.0 ** -140)}
+    pairs = Wr is not None and T * E * Wr.shape[1] >= 1 << 24  # the sizes that multiply pairs of fp16 parts
     if Wr is not None:
-        v, e = mm(G, cpu64(Wr), ea=eG)
+        v, e = mm(G, cpu64(Wr), ea=eG, pairs=pairs)
         out["dx"] = (v, e + 2.0 ** -140)
     if x is not None:
         x = cpu64(x)
         if mask is not None:
             x[~mask] = 0.0
-        v, e = mm(G.t().contiguous(), x, ea=eG.t().contiguous())
+        v, e = mm(G.t().contiguous(), x, ea=eG.t().contiguous(), pairs=pairs)
         out["dWr"] = (v, e + 2.0 ** -140)
     return out
 
