@@ -4,9 +4,14 @@
 //   G        = dlogits_in + ds scattered to the chosen experts (masked tokens: 0)
 //   dx       = G Wr        [T][H], over E
 //   dWr      = G^T x       [E][H], over T
-// k_rg_logits writes G (one wave per token), k_rg_gemm runs both products as
-// one launch, and k_rg_reduce adds the parts of products whose long axis was
-// split. Everything in fp32: operands, v_mfma_f32_16x16x4_f32, sums.
+// Two forms of the two products, chosen by their size (kPairFrom):
+//   fp32  k_rg_logits writes G, k_rg_gemm runs both products as one launch on
+//         v_mfma_f32_16x16x4_f32.
+//   pair  operands as pairs of fp16 parts (see pair_exp): k_rg_prep writes G
+//         and the parts of G's rows, x and Wr in the order in which the
+//         products load them, k_rg_gt those of G's columns, and k_rg_pair
+//         runs both products as one launch on v_mfma_f32_32x32x16_f16.
+// Where a product's long axis was split, k_rg_reduce adds its parts in order.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -19,56 +24,68 @@ namespace moe {
 
 namespace {
 
-constexpr int kTM = 128, kTN = 128, kTK = 32;  // tile of the products
-constexpr int kLogitRows = 32;                 // tokens of a workgroup of k_rg_logits (pair form): a word of bits
-constexpr int kMaxRows = 128;                  // rows of a workgroup's column maxima
+constexpr int kTM = 128, kTN = 128, kTK = 32;  // tile of the products (fp32 form; pair form: see k_rg_pair)
+constexpr int kMaxPart = 1024;                 // rows of a part of a product's long axis
 
 // Multiplications (T E H) from which the products run by pairs of fp16 parts.
 constexpr int64_t kPairFrom = (int64_t)1 << 24;
 
+typedef _Float16 h2v __attribute__((ext_vector_type(2)));
+typedef _Float16 h8v __attribute__((ext_vector_type(8)));
+typedef float f16v __attribute__((ext_vector_type(16)));
+typedef uint32_t u4v __attribute__((ext_vector_type(4)));  // a chunk: 8 consecutive k of one row or column, one part
+
 struct RgPlan {
-    int MW;               // 0: fp32 form; else the pair form with tiles of 128 MW rows
-    int gb, xb, wb;       // parts of the column maxima of G, x and Wr
+    int BM;               // 0: fp32 form; else the pair form with tiles of BM rows
     int Ep;               // columns of G in the workspace (E rounded up to kTK, zero-padded)
     int mt, nt;           // dx: row tiles; both: column tiles
     int et;               // dWr: row tiles
     int sx, sw;           // parts of the long axis of dx (over E) and dWr (over T)
-    int kx, kw;           // its length in a part (multiples of kTK)
-    size_t g, exps, max, px, pw, total;
+    int kx, kw;           // its length in a part (multiples of kTK; pair form: powers of 2)
+    size_t g, egr, egc, ex, ew, ga, gt, xb, wb, px, pw, total;
 };
 
 RgPlan rg_plan(int H, int E, int T) {
-    RgPlan p;
+    RgPlan p = {};
     p.Ep = (E + kTK - 1) / kTK * kTK;
     p.nt = (H + kTN - 1) / kTN;
-    p.MW = 0;
     if ((int64_t)T * E * H >= kPairFrom) {
         // 256-row tiles read less per product; 128-row ones where the larger
         // would leave compute units idle
         const int64_t large = ((int64_t)(T + 255) / 256 + (E + 255) / 256) * p.nt;
-        p.MW = large >= 512 ? 2 : 1;
+        p.BM = large >= 512 ? 256 : 128;
     }
-    const int tm = p.MW ? 128 * p.MW : kTM;
+    const int tm = p.BM ? p.BM : kTM;
     p.mt = (T + tm - 1) / tm;
     p.et = (E + tm - 1) / tm;
-    // parts of the long axis until one workgroup per compute unit has work, of
-    // two steps at least, and none above 1024
-    auto split = [](int64_t tiles, int64_t len, int& parts, int& per) {
-        parts = 1;
-        per = kTK;
-        if (tiles < 1 || len < 1) return;  // no tokens
-        int64_t n = (256 + tiles - 1) / tiles;
-        if (len / 1024 > n) n = len / 1024;
-        const int64_t most = (len + 2 * kTK - 1) / (2 * kTK);
-        if (n > most) n = most;
-        if (n < 1) n = 1;
-        int64_t l = (len + n - 1) / n;
-        l = (l + kTK - 1) / kTK * kTK;
-        per = (int)l;
-        parts = (int)((len + l - 1) / l);
-    };
-    split((int64_t)p.mt * p.nt, E, p.sx, p.kx);
-    split((int64_t)p.et * p.nt, T, p.sw, p.kw);
+    if (p.BM) {
+        auto split = [](int64_t tiles, int64_t len, int& parts, int& per) {
+            per = kMaxPart;
+            while (per > 64 && tiles * ((len + per - 1) / per) < 128) per /= 2;
+            parts = (int)((len + per - 1) / per);
+        };
+        split((int64_t)p.mt * p.nt, E, p.sx, p.kx);
+        split((int64_t)p.et * p.nt, T, p.sw, p.kw);
+    } else {
+        // parts until one workgroup per compute unit has work, of two steps
+        // at least, and none above kMaxPart
+        auto split = [](int64_t tiles, int64_t len, int& parts, int& per) {
+            parts = 1;
+            per = kTK;
+            if (tiles < 1 || len < 1) return;  // no tokens
+            int64_t n = (256 + tiles - 1) / tiles;
+            if (len / kMaxPart > n) n = len / kMaxPart;
+            const int64_t most = (len + 2 * kTK - 1) / (2 * kTK);
+            if (n > most) n = most;
+            if (n < 1) n = 1;
+            int64_t l = (len + n - 1) / n;
+            l = (l + kTK - 1) / kTK * kTK;
+            per = (int)l;
+            parts = (int)((len + l - 1) / l);
+        };
+        split((int64_t)p.mt * p.nt, E, p.sx, p.kx);
+        split((int64_t)p.et * p.nt, T, p.sw, p.kw);
+    }
     size_t o = kCounterBytes;
     auto take = [&o](size_t bytes) {
         const size_t at = o;
@@ -76,15 +93,69 @@ RgPlan rg_plan(int H, int E, int T) {
         return at;
     };
     p.g = take((size_t)T * p.Ep * 4);
-    p.gb = (T + kLogitRows - 1) / kLogitRows;
-    p.xb = (T + kMaxRows - 1) / kMaxRows;
-    p.wb = (E + kMaxRows - 1) / kMaxRows;
-    p.exps = take(p.MW ? ((size_t)T + p.gb + p.Ep + 2 * (size_t)H) * 4 : 0);
-    p.max = take(p.MW ? ((size_t)p.gb * p.Ep + ((size_t)p.xb + p.wb) * H) * 4 : 0);
+    if (p.BM) {
+        p.egr = take((size_t)T * 4);
+        p.egc = take((size_t)p.sw * p.Ep * 4);
+        p.ex = take((size_t)p.sw * H * 4);
+        p.ew = take((size_t)p.sx * H * 4);
+        p.ga = take((size_t)p.mt * p.BM * p.Ep * 4);
+        p.gt = take((size_t)p.sw * p.kw * p.et * p.BM * 4);
+        p.xb = take((size_t)p.sw * p.kw * H * 4);
+        p.wb = take((size_t)p.sx * p.kx * H * 4);
+    }
     p.px = take(p.sx > 1 ? (size_t)p.sx * T * H * 4 : 0);
     p.pw = take(p.sw > 1 ? (size_t)p.sw * E * H * 4 : 0);
     p.total = o;
     return p;
+}
+
+// Adds the routing's part to one token's row of G, lane i of which holds the
+// columns col(0), col(1), ... (one wave; lanes below k hold the token's
+// routing). In increasing j, so an expert named twice adds in that order. An
+// index outside [0, E) makes the row NaN.
+template <int NV, class COL>
+__device__ __forceinline__ void add_routing(float (&v)[NV], COL col, int E, int k, int me, float mw, float md) {
+    const int lane = threadIdx.x & 63;
+    const float dot = wave_sum(lane < k ? mw * md : 0.0f);
+    const float ds = mw * (md - dot);
+    for (int j = 0; j < k; j++) {
+        const int e = __builtin_amdgcn_readlane(me, j);
+        const float d = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ds), j));
+#pragma unroll
+        for (int i = 0; i < NV; i++) v[i] += col(i) == e ? d : 0.0f;
+    }
+    if (__ballot(lane < k && (unsigned)me >= (unsigned)E))
+#pragma unroll
+        for (int i = 0; i < NV; i++) v[i] = __builtin_nanf("");
+}
+
+// ---------------------------------------------------------------------------
+// fp32 form
+
+// grid ceil(T / 4), 256 threads: one wave per token; lane owns columns
+// lane + 64 i (i < NV).
+template <int NV>
+__global__ __launch_bounds__(256) void k_rg_logits(const float* __restrict__ din, const int32_t* __restrict__ idx,
+                                                   const float* __restrict__ w, const float* __restrict__ dw,
+                                                   const uint8_t* __restrict__ mask, int T, int E, int Ep, int k,
+                                                   float* __restrict__ G, float* dout) {
+    const int lane = threadIdx.x & 63, t = blockIdx.x * 4 + wave_id();
+    if (t >= T) return;
+    const bool on = !mask || mask[t], live = dw && lane < k;
+    float v[NV];
+    const int me = live ? idx[(size_t)t * k + lane] : 0;
+    const float mw = live ? w[(size_t)t * k + lane] : 0.0f, md = live ? dw[(size_t)t * k + lane] : 0.0f;
+    auto col = [lane](int i) { return lane + 64 * i; };
+#pragma unroll
+    for (int i = 0; i < NV; i++) v[i] = din && col(i) < E ? din[(size_t)t * E + col(i)] : 0.0f;
+    if (dw) add_routing<NV>(v, col, E, k, me, mw, md);
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        const int e = col(i);
+        if (e >= E || !on) v[i] = 0.0f;
+        if (e < Ep) G[(size_t)t * Ep + e] = v[i];
+        if (dout && e < E) dout[(size_t)t * E + e] = v[i];
+    }
 }
 
 // One tile of C[M][H] = A B over [k0, k1). A(m, k) is G[m][k] (dx: KMAJ
@@ -104,9 +175,6 @@ struct RgArgs {
     float *dx, *dWr;  // outputs, or the parts [s][rows][H]
     int acc_x, acc_w;
     int sx, sw, kx, kw, mt, nt, et, nx;  // nx: workgroups of dx
-    // pair form: exponents of G's rows and columns, x's and Wr's columns; a bit per token that counts
-    const int *egr, *egc, *ex, *ew;
-    const uint32_t* keep;
 };
 
 constexpr int kLdsRow = kTM + 4;
@@ -204,103 +272,137 @@ __global__ __launch_bounds__(256) void k_rg_gemm(RgArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// The products by pairs of fp16 parts.
+// Pair form
 //
 // v_mfma_f32_32x32x16_f16 runs at 16 times the rate of the fp32 form, so an
 // operand a is taken as 2^e (h + l): e brings the largest finite magnitude of
-// its row (or column, whichever does not run along the sum) into [2^14, 2^15),
-// h = fp16(a 2^-e), l = fp16(a 2^-e - h), both to nearest. h + l is a up to
-// 2^-22 of it, except that values below 2^-17 of that largest one lose more
-// (half the smallest step of l is 2^-25, 2^-39 of the largest). Each product
-// is h h' + h l' + l h' (l l' is at most 2^-22 of it), summed in fp32: 3 2^-22
-// of every product at most, where the roundings of an fp32 sum of K products
-// may take K 2^-24.
-// A value that is infinite or NaN makes the outputs it reaches NaN.
+// its row (or column, whichever does not run along the sum; within a part of
+// the sum) into [2^14, 2^15), h = fp16(a 2^-e), l = fp16(a 2^-e - h), both to
+// nearest. h + l is a up to 2^-22 of it, except that values below 2^-17 of
+// that largest one lose more (half the smallest step of l is 2^-25, 2^-39 of
+// the largest). Each product is h h' + h l' + l h' (l l' is at most 2^-22 of
+// it), summed in fp32: 3 2^-22 of every product at most, where the roundings
+// of an fp32 sum of K products may take K 2^-24. A value that is infinite or
+// NaN makes the outputs it reaches NaN.
 
-// Largest finite magnitude, as the bits of an fp32 (0 if there is none).
 __device__ __forceinline__ float finite_mag(float v) {
     const float a = fabsf(v);
     return a < INFINITY ? a : 0.0f;
 }
-// e of the pair form for a row whose largest finite magnitude is m; 2^-e is a
-// normal fp32 (a row below 2^-111 keeps smaller parts).
+// e for a largest finite magnitude m; 2^-e is a normal fp32 (rows below
+// 2^-111 keep smaller parts).
 __device__ __forceinline__ int pair_exp(float m) {
     const int e = (int)(__float_as_uint(m) >> 23) - 127 - 14;
     return m == 0.0f ? 0 : max(e, -125);
 }
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// Each column's largest finite magnitude over kMaxRows rows: 256 columns and
-// 16 x 8 rows a workgroup of 1024, every load of a lane in flight at once
-// (rows behind the end and masked ones are loaded and left out).
-struct MaxJob {
+// Eight values -> the chunks of their parts.
+__device__ __forceinline__ void pair8(const float (&v)[8], float scale, u4v& h, u4v& l) {
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+        const float a = v[2 * q] * scale, b = v[2 * q + 1] * scale;
+        const h2v hp = __builtin_convertvector((f2v{a, b}), h2v);
+        const h2v lp = __builtin_convertvector((f2v{a - (float)hp[0], b - (float)hp[1]}), h2v);
+        h[q] = __builtin_bit_cast(uint32_t, hp);
+        l[q] = __builtin_bit_cast(uint32_t, lp);
+    }
+}
+
+// Position of column n in its operand: within 64, even columns first, so that
+// a lane of a product ends with two neighbouring columns.
+__device__ __forceinline__ int place(int n) { return n / 64 * 64 + n % 2 * 32 + n / 2 % 32; }
+
+// The parts of a matrix whose rows run along the sum: out[part][2][kw / 8][W]
+// chunks from p [rows][cols]. A workgroup of 1024 takes the kw = 2^kwl rows
+// of a part and 32 * 1024 / kw columns, each thread 8 rows and 4 columns: it
+// holds them in registers while the columns' maxima are found, so memory is
+// read once and written once. Rows behind the end and masked ones are loaded
+// (from the last row) and become zeros.
+struct Panel {
     const float* p;
     const uint8_t* mask;  // rows that do not count, or null
-    int rows, cols;       // cols a multiple of 256
-    float* part;          // [ceil(rows / kMaxRows)][cols]
-    int nb;               // workgroups
+    int rows, cols;       // cols a multiple of 32
+    int kwl, W;
+    u4v* out;
+    int* e;               // exponents [part][cols]
+    int cb, nb;           // workgroups per part, and all
 };
-__device__ __forceinline__ void col_max(const MaxJob& j, int b, float (*red)[256]) {
-    const int cb = j.cols / 256, c = b % cb * 256, wave = wave_id(), lane = threadIdx.x & 63;
-    const int r0 = b / cb * kMaxRows + wave * 8;
+__device__ __forceinline__ void make_panel(const Panel& j, int b, f4v (*red)[8]) {
+    const int kw = 1 << j.kwl, part = b / j.cb, tid = threadIdx.x, wave = wave_id(), c4 = tid & 7;
+    const int sub = tid >> j.kwl, r8 = (tid & (kw - 1)) >> 3;
+    const int col = ((b % j.cb << (10 - j.kwl)) + sub) * 32 + 4 * c4, r0 = part * kw + 8 * r8;
+    const bool in = col < j.cols;
     f4v v[8];
     bool on[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         const int r = min(r0 + i, j.rows - 1);
-        v[i] = *reinterpret_cast<const f4v*>(j.p + (size_t)r * j.cols + c + 4 * lane);
+        v[i] = *reinterpret_cast<const f4v*>(j.p + (size_t)r * j.cols + (in ? col : 0));
         on[i] = r0 + i < j.rows && (!j.mask || j.mask[r]);
     }
     f4v m = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 8; i++)
 #pragma unroll
-        for (int q = 0; q < 4; q++) m[q] = fmaxf(m[q], on[i] ? finite_mag(v[i][q]) : 0.0f);
-    *reinterpret_cast<f4v*>(&red[wave][4 * lane]) = m;
-    __syncthreads();
-    if (threadIdx.x < 256) {
-        float a = red[0][threadIdx.x];
+        for (int q = 0; q < 4; q++) {
+            if (!on[i]) v[i][q] = 0.0f;
+            m[q] = fmaxf(m[q], finite_mag(v[i][q]));
+        }
 #pragma unroll
-        for (int i = 1; i < 16; i++) a = fmaxf(a, red[i][threadIdx.x]);
-        j.part[(size_t)(b / cb) * j.cols + c + threadIdx.x] = a;
+    for (int q = 0; q < 4; q++)
+#pragma unroll
+        for (int o = 8; o < 64; o <<= 1) m[q] = fmaxf(m[q], __shfl_xor(m[q], o, 64));
+    if ((tid & 63) < 8) red[wave][c4] = m;
+    __syncthreads();
+    const int nw = kw / 64;
+    for (int i = 0; i < nw; i++) {
+        const f4v o = red[sub * nw + i][c4];
+#pragma unroll
+        for (int q = 0; q < 4; q++) m[q] = fmaxf(m[q], o[q]);
+    }
+    if (!in) return;
+    u4v* out = j.out + (size_t)part * (kw / 4) * j.W;
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+        const int e = pair_exp(m[q]);
+        if (r8 == 0) j.e[(size_t)part * j.cols + col + q] = e;
+        float c[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) c[i] = v[i][q];
+        u4v h, l;
+        pair8(c, pow2i(-e), h, l);
+        out[(size_t)r8 * j.W + place(col + q)] = h;
+        out[(size_t)(kw / 8 + r8) * j.W + place(col + q)] = l;
     }
 }
 
-// G: one wave per token, a lane the columns lane + 64 i (i < NV). Fp32 form:
-// 4 tokens a workgroup of 256. Pair form (PAIR): 32 tokens a workgroup of
-// 1024, which also writes the exponent of each row, its tokens' column maxima
-// and a word that says which of them count; further workgroups make the
-// column maxima of x and Wr. Rows that do not count are loaded and left out:
-// a load that waits for its mask byte doubles the latency.
-template <int NV, bool PAIR>
-__global__ __launch_bounds__(PAIR ? 1024 : 256) void k_rg_logits(
-    const float* __restrict__ din, const int32_t* __restrict__ idx, const float* __restrict__ w,
-    const float* __restrict__ dw, const uint8_t* __restrict__ mask, int T, int E, int Ep, int k, float* __restrict__ G,
-    float* dout, int* __restrict__ egr, uint32_t* __restrict__ keep, float* __restrict__ gpart, int ng, MaxJob jx,
-    MaxJob jw) {
-    __shared__ __align__(16) float red[PAIR ? 16 : 1][256];  // column maxima: of x and Wr, or as bits of G
-    uint32_t* gm = reinterpret_cast<uint32_t*>(red);
-    __shared__ uint32_t kept;
-    if constexpr (PAIR) {
-        if ((int)blockIdx.x >= ng) {
-            const int b = (int)blockIdx.x - ng;
-            if (b < jx.nb) col_max(jx, b, red); else col_max(jw, b - jx.nb, red);
-            return;
-        }
-        for (int e = threadIdx.x; e < Ep; e += 1024) gm[e] = 0;
-        if (threadIdx.x == 0) kept = 0;
-        __syncthreads();
+// grid ceil(T / 32) + panels of x + panels of Wr, 1024 threads. The first
+// workgroups make G (a wave two tokens, a lane the columns 8 lane + 512 c + i):
+// in fp32 for k_rg_gt, and its rows' parts ga [tile][2][Ep / 8][BM].
+// Everything a wave needs is loaded before its mask bytes are looked at.
+template <int NC>
+__global__ __launch_bounds__(1024) void k_rg_prep(const float* __restrict__ din, const int32_t* __restrict__ idx,
+                                                  const float* __restrict__ w, const float* __restrict__ dw,
+                                                  const uint8_t* __restrict__ mask, int T, int E, int Ep, int k,
+                                                  int vec, float* __restrict__ G, float* dout, u4v* __restrict__ ga,
+                                                  int BM, int* __restrict__ egr, int ng, Panel px, Panel pw) {
+    __shared__ f4v red[16][8];
+    if ((int)blockIdx.x >= ng) {
+        const int b = (int)blockIdx.x - ng;
+        if (b < px.nb) make_panel(px, b, red); else make_panel(pw, b - px.nb, red);
+        return;
     }
-    const int lane = threadIdx.x & 63, wave = wave_id();
-    constexpr int PER = PAIR ? 2 : 1;  // tokens of a wave
-    const int t0 = (int)blockIdx.x * (PAIR ? kLogitRows : 4) + wave * PER;
-    float v[PER][NV], mw[PER], md[PER];
-    int me[PER];
-    bool on[PER];
+    constexpr int NV = 8 * NC;
+    const int lane = threadIdx.x & 63, t0 = (int)blockIdx.x * 32 + wave_id() * 2;
+    auto col = [lane](int i) { return 8 * lane + i / 8 * 512 + i % 8; };
+    float v[2][NV], mw[2], md[2];
+    int me[2];
+    bool on[2];
 #pragma unroll
-    for (int u = 0; u < PER; u++) {
+    for (int u = 0; u < 2; u++) {
         const size_t t = min(t0 + u, T - 1);
-        on[u] = t0 + u < T && (!mask || mask[t]);
+        on[u] = !mask || mask[t];
         me[u] = 0;
         mw[u] = md[u] = 0.0f;
         if (dw && lane < k) {
@@ -309,285 +411,243 @@ __global__ __launch_bounds__(PAIR ? 1024 : 256) void k_rg_logits(
             md[u] = dw[t * k + lane];
         }
 #pragma unroll
-        for (int i = 0; i < NV; i++) {
-            const int e = lane + 64 * i;
-            v[u][i] = din && e < E ? din[t * E + e] : 0.0f;
+        for (int i = 0; i < NV; i++) v[u][i] = 0.0f;
+        if (din) {
+            if (vec) {  // E % 8 == 0: a lane's eight columns are all in or all out
+#pragma unroll
+                for (int c = 0; c < NC; c++)
+                    if (col(8 * c) < E) {
+                        const f4v* p = reinterpret_cast<const f4v*>(din + t * E + col(8 * c));
+                        const f4v a = p[0], b = p[1];
+#pragma unroll
+                        for (int q = 0; q < 4; q++) {
+                            v[u][8 * c + q] = a[q];
+                            v[u][8 * c + 4 + q] = b[q];
+                        }
+                    }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NV; i++)
+                    if (col(i) < E) v[u][i] = din[t * E + col(i)];
+            }
         }
     }
 #pragma unroll
-    for (int u = 0; u < PER; u++) {
+    for (int u = 0; u < 2; u++) {
         const int t = t0 + u;
         if (t >= T) break;
-        if (dw) {
-            const float dot = wave_sum(lane < k ? mw[u] * md[u] : 0.0f);
-            const float ds = mw[u] * (md[u] - dot);
-            for (int j = 0; j < k; j++) {  // in increasing j, so an expert named twice adds in that order
-                const int e = __builtin_amdgcn_readlane(me[u], j);
-                const float d = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ds), j));
-#pragma unroll
-                for (int i = 0; i < NV; i++) v[u][i] += lane + 64 * i == e ? d : 0.0f;
-            }
-            if (__ballot(lane < k && (unsigned)me[u] >= (unsigned)E))
-#pragma unroll
-                for (int i = 0; i < NV; i++) v[u][i] = __builtin_nanf("");
-        }
+        if (dw) add_routing<NV>(v[u], col, E, k, me[u], mw[u], md[u]);
         float rm = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const int e = lane + 64 * i;
-            if (e >= E || !on[u]) v[u][i] = 0.0f;
-            if (e < Ep) G[(size_t)t * Ep + e] = v[u][i];
-            if (dout && e < E) dout[(size_t)t * E + e] = v[u][i];
-            if constexpr (PAIR) {
-                const float a = finite_mag(v[u][i]);
-                rm = fmaxf(rm, a);
-                if (e < Ep) atomicMax(&gm[e], __float_as_uint(a));
+            if (!on[u] || col(i) >= E) v[u][i] = 0.0f;
+            rm = fmaxf(rm, finite_mag(v[u][i]));
+        }
+        const int e = pair_exp(wave_max(rm));
+        if (lane == 0) egr[t] = e;
+        const float scale = pow2i(-e);
+        u4v* tile = ga + (size_t)(t / BM) * (Ep / 4) * BM + t % BM;
+#pragma unroll
+        for (int c = 0; c < NC; c++) {
+            const int c0 = col(8 * c);
+            if (c0 >= Ep) continue;
+            float o[8];
+#pragma unroll
+            for (int q = 0; q < 8; q++) o[q] = v[u][8 * c + q];
+            f4v* g = reinterpret_cast<f4v*>(G + (size_t)t * Ep + c0);
+            g[0] = f4v{o[0], o[1], o[2], o[3]};
+            g[1] = f4v{o[4], o[5], o[6], o[7]};
+            if (ga) {
+                u4v h, l;
+                pair8(o, scale, h, l);
+                tile[(size_t)(c0 / 8) * BM] = h;
+                tile[(size_t)(Ep / 8 + c0 / 8) * BM] = l;
+            }
+            if (dout) {
+                if (vec) {
+                    if (c0 < E) {
+                        f4v* d = reinterpret_cast<f4v*>(dout + (size_t)t * E + c0);
+                        d[0] = f4v{o[0], o[1], o[2], o[3]};
+                        d[1] = f4v{o[4], o[5], o[6], o[7]};
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 8; q++)
+                        if (c0 + q < E) dout[(size_t)t * E + c0 + q] = o[q];
+                }
             }
         }
-        if constexpr (PAIR) {
-            rm = wave_max(rm);
-            if (lane == 0) {
-                egr[t] = pair_exp(rm);
-                if (on[u]) atomicOr(&kept, 1u << (t & 31));
-            }
-        }
-    }
-    if constexpr (PAIR) {
-        __syncthreads();
-        for (int e = threadIdx.x; e < Ep; e += 1024) gpart[(size_t)blockIdx.x * Ep + e] = __uint_as_float(gm[e]);
-        if (threadIdx.x == 0) keep[blockIdx.x] = kept;
     }
 }
 
-// grid ceil(columns / 16) of the jobs in turn, 1024 threads: exponents of the
-// columns from the parts' maxima (cols are multiples of 16).
-struct ExpJob {
-    const float* part;
-    int rows, cols;
-    int* e;
-    int nb;
+// The parts of G's columns.
+__global__ __launch_bounds__(1024) void k_rg_gt(Panel pg) {
+    __shared__ f4v red[16][8];
+    make_panel(pg, blockIdx.x, red);
+}
+
+// An operand of a product tile: chunks [2][KC][W], the tile's columns from
+// `off`.
+struct PairIn {
+    const u4v* p;
+    int KC, W, off;
 };
-__global__ __launch_bounds__(1024) void k_rg_exps(ExpJob a, ExpJob b, ExpJob c) {
-    __shared__ float red[64][17];
-    int blk = blockIdx.x;
-    ExpJob j = a;
-    if (blk >= a.nb) {
-        blk -= a.nb;
-        j = b;
-        if (blk >= b.nb) {
-            blk -= b.nb;
-            j = c;
-        }
-    }
-    const int col = threadIdx.x & 15, g = threadIdx.x >> 4, cc = blk * 16 + col;
-    float m = 0.0f;
-#pragma unroll 4
-    for (int r = g; r < j.rows; r += 64) m = fmaxf(m, j.part[(size_t)r * j.cols + cc]);
-    red[g][col] = m;
-    __syncthreads();
-#pragma unroll
-    for (int h = 32; h >= 1; h >>= 1) {
-        if (g < h) red[g][col] = fmaxf(red[g][col], red[g + h][col]);
-        __syncthreads();
-    }
-    if (g == 0) j.e[cc] = pair_exp(red[0][col]);
+
+// Wait until at most N vector memory operations of this wave are outstanding
+// (they complete in issue order) and its LDS reads are done, then a workgroup
+// barrier: the loads go from memory straight into LDS, so no register tells
+// the compiler when they are there.
+template <int N>
+__device__ __forceinline__ void ring_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-typedef _Float16 h8v __attribute__((ext_vector_type(8)));
-typedef float f16v __attribute__((ext_vector_type(16)));
-typedef uint32_t u4v __attribute__((ext_vector_type(4)));
-typedef uint32_t u2v __attribute__((ext_vector_type(2)));
+struct PairArgs {
+    const u4v *ga, *gt, *xb, *wb;
+    const int *egr, *egc, *ex, *ew;
+    int T, Tk, E, Ep, H;                 // Tk: T rounded up to kTK
+    float *dx, *dWr;                     // outputs, or the parts [s][rows][H]
+    int acc_x, acc_w;
+    int sx, sw, kx, kw, mt, nt, et, nx;  // nx: workgroups of dx
+};
 
-// Two values (already scaled) -> their packed h and l parts.
-typedef _Float16 h2v __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ void pair2(float a, float b, uint32_t& h, uint32_t& l) {
-    const h2v hp = __builtin_convertvector((f2v{a, b}), h2v);
-    const h2v lp = __builtin_convertvector((f2v{a - (float)hp[0], b - (float)hp[1]}), h2v);
-    h = __builtin_bit_cast(uint32_t, hp);
-    l = __builtin_bit_cast(uint32_t, lp);
-}
-
-// One tile of 128 MW x 128 of C = A B over [k0, k1), as rg_tile. LDS holds
-// chunks of 8 consecutive k of one row (column) of either part; a row m of A
-// from G[k][m], and a column n of B, sits at position
-// 128 (n / 128) + 32 (n % 4) + n / 4 % 32, so that threads with neighbouring
-// float4 of a memory row write neighbouring chunks, MFMA j covers the columns
-// 4 i + j, and a lane of C ends with 4 consecutive columns of each row. Wave w
-// has the 32 MW positions of rows from 32 MW w and all 128 columns.
-template <int MW, bool KMAJ>
-__device__ __forceinline__ void rg_pair_tile(const RgArgs& a, int tile, int part, u4v* lds) {
-    constexpr int MT = 128 * MW;
-    const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
-    const int M = KMAJ ? a.E : a.T, klen = KMAJ ? a.T : a.E;
-    const int m0 = tile / a.nt * MT, n0 = tile % a.nt * kTN;
-    const int per = KMAJ ? a.kw : a.kx;
-    const int k0 = part * per, k1 = min(klen, k0 + per);
-    const float* B = KMAJ ? a.x : a.Wr;
-    const int* eb = KMAJ ? a.ex : a.ew;       // exponents of B's columns
-    const int* ea = KMAJ ? a.egc : a.egr;     // exponents of A's rows
-    u4v* As = lds;               // [2][4][MT]
-    u4v* Bs = lds + 8 * MT;      // [2][4][128]
-    f16v acc[MW][4];
+// One tile of BM x 128 of C, 2 BM threads: BM / 32 waves of 64 x 64. Steps of
+// 32 k: LDS holds three of them as chunks [2][4][BM] of A and [2][4][128] of
+// B; step s + 2 is on its way from memory while step s is multiplied.
+template <int BM>
+__device__ __forceinline__ void pair_tile(const PairIn& A, const PairIn& B, int steps, const int* __restrict__ ea,
+                                          const int* __restrict__ eb, bool permuted, int m0, int M, int n0, int H,
+                                          float* C, bool add, u4v (*ring)[8 * BM + 8 * 128]) {
+    constexpr int NW = BM / 32, NA = BM / 8 / NW, NB = 16 / NW, NI = NA + NB;  // 1 KB loads of a wave and step
+    const int lane = threadIdx.x & 63, wave = wave_id(), wm = wave >> 1, wn = wave & 1;
+    const rsrc_t rA = make_rsrc(A.p, (uint32_t)A.KC * (uint32_t)A.W * 32u);
+    const rsrc_t rB = make_rsrc(B.p, (uint32_t)B.KC * (uint32_t)B.W * 32u);
+    uint32_t oa[NA], ob[NB];  // byte offsets of the wave's loads at step 0
 #pragma unroll
-    for (int i = 0; i < MW; i++)
+    for (int i = 0; i < NA; i++) {
+        const int q = wave + NW * i, row = q / (BM / 64), seg = q % (BM / 64);
+        oa[i] = ((uint32_t)((row >> 2) * A.KC + (row & 3)) * (uint32_t)A.W + (uint32_t)(A.off + 64 * seg + lane)) * 16u;
+    }
 #pragma unroll
-        for (int j = 0; j < 4; j++)
+    for (int i = 0; i < NB; i++) {
+        const int q = wave + NW * i, row = q / 2, seg = q % 2;
+        ob[i] = ((uint32_t)((row >> 2) * B.KC + (row & 3)) * (uint32_t)B.W + (uint32_t)(B.off + 64 * seg + lane)) * 16u;
+    }
+    const uint32_t da = (uint32_t)A.W * 64u, db = (uint32_t)B.W * 64u;  // four chunk rows a step
+    // every step issues the same loads; those behind the last one read nothing
+    auto issue = [&](int s, u4v* to) {
+        const bool on = s < steps;
+#pragma unroll
+        for (int i = 0; i < NA; i++)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rA, (__attribute__((address_space(3))) void*)(to + 64 * (wave + NW * i)), 16,
+                on ? oa[i] + (uint32_t)s * da : kOOB, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < NB; i++)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rB, (__attribute__((address_space(3))) void*)(to + 8 * BM + 64 * (wave + NW * i)), 16,
+                on ? ob[i] + (uint32_t)s * db : kOOB, 0, 0, 0);
+    };
+    f16v acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+        for (int j = 0; j < 2; j++)
 #pragma unroll
             for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
-
-    // B: thread (n2 = tid % 64, kc = tid / 64) has columns 2 n2, 2 n2 + 1 of
-    // the 8 rows of chunk kc (H is a multiple of 256: columns are whole)
-    const int bn = tid % 64 * 2, bk = wave * 8;
-    const float sb0 = pow2i(-eb[n0 + bn]), sb1 = pow2i(-eb[n0 + bn + 1]);
-    u2v rb[8];
-    // A from G[k][m]: the same with MW times 2 columns; A from G[m][k]: rows
-    // tid % 16 + 16 (tid / 64) + 64 i, chunk tid / 16 % 4
-    const int an = tid % 64 * 2 * MW;
-    const int am = tid % 16 + tid / 64 * 16, ac = tid / 16 % 4 * 8;
-    float sa[2 * MW];
-#pragma unroll
-    for (int i = 0; i < 2 * MW; i++) {
-        const int m = KMAJ ? m0 + an + i : m0 + am + 64 * i;
-        sa[i] = pow2i(-ea[min(m, (KMAJ ? a.Ep : M) - 1)]);
-    }
-    // Loads go through buffer resources over the rows of this part: offsets
-    // behind them (rows past k1 or M, rows that do not count, columns past
-    // Ep) read 0, so no load waits for a branch.
-    const rsrc_t rB = make_rsrc(B + (size_t)k0 * a.H, (uint32_t)(k1 - k0) * (uint32_t)a.H * 4u);
-    const rsrc_t rA = KMAJ ? make_rsrc(a.G + (size_t)k0 * a.Ep, (uint32_t)(k1 - k0) * (uint32_t)a.Ep * 4u)
-                           : make_rsrc(a.G + (size_t)m0 * a.Ep, (uint32_t)min(MT, M - m0) * (uint32_t)a.Ep * 4u);
-    const uint32_t ob = (uint32_t)(n0 + bn) * 4u;
-    const uint32_t oa = KMAJ ? (m0 + an < a.Ep ? (uint32_t)(m0 + an) * 4u : kOOB) : (uint32_t)(am * a.Ep + ac) * 4u;
-    u4v ra4[KMAJ ? (MW == 2 ? 8 : 1) : 4 * MW];  // a row's columns, or the halves of a row's chunk
-    u2v ra2[KMAJ && MW == 1 ? 8 : 1];
-    auto fetch = [&](int k) {
-        const uint32_t kp = KMAJ ? a.keep[k / 32] >> bk : 0xFFu;  // k0 is a multiple of 32
-#pragma unroll
-        for (int r = 0; r < 8; r++) {
-            const uint32_t row = (uint32_t)(k - k0 + bk + r);
-            const uint32_t o = kp >> r & 1u ? row * (uint32_t)a.H * 4u : kOOB;
-            rb[r] = __builtin_bit_cast(u2v, __builtin_amdgcn_raw_buffer_load_b64(rB, o + ob, 0, 0));
-            if constexpr (KMAJ) {
-                const uint32_t q = row * (uint32_t)a.Ep * 4u + oa;
-                if constexpr (MW == 2)
-                    ra4[r] = __builtin_bit_cast(u4v, __builtin_amdgcn_raw_buffer_load_b128(rA, q, 0, 0));
-                else
-                    ra2[r] = __builtin_bit_cast(u2v, __builtin_amdgcn_raw_buffer_load_b64(rA, q, 0, 0));
-            }
-        }
-        if constexpr (!KMAJ) {
-#pragma unroll
-            for (int i = 0; i < 2 * MW; i++) {
-                const uint32_t q = oa + (uint32_t)(64 * i * a.Ep + k) * 4u;
-                ra4[2 * i] = __builtin_bit_cast(u4v, __builtin_amdgcn_raw_buffer_load_b128(rA, q, 0, 0));
-                ra4[2 * i + 1] = __builtin_bit_cast(u4v, __builtin_amdgcn_raw_buffer_load_b128(rA, q + 16u, 0, 0));
-            }
-        }
-    };
-    // element r of the chunk of A's i-th row or column
-    auto elem = [&](int i, int r) -> float {
-        uint32_t b;
-        if constexpr (!KMAJ)
-            b = ra4[2 * i + r / 4][r % 4];
-        else if constexpr (MW == 2)
-            b = ra4[r][i];
-        else
-            b = ra2[r][i];
-        return __uint_as_float(b);
-    };
-    auto put = [&](u4v* to, int plane, int at, const float (&v)[8]) {  // a chunk of both parts
-        u4v h, l;
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-            uint32_t hq, lq;
-            pair2(v[2 * q], v[2 * q + 1], hq, lq);
-            h[q] = hq;
-            l[q] = lq;
-        }
-        to[at] = h;
-        to[plane + at] = l;
-    };
-    auto place = [](int n) { return n / 128 * 128 + n % 4 * 32 + n / 4 % 32; };
-    fetch(k0);
-    for (int k = k0; k < k1; k += kTK) {
-        __syncthreads();
-        {
-            float v[8];
-#pragma unroll
-            for (int r = 0; r < 8; r++) v[r] = __uint_as_float(rb[r].x) * sb0;
-            put(Bs, 4 * 128, bk / 8 * 128 + place(bn), v);
-#pragma unroll
-            for (int r = 0; r < 8; r++) v[r] = __uint_as_float(rb[r].y) * sb1;
-            put(Bs, 4 * 128, bk / 8 * 128 + place(bn + 1), v);
-#pragma unroll
-            for (int i = 0; i < 2 * MW; i++) {
-#pragma unroll
-                for (int r = 0; r < 8; r++) v[r] = elem(i, r) * sa[i];
-                put(As, 4 * MT, KMAJ ? bk / 8 * MT + place(an + i) : ac / 8 * MT + am + 64 * i, v);
-            }
-        }
-        __syncthreads();
-        if (k + kTK < k1) fetch(k + kTK);
+    issue(0, ring[0]);
+    issue(1, ring[1]);
+    int cur = 0;
+    for (int s = 0; s < steps; s++) {
+        ring_barrier<NI>();  // step s is there, and every wave is done with step s - 1
+        issue(s + 2, ring[cur == 0 ? 2 : cur - 1]);
+        const u4v* a = ring[cur] + 64 * wm + (lane & 31);
+        const u4v* b = ring[cur] + 8 * BM + 64 * wn + (lane & 31);
 #pragma unroll
         for (int ks = 0; ks < 2; ks++) {
-            const int kc = 2 * ks + (lane >> 5), p = lane & 31;
-            h8v fa[2][MW], fb[2][4];
+            const int kc = 2 * ks + (lane >> 5);
+            h8v fa[2][2], fb[2][2];
 #pragma unroll
-            for (int t = 0; t < 2; t++) {
+            for (int t = 0; t < 2; t++)
 #pragma unroll
-                for (int i = 0; i < MW; i++)
-                    fa[t][i] = __builtin_bit_cast(h8v, As[(4 * t + kc) * MT + 32 * (MW * wave + i) + p]);
-#pragma unroll
-                for (int j = 0; j < 4; j++) fb[t][j] = __builtin_bit_cast(h8v, Bs[(4 * t + kc) * 128 + 32 * j + p]);
-            }
-#pragma unroll
-            for (int i = 0; i < MW; i++)
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[1][i], fb[0][j], acc[i][j], 0, 0, 0);
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[0][i], fb[1][j], acc[i][j], 0, 0, 0);
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[0][i], fb[0][j], acc[i][j], 0, 0, 0);
+                for (int i = 0; i < 2; i++) {
+                    fa[t][i] = __builtin_bit_cast(h8v, a[(4 * t + kc) * BM + 32 * i]);
+                    fb[t][i] = __builtin_bit_cast(h8v, b[(4 * t + kc) * 128 + 32 * i]);
                 }
+#pragma unroll
+            for (int t = 0; t < 3; t++)  // l h', h l', h h'
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+#pragma unroll
+                    for (int j = 0; j < 2; j++)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[t == 0][i], fb[t == 1][j], acc[i][j], 0, 0, 0);
         }
+        cur = cur == 2 ? 0 : cur + 1;
     }
-    const int parts = KMAJ ? a.sw : a.sx;
-    float* C = (KMAJ ? a.dWr : a.dx) + (parts > 1 ? (size_t)part * M * a.H : 0);
-    const bool add = parts == 1 && (KMAJ ? a.acc_w : a.acc_x);
-    const int n = n0 + 4 * (lane & 31);
-    int en[4];
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const int n = n0 + 64 * wn + 2 * (lane & 31), e0 = eb[n], e1 = eb[n + 1];
+    auto row = [&](int i, int r) {
+        const int q = 8 * (r / 4) + 4 * (lane >> 5) + r % 4;  // row of the MFMA tile
+        return m0 + 64 * wm + (permuted ? 2 * q + i : 32 * i + q);
+    };
+    int em[2][16];
 #pragma unroll
-    for (int j = 0; j < 4; j++) en[j] = eb[n + j];
+    for (int i = 0; i < 2; i++)
 #pragma unroll
-    for (int i = 0; i < MW; i++)
+        for (int r = 0; r < 16; r++) em[i][r] = ea[min(row(i, r), M - 1)];
+    if (add) {
 #pragma unroll
-        for (int r = 0; r < 16; r++) {
-            // row of the MFMA tile, then of the workgroup's tile
-            const int pr = 32 * (MW * wave + i) + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
-            const int m = m0 + (KMAJ ? pr / 128 * 128 + pr % 32 * 4 + pr % 128 / 32 : pr);
-            if (m >= M) continue;
-            const int em = ea[m];
-            f4v* c = reinterpret_cast<f4v*>(C + (size_t)m * a.H + n);
-            f4v v;
+        for (int i = 0; i < 2; i++) {
+            f2v old[16];
 #pragma unroll
-            for (int j = 0; j < 4; j++) v[j] = ldexpf(acc[i][j][r], em + en[j]);
-            if (add) v += *c;
-            *c = v;
+            for (int r = 0; r < 16; r++)
+                old[r] = *reinterpret_cast<const f2v*>(C + (size_t)min(row(i, r), M - 1) * H + n);
+#pragma unroll
+            for (int r = 0; r < 16; r++)
+                if (row(i, r) < M)
+                    *reinterpret_cast<f2v*>(C + (size_t)row(i, r) * H + n) =
+                        f2v{old[r].x + ldexpf(acc[i][0][r], em[i][r] + e0), old[r].y + ldexpf(acc[i][1][r], em[i][r] + e1)};
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int r = 0; r < 16; r++)
+                if (row(i, r) < M)
+                    *reinterpret_cast<f2v*>(C + (size_t)row(i, r) * H + n) =
+                        f2v{ldexpf(acc[i][0][r], em[i][r] + e0), ldexpf(acc[i][1][r], em[i][r] + e1)};
+    }
 }
 
 // The products' tiles: those of dWr first (their sums are the longer ones),
 // then those of dx. Consecutive tiles share rows of A, so each XCD (workgroups
-// go to the eight in turn) takes a run of them.
-template <int MW>
-__global__ __launch_bounds__(256, 2) void k_rg_pair(RgArgs a) {
-    __shared__ u4v lds[8 * 128 * MW + 8 * 128];
-    const int n = gridDim.x, q = n / 8, r = n % 8, xcd = blockIdx.x % 8, i = blockIdx.x / 8;
-    const int b = xcd * q + min(xcd, r) + i;
-    const int nw = n - a.nx;
-    if (b < nw)
-        rg_pair_tile<MW, true>(a, b % (a.et * a.nt), b / (a.et * a.nt), lds);
-    else
-        rg_pair_tile<MW, false>(a, (b - nw) % (a.mt * a.nt), (b - nw) / (a.mt * a.nt), lds);
+// go to the eight in turn) takes a run of each product's.
+template <int BM>
+__global__ __launch_bounds__(2 * BM) void k_rg_pair(PairArgs a) {
+    __shared__ u4v ring[3][8 * BM + 8 * 128];
+    const int nw = (int)gridDim.x - a.nx;
+    // tile number at place i of the launch among n, for the XCD of workgroup g
+    auto turn = [](int n, int i, int g) {
+        const int x0 = (g - i) % 8;  // XCD of place 0
+        const int x = (i + x0) % 8, q = n / 8, r = n % 8, first = (x - x0 + 8) % 8;
+        return first * q + min(first, r) + i / 8;
+    };
+    const bool w = (int)blockIdx.x < nw;
+    const int b = w ? turn(nw, blockIdx.x, blockIdx.x) : turn(a.nx, (int)blockIdx.x - nw, blockIdx.x);
+    if (w) {
+        const int tile = b % (a.et * a.nt), part = b / (a.et * a.nt), m = tile / a.nt * BM, c = tile % a.nt * 128;
+        const int KC = a.kw / 8, W = a.et * BM;
+        const PairIn A = {a.gt + (size_t)part * 2 * KC * W, KC, W, m};
+        const PairIn B = {a.xb + (size_t)part * 2 * KC * a.H, KC, a.H, c};
+        pair_tile<BM>(A, B, min(a.kw, a.Tk - part * a.kw) / kTK, a.egc + (size_t)part * a.Ep, a.ex + (size_t)part * a.H,
+                      true, m, a.E, c, a.H, a.dWr + (a.sw > 1 ? (size_t)part * a.E * a.H : 0), a.sw == 1 && a.acc_w, ring);
+    } else {
+        const int tile = b % (a.mt * a.nt), part = b / (a.mt * a.nt), m = tile / a.nt * BM, c = tile % a.nt * 128;
+        const PairIn A = {a.ga + (size_t)(tile / a.nt) * (a.Ep / 4) * BM + (size_t)part * (a.kx / 8) * BM, a.Ep / 8, BM, 0};
+        const PairIn B = {a.wb + (size_t)part * (a.kx / 4) * a.H, a.kx / 8, a.H, c};
+        pair_tile<BM>(A, B, min(a.kx, a.Ep - part * a.kx) / kTK, a.egr, a.ew + (size_t)part * a.H, false, m, a.T, c, a.H,
+                      a.dx + (a.sx > 1 ? (size_t)part * a.T * a.H : 0), a.sx == 1 && a.acc_x, ring);
+    }
 }
 
 // out (+)= the parts, in increasing order.
@@ -626,76 +686,66 @@ hipError_t launch_route_backward(int H, int E, int k, const float* x, int T, con
     const RgPlan p = rg_plan(H, E, T);
     char* base = reinterpret_cast<char*>(ws);
     float* G = reinterpret_cast<float*>(base + p.g);
+    const int nx = dx && T > 0 ? p.mt * p.nt * p.sx : 0, nw = dWr ? p.et * p.nt * p.sw : 0;
+    const int acc_x = accumulate & 1, acc_w = (accumulate >> 1) & 1;
+    float* ox = p.sx > 1 ? reinterpret_cast<float*>(base + p.px) : dx;
+    float* ow = p.sw > 1 ? reinterpret_cast<float*>(base + p.pw) : dWr;
     hipError_t r = hipSuccess;
-    RgArgs a = {};
-    a.G = G;
-    a.Ep = p.Ep;
-    a.Wr = Wr;
-    a.x = x;
-    a.mask = mask;
-    a.T = T;
-    a.E = E;
-    a.H = H;
-    a.acc_x = accumulate & 1;
-    a.acc_w = (accumulate >> 1) & 1;
-    a.sx = p.sx;
-    a.sw = p.sw;
-    a.kx = p.kx;
-    a.kw = p.kw;
-    a.mt = p.mt;
-    a.nt = p.nt;
-    a.et = p.et;
-    a.dx = p.sx > 1 ? reinterpret_cast<float*>(base + p.px) : dx;
-    a.dWr = p.sw > 1 ? reinterpret_cast<float*>(base + p.pw) : dWr;
-    a.nx = dx && T > 0 ? p.mt * p.nt * p.sx : 0;
-    const int nw = dWr ? p.et * p.nt * p.sw : 0;
-    int* egr = reinterpret_cast<int*>(base + p.exps);
-    uint32_t* keep = reinterpret_cast<uint32_t*>(egr + T);
-    int *egc = egr + T + p.gb, *ex = egc + p.Ep, *ew = ex + H;
-    float* gpart = reinterpret_cast<float*>(base + p.max);
-    float *xpart = gpart + (size_t)p.gb * p.Ep, *wpart = xpart + (size_t)p.xb * H;
-    const bool products = a.nx + nw > 0;
-    const bool pair = p.MW && products;
-    if (T > 0) {
-        const int cb = H / 256;
-        const MaxJob jx = {x, mask, T, H, xpart, pair && dWr ? p.xb * cb : 0};
-        const MaxJob jw = {Wr, nullptr, E, H, wpart, pair && dx ? p.wb * cb : 0};
-        const int ng = pair ? p.gb : (T + 3) / 4;
-#define RL(NV)                                                                                                     \
-    if (pair)                                                                                                      \
-        hipLaunchKernelGGL((k_rg_logits<NV, true>), dim3(ng + jx.nb + jw.nb), dim3(1024), 0, s, dlogits_in, idx, w, dw, \
-                           mask, T, E, p.Ep, k, G, dlogits_out, egr, keep, gpart, ng, jx, jw);                             \
-    else                                                                                                           \
-        hipLaunchKernelGGL((k_rg_logits<NV, false>), dim3(ng), dim3(256), 0, s, dlogits_in, idx, w, dw, mask, T, E,  \
-                           p.Ep, k, G, dlogits_out, egr, keep, gpart, ng, jx, jw)
-        if (p.Ep <= 256) { RL(4); } else if (p.Ep <= 512) { RL(8); } else { RL(16); }
-#undef RL
+    if (p.BM && nx + nw) {
+        int *egr = reinterpret_cast<int*>(base + p.egr), *egc = reinterpret_cast<int*>(base + p.egc);
+        int *ex = reinterpret_cast<int*>(base + p.ex), *ew = reinterpret_cast<int*>(base + p.ew);
+        u4v *ga = reinterpret_cast<u4v*>(base + p.ga), *gt = reinterpret_cast<u4v*>(base + p.gt);
+        u4v *xb = reinterpret_cast<u4v*>(base + p.xb), *wb = reinterpret_cast<u4v*>(base + p.wb);
+        auto panel = [](const float* m, const uint8_t* mk, int rows, int cols, int kw, int parts, int W, u4v* out, int* e,
+                        bool used) {
+            Panel q = {m, mk, rows, cols, 0, W, out, e, 0, 0};
+            while ((1 << q.kwl) < kw) q.kwl++;
+            const int width = 32 * (kMaxPart / kw);
+            q.cb = (cols + width - 1) / width;
+            q.nb = used ? q.cb * parts : 0;
+            return q;
+        };
+        const Panel px = panel(x, mask, T, H, p.kw, p.sw, H, xb, ex, nw > 0);
+        const Panel pw = panel(Wr, nullptr, E, H, p.kx, p.sx, H, wb, ew, nx > 0);
+        const Panel pg = panel(G, nullptr, T, p.Ep, p.kw, p.sw, p.et * p.BM, gt, egc, nw > 0);
+        const int ng = (T + 31) / 32;
+        const int vec = E % 8 == 0 && (reinterpret_cast<uintptr_t>(dlogits_in) | reinterpret_cast<uintptr_t>(dlogits_out)) % 16 == 0;
+#define RP(NC)                                                                                                       \
+    hipLaunchKernelGGL((k_rg_prep<NC>), dim3(ng + px.nb + pw.nb), dim3(1024), 0, s, dlogits_in, idx, w, dw, mask, T, E, \
+                       p.Ep, k, vec, G, dlogits_out, nx ? ga : nullptr, p.BM, egr, ng, px, pw)
+        if (p.Ep <= 512) RP(1); else RP(2);
+#undef RP
         if ((r = hipGetLastError()) != hipSuccess) return r;
-    }
-    if (!products) return hipSuccess;
-    if (pair) {
-        const ExpJob jg = {gpart, p.gb, p.Ep, egc, dWr ? p.Ep / 16 : 0};
-        const ExpJob jx = {xpart, p.xb, H, ex, dWr ? H / 16 : 0}, jw = {wpart, p.wb, H, ew, dx ? H / 16 : 0};
-        hipLaunchKernelGGL(k_rg_exps, dim3(jg.nb + jx.nb + jw.nb), dim3(1024), 0, s, jg, jx, jw);
-        if ((r = hipGetLastError()) != hipSuccess) return r;
-        a.egr = egr;
-        a.keep = keep;
-        a.egc = egc;
-        a.ex = ex;
-        a.ew = ew;
-        if (p.MW == 2)
-            hipLaunchKernelGGL((k_rg_pair<2>), dim3(a.nx + nw), dim3(256), 0, s, a);
+        if (nw) {
+            hipLaunchKernelGGL(k_rg_gt, dim3(pg.nb), dim3(1024), 0, s, pg);
+            if ((r = hipGetLastError()) != hipSuccess) return r;
+        }
+        const PairArgs a = {ga, gt, xb, wb, egr, egc, ex, ew, T, (T + kTK - 1) / kTK * kTK, E, p.Ep, H, ox, ow,
+                            acc_x, acc_w, p.sx, p.sw, p.kx, p.kw, p.mt, p.nt, p.et, nx};
+        if (p.BM == 256)
+            hipLaunchKernelGGL((k_rg_pair<256>), dim3(nx + nw), dim3(512), 0, s, a);
         else
-            hipLaunchKernelGGL((k_rg_pair<1>), dim3(a.nx + nw), dim3(256), 0, s, a);
+            hipLaunchKernelGGL((k_rg_pair<128>), dim3(nx + nw), dim3(256), 0, s, a);
     } else {
-        hipLaunchKernelGGL(k_rg_gemm, dim3(a.nx + nw), dim3(256), 0, s, a);
+        if (T > 0) {
+            const dim3 grid((T + 3) / 4), block(256);
+#define RL(NV)                                                                                                     \
+    hipLaunchKernelGGL((k_rg_logits<NV>), grid, block, 0, s, dlogits_in, idx, w, dw, mask, T, E, p.Ep, k, G, dlogits_out)
+            if (p.Ep <= 256) RL(4); else if (p.Ep <= 512) RL(8); else RL(16);
+#undef RL
+            if ((r = hipGetLastError()) != hipSuccess) return r;
+        }
+        if (nx + nw == 0) return hipSuccess;
+        const RgArgs a = {G, p.Ep, Wr, x, mask, T, E, H, ox, ow, acc_x, acc_w,
+                          p.sx, p.sw, p.kx, p.kw, p.mt, p.nt, p.et, nx};
+        hipLaunchKernelGGL(k_rg_gemm, dim3(nx + nw), dim3(256), 0, s, a);
     }
     if ((r = hipGetLastError()) != hipSuccess) return r;
-    const size_t qx = a.nx && p.sx > 1 ? (size_t)T * H / 4 : 0, qw = dWr && p.sw > 1 ? (size_t)E * H / 4 : 0;
+    const size_t qx = nx && p.sx > 1 ? (size_t)T * H / 4 : 0, qw = nw && p.sw > 1 ? (size_t)E * H / 4 : 0;
     if (qx + qw) {
         hipLaunchKernelGGL(k_rg_reduce, dim3((unsigned)((qx + qw + 255) / 256)), dim3(256), 0, s,
-                           reinterpret_cast<const f4v*>(base + p.px), p.sx, qx, reinterpret_cast<f4v*>(dx), a.acc_x,
-                           reinterpret_cast<const f4v*>(base + p.pw), p.sw, qw, reinterpret_cast<f4v*>(dWr), a.acc_w);
+                           reinterpret_cast<const f4v*>(base + p.px), p.sx, qx, reinterpret_cast<f4v*>(dx), acc_x,
+                           reinterpret_cast<const f4v*>(base + p.pw), p.sw, qw, reinterpret_cast<f4v*>(dWr), acc_w);
         r = hipGetLastError();
     }
     return r;
