@@ -61,7 +61,7 @@ RgPlan rg_plan(int H, int E, int T) {
     if (p.BM) {
         auto split = [](int64_t tiles, int64_t len, int& parts, int& per) {
             per = kMaxPart;
-            while (per > 64 && tiles * ((len + per - 1) / per) < 128) per /= 2;
+            while (per > 64 && tiles * ((len + per - 1) / per) < 64) per /= 2;
             parts = (int)((len + per - 1) / per);
         };
         split((int64_t)p.mt * p.nt, E, p.sx, p.kx);
@@ -314,16 +314,16 @@ __device__ __forceinline__ void pair8(const float (&v)[8], float scale, u4v& h, 
 __device__ __forceinline__ int place(int n) { return n / 64 * 64 + n % 2 * 32 + n / 2 % 32; }
 
 // The parts of a matrix whose rows run along the sum: out[part][2][kw / 8][W]
-// chunks from p [rows][cols]. A workgroup of 1024 takes the kw = 2^kwl rows
-// of a part and 32 * 1024 / kw columns, each thread 8 rows and 4 columns: it
-// holds them in registers while the columns' maxima are found, so memory is
+// chunks from p [rows][cols]. A workgroup of NT = 2^ntl threads (at least
+// kw) takes the kw = 2^kwl rows of a part and 32 NT / kw columns, each thread
+// 8 rows and 4 columns: it holds them in registers while the columns' maxima are found, so memory is
 // read once and written once. Rows behind the end and masked ones are loaded
 // (from the last row) and become zeros.
 struct Panel {
     const float* p;
     const uint8_t* mask;  // rows that do not count, or null
     int rows, cols;       // cols a multiple of 32
-    int kwl, W;
+    int kwl, ntl, W;
     u4v* out;
     int* e;               // exponents [part][cols]
     int cb, nb;           // workgroups per part, and all
@@ -331,7 +331,7 @@ struct Panel {
 __device__ __forceinline__ void make_panel(const Panel& j, int b, f4v (*red)[8]) {
     const int kw = 1 << j.kwl, part = b / j.cb, tid = threadIdx.x, wave = wave_id(), c4 = tid & 7;
     const int sub = tid >> j.kwl, r8 = (tid & (kw - 1)) >> 3;
-    const int col = ((b % j.cb << (10 - j.kwl)) + sub) * 32 + 4 * c4, r0 = part * kw + 8 * r8;
+    const int col = ((b % j.cb << (j.ntl - j.kwl)) + sub) * 32 + 4 * c4, r0 = part * kw + 8 * r8;
     const bool in = col < j.cols;
     f4v v[8];
     bool on[8];
@@ -377,9 +377,9 @@ __device__ __forceinline__ void make_panel(const Panel& j, int b, f4v (*red)[8])
     }
 }
 
-// grid ceil(T / 32) + panels of x + panels of Wr, 1024 threads. The first
+// grid ng + panels of x + panels of Wr, 1024 threads or fewer. The first ng
 // workgroups make G (a wave two tokens, a lane the columns 8 lane + 512 c + i):
-// in fp32 for k_rg_gt, and its rows' parts ga [tile][2][Ep / 8][BM].
+// in fp32 for k_rg_gt (unless dout serves), and its rows' parts ga [tile][2][Ep / 8][BM].
 // Everything a wave needs is loaded before its mask bytes are looked at.
 template <int NC>
 __global__ __launch_bounds__(1024) void k_rg_prep(const float* __restrict__ din, const int32_t* __restrict__ idx,
@@ -394,7 +394,7 @@ __global__ __launch_bounds__(1024) void k_rg_prep(const float* __restrict__ din,
         return;
     }
     constexpr int NV = 8 * NC;
-    const int lane = threadIdx.x & 63, t0 = (int)blockIdx.x * 32 + wave_id() * 2;
+    const int lane = threadIdx.x & 63, t0 = (int)(blockIdx.x * (blockDim.x >> 6) + wave_id()) * 2;
     auto col = [lane](int i) { return 8 * lane + i / 8 * 512 + i % 8; };
     float v[2][NV], mw[2], md[2];
     int me[2];
@@ -454,9 +454,11 @@ __global__ __launch_bounds__(1024) void k_rg_prep(const float* __restrict__ din,
             float o[8];
 #pragma unroll
             for (int q = 0; q < 8; q++) o[q] = v[u][8 * c + q];
-            f4v* g = reinterpret_cast<f4v*>(G + (size_t)t * Ep + c0);
-            g[0] = f4v{o[0], o[1], o[2], o[3]};
-            g[1] = f4v{o[4], o[5], o[6], o[7]};
+            if (G) {
+                f4v* g = reinterpret_cast<f4v*>(G + (size_t)t * Ep + c0);
+                g[0] = f4v{o[0], o[1], o[2], o[3]};
+                g[1] = f4v{o[4], o[5], o[6], o[7]};
+            }
             if (ga) {
                 u4v h, l;
                 pair8(o, scale, h, l);
@@ -511,111 +513,134 @@ struct PairArgs {
     int sx, sw, kx, kw, mt, nt, et, nx;  // nx: workgroups of dx
 };
 
-// One tile of BM x 128 of C, 2 BM threads: BM / 32 waves of 64 x 64. Steps of
-// 32 k: LDS holds three of them as chunks [2][4][BM] of A and [2][4][128] of
-// B; step s + 2 is on its way from memory while step s is multiplied.
+// Steps of the ring of a tile, 24 KB (BM 256) or 16 KB (BM 128) each: two or
+// three workgroups fit a compute unit, so that one multiplies while another
+// starts or writes its tile (a ring of 6 with one workgroup: 175 us against
+// 166 at 8191 x 512 x 2560).
+constexpr int kRing = 3;
+
+// One tile of BM x 128 of C, four waves of BM / 2 x 64, in steps of 16 k. LDS
+// is a ring of steps, each as chunks [2][2][BM] of A and [2][2][128] of B.
+// While the matrix instructions of step s run from one set of registers, the
+// fragments of step s + 1 are read into the other, and the steps up to
+// s + kRing are on their way from memory. The wave's square is as large as
+// the registers allow: LDS feeds 128 bytes a cycle, and 128 x 64 needs 48 KB
+// per workgroup and step where the matrix units take 768 cycles, 64 x 64
+// 64 KB.
 template <int BM>
 __device__ __forceinline__ void pair_tile(const PairIn& A, const PairIn& B, int steps, const int* __restrict__ ea,
                                           const int* __restrict__ eb, bool permuted, int m0, int M, int n0, int H,
-                                          float* C, bool add, u4v (*ring)[8 * BM + 8 * 128]) {
-    constexpr int NW = BM / 32, NA = BM / 8 / NW, NB = 16 / NW, NI = NA + NB;  // 1 KB loads of a wave and step
+                                          float* C, bool add, u4v* lds) {
+    constexpr int R = kRing, MI = BM / 64, NA = BM / 64, NB = 2, NI = NA + NB;  // NI: 1 KB loads of a wave and step
+    constexpr int STEP = 4 * BM + 4 * 128;
+    int* exps = reinterpret_cast<int*>(lds + R * STEP);  // of the tile's rows and columns
     const int lane = threadIdx.x & 63, wave = wave_id(), wm = wave >> 1, wn = wave & 1;
     const rsrc_t rA = make_rsrc(A.p, (uint32_t)A.KC * (uint32_t)A.W * 32u);
     const rsrc_t rB = make_rsrc(B.p, (uint32_t)B.KC * (uint32_t)B.W * 32u);
     uint32_t oa[NA], ob[NB];  // byte offsets of the wave's loads at step 0
 #pragma unroll
     for (int i = 0; i < NA; i++) {
-        const int q = wave + NW * i, row = q / (BM / 64), seg = q % (BM / 64);
-        oa[i] = ((uint32_t)((row >> 2) * A.KC + (row & 3)) * (uint32_t)A.W + (uint32_t)(A.off + 64 * seg + lane)) * 16u;
+        const int q = wave + 4 * i, row = q / (BM / 64), seg = q % (BM / 64);  // row: part, chunk of the step
+        oa[i] = ((uint32_t)((row >> 1) * A.KC + (row & 1)) * (uint32_t)A.W + (uint32_t)(A.off + 64 * seg + lane)) * 16u;
     }
 #pragma unroll
     for (int i = 0; i < NB; i++) {
-        const int q = wave + NW * i, row = q / 2, seg = q % 2;
-        ob[i] = ((uint32_t)((row >> 2) * B.KC + (row & 3)) * (uint32_t)B.W + (uint32_t)(B.off + 64 * seg + lane)) * 16u;
+        const int q = wave + 4 * i, row = q / 2, seg = q % 2;
+        ob[i] = ((uint32_t)((row >> 1) * B.KC + (row & 1)) * (uint32_t)B.W + (uint32_t)(B.off + 64 * seg + lane)) * 16u;
     }
-    const uint32_t da = (uint32_t)A.W * 64u, db = (uint32_t)B.W * 64u;  // four chunk rows a step
+    const uint32_t da = (uint32_t)A.W * 32u, db = (uint32_t)B.W * 32u;  // two chunk rows a step
     // every step issues the same loads; those behind the last one read nothing
     auto issue = [&](int s, u4v* to) {
         const bool on = s < steps;
 #pragma unroll
         for (int i = 0; i < NA; i++)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rA, (__attribute__((address_space(3))) void*)(to + 64 * (wave + NW * i)), 16,
+                rA, (__attribute__((address_space(3))) void*)(to + 64 * (wave + 4 * i)), 16,
                 on ? oa[i] + (uint32_t)s * da : kOOB, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < NB; i++)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rB, (__attribute__((address_space(3))) void*)(to + 8 * BM + 64 * (wave + NW * i)), 16,
+                rB, (__attribute__((address_space(3))) void*)(to + 4 * BM + 64 * (wave + 4 * i)), 16,
                 on ? ob[i] + (uint32_t)s * db : kOOB, 0, 0, 0);
     };
-    f16v acc[2][2];
+    struct Frags {
+        h8v a[2][MI], b[2][2];
+    };
+    const int pa = (lane >> 5) * BM + 32 * MI * wm + (lane & 31), pb = 4 * BM + (lane >> 5) * 128 + 64 * wn + (lane & 31);
+    auto read = [&](const u4v* from, Frags& f) {
 #pragma unroll
-    for (int i = 0; i < 2; i++)
+        for (int t = 0; t < 2; t++) {
+#pragma unroll
+            for (int i = 0; i < MI; i++) f.a[t][i] = __builtin_bit_cast(h8v, from[pa + 2 * t * BM + 32 * i]);
+#pragma unroll
+            for (int j = 0; j < 2; j++) f.b[t][j] = __builtin_bit_cast(h8v, from[pb + 2 * t * 128 + 32 * j]);
+        }
+    };
+    f16v acc[MI][2];
+#pragma unroll
+    for (int i = 0; i < MI; i++)
 #pragma unroll
         for (int j = 0; j < 2; j++)
 #pragma unroll
             for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
-    issue(0, ring[0]);
-    issue(1, ring[1]);
-    int cur = 0;
-    for (int s = 0; s < steps; s++) {
-        ring_barrier<NI>();  // step s is there, and every wave is done with step s - 1
-        issue(s + 2, ring[cur == 0 ? 2 : cur - 1]);
-        const u4v* a = ring[cur] + 64 * wm + (lane & 31);
-        const u4v* b = ring[cur] + 8 * BM + 64 * wn + (lane & 31);
+    auto multiply = [&](const Frags& f) {
 #pragma unroll
-        for (int ks = 0; ks < 2; ks++) {
-            const int kc = 2 * ks + (lane >> 5);
-            h8v fa[2][2], fb[2][2];
+        for (int t = 0; t < 3; t++)  // l h', h l', h h'
 #pragma unroll
-            for (int t = 0; t < 2; t++)
+            for (int i = 0; i < MI; i++)
 #pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    fa[t][i] = __builtin_bit_cast(h8v, a[(4 * t + kc) * BM + 32 * i]);
-                    fb[t][i] = __builtin_bit_cast(h8v, b[(4 * t + kc) * 128 + 32 * i]);
-                }
+                for (int j = 0; j < 2; j++)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.a[t == 0][i], f.b[t == 1][j], acc[i][j], 0, 0, 0);
+    };
+    const int er = (int)threadIdx.x < BM ? ea[min(m0 + (int)threadIdx.x, M - 1)] : 0;
+    const int ec = (int)threadIdx.x < 128 ? eb[n0 + threadIdx.x] : 0;
+    if ((int)threadIdx.x < BM) exps[threadIdx.x] = er;
+    if ((int)threadIdx.x < 128) exps[BM + threadIdx.x] = ec;
 #pragma unroll
-            for (int t = 0; t < 3; t++)  // l h', h l', h h'
-#pragma unroll
-                for (int i = 0; i < 2; i++)
-#pragma unroll
-                    for (int j = 0; j < 2; j++)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[t == 0][i], fb[t == 1][j], acc[i][j], 0, 0, 0);
-        }
-        cur = cur == 2 ? 0 : cur + 1;
+    for (int s = 0; s < R; s++) issue(s, lds + s * STEP);
+    ring_barrier<(R - 1) * NI>();  // step 0 is there
+    Frags f0, f1;
+    read(lds, f0);
+    int at = 0;  // s % R
+    auto next = [](int q) { return q + 1 == R ? 0 : q + 1; };
+    // step s from f, the fragments of step s + 1 into g: step s + 1 is there
+    // and every wave has read step s, whose place the load of step s + R takes
+    auto turn = [&](int s, const Frags& f, Frags& g) {
+        ring_barrier<(R - 2) * NI>();
+        issue(s + R, lds + at * STEP);
+        at = next(at);
+        read(lds + at * STEP, g);
+        __builtin_amdgcn_sched_barrier(0);  // the reads go out before the products, not when g is needed
+        multiply(f);
+    };
+    for (int s = 0; s < steps; s += 2) {  // steps are even
+        turn(s, f0, f1);
+        turn(s + 1, f1, f0);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    const int n = n0 + 64 * wn + 2 * (lane & 31), e0 = eb[n], e1 = eb[n + 1];
-    auto row = [&](int i, int r) {
-        const int q = 8 * (r / 4) + 4 * (lane >> 5) + r % 4;  // row of the MFMA tile
-        return m0 + 64 * wm + (permuted ? 2 * q + i : 32 * i + q);
+    const int nl = 64 * wn + 2 * (lane & 31), n = n0 + nl, e0 = exps[BM + nl], e1 = exps[BM + nl + 1];
+    auto row = [&](int i, int r) {  // of the workgroup's tile
+        const int q = 8 * (r / 4) + 4 * (lane >> 5) + r % 4;  // of the MFMA tile
+        return 32 * MI * wm + (permuted ? i / 2 * 64 + 2 * q + i % 2 : 32 * i + q);
     };
-    int em[2][16];
+    C += (size_t)m0 * H + n;
+    const int rows = M - m0;
 #pragma unroll
-    for (int i = 0; i < 2; i++)
+    for (int i = 0; i < MI; i++) {
+        f2v old[16];
 #pragma unroll
-        for (int r = 0; r < 16; r++) em[i][r] = ea[min(row(i, r), M - 1)];
-    if (add) {
+        for (int r = 0; r < 16; r++)
+            old[r] = add ? *reinterpret_cast<const f2v*>(C + (size_t)min(row(i, r), rows - 1) * H) : f2v{0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-            f2v old[16];
-#pragma unroll
-            for (int r = 0; r < 16; r++)
-                old[r] = *reinterpret_cast<const f2v*>(C + (size_t)min(row(i, r), M - 1) * H + n);
-#pragma unroll
-            for (int r = 0; r < 16; r++)
-                if (row(i, r) < M)
-                    *reinterpret_cast<f2v*>(C + (size_t)row(i, r) * H + n) =
-                        f2v{old[r].x + ldexpf(acc[i][0][r], em[i][r] + e0), old[r].y + ldexpf(acc[i][1][r], em[i][r] + e1)};
+        for (int r = 0; r < 16; r++) {
+            const int m = row(i, r), em = exps[m];
+            f2v v = {ldexpf(acc[i][0][r], em + e0), ldexpf(acc[i][1][r], em + e1)};
+            if (add) {
+                v.x += old[r].x;
+                v.y += old[r].y;
+            }
+            if (m < rows) *reinterpret_cast<f2v*>(C + (size_t)m * H) = v;
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 2; i++)
-#pragma unroll
-            for (int r = 0; r < 16; r++)
-                if (row(i, r) < M)
-                    *reinterpret_cast<f2v*>(C + (size_t)row(i, r) * H + n) =
-                        f2v{ldexpf(acc[i][0][r], em[i][r] + e0), ldexpf(acc[i][1][r], em[i][r] + e1)};
     }
 }
 
@@ -623,8 +648,10 @@ __device__ __forceinline__ void pair_tile(const PairIn& A, const PairIn& B, int 
 // then those of dx. Consecutive tiles share rows of A, so each XCD (workgroups
 // go to the eight in turn) takes a run of each product's.
 template <int BM>
-__global__ __launch_bounds__(2 * BM) void k_rg_pair(PairArgs a) {
-    __shared__ u4v ring[3][8 * BM + 8 * 128];
+__global__ __launch_bounds__(256, 2) void k_rg_pair(PairArgs a) {
+    // One array: with a second one beside it the compiler waits for every load
+    // in flight before each LDS read.
+    __shared__ u4v lds[kRing * (4 * BM + 4 * 128) + (BM + 128) / 4];
     const int nw = (int)gridDim.x - a.nx;
     // tile number at place i of the launch among n, for the XCD of workgroup g
     auto turn = [](int n, int i, int g) {
@@ -639,14 +666,14 @@ __global__ __launch_bounds__(2 * BM) void k_rg_pair(PairArgs a) {
         const int KC = a.kw / 8, W = a.et * BM;
         const PairIn A = {a.gt + (size_t)part * 2 * KC * W, KC, W, m};
         const PairIn B = {a.xb + (size_t)part * 2 * KC * a.H, KC, a.H, c};
-        pair_tile<BM>(A, B, min(a.kw, a.Tk - part * a.kw) / kTK, a.egc + (size_t)part * a.Ep, a.ex + (size_t)part * a.H,
-                      true, m, a.E, c, a.H, a.dWr + (a.sw > 1 ? (size_t)part * a.E * a.H : 0), a.sw == 1 && a.acc_w, ring);
+        pair_tile<BM>(A, B, min(a.kw, a.Tk - part * a.kw) / 16, a.egc + (size_t)part * a.Ep, a.ex + (size_t)part * a.H,
+                      true, m, a.E, c, a.H, a.dWr + (a.sw > 1 ? (size_t)part * a.E * a.H : 0), a.sw == 1 && a.acc_w, lds);
     } else {
         const int tile = b % (a.mt * a.nt), part = b / (a.mt * a.nt), m = tile / a.nt * BM, c = tile % a.nt * 128;
         const PairIn A = {a.ga + (size_t)(tile / a.nt) * (a.Ep / 4) * BM + (size_t)part * (a.kx / 8) * BM, a.Ep / 8, BM, 0};
         const PairIn B = {a.wb + (size_t)part * (a.kx / 4) * a.H, a.kx / 8, a.H, c};
-        pair_tile<BM>(A, B, min(a.kx, a.Ep - part * a.kx) / kTK, a.egr, a.ew + (size_t)part * a.H, false, m, a.T, c, a.H,
-                      a.dx + (a.sx > 1 ? (size_t)part * a.T * a.H : 0), a.sx == 1 && a.acc_x, ring);
+        pair_tile<BM>(A, B, min(a.kx, a.Ep - part * a.kx) / 16, a.egr, a.ew + (size_t)part * a.H, false, m, a.T, c, a.H,
+                      a.dx + (a.sx > 1 ? (size_t)part * a.T * a.H : 0), a.sx == 1 && a.acc_x, lds);
     }
 }
 
@@ -696,34 +723,41 @@ hipError_t launch_route_backward(int H, int E, int k, const float* x, int T, con
         int *ex = reinterpret_cast<int*>(base + p.ex), *ew = reinterpret_cast<int*>(base + p.ew);
         u4v *ga = reinterpret_cast<u4v*>(base + p.ga), *gt = reinterpret_cast<u4v*>(base + p.gt);
         u4v *xb = reinterpret_cast<u4v*>(base + p.xb), *wb = reinterpret_cast<u4v*>(base + p.wb);
-        auto panel = [](const float* m, const uint8_t* mk, int rows, int cols, int kw, int parts, int W, u4v* out, int* e,
-                        bool used) {
-            Panel q = {m, mk, rows, cols, 0, W, out, e, 0, 0};
+        // dlogits_out has G as the workspace would, where E needs no padding
+        // (k_rg_gt reads it with 16-byte loads)
+        const bool own_g = !dlogits_out || p.Ep != E || reinterpret_cast<uintptr_t>(dlogits_out) % 16;
+        const float* Gp = own_g ? G : dlogits_out;
+        float* Gw = own_g && nw ? G : nullptr;
+        auto panel = [](const float* m, const uint8_t* mk, int rows, int cols, int kw, int nt, int parts, int W, u4v* out,
+                        int* e, bool used) {
+            Panel q = {m, mk, rows, cols, 0, 0, W, out, e, 0, 0};
             while ((1 << q.kwl) < kw) q.kwl++;
-            const int width = 32 * (kMaxPart / kw);
+            while ((1 << q.ntl) < nt) q.ntl++;
+            const int width = 32 * (nt / kw);
             q.cb = (cols + width - 1) / width;
             q.nb = used ? q.cb * parts : 0;
             return q;
         };
-        const Panel px = panel(x, mask, T, H, p.kw, p.sw, H, xb, ex, nw > 0);
-        const Panel pw = panel(Wr, nullptr, E, H, p.kx, p.sx, H, wb, ew, nx > 0);
-        const Panel pg = panel(G, nullptr, T, p.Ep, p.kw, p.sw, p.et * p.BM, gt, egc, nw > 0);
-        const int ng = (T + 31) / 32;
+        const int nt = p.kw > p.kx ? p.kw : p.kx;  // threads: one panel's at least
+        const Panel px = panel(x, mask, T, H, p.kw, nt, p.sw, H, xb, ex, nw > 0);
+        const Panel pw = panel(Wr, nullptr, E, H, p.kx, nt, p.sx, H, wb, ew, nx > 0);
+        const Panel pg = panel(Gp, nullptr, T, p.Ep, p.kw, p.kw, p.sw, p.et * p.BM, gt, egc, nw > 0);
+        const int ng = (T + nt / 32 - 1) / (nt / 32);
         const int vec = E % 8 == 0 && (reinterpret_cast<uintptr_t>(dlogits_in) | reinterpret_cast<uintptr_t>(dlogits_out)) % 16 == 0;
 #define RP(NC)                                                                                                       \
-    hipLaunchKernelGGL((k_rg_prep<NC>), dim3(ng + px.nb + pw.nb), dim3(1024), 0, s, dlogits_in, idx, w, dw, mask, T, E, \
-                       p.Ep, k, vec, G, dlogits_out, nx ? ga : nullptr, p.BM, egr, ng, px, pw)
+    hipLaunchKernelGGL((k_rg_prep<NC>), dim3(ng + px.nb + pw.nb), dim3(nt), 0, s, dlogits_in, idx, w, dw, mask, T, E, \
+                       p.Ep, k, vec, Gw, dlogits_out, nx ? ga : nullptr, p.BM, egr, ng, px, pw)
         if (p.Ep <= 512) RP(1); else RP(2);
 #undef RP
         if ((r = hipGetLastError()) != hipSuccess) return r;
         if (nw) {
-            hipLaunchKernelGGL(k_rg_gt, dim3(pg.nb), dim3(1024), 0, s, pg);
+            hipLaunchKernelGGL(k_rg_gt, dim3(pg.nb), dim3(p.kw), 0, s, pg);
             if ((r = hipGetLastError()) != hipSuccess) return r;
         }
         const PairArgs a = {ga, gt, xb, wb, egr, egc, ex, ew, T, (T + kTK - 1) / kTK * kTK, E, p.Ep, H, ox, ow,
                             acc_x, acc_w, p.sx, p.sw, p.kx, p.kw, p.mt, p.nt, p.et, nx};
         if (p.BM == 256)
-            hipLaunchKernelGGL((k_rg_pair<256>), dim3(nx + nw), dim3(512), 0, s, a);
+            hipLaunchKernelGGL((k_rg_pair<256>), dim3(nx + nw), dim3(256), 0, s, a);
         else
             hipLaunchKernelGGL((k_rg_pair<128>), dim3(nx + nw), dim3(256), 0, s, a);
     } else {
