@@ -29,6 +29,7 @@ namespace moe {
 
 namespace {
 
+constexpr int kMaxParts = 4;  // parts of a sequence's counts that k_bal_main adds
 constexpr int kBadSeq = -1;  // n_s of a sequence with a bad offset or a bad expert index
 
 constexpr int kSelfCount = 8192;  // T * k up to which k_bal_main counts by itself
@@ -46,12 +47,12 @@ BalWs bal_ws(int T, int E, int S) {
     BalWs b;
     // about 1024 tokens per counting workgroup, 64 parts at most; several
     // sequences, which may be of unlike lengths, get 4 parts where that still
-    // leaves 128 tokens each; the main launch adds up to 4 parts itself
+    // leaves 128 tokens each; the main launch adds up to kMaxParts itself
     const int64_t per = ((int64_t)T + S - 1) / S;
     b.J = (int)((per + 1023) / 1024);
-    if (S > 1 && b.J < 4) b.J = (int)(per / 128 < 4 ? per / 128 : 4);
+    if (S > 1 && b.J < kMaxParts) b.J = (int)(per / 128 < kMaxParts ? per / 128 : kMaxParts);
     b.J = b.J < 1 ? 1 : (b.J > 64 ? 64 : b.J);
-    b.JM = b.J <= 4 ? b.J : 1;
+    b.JM = b.J <= kMaxParts ? b.J : 1;
     // about 1024 chunks (four workgroups per compute unit) of whole rounds of
     // the four waves
     b.TB = (int)(((int64_t)T + 1023) / 1024);
@@ -83,36 +84,49 @@ __device__ __forceinline__ bool seq_bounds(const int32_t* __restrict__ off, int 
     return lo >= 0 && lo <= hi && hi <= T;
 }
 
-// Adds the routing of tokens a .. b - 1 to hist (LDS) by NT threads, eight
-// loads in flight each; returns whether this thread saw a bad index, and its
-// share of the counted tokens in `mine`.
+// Adds the routing of tokens a .. b - 1 to hist (LDS) by NT threads; returns
+// whether this thread saw a bad index, and its share of the counted tokens in
+// `mine`. Without a mask the indices are one list, eight loads a thread at
+// once; with one a thread takes a token, its mask byte beside its indices
+// (finding the token of each index of the list and then its mask: 12 us
+// against 9 at 32768 tokens; token by token without a mask: 8 against 4 at
+// 2451).
 template <int NT>
 __device__ __forceinline__ bool bal_hist(const int32_t* __restrict__ idx, const uint8_t* __restrict__ mask, int a,
                                          int b, int E, int k, int* hist, int& mine) {
-    constexpr int U = 8;
-    const int64_t i1 = (int64_t)b * k;
     bool bad = false;
     mine = 0;
-    if (mask)
-        for (int t = a + (int)threadIdx.x; t < b; t += NT) mine += mask[t] != 0;
-    else if (threadIdx.x == 0)
-        mine = b - a;
-    for (int64_t i = (int64_t)a * k + threadIdx.x; i < i1; i += U * NT) {
-        int e[U];
-        bool on[U];
+    if (!mask) {
+        if (threadIdx.x == 0) mine = b - a;
+        const int i1 = b * k;  // T k <= 2^29
+        for (int i = a * k + (int)threadIdx.x; i < i1; i += 8 * NT) {
+            int e[8];
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int64_t q = i + u * NT;
-            on[u] = q < i1;
-            e[u] = on[u] ? idx[q] : 0;
-            if (mask && on[u]) on[u] = mask[(uint32_t)q / (uint32_t)k] != 0;  // T * k < 2^30
-        }
+            for (int u = 0; u < 8; u++) e[u] = i + u * NT < i1 ? idx[i + u * NT] : 0;
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            const bool in = (unsigned)e[u] < (unsigned)E;
-            if (on[u] && in) atomicAdd(&hist[e[u]], 1);
-            bad |= on[u] && !in;
+            for (int u = 0; u < 8; u++) {
+                const bool in = (unsigned)e[u] < (unsigned)E, use = i + u * NT < i1;
+                if (use && in) atomicAdd(&hist[e[u]], 1);
+                bad |= use && !in;
+            }
         }
+        return bad;
+    }
+    for (int t = a + (int)threadIdx.x; t < b; t += NT) {
+        const bool on = mask[t] != 0;
+        const int32_t* it = idx + (size_t)t * k;
+        for (int i = 0; i < k; i += 8) {
+            int e[8];
+#pragma unroll
+            for (int u = 0; u < 8; u++) e[u] = it[min(i + u, k - 1)];
+#pragma unroll
+            for (int u = 0; u < 8; u++) {
+                const bool in = (unsigned)e[u] < (unsigned)E, use = on && i + u < k;
+                if (use && in) atomicAdd(&hist[e[u]], 1);
+                bad |= use && !in;
+            }
+        }
+        mine += on;
     }
     return bad;
 }
@@ -168,34 +182,45 @@ __global__ __launch_bounds__(256) void k_bal_merge(const int32_t* __restrict__ p
     }
 }
 
-// Counted tokens of sequence s from its parts; kBadSeq if one of them is bad.
+// Counted tokens of sequence s from its J <= kMaxParts parts, loaded together;
+// kBadSeq if one of them is bad.
 __device__ __forceinline__ int seq_n(const int32_t* __restrict__ n, int s, int J) {
-    int a = 0;
+    int v[kMaxParts], a = 0;
     bool bad = false;
-    for (int j = 0; j < J; j++) {
-        const int v = n[(size_t)s * J + j];
-        bad |= v < 0;
-        a += v;
+#pragma unroll
+    for (int j = 0; j < kMaxParts; j++) v[j] = n[(size_t)s * J + min(j, J - 1)];
+#pragma unroll
+    for (int j = 0; j < kMaxParts; j++) {
+        bad |= v[j] < 0;
+        a += j < J ? v[j] : 0;
     }
     return bad ? kBadSeq : a;
 }
 
-// Live sequences and counted tokens over all S (every thread of a workgroup
-// of NT threads gets them); false if any sequence is bad.
+// What a workgroup has to know of all sequences: the live ones, the counted
+// tokens, the first one that ends behind token t0 (the offsets do not decrease
+// where all are fine), and whether all are fine. One round of loads; the first
+// kSeqLds sequences' numbers stay in LDS for what follows.
+constexpr int kSeqLds = 256;
+struct Seqs {
+    int live, total, first;
+    bool fine;
+};
 template <int NT>
-__device__ __forceinline__ bool bal_totals(const int32_t* __restrict__ n, int S, int J, int& live, int& total) {
-    if (S == 1) {
-        const int v = seq_n(n, 0, J);
-        live = v > 0;
-        total = v;
-        return v >= 0;
-    }
-    __shared__ int acc[3];
-    if (threadIdx.x < 3) acc[threadIdx.x] = 0;
+__device__ __forceinline__ Seqs bal_totals(const int32_t* __restrict__ n, const int32_t* __restrict__ off, int T,
+                                           int t0, int S, int J, int* sn, int* so) {
+    __shared__ int acc[4];
+    if (threadIdx.x < 4) acc[threadIdx.x] = 0;
     __syncthreads();
-    int l = 0, t = 0, b = 0;
+    int l = 0, t = 0, b = 0, f = 0;
     for (int s = threadIdx.x; s < S; s += NT) {
-        const int v = seq_n(n, s, J);
+        const int v = seq_n(n, s, J), lo = off ? off[s] : 0, hi = off ? off[s + 1] : T;
+        if (s < kSeqLds) {
+            sn[s] = v;
+            so[2 * s] = lo;
+            so[2 * s + 1] = hi;
+        }
+        f += hi <= t0;
         l += v > 0;
         t += max(v, 0);
         b |= v < 0;
@@ -205,10 +230,9 @@ __device__ __forceinline__ bool bal_totals(const int32_t* __restrict__ n, int S,
         atomicAdd(&acc[1], t);
     }
     if (b) atomicOr(&acc[2], 1);
+    if (f) atomicAdd(&acc[3], f);
     __syncthreads();
-    live = acc[0];
-    total = acc[1];
-    return acc[2] == 0;
+    return Seqs{acc[0], acc[1], acc[3], acc[2] == 0};
 }
 
 // Column i (< NV) of this lane: vector form 4 lane + 256 (i / 4) + i % 4,
@@ -274,8 +298,9 @@ __global__ __launch_bounds__(256) void k_bal_main(const float* __restrict__ logi
     __shared__ float zred[4];
     const int lane = threadIdx.x & 63, wave = wave_id(), c = blockIdx.x;
     const int t0 = c * TB, t1 = min(T, t0 + TB);
-    int live, total;
-    bool fine;
+    __shared__ int sn[kSeqLds], so[2 * kSeqLds];  // counted tokens and bounds of the sequences
+    Seqs all;
+    const float up = dloss ? *dloss : 1.0f;
     __shared__ int hist[SELF ? 64 * NV : 1];
     __shared__ int tot[2];
     if constexpr (SELF) {
@@ -288,21 +313,25 @@ __global__ __launch_bounds__(256) void k_bal_main(const float* __restrict__ logi
         if (!bad) bad = bal_hist<256>(idx, mask, lo, hi, E, k, hist, mine);
         if (mine) atomicAdd(&tot[0], mine);
         if (bad) atomicOr(&tot[1], 1);
+        if (tid == 0) {
+            so[0] = lo;
+            so[1] = hi;
+        }
         __syncthreads();
-        total = tot[0];
-        live = total > 0;
-        fine = tot[1] == 0;
+        all = Seqs{tot[0] > 0, tot[0], hi <= t0, tot[1] == 0};
+        if (tid == 0) sn[0] = all.total;
         if (c == 0) {
             for (int e = tid; e < E; e += 256) cnt[e] = hist[e];
             if (tid == 0) {
-                *n = fine ? total : kBadSeq;
+                *n = all.fine ? all.total : kBadSeq;
                 *ticket = 0;
             }
         }
+        __syncthreads();
     } else {
-        fine = bal_totals<256>(n, S, J, live, total);
+        all = bal_totals<256>(n, off, T, t0, S, J, sn, so);
     }
-    if (!fine) {
+    if (!all.fine) {
         if (dlogits) {
             float q[NV];
 #pragma unroll
@@ -311,89 +340,154 @@ __global__ __launch_bounds__(256) void k_bal_main(const float* __restrict__ logi
         }
         return;
     }
-    const float up = dloss ? *dloss : 1.0f;
+    const int live = all.live, total = all.total;
     float zero[NV];
 #pragma unroll
     for (int i = 0; i < NV; i++) zero[i] = 0.0f;
-    // the first sequence that ends behind t0 (the offsets do not decrease: fine)
-    int s = 0;
-    if (off) {
-        int lo = 0, hi = S;
-        while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (off[mid + 1] > t0) hi = mid; else lo = mid + 1;
-        }
-        s = lo;
-    }
-    int t = t0;
+    int t = t0, s = all.first;
     while (t < t1) {
-        const int a = s < S ? max(t, min(t1, off ? off[s] : 0)) : t1;
-        const int b = s < S ? max(a, min(t1, off ? off[s + 1] : T)) : t1;
+        int lo = t1, hi = t1, ns = 0;
+        if (s < kSeqLds) {
+            if (s < S) {
+                lo = so[2 * s];
+                hi = so[2 * s + 1];
+                ns = sn[s];
+            }
+        } else if (s < S) {
+            lo = off[s];
+            hi = off[s + 1];
+            ns = seq_n(n, s, J);
+        }
+        const int a = __builtin_amdgcn_readfirstlane(max(t, min(t1, lo)));
+        const int b = __builtin_amdgcn_readfirstlane(max(a, min(t1, hi)));
         if (dlogits)
             for (int u = t + wave; u < a; u += 4) row_store<NV, VEC>(dlogits + (size_t)u * E, E, lane, zero);
         if (a < b) {
-            const int ns = SELF ? total : seq_n(n, s, J);
             const float cf = ns > 0 ? cb * (float)E / ((float)live * (float)k * (float)ns * (float)ns) : 0.0f;
             const float zf = cz != 0.0f && total > 0 ? cz * 2.0f / (float)total : 0.0f;
-            float co[NV], ps[NV], v[NV], nx[NV];
-            // the row of token u; masked (and missing) ones are not read
-            auto fetch = [&](int u, float (&to)[NV]) {
-                const bool on = u < b && (!mask || mask[u]);
-                if (on) row_load<NV, VEC>(logits + (size_t)u * E, E, lane, -INFINITY, to);
-                return on;
-            };
-            bool on = fetch(a + wave, nx);
+            float co[NV], ps[NV], nx[2][NV];
+            uint32_t on[2];
+            // Rows go through buffer resources over the piece: rows behind it
+            // and columns behind E read 0 and store nothing, and nothing in
+            // the loop branches. (A load or store behind a branch makes the
+            // compiler wait for every store in flight before the next row is
+            // used.) Masked rows are
+            // loaded too and left out.
+            const uint32_t rowb = (uint32_t)E * 4u, bytes = (uint32_t)(b - a) * rowb;
+            const rsrc_t rl = make_rsrc(logits + (size_t)a * E, bytes);
+            const rsrc_t rd = make_rsrc(dlogits ? dlogits + (size_t)a * E : nullptr, dlogits ? bytes : 0u);
+            const rsrc_t rm = make_rsrc(mask ? mask + a : nullptr, mask ? (uint32_t)(b - a) : 0u);
+            uint32_t colo[VEC ? NV / 4 : NV];
 #pragma unroll
-            for (int i = 0; i < NV; i++) {
-                const int e = bal_col<VEC>(lane, i);
-                int h = 0;
-                if (e < E) {
-                    if constexpr (SELF)
-                        h = hist[e];
-                    else
-                        for (int j = 0; j < J; j++) h += cnt[((size_t)s * J + j) * E + e];
+            for (int q = 0; q < (VEC ? NV / 4 : NV); q++) {
+                const int e = VEC ? 4 * lane + 256 * q : lane + 64 * q;
+                colo[q] = e < E ? (uint32_t)e * 4u : kOOB;
+            }
+            auto fetch = [&](int u) {
+#pragma unroll
+                for (int r = 0; r < 2; r++) {
+                    const uint32_t row = (uint32_t)(u + 4 * r);  // of the piece
+                    on[r] = mask ? ld_b8(rm, row) : (uint32_t)((int)row < b - a);
+#pragma unroll
+                    for (int q = 0; q < (VEC ? NV / 4 : NV); q++) {
+                        if constexpr (VEC) {
+                            const auto x = __builtin_amdgcn_raw_buffer_load_b128(rl, row * rowb + colo[q], 0, 0);
+#pragma unroll
+                            for (int h = 0; h < 4; h++) nx[r][4 * q + h] = __uint_as_float(x[h]);
+                        } else {
+                            nx[r][q] = __uint_as_float(ld_b32(rl, row * rowb + colo[q]));
+                        }
+                    }
                 }
-                co[i] = cf * (float)h;
-                ps[i] = 0.0f;
+            };
+            fetch(wave);
+#pragma unroll
+            for (int i = 0; i < NV; i++) ps[i] = 0.0f;
+            if constexpr (SELF) {
+#pragma unroll
+                for (int i = 0; i < NV; i++) {
+                    const int e = bal_col<VEC>(lane, i);
+                    co[i] = e < E ? cf * (float)hist[e] : 0.0f;
+                }
+            } else {
+                // the parts' counts, all loads together (those past part J read 0)
+                const rsrc_t rc = make_rsrc(cnt + (size_t)s * J * E, (uint32_t)J * rowb);
+                uint32_t h[kMaxParts][NV];
+#pragma unroll
+                for (int j = 0; j < kMaxParts; j++)
+#pragma unroll
+                    for (int q = 0; q < (VEC ? NV / 4 : NV); q++) {
+                        if constexpr (VEC) {
+                            const auto x = __builtin_amdgcn_raw_buffer_load_b128(rc, (uint32_t)j * rowb + colo[q], 0, 0);
+#pragma unroll
+                            for (int g = 0; g < 4; g++) h[j][4 * q + g] = x[g];
+                        } else {
+                            h[j][q] = ld_b32(rc, (uint32_t)j * rowb + colo[q]);
+                        }
+                    }
+#pragma unroll
+                for (int i = 0; i < NV; i++) co[i] = cf * (float)(int)((h[0][i] + h[1][i]) + (h[2][i] + h[3][i]));
+                static_assert(kMaxParts == 4, "four parts are added");
             }
             float zs = 0.0f;
-            for (int u = a + wave; u < b; u += 4) {
-                const bool mine = on;
+            for (int u = wave; u < b - a; u += 8) {
+                float v[2][NV], m[2], z[2], dot[2];
+                bool mine[2];
 #pragma unroll
-                for (int i = 0; i < NV; i++) v[i] = nx[i];
-                on = fetch(u + 4, nx);
-                if (!mine) {
-                    if (dlogits) row_store<NV, VEC>(dlogits + (size_t)u * E, E, lane, zero);
-                    continue;
+                for (int r = 0; r < 2; r++) {
+                    mine[r] = on[r] != 0;
+#pragma unroll
+                    for (int i = 0; i < NV; i++) v[r][i] = bal_col<VEC>(lane, i) < E ? nx[r][i] : -INFINITY;
                 }
-                float m = v[0];
+                fetch(u + 8);
 #pragma unroll
-                for (int i = 1; i < NV; i++) m = fmaxf(m, v[i]);
-                m = wave_max(m);
-                if (m == -INFINITY) m = 0.0f;  // nothing finite: every e^v is 0 (or NaN)
-                float z = 0.0f;
+                for (int r = 0; r < 2; r++) {
+                    m[r] = v[r][0];
 #pragma unroll
-                for (int i = 0; i < NV; i++) {
-                    v[i] = expf(v[i] - m);
-                    z += v[i];
+                    for (int i = 1; i < NV; i++) m[r] = fmaxf(m[r], v[r][i]);
+                    m[r] = wave_max(m[r]);
+                    m[r] = m[r] == -INFINITY ? 0.0f : m[r];  // nothing finite: every e^v is 0 (or NaN)
                 }
-                z = wave_sum(z);
-                const float inv = z == 0.0f ? 0.0f : 1.0f / z;
-                const float lse = z == 0.0f ? 0.0f : m + logf(z);
-                zs += lse * lse;
-                float dot = 0.0f;
 #pragma unroll
-                for (int i = 0; i < NV; i++) {
-                    v[i] *= inv;
-                    ps[i] += v[i];
-                    dot = fmaf(co[i], v[i], dot);
+                for (int r = 0; r < 2; r++) {
+                    z[r] = dot[r] = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < NV; i++) {
+                        // e^d by the hardware's 2^x: rounding d log2(e) adds |d| 2^-24
+                        // relative, as much as rounding v - m did
+                        v[r][i] = __builtin_amdgcn_exp2f((v[r][i] - m[r]) * 1.44269504f);
+                        z[r] += v[r][i];
+                        dot[r] = fmaf(co[i], v[r][i], dot[r]);
+                    }
                 }
-                if (dlogits) {
-                    dot = wave_sum(dot);
-                    const float sh = (zf != 0.0f ? zf * lse : 0.0f) - dot;
 #pragma unroll
-                    for (int i = 0; i < NV; i++) v[i] = up * (v[i] * (co[i] + sh));
-                    row_store<NV, VEC>(dlogits + (size_t)u * E, E, lane, v);
+                for (int r = 0; r < 2; r++) {
+                    z[r] = wave_sum(z[r]);
+                    dot[r] = wave_sum(dot[r]);
+                }
+#pragma unroll
+                for (int r = 0; r < 2; r++) {
+                    const float inv = z[r] == 0.0f ? 0.0f : 1.0f / z[r];
+                    const float lse = z[r] == 0.0f ? 0.0f : m[r] + logf(z[r]);
+                    zs += mine[r] ? lse * lse : 0.0f;
+                    const float sh = (zf != 0.0f ? zf * lse : 0.0f) - dot[r] * inv, ui = up * inv;
+#pragma unroll
+                    for (int i = 0; i < NV; i++) {
+                        ps[i] += mine[r] ? v[r][i] * inv : 0.0f;
+                        v[r][i] = mine[r] ? ui * (v[r][i] * (co[i] + sh)) : 0.0f;
+                    }
+                    const uint32_t ro = (uint32_t)(u + 4 * r) * rowb;
+#pragma unroll
+                    for (int q = 0; q < (VEC ? NV / 4 : NV); q++) {
+                        if constexpr (VEC) {
+                            typedef uint32_t w4 __attribute__((ext_vector_type(4)));
+                            const w4 x = {__float_as_uint(v[r][4 * q]), __float_as_uint(v[r][4 * q + 1]),
+                                          __float_as_uint(v[r][4 * q + 2]), __float_as_uint(v[r][4 * q + 3])};
+                            __builtin_amdgcn_raw_buffer_store_b128(x, rd, ro + colo[q], 0, 0);
+                        } else {
+                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[r][q]), rd, ro + colo[q], 0, 0);
+                        }
+                    }
                 }
             }
             __syncthreads();
@@ -416,33 +510,47 @@ __global__ __launch_bounds__(256) void k_bal_main(const float* __restrict__ logi
     }
 }
 
-// grid (ceil(E / 16), S), 16 RG threads: 16 columns x RG row groups over the
-// pieces of sequence s; the last workgroup to finish adds the sequences up.
-template <int RG>
-__global__ __launch_bounds__(16 * RG) void k_bal_reduce(const int32_t* __restrict__ off, int T, int E, int k, int S,
+// grid (ceil(E / CB), S), 1024 threads: CB columns x 1024 / CB row groups over
+// the pieces of sequence s; the last workgroup to finish adds the sequences
+// up. Every workgroup takes a ticket from one counter, about 15 ns each, so
+// many sequences get wide blocks (22 us against 8 with 16 columns at 32768 x
+// 512 in 37 sequences), and few get narrow ones, many pieces at a time.
+template <int CB>
+__global__ __launch_bounds__(1024) void k_bal_reduce(const int32_t* __restrict__ off, int T, int E, int k, int S,
                                                      int TB, int J, const int32_t* __restrict__ cnt,
                                                      const int32_t* __restrict__ n, float cb, float cz,
                                                      const float* __restrict__ psum, const float* __restrict__ zsum,
                                                      float* __restrict__ q, uint32_t* __restrict__ ticket,
                                                      float* __restrict__ loss, int32_t* __restrict__ counts,
                                                      float* __restrict__ probs) {
-    constexpr int NT = 16 * RG, NW = NT / 64;
-    __shared__ float red[RG][17];
-    __shared__ float zr[NW];
+    constexpr int NT = 1024, NW = 16, RG = NT / CB;
+    __shared__ float red[RG][CB + 1];
+    __shared__ float wr[2][NW];
     __shared__ uint32_t last;
-    const int tid = threadIdx.x, col = tid & 15, g = tid >> 4, s = blockIdx.y;
-    const int EB = gridDim.x, e = blockIdx.x * 16 + col;
-    int live, total;
-    const bool fine = bal_totals<NT>(n, S, J, live, total);
-    int lo = 0, hi = 0;
-    if (fine) seq_bounds(off, s, T, lo, hi);
+    const int tid = threadIdx.x, col = tid % CB, g = tid / CB, s = blockIdx.y;
+    const int EB = gridDim.x, e = blockIdx.x * CB + col;
+    __shared__ int sn[kSeqLds], so[2 * kSeqLds];
     const int ns = seq_n(n, s, J);
-    const bool any = fine && hi > lo;
+    int lo, hi, c = 0;
+    const bool mine = seq_bounds(off, s, T, lo, hi);
+    if (tid < CB && e < E) {
+        int h[kMaxParts];
+#pragma unroll
+        for (int j = 0; j < kMaxParts; j++) h[j] = cnt[((size_t)s * J + min(j, J - 1)) * E + e];
+#pragma unroll
+        for (int j = 0; j < kMaxParts; j++) c += j < J ? h[j] : 0;
+    }
+    const Seqs all = bal_totals<NT>(n, off, T, 0, S, J, sn, so);
+    const int live = all.live, total = all.total;
+    const bool fine = all.fine, any = fine && mine && hi > lo;
     const int r0 = any ? lo / TB + s : 0, r1 = any ? (hi - 1) / TB + s + 1 : 0;
     float a = 0.0f;
     if (e < E)
 #pragma unroll 4
         for (int r = r0 + g; r < r1; r += RG) a += psum[(size_t)r * E + e];
+    float z = 0.0f;  // this sequence's sum of lse^2, by the first column block
+    if (blockIdx.x == 0)
+        for (int r = r0 + tid; r < r1; r += NT) z += zsum[r];
     red[g][col] = a;
     __syncthreads();
 #pragma unroll
@@ -450,32 +558,31 @@ __global__ __launch_bounds__(16 * RG) void k_bal_reduce(const int32_t* __restric
         if (g < h) red[g][col] += red[g + h][col];
         __syncthreads();
     }
-    if (tid < 16) {
+    float v = 0.0f;
+    if (tid < CB && e < E) {
         float p = ns > 0 ? red[0][col] / (float)ns : 0.0f;
         if (!fine) p = __builtin_nanf("");
-        int c = 0;
-        if (e < E) {
-            for (int j = 0; j < J; j++) c += cnt[((size_t)s * J + j) * E + e];
-            if (probs) probs[(size_t)s * E + e] = p;
-            if (counts) counts[(size_t)s * E + e] = fine ? c : -1;
-        }
-        float v = e < E ? (float)c * p : 0.0f;
-        v = row16_sum(v);
-        if (ns > 0) v *= (float)E / ((float)live * (float)k * (float)ns);
-        if (col == 0)
-            __hip_atomic_store(&q[(size_t)s * (EB + 1) + blockIdx.x], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (probs) probs[(size_t)s * E + e] = p;
+        if (counts) counts[(size_t)s * E + e] = fine ? c : -1;
+        v = (float)c * p;
     }
-    if (blockIdx.x == 0) {  // this sequence's sum of lse^2
-        float z = 0.0f;
-        for (int r = r0 + tid; r < r1; r += NT) z += zsum[r];
-        z = wave_sum(z);
-        if ((tid & 63) == 0) zr[tid >> 6] = z;
-        __syncthreads();
-        if (tid == 0) {
-            z = 0.0f;
-            for (int i = 0; i < NW; i++) z += zr[i];
-            __hip_atomic_store(&q[(size_t)s * (EB + 1) + EB], z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    v = wave_sum(v);
+    z = wave_sum(z);
+    if ((tid & 63) == 0) {
+        wr[0][tid >> 6] = v;
+        wr[1][tid >> 6] = z;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        v = z = 0.0f;
+        for (int i = 0; i < NW; i++) {
+            v += wr[0][i];
+            z += wr[1][i];
         }
+        if (ns > 0) v *= (float)E / ((float)live * (float)k * (float)ns);
+        __hip_atomic_store(&q[(size_t)s * (EB + 1) + blockIdx.x], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (blockIdx.x == 0)
+            __hip_atomic_store(&q[(size_t)s * (EB + 1) + EB], z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     // Thread 0 made this workgroup's one or two stores of q itself, with
     // device-coherent stores: it waits for them, then takes the ticket. (A
@@ -488,24 +595,25 @@ __global__ __launch_bounds__(16 * RG) void k_bal_reduce(const int32_t* __restric
     }
     __syncthreads();
     if (!last) return;
-    float bal = 0.0f, z = 0.0f;
+    float bal = 0.0f;
+    z = 0.0f;
     const size_t cells = (size_t)S * (EB + 1);
     for (size_t i = tid; i < cells; i += NT) {
-        const float v = __hip_atomic_load(&q[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if (i % (EB + 1) == (size_t)EB) z += v; else bal += v;
+        const float x = __hip_atomic_load(&q[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (i % (EB + 1) == (size_t)EB) z += x; else bal += x;
     }
     bal = wave_sum(bal);
     z = wave_sum(z);
     if ((tid & 63) == 0) {
-        red[tid >> 6][0] = bal;
-        red[tid >> 6][1] = z;
+        wr[0][tid >> 6] = bal;
+        wr[1][tid >> 6] = z;
     }
     __syncthreads();
     if (tid == 0) {
         bal = z = 0.0f;
         for (int i = 0; i < NW; i++) {
-            bal += red[i][0];
-            z += red[i][1];
+            bal += wr[0][i];
+            z += wr[1][i];
         }
         z = total > 0 ? z / (float)total : 0.0f;
         if (!fine) bal = z = __builtin_nanf("");
@@ -560,12 +668,10 @@ hipError_t launch_balance(int E, int k, const float* logits, int T, const int32_
 #undef BM
         if ((r = hipGetLastError()) != hipSuccess) return r;
     }
-    // a row group per piece of an average sequence, about
-    const dim3 grid((E + 15) / 16, S);
-#define BR(RG)                                                                                                      \
-    hipLaunchKernelGGL((k_bal_reduce<RG>), grid, dim3(16 * RG), 0, s, seq_off, T, E, k, S, b.TB, J, cnt, n, cb, cz, psum, \
-                       zsum, q, ticket, loss, counts, probs)
-    if (b.chunks / S >= 64) BR(64); else BR(16);
+#define BR(CB)                                                                                                         \
+    hipLaunchKernelGGL((k_bal_reduce<CB>), dim3((E + CB - 1) / CB, S), dim3(1024), 0, s, seq_off, T, E, k, S, b.TB, J, cnt, \
+                       n, cb, cz, psum, zsum, q, ticket, loss, counts, probs)
+    if (S <= 4) BR(16); else BR(128);
 #undef BR
     return hipGetLastError();
 }

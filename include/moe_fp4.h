@@ -273,8 +273,7 @@ int moe_gemv_fp8(const uint8_t *W, const float *row_scale, const float *x, int32
  * gradient of the logits. A batch is T tokens in S sequences: sequence s
  * holds the tokens seq_off[s] <= t < seq_off[s + 1] with mask[t] != 0 (its
  * counted tokens, n_s of them); tokens before seq_off[0], behind seq_off[S]
- * or with mask[t] == 0 are not counted, and nothing of them is read but the
- * mask. With p_t = softmax(logits[t]) over all E, lse_t its log-sum-exp,
+ * or with mask[t] == 0 are not counted, and their values do not matter. With p_t = softmax(logits[t]) over all E, lse_t its log-sum-exp,
  * live = the sequences with n_s > 0 and N = sum n_s:
  *   counts[s][e] = #{(t, j): t counted in s, idx[t][j] = e}
  *   probs[s][e]  = mean of p_t[e] over the counted tokens of s (0 if none)
@@ -318,8 +317,7 @@ int moe_balance_loss(const moe_desc *d, const float *logits, int32_t T, const in
  *   ds[t][j] = w[t][j] * (dw[t][j] - sum_i w[t][i] dw[t][i])
  *   G[t][e]  = dlogits_in[t][e] + sum_{j: idx[t][j] = e} ds[t][j]
  *   dx = G Wr ([T][H]),  dWr = G^T x ([E][H])
- * Tokens with mask[t] == 0 have G = 0, and nothing of them is read but the
- * mask. A token with an index outside [0, E) (dw given) has G = NaN in its
+ * Tokens with mask[t] == 0 have G = 0, and their values do not matter. A token with an index outside [0, E) (dw given) has G = NaN in its
  * whole row. fp32 operands, products and sums; results are bit-identical
  * from run to run.
  *   x [T][H], Wr [E][H] fp32, 16-B aligned (x may be NULL without dWr, Wr
