@@ -179,9 +179,15 @@ struct Group {
     int32_t row, rows;
 };
 
+// The low values u and v, as "down" leaves them for what follows, in bf16
+// parts (chunks of 8 values of one part):
+//   by token  [3][T][R32 / 8]             grouped rows, for "up" (R32: at least 32)
+//   by rank   [tile slot][3][R16][8]      chunk c (tokens 8 c .. of the tile) of
+//             rank k at place c ^ (k & 7), so that neighbouring ranks' reads
+//             from LDS fall on different banks, for "grad"
 struct LoraWs {
-    int R16, slots, piece, pslots, ks;
-    size_t perm, groups, tiles, pieces, u, v, grad, total;
+    int R16, R32, slots, piece, pslots, ks;
+    size_t perm, groups, tiles, pieces, tickets, part, ut, vt, ur, vr, grad, total;
 };
 
 int col_blocks(int cols) { return (cols + kUpCols - 1) / kUpCols; }
@@ -189,6 +195,7 @@ int col_blocks(int cols) { return (cols + kUpCols - 1) / kUpCols; }
 LoraWs lora_ws(int K, int N, int n, int R, int T, bool backward) {
     LoraWs w = {};
     w.R16 = R <= 16 ? 16 : (R <= 32 ? 32 : (R <= 64 ? 64 : 128));
+    w.R32 = w.R16 < 32 ? 32 : w.R16;
     w.slots = T / kTile + n + 3;
     // tokens of a piece of the gradient: about 512 workgroups, so that the
     // parts that k_lora_grad_reduce adds stay few
@@ -210,16 +217,22 @@ LoraWs lora_ws(int K, int N, int n, int R, int T, bool backward) {
         return at;
     };
     if (!backward && T <= kDirectMaxT) {
-        w.u = take((size_t)T * R * 4);
+        w.ut = take((size_t)T * R * 4);
         w.total = o;
         return w;
     }
+    const int sides = backward ? 2 : 1;
     w.perm = take((size_t)T * 4);
     w.groups = take((size_t)(n + 2) * sizeof(Group));
     w.tiles = take((size_t)w.slots * sizeof(Slot));
     w.pieces = take(backward ? (size_t)w.pslots * sizeof(Slot) : 0);
-    w.u = take((size_t)w.ks * T * w.R16 * 4);
-    w.v = take(backward ? (size_t)w.ks * T * w.R16 * 4 : 0);
+    w.tickets = take((size_t)w.slots * 2 * 4);
+    w.part = take(ks > 1 ? (size_t)sides * ks * T * w.R16 * 4 : 0);
+    const size_t by_token = (size_t)T * w.R32 * 6, by_rank = (size_t)w.slots * w.R16 * kTile * 6;
+    w.ut = take(backward ? 0 : by_token);
+    w.vt = take(backward ? by_token : 0);
+    w.ur = take(backward ? by_rank : 0);
+    w.vr = take(backward ? by_rank : 0);
     w.grad = take(backward ? (size_t)w.pslots * w.R16 * ((size_t)K + N) * 4 : 0);
     w.total = o;
     return w;
@@ -232,9 +245,10 @@ LoraWs lora_ws(int K, int N, int n, int R, int T, bool backward) {
 constexpr int kPlanIds = 8;
 __global__ __launch_bounds__(1024) void k_lora_plan(const int32_t* __restrict__ ids, int T, int n,
                                                     int32_t* __restrict__ perm, Group* __restrict__ groups,
-                                                    Slot* __restrict__ tiles, Slot* __restrict__ pieces, int piece) {
+                                                    Slot* __restrict__ tiles, Slot* __restrict__ pieces, int piece,
+                                                    uint32_t* __restrict__ tickets, int slots) {
     __shared__ int acc[2];
-    __shared__ int wsum[kPlanIds][16];
+    __shared__ int wsum[kPlanIds * 16];  // own tokens of each wave's 64 ids, then the places of their first
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = blockIdx.x;
     constexpr int SPAN = 1024 * kPlanIds;
     int key[kPlanIds];  // -1 behind the end
@@ -268,19 +282,29 @@ __global__ __launch_bounds__(1024) void k_lora_plan(const int32_t* __restrict__ 
 #pragma unroll
         for (int i = 0; i < kPlanIds; i++) {
             mine[i] = __ballot(key[i] == g);
-            if (lane == 0) wsum[i][wave] = __popcll(mine[i]);
+            if (lane == 0) wsum[16 * i + wave] = __popcll(mine[i]);
         }
         __syncthreads();
-        int before = 0;  // own tokens of this span before place (i, wave)
+        int all = 0;
+        if (wave == 0) {  // exclusive sums of the 128 counts, two a lane
+            const int a = wsum[2 * lane], b = wsum[2 * lane + 1];
+            int v = a + b;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int w = __shfl_up(v, o, 64);
+                if (lane >= o) v += w;
+            }
+            wsum[2 * lane] = v - a - b;
+            wsum[2 * lane + 1] = v - b;
+            if (lane == 63) acc[0] = v;
+        }
+        __syncthreads();
+        all = acc[0];
 #pragma unroll
         for (int i = 0; i < kPlanIds; i++)
-#pragma unroll
-            for (int v = 0; v < 16; v++) {
-                if (v == wave && key[i] == g)
-                    perm[at + before + __popcll(mine[i] & ((1ull << lane) - 1))] = t0 + 1024 * i + tid;
-                before += wsum[i][v];
-            }
-        at += before;
+            if (key[i] == g)
+                perm[at + wsum[16 * i + wave] + __popcll(mine[i] & ((1ull << lane) - 1))] = t0 + 1024 * i + tid;
+        at += all;
         __syncthreads();
     }
     if (tid == 0) groups[g] = Group{first, count};
@@ -294,6 +318,8 @@ __global__ __launch_bounds__(1024) void k_lora_plan(const int32_t* __restrict__ 
     };
     list(tiles, kTile);
     if (pieces) list(pieces, piece);
+    // the tickets of "down"
+    for (int i = g * 1024 + tid; i < 2 * slots; i += (n + 2) * 1024) tickets[i] = 0;
 }
 
 // ---- bf16 parts of fp32 ----
@@ -332,7 +358,9 @@ struct DownJob {
     size_t ldx;
     int K;
     const void* const* fac;
-    float* u;
+    float* part;    // [parts][T][R16]
+    u4v* by_token;  // either may be null
+    u4v* by_rank;
 };
 
 // Sixteen consecutive activations of a row, as loaded.
@@ -341,13 +369,6 @@ struct Raw {
     static constexpr int W = ACT == kActF32 ? 4 : 2;
     u4v w[W];
 };
-template <int ACT>
-__device__ __forceinline__ Raw<ACT> raw_load(const typename Act<ACT>::T* x) {
-    Raw<ACT> r;
-#pragma unroll
-    for (int i = 0; i < Raw<ACT>::W; i++) r.w[i] = reinterpret_cast<const u4v*>(x)[i];
-    return r;
-}
 // c += the product of half h (eight values) of x rows and w rows.
 template <int ACT>
 __device__ __forceinline__ f4v down_mma(const Raw<ACT>& x, int h, u4v w, f4v c) {
@@ -366,102 +387,110 @@ __device__ __forceinline__ f4v down_mma(const Raw<ACT>& x, int h, u4v w, f4v c) 
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8v, x.w[h]), __builtin_bit_cast(h8v, w), c, 0, 0, 0);
     }
 }
+__device__ __forceinline__ u4v ld_b128(rsrc_t r, uint32_t off) {
+    return __builtin_bit_cast(u4v, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
 
 // Steps s0 .. s1 - 1 of 64 of the long axis for NB x 16 tokens and RW x 16
 // ranks: lane (i = lane % 16, q = lane / 16) holds the elements 64 s + 16 q ..
 // + 15 of rows i, so a row's 128 bytes (16-bit types) arrive by neighbouring
 // lanes; which elements a matrix instruction pairs does not matter as long as
 // both operands agree. The loads of step s + 1 are under way during step s.
-// A last step behind K's end (tail) has its missing elements set to 0.
+// The elements of the last step that lie behind K are set to 0.
 template <int ACT, int NB, int RW>
 __device__ __forceinline__ void down_steps(f4v (&acc)[4][RW], const typename Act<ACT>::T* const (&xr)[4], int b0,
-                                           const uint16_t* const (&wr)[RW], int s0, int s1, int K) {
-    const int lq = (threadIdx.x & 63) >> 4, full = min(s1, K / 64);
-    if (s0 < full) {
+                                           rsrc_t rf, const uint32_t (&wo)[RW], int s0, int s1, int K) {
+    const int lq = (threadIdx.x & 63) >> 4;
+    struct Set {
         Raw<ACT> x[NB];
         u4v w[RW][2];
-        auto load = [&](int s) {
-#pragma unroll
-            for (int b = 0; b < NB; b++) x[b] = raw_load<ACT>(xr[b0 + b] + 64 * s);
-#pragma unroll
-            for (int j = 0; j < RW; j++) {
-                w[j][0] = *reinterpret_cast<const u4v*>(wr[j] + 64 * s);
-                w[j][1] = *reinterpret_cast<const u4v*>(wr[j] + 64 * s + 8);
-            }
-        };
-        load(s0);
-        for (int s = s0; s < full; s++) {
-            Raw<ACT> y[NB];
-            u4v z[RW][2];
-#pragma unroll
-            for (int b = 0; b < NB; b++) y[b] = x[b];
-#pragma unroll
-            for (int j = 0; j < RW; j++) {
-                z[j][0] = w[j][0];
-                z[j][1] = w[j][1];
-            }
-            load(min(s + 1, full - 1));
-#pragma unroll
-            for (int h = 0; h < 2; h++)
-#pragma unroll
-                for (int b = 0; b < NB; b++)
-#pragma unroll
-                    for (int j = 0; j < RW; j++) acc[b0 + b][j] = down_mma<ACT>(y[b], h, z[j][h], acc[b0 + b][j]);
-        }
-    }
-    if (s1 > K / 64) {  // the elements behind the last whole step (K is a multiple of 8)
-        const int k0 = K / 64 * 64;
+    } p, q;
+    auto load = [&](int s, Set& t) {
+        // pieces of eight behind K read the row's first ones
+        const int k = 64 * s + 16 * lq;
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            const bool in = k0 + 16 * lq + 8 * h < K;
-            const int o = in ? k0 + 8 * h : 0;
+            const int o = k + 8 * h < K ? 64 * s + 8 * h : -16 * lq;
 #pragma unroll
-            for (int b = 0; b < NB; b++) {
-                Raw<ACT> x = {};
-                if (in) {
+            for (int b = 0; b < NB; b++)
 #pragma unroll
-                    for (int i = 0; i < Raw<ACT>::W / 2; i++)
-                        x.w[h * Raw<ACT>::W / 2 + i] = reinterpret_cast<const u4v*>(xr[b0 + b] + o)[i];
-                }
+                for (int i = 0; i < Raw<ACT>::W / 2; i++)
+                    t.x[b].w[h * Raw<ACT>::W / 2 + i] = reinterpret_cast<const u4v*>(xr[b0 + b] + o)[i];
 #pragma unroll
-                for (int j = 0; j < RW; j++) {
-                    const u4v w = in ? *reinterpret_cast<const u4v*>(wr[j] + o) : u4v{0, 0, 0, 0};
-                    acc[b0 + b][j] = down_mma<ACT>(x, h, w, acc[b0 + b][j]);
+            for (int j = 0; j < RW; j++) t.w[j][h] = ld_b128(rf, wo[j] + (uint32_t)o * 2u);
+        }
+    };
+    auto multiply = [&](int s, Set& t) {
+        if (64 * s + 64 > K) {  // uniform: the last step only
+            const int k = 64 * s + 16 * lq;
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const bool in = k + 8 * h < K;
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+#pragma unroll
+                    for (int b = 0; b < NB; b++)
+#pragma unroll
+                        for (int i = 0; i < Raw<ACT>::W / 2; i++)
+                            t.x[b].w[h * Raw<ACT>::W / 2 + i][e] = in ? t.x[b].w[h * Raw<ACT>::W / 2 + i][e] : 0u;
+#pragma unroll
+                    for (int j = 0; j < RW; j++) t.w[j][h][e] = in ? t.w[j][h][e] : 0u;
                 }
             }
         }
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int b = 0; b < NB; b++)
+#pragma unroll
+                for (int j = 0; j < RW; j++) acc[b0 + b][j] = down_mma<ACT>(t.x[b], h, t.w[j][h], acc[b0 + b][j]);
+    };
+    if (s0 >= s1) return;
+    load(s0, p);
+    for (int s = s0; s < s1; s += 2) {
+        load(min(s + 1, s1 - 1), q);
+        __builtin_amdgcn_sched_barrier(0);  // the loads stay before the products
+        multiply(s, p);
+        if (s + 1 >= s1) break;
+        load(min(s + 2, s1 - 1), p);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(s + 1, q);
     }
 }
 
-// grid (slots, parts of the long axis, sides): u of one tile over one part.
-// Four waves: each takes a quarter of the part's steps and all ranks, or
-// above 64 ranks a half of the steps and 64 ranks; operands go from memory to
-// registers, and the waves' sums are added in order through LDS.
+// grid (slots, parts of the long axis, sides): the low values of one tile over
+// one part. Four waves: each takes a quarter of the part's steps and all
+// ranks, or above 64 ranks a half of the steps and 64 ranks; operands go from
+// memory to registers, and the waves' sums are added in order through LDS.
+// Where the axis is in several parts, every workgroup leaves its own with
+// device-coherent stores, and the last one of a tile to finish (by a ticket)
+// adds them in order. Out go the bf16 parts of the scaled values.
 template <int ACT, int RB>
 __global__ __launch_bounds__(256) void k_lora_down(DownJob ja, DownJob jb, int n, int R,
                                                    const int32_t* __restrict__ ranks, const float* __restrict__ scales,
                                                    const int32_t* __restrict__ perm, const Slot* __restrict__ tiles,
-                                                   int T) {
+                                                   int T, uint32_t* __restrict__ tickets) {
     constexpr int RW = RB > 4 ? 4 : RB, KW = 4 * RW / RB;  // rank blocks of a wave, waves along the long axis
-    __shared__ float red[kTile][RB * 16 + 1];
+    constexpr int R16 = RB * 16, CH = (R16 < 32 ? 32 : R16) / 8;
+    __shared__ float red[kTile][R16 + 1];
+    __shared__ uint32_t ticket;
     const Slot sl = tiles[blockIdx.x];
     if (sl.rows == 0 || sl.g >= n) return;
     const DownJob j = blockIdx.z ? jb : ja;
     const int r = rank_of(ranks, sl.g, R);
     if (r < 0) return;
-    const int lane = threadIdx.x & 63, wave = wave_id(), li = lane & 15, lq = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), li = lane & 15, lq = lane >> 4;
     const int kw = wave % KW, r0 = wave / KW * RW;
-    const uint16_t* F = reinterpret_cast<const uint16_t*>(uniform_ptr(j.fac[sl.g]));
     const typename Act<ACT>::T* xr[4];
-    const uint16_t* wr[RW];
-    // rows behind the tile's tokens and behind the rank repeat the last one;
-    // their sums are not written
+    // rows behind the tile's tokens repeat the last one; their sums are not used
 #pragma unroll
     for (int b = 0; b < 4; b++)
         xr[b] = reinterpret_cast<const typename Act<ACT>::T*>(j.x) +
                 (size_t)perm[sl.row + min(16 * b + li, sl.rows - 1)] * j.ldx + 16 * lq;
+    const rsrc_t rf = make_rsrc(j.fac[sl.g], (uint32_t)r * (uint32_t)j.K * 2u);  // rows behind the rank read 0
+    uint32_t wo[RW];
 #pragma unroll
-    for (int i = 0; i < RW; i++) wr[i] = F + (size_t)max(min(16 * (r0 + i) + li, r - 1), 0) * j.K + 16 * lq;
+    for (int i = 0; i < RW; i++) wo[i] = ((uint32_t)(16 * (r0 + i) + li) * (uint32_t)j.K + (uint32_t)(16 * lq)) * 2u;
     f4v acc[4][RW];
 #pragma unroll
     for (int b = 0; b < 4; b++)
@@ -469,16 +498,16 @@ __global__ __launch_bounds__(256) void k_lora_down(DownJob ja, DownJob jb, int n
         for (int i = 0; i < RW; i++) acc[b][i] = f4v{0.f, 0.f, 0.f, 0.f};
     const int steps = (j.K + 63) / 64, parts = gridDim.y * KW, part = blockIdx.y * KW + kw;
     const int s0 = (int)((int64_t)steps * part / parts), s1 = (int)((int64_t)steps * (part + 1) / parts);
-    if (r > 0 && 16 * r0 < r) {
+    if (16 * r0 < r) {
         if (sl.rows <= 16) {
-            down_steps<ACT, 1, RW>(acc, xr, 0, wr, s0, s1, j.K);
+            down_steps<ACT, 1, RW>(acc, xr, 0, rf, wo, s0, s1, j.K);
         } else if (sl.rows <= 32) {
-            down_steps<ACT, 2, RW>(acc, xr, 0, wr, s0, s1, j.K);
+            down_steps<ACT, 2, RW>(acc, xr, 0, rf, wo, s0, s1, j.K);
         } else if constexpr (ACT == kActF32) {  // fp32 rows take twice the registers
-            down_steps<ACT, 2, RW>(acc, xr, 0, wr, s0, s1, j.K);
-            down_steps<ACT, 2, RW>(acc, xr, 2, wr, s0, s1, j.K);
+            down_steps<ACT, 2, RW>(acc, xr, 0, rf, wo, s0, s1, j.K);
+            down_steps<ACT, 2, RW>(acc, xr, 2, rf, wo, s0, s1, j.K);
         } else {
-            down_steps<ACT, 4, RW>(acc, xr, 0, wr, s0, s1, j.K);
+            down_steps<ACT, 4, RW>(acc, xr, 0, rf, wo, s0, s1, j.K);
         }
     }
     for (int w = 0; w < KW; w++) {
@@ -494,12 +523,55 @@ __global__ __launch_bounds__(256) void k_lora_down(DownJob ja, DownJob jb, int n
                     }
         __syncthreads();
     }
-    const float sc = scales[sl.g];
-    float* out = j.u + ((size_t)blockIdx.y * T + sl.row) * (RB * 16);
-    for (int i = threadIdx.x; i < sl.rows * RB * 16; i += 256) {
-        const int c = i % (RB * 16);
-        out[i] = c < r ? sc * red[i / (RB * 16)][c] : 0.0f;
+    const int ks = gridDim.y, cells = sl.rows * R16;
+    if (ks > 1) {
+        float* mine = j.part + ((size_t)blockIdx.y * T + sl.row) * R16;
+        for (int i = tid; i < cells; i += 256)
+            __hip_atomic_store(mine + i, red[i / R16][i % R16], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        // each wave waits for its own stores, then one ticket for all of them
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (tid == 0)
+            ticket = __hip_atomic_fetch_add(tickets + blockIdx.z * gridDim.x + blockIdx.x, 1u, __ATOMIC_RELAXED,
+                                            __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        if (ticket + 1 != (uint32_t)ks) return;
+        for (int i = tid; i < cells; i += 256) {
+            float v[8];
+#pragma unroll
+            for (int q = 0; q < 8; q++)
+                v[q] = __hip_atomic_load(j.part + ((size_t)min(q, ks - 1) * T + sl.row) * R16 + i, __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
+            float a = v[0];
+#pragma unroll
+            for (int q = 1; q < 8; q++) a += q < ks ? v[q] : 0.0f;
+            red[i / R16][i % R16] = a;
+        }
+        __syncthreads();
     }
+    const float sc = scales[sl.g];
+    if (j.by_token)
+        for (int i = tid; i < sl.rows * CH; i += 256) {
+            const int p = i / CH, c = i % CH;
+            float v[8];
+#pragma unroll
+            for (int q = 0; q < 8; q++) v[q] = 8 * c + q < r ? sc * red[p][min(8 * c + q, R16 - 1)] : 0.0f;
+            u4v o[3];
+            parts8<3>(v, o);
+#pragma unroll
+            for (int h = 0; h < 3; h++) j.by_token[((size_t)h * T + sl.row + p) * CH + c] = o[h];
+        }
+    if (j.by_rank)
+        for (int i = tid; i < R16 * 8; i += 256) {
+            const int k = i % R16, c = i / R16;
+            float v[8];
+#pragma unroll
+            for (int q = 0; q < 8; q++) v[q] = 8 * c + q < sl.rows && k < r ? sc * red[8 * c + q][k] : 0.0f;
+            u4v o[3];
+            parts8<3>(v, o);
+#pragma unroll
+            for (int h = 0; h < 3; h++) j.by_rank[(((size_t)blockIdx.x * 3 + h) * R16 + k) * 8 + (c ^ (k & 7))] = o[h];
+        }
 }
 
 // Eight rows of four neighbouring 16-bit columns -> for each column a chunk
@@ -556,26 +628,24 @@ __device__ __forceinline__ f4v mma_parts(const u4v (&a)[3], const u4v (&b)[PB], 
 }
 
 // ---------------------------------------------------------------------------
-// "up": grid (slots, ceil(N / 256)): y of one tile and 256 columns, 64 a wave.
-// The base rows are requested before anything else is waited for. u's parts
-// go through LDS ([3][64 tokens][ranks], a row padded by a chunk); of the
-// factor, lane (i, q) loads ranks 8 q .. + 7 of 4 neighbouring columns 4 i + j
-// and turns them into one operand for each column, so that a lane ends with 4
-// neighbouring columns of its rows.
+// "up": grid (slots, ceil(N / 256)): y of one tile and 256 columns, 64 a wave,
+// everything from memory to registers. The base rows are requested first. Of
+// the factor, lane (i, q) loads ranks 8 q .. + 7 of 4 neighbouring columns
+// 4 i + j and turns them into one operand for each column, so that a lane ends
+// with 4 neighbouring columns of its rows.
 template <int ACT, int RB>
-__global__ __launch_bounds__(256) void k_lora_up(const float* __restrict__ u, int T, int ks, int N, int n, int R,
+__global__ __launch_bounds__(256) void k_lora_up(const u4v* __restrict__ u, int T, int N, int n, int R,
                                                  const void* const* __restrict__ fac,
                                                  const int32_t* __restrict__ ranks, const int32_t* __restrict__ perm,
                                                  const Slot* __restrict__ tiles, const typename Act<ACT>::T* base,
                                                  size_t ldb, typename Act<ACT>::T* y, size_t ldy) {
-    constexpr int R16 = RB * 16, R32 = R16 < 32 ? 32 : R16, CH = R32 / 8, ROW = CH + 1;  // chunks of a row
+    constexpr int R16 = RB * 16, R32 = R16 < 32 ? 32 : R16, CH = R32 / 8;
     constexpr bool F16 = ACT == kActF16;
-    __shared__ u4v us[3][kTile][ROW];
     const Slot sl = tiles[blockIdx.x];
     if (sl.rows == 0) return;
     const bool none = sl.g == n + 1;
     if (none && base == y) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), li = lane & 15, lq = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = wave_id(), li = lane & 15, lq = lane >> 4;
     const int c0 = blockIdx.y * kUpCols + wave * 64 + 4 * li, cl = min(c0, N - 4);
     const int mine = perm[sl.row + min(lane, sl.rows - 1)];
     int t[4][4];  // tokens of the lane's rows; rows behind the tile repeat the last one and are not written
@@ -599,51 +669,34 @@ __global__ __launch_bounds__(256) void k_lora_up(const float* __restrict__ u, in
 #pragma unroll
         for (int j = 0; j < 4; j++) acc[b][j] = f4v{0.f, 0.f, 0.f, 0.f};
     if (r > 0) {
-        const uint16_t* F = reinterpret_cast<const uint16_t*>(uniform_ptr(fac[sl.g])) + cl;
-        u2v w[R32 / 32][8];
-#pragma unroll
-        for (int g = 0; g < R32 / 32; g++)
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const int k = 32 * g + 8 * lq + i;
-                w[g][i] = *reinterpret_cast<const u2v*>(F + (size_t)min(k, r - 1) * N);
-                if (k >= r) w[g][i] = u2v{0, 0};
-            }
-        for (int i = tid; i < kTile * CH; i += 256) {
-            const int p = i / CH, c = i % CH;
-            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (p < sl.rows && 8 * c < R16)
-                for (int q = 0; q < ks; q++) {
-                    const f4v* s = reinterpret_cast<const f4v*>(u + ((size_t)q * T + sl.row + p) * R16 + 8 * c);
-                    const f4v a = s[0], b = s[1];
-#pragma unroll
-                    for (int h = 0; h < 4; h++) {
-                        v[h] += a[h];
-                        v[4 + h] += b[h];
-                    }
-                }
-            u4v o[3];
-            parts8<3>(v, o);
-#pragma unroll
-            for (int h = 0; h < 3; h++) us[h][p][c] = o[h];
-        }
-        __syncthreads();
+        const rsrc_t rf = make_rsrc(fac[sl.g], (uint32_t)r * (uint32_t)N * 2u);  // rows behind the rank read 0
+        const int nb = (sl.rows + 15) / 16;
 #pragma unroll
         for (int g = 0; g < R32 / 32; g++) {
             if (32 * g >= r) break;
+            u2v w[8];
+            u4v a[4][3];
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const uint2 x = ld_b64(rf, ((uint32_t)(32 * g + 8 * lq + i) * (uint32_t)N + (uint32_t)cl) * 2u);
+                w[i] = u2v{x.x, x.y};
+            }
+#pragma unroll
+            for (int b = 0; b < 4; b++)
+#pragma unroll
+                for (int h = 0; h < 3; h++)
+                    a[b][h] = u[((size_t)h * T + sl.row + min(16 * b + li, sl.rows - 1)) * CH + 4 * g + lq];
             Cols16<F16> f;
-            cols16<F16>(w[g], f);
+            cols16<F16>(w, f);
 #pragma unroll
             for (int b = 0; b < 4; b++) {
-                u4v a[3];
-#pragma unroll
-                for (int h = 0; h < 3; h++) a[h] = us[h][16 * b + li][4 * g + lq];
+                if (b >= nb) break;
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     u4v p[Cols16<F16>::P];
 #pragma unroll
                     for (int h = 0; h < Cols16<F16>::P; h++) p[h] = f.c[h][j];
-                    acc[b][j] = mma_parts<Cols16<F16>::P>(a, p, acc[b][j]);
+                    acc[b][j] = mma_parts<Cols16<F16>::P>(a[b], p, acc[b][j]);
                 }
             }
         }
@@ -672,7 +725,7 @@ __global__ __launch_bounds__(256) void k_lora_up(const float* __restrict__ u, in
 // One side of the gradient: D [r][cols] = sum over a piece's tokens of
 // low[t][.] row[t][.].
 struct GradSide {
-    const float* low;        // u or v, grouped order, parts [ks][T][R16]
+    const u4v* low;          // u or v by rank
     const void* row;         // dy or x
     size_t ld;
     int cols;
@@ -680,21 +733,20 @@ struct GradSide {
 };
 
 // grid (piece slots, column blocks of A then of B): 256 columns, 64 a wave,
-// over one piece, 64 tokens at a time: low's parts in LDS as [3][ranks][64
-// tokens] (two sets, the next one made while one is multiplied), the rows'
-// values by lane (i, q) as tokens 8 q .. + 7 of 4 neighbouring columns, turned
-// into an operand for each column, the next 32 tokens' under way. An adapter
-// of one piece writes its gradient, others the piece's part for
-// k_lora_grad_reduce.
+// over one piece, a tile of 64 tokens at a time: low's parts go from memory
+// straight into LDS, the rows' values into registers, by lane (i, q) as tokens
+// 8 q .. + 7 (and 32 more) of 4 neighbouring columns, both a tile ahead; the
+// values are turned into an operand for each column. An adapter of one piece
+// writes its gradient, others the piece's part for k_lora_grad_reduce.
 template <int ACT, int RB>
-__global__ __launch_bounds__(256) void k_lora_grad(GradSide ga, GradSide gb, int T, int ks, int n, int R, int piece,
+__global__ __launch_bounds__(256) void k_lora_grad(GradSide ga, GradSide gb, int n, int R, int piece,
                                                    const int32_t* __restrict__ ranks, const int32_t* __restrict__ perm,
                                                    const Group* __restrict__ groups, const Slot* __restrict__ pieces,
                                                    int accumulate, float* __restrict__ part) {
-    constexpr int R16 = RB * 16, JOBS = (R16 * 8 + 255) / 256;  // a job: 8 tokens of one rank
-    constexpr int WB = ACT == kActF32 ? 4 : 2;
+    constexpr int R16 = RB * 16, TILE = 3 * R16 * 8;  // chunks of a tile's low values
+    constexpr int WB = ACT == kActF32 ? 4 : 2, PX = ACT == kActF32 ? 3 : (ACT == kActF16 ? 2 : 1);
     typedef uint32_t wv __attribute__((ext_vector_type(WB)));
-    __shared__ u4v us[2][3][R16][9];
+    __shared__ u4v us[2 * TILE];
     const Slot sl = pieces[blockIdx.x];
     if (sl.rows == 0 || sl.g >= n) return;
     const int r = rank_of(ranks, sl.g, R);
@@ -704,84 +756,66 @@ __global__ __launch_bounds__(256) void k_lora_grad(GradSide ga, GradSide gb, int
     const GradSide side = second ? gb : ga;
     float* out = side.out ? side.out[sl.g] : nullptr;
     if (!out) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), li = lane & 15, lq = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = wave_id(), li = lane & 15, lq = lane >> 4;
     const int cols = side.cols, c0 = ((int)blockIdx.y - (second ? nba : 0)) * kUpCols + wave * 64 + 4 * li;
     const typename Act<ACT>::T* X = reinterpret_cast<const typename Act<ACT>::T*>(side.row) + min(c0, cols - 4);
+    const Group grp = groups[sl.g];
+    // the piece's tiles follow one another from this slot
+    const u4v* low = side.low + (size_t)(grp.row / kTile + sl.g + (sl.row - grp.row) / kTile) * TILE;
+    const rsrc_t rl = make_rsrc(low, (uint32_t)((sl.rows + kTile - 1) / kTile) * (uint32_t)(TILE * 16));
+    const int tiles = (sl.rows + kTile - 1) / kTile;
     f4v acc[RB][4];
 #pragma unroll
     for (int b = 0; b < RB; b++)
 #pragma unroll
         for (int j = 0; j < 4; j++) acc[b][j] = f4v{0.f, 0.f, 0.f, 0.f};
-    float low[JOBS][8];
-    // low of the 64 tokens from p0; tokens behind the piece are 0
-    auto fetch_low = [&](int p0) {
+    wv x[2][8];
+    auto token = [&](int k) { return perm[sl.row + min(64 * k + lane, sl.rows - 1)]; };
+    auto fetch = [&](int k, int tok) {
 #pragma unroll
-        for (int j = 0; j < JOBS; j++) {
-            const int job = tid + 256 * j, rk = job % R16, c = job / R16 % 8;
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const int p = p0 + 8 * c + i;
-                const float* s = side.low + (size_t)(sl.row + min(p, sl.rows - 1)) * R16 + rk;
-                float v = s[0];
-                for (int q = 1; q < ks; q++) v += s[(size_t)q * T * R16];
-                low[j][i] = p < sl.rows ? v : 0.0f;
-            }
+        for (int i = 0; i < TILE / 256 + (TILE % 256 ? 1 : 0); i++) {
+            const int c = 256 * i + 64 * wave;  // TILE is a multiple of 64: whole waves are in or out
+            if (TILE % 256 == 0 || c < TILE)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    rl, (__attribute__((address_space(3))) void*)(us + (k & 1) * TILE + c), 16,
+                    (uint32_t)(k * TILE + c + lane) * 16u, 0, 0, 0);
         }
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                x[h][i] = *reinterpret_cast<const wv*>(X + (size_t)__shfl(tok, 32 * h + 8 * lq + i, 64) * side.ld);
     };
-    auto put_low = [&](int set) {
+    int tok = token(0);
+    fetch(0, tok);
+    tok = token(1);
+    for (int k = 0; k < tiles; k++) {
+        // tile k is there, and every wave is done with tile k - 1
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        // values of tokens behind the piece are set to 0: they may be NaN
+        wv w[2][8];
 #pragma unroll
-        for (int j = 0; j < JOBS; j++) {
-            const int job = tid + 256 * j;
-            u4v o[3];
-            parts8<3>(low[j], o);
-            if (R16 * 8 >= 256 || job < R16 * 8)
+        for (int h = 0; h < 2; h++)
 #pragma unroll
-                for (int h = 0; h < 3; h++) us[set][h][job % R16][job / R16 % 8] = o[h];
+            for (int i = 0; i < 8; i++)
+#pragma unroll
+                for (int d = 0; d < WB; d++) w[h][i][d] = 64 * k + 32 * h + 8 * lq + i < sl.rows ? x[h][i][d] : 0u;
+        if (k + 1 < tiles) {
+            fetch(k + 1, tok);
+            tok = token(k + 2);
         }
-    };
-    wv x[8];
-    int tok = 0;  // token of grouped row (64-token block) + lane
-    auto fetch_tok = [&](int p0) { tok = perm[sl.row + min(p0 + lane, sl.rows - 1)]; };
-    auto fetch_x = [&](int h) {  // rows 32 h + 8 lq + i of the block that `tok` holds
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-            x[i] = *reinterpret_cast<const wv*>(X + (size_t)__shfl(tok, 32 * h + 8 * lq + i, 64) * side.ld);
-    };
-    fetch_tok(0);
-    fetch_low(0);
-    fetch_x(0);
-    put_low(0);
-    int set = 0;
-    for (int p0 = 0; p0 < sl.rows; p0 += kTile, set ^= 1) {
-        __syncthreads();
-        const bool more = p0 + kTile < sl.rows;
-        if (more) fetch_low(p0 + kTile);
+        __builtin_amdgcn_sched_barrier(0);  // the next tile's loads stay before this one's products
+        const u4v* us_k = us + (k & 1) * TILE;
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            if (p0 + 32 * h >= sl.rows) break;
-            // values of tokens behind the piece are set to 0: they may be NaN
-            wv w[8];
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                w[i] = x[i];
-                if (p0 + 32 * h + 8 * lq + i >= sl.rows)
-#pragma unroll
-                    for (int d = 0; d < WB; d++) w[i][d] = 0;
-            }
-            if (h == 0)
-                fetch_x(1);
-            else if (more) {
-                fetch_tok(p0 + kTile);
-                fetch_x(0);
-            }
-            constexpr int PX = ACT == kActF32 ? 3 : (ACT == kActF16 ? 2 : 1);
+            if (64 * k + 32 * h >= sl.rows) break;
             u4v f[PX][4];
             if constexpr (ACT == kActF32) {
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     float v[8];
 #pragma unroll
-                    for (int i = 0; i < 8; i++) v[i] = __uint_as_float(w[i][j]);
+                    for (int i = 0; i < 8; i++) v[i] = __uint_as_float(w[h][i][j]);
                     u4v o[3];
                     parts8<3>(v, o);
 #pragma unroll
@@ -789,7 +823,7 @@ __global__ __launch_bounds__(256) void k_lora_grad(GradSide ga, GradSide gb, int
                 }
             } else {
                 Cols16<ACT == kActF16> c;
-                cols16<ACT == kActF16>(w, c);
+                cols16<ACT == kActF16>(w[h], c);
 #pragma unroll
                 for (int q = 0; q < PX; q++)
 #pragma unroll
@@ -799,7 +833,7 @@ __global__ __launch_bounds__(256) void k_lora_grad(GradSide ga, GradSide gb, int
             for (int b = 0; b < RB; b++) {
                 u4v a[3];
 #pragma unroll
-                for (int q = 0; q < 3; q++) a[q] = us[set][q][16 * b + li][4 * h + lq];
+                for (int q = 0; q < 3; q++) a[q] = us_k[(q * R16 + 16 * b + li) * 8 + ((4 * h + lq) ^ (li & 7))];
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     u4v o[PX];
@@ -809,10 +843,10 @@ __global__ __launch_bounds__(256) void k_lora_grad(GradSide ga, GradSide gb, int
                 }
             }
         }
-        if (more) put_low(set ^ 1);
     }
     if (c0 >= cols) return;
-    const bool whole = groups[sl.g].rows <= piece;
+    const bool whole = grp.rows <= piece;
+    typedef __attribute__((address_space(1))) f4v* gp;  // the table's pointers are to global memory
     float* to = whole ? out : part + (size_t)blockIdx.x * R16 * ((size_t)ga.cols + gb.cols) +
                                   (second ? (size_t)R16 * ga.cols : 0);
 #pragma unroll
@@ -821,7 +855,7 @@ __global__ __launch_bounds__(256) void k_lora_grad(GradSide ga, GradSide gb, int
         for (int q = 0; q < 4; q++) {
             const int m = 16 * b + 4 * lq + q;
             if (m >= r) continue;
-            f4v* p = reinterpret_cast<f4v*>(to + (size_t)m * cols + c0);
+            gp p = (gp)(uintptr_t)(to + (size_t)m * cols + c0);
             f4v v = {acc[b][0][q], acc[b][1][q], acc[b][2][q], acc[b][3][q]};
             if (whole && accumulate) v += *p;
             *p = v;
@@ -859,53 +893,76 @@ __global__ __launch_bounds__(256) void k_lora_grad_reduce(int ca, int cb, float*
 // ---- launches ----
 
 template <int ACT>
-hipError_t down(int RB, dim3 grid, hipStream_t s, const DownJob& a, const DownJob& b, int n, int R,
-                const LoraTable& tab, const int32_t* perm, const Slot* tiles, int T) {
-#define DN(B) \
-    hipLaunchKernelGGL((k_lora_down<ACT, B>), grid, dim3(256), 0, s, a, b, n, R, tab.ranks, tab.scales, perm, tiles, T)
-    if (RB == 1) DN(1); else if (RB == 2) DN(2); else if (RB == 4) DN(4); else DN(8);
+hipError_t down(const LoraWs& w, int sides, hipStream_t s, const DownJob& a, const DownJob& b, int n, int R,
+                const LoraTable& tab, const int32_t* perm, const Slot* tiles, int T, uint32_t* tickets) {
+    const dim3 grid(w.slots, w.ks, sides);
+#define DN(B)                                                                                                       \
+    hipLaunchKernelGGL((k_lora_down<ACT, B>), grid, dim3(256), 0, s, a, b, n, R, tab.ranks, tab.scales, perm, tiles, T, \
+                       tickets)
+    if (w.R16 == 16) DN(1); else if (w.R16 == 32) DN(2); else if (w.R16 == 64) DN(4); else DN(8);
 #undef DN
     return hipGetLastError();
 }
 
 template <int ACT>
-hipError_t up(int RB, dim3 grid, hipStream_t s, const float* u, int T, int ks, int N, int n, int R,
-              const void* const* fac, const LoraTable& tab, const int32_t* perm, const Slot* tiles, const void* base,
-              size_t ldb, void* y, size_t ldy) {
+hipError_t up(const LoraWs& w, hipStream_t s, const u4v* u, int T, int N, int n, int R, const void* const* fac,
+              const LoraTable& tab, const int32_t* perm, const Slot* tiles, const void* base, size_t ldb, void* y,
+              size_t ldy) {
     typedef typename Act<ACT>::T E;
-#define UP(B)                                                                                                    \
-    hipLaunchKernelGGL((k_lora_up<ACT, B>), grid, dim3(256), 0, s, u, T, ks, N, n, R, fac, tab.ranks, perm, tiles, \
-                       (const E*)base, ldb, (E*)y, ldy)
-    if (RB == 1) UP(1); else if (RB == 2) UP(2); else if (RB == 4) UP(4); else UP(8);
+    const dim3 grid(w.slots, col_blocks(N));
+#define UP(B)                                                                                                      \
+    hipLaunchKernelGGL((k_lora_up<ACT, B>), grid, dim3(256), 0, s, u, T, N, n, R, fac, tab.ranks, perm, tiles, (const E*)base, \
+                       ldb, (E*)y, ldy)
+    if (w.R16 == 16) UP(1); else if (w.R16 == 32) UP(2); else if (w.R16 == 64) UP(4); else UP(8);
 #undef UP
     return hipGetLastError();
 }
+
+// The workspace's regions.
+struct LoraMem {
+    int32_t* perm;
+    Group* groups;
+    Slot *tiles, *pieces;
+    uint32_t* tickets;
+    float *part, *grad;
+    u4v *ut, *vt, *ur, *vr;
+    LoraMem(const LoraWs& w, void* ws) {
+        char* b = reinterpret_cast<char*>(ws);
+        perm = reinterpret_cast<int32_t*>(b + w.perm);
+        groups = reinterpret_cast<Group*>(b + w.groups);
+        tiles = reinterpret_cast<Slot*>(b + w.tiles);
+        pieces = reinterpret_cast<Slot*>(b + w.pieces);
+        tickets = reinterpret_cast<uint32_t*>(b + w.tickets);
+        part = reinterpret_cast<float*>(b + w.part);
+        grad = reinterpret_cast<float*>(b + w.grad);
+        ut = reinterpret_cast<u4v*>(b + w.ut);
+        vt = reinterpret_cast<u4v*>(b + w.vt);
+        ur = reinterpret_cast<u4v*>(b + w.ur);
+        vr = reinterpret_cast<u4v*>(b + w.vr);
+    }
+};
 
 template <int ACT>
 hipError_t apply(int K, int N, int n, int R, const void* x, size_t ldx, int T, const LoraTable& tab, const void* base,
                  size_t ldb, void* y, size_t ldy, void* ws, hipStream_t s) {
     typedef typename Act<ACT>::T E;
     const LoraWs w = lora_ws(K, N, n, R, T, false);
-    char* b = reinterpret_cast<char*>(ws);
-    float* u = reinterpret_cast<float*>(b + w.u);
+    const LoraMem m(w, ws);
     hipError_t r;
     if (T <= kDirectMaxT) {
+        float* u = reinterpret_cast<float*>(m.ut);
         hipLaunchKernelGGL((k_lora_down_tok<ACT>), dim3(T, (R + 3) / 4), dim3(256), 0, s, (const E*)x, ldx, K, n, R, tab, u);
         if ((r = hipGetLastError()) != hipSuccess) return r;
         hipLaunchKernelGGL((k_lora_up_tok<ACT>), dim3(T, (N + 1023) / 1024), dim3(256), 0, s, u, N, n, R, tab,
                            (const E*)base, ldb, (E*)y, ldy);
         return hipGetLastError();
     }
-    int32_t* perm = reinterpret_cast<int32_t*>(b + w.perm);
-    Slot* tiles = reinterpret_cast<Slot*>(b + w.tiles);
-    hipLaunchKernelGGL(k_lora_plan, dim3(n + 2), dim3(1024), 0, s, tab.ids, T, n, perm,
-                       reinterpret_cast<Group*>(b + w.groups), tiles, (Slot*)nullptr, w.piece);
+    hipLaunchKernelGGL(k_lora_plan, dim3(n + 2), dim3(1024), 0, s, tab.ids, T, n, m.perm, m.groups, m.tiles,
+                       (Slot*)nullptr, w.piece, m.tickets, w.slots);
     if ((r = hipGetLastError()) != hipSuccess) return r;
-    const DownJob j = {x, ldx, K, tab.a, u};
-    r = down<ACT>(w.R16 / 16, dim3(w.slots, w.ks), s, j, j, n, R, tab, perm, tiles, T);
-    if (r != hipSuccess) return r;
-    return up<ACT>(w.R16 / 16, dim3(w.slots, (N + kUpCols - 1) / kUpCols), s, u, T, w.ks, N, n, R, tab.b, tab, perm,
-                   tiles, base, ldb, y, ldy);
+    const DownJob j = {x, ldx, K, tab.a, m.part, m.ut, nullptr};
+    if ((r = down<ACT>(w, 1, s, j, j, n, R, tab, m.perm, m.tiles, T, m.tickets)) != hipSuccess) return r;
+    return up<ACT>(w, s, m.ut, T, N, n, R, tab.b, tab, m.perm, m.tiles, base, ldb, y, ldy);
 }
 
 template <int ACT>
@@ -913,42 +970,35 @@ hipError_t backward(int K, int N, int n, int R, const void* x, size_t ldx, const
                     const LoraTable& tab, const void* dxb, size_t lddxb, void* dx, size_t lddx, float* const* da,
                     float* const* db, int accumulate, void* ws, hipStream_t s) {
     const LoraWs w = lora_ws(K, N, n, R, T, true);
-    char* b = reinterpret_cast<char*>(ws);
-    float* u = reinterpret_cast<float*>(b + w.u);
-    float* v = reinterpret_cast<float*>(b + w.v);
-    int32_t* perm = reinterpret_cast<int32_t*>(b + w.perm);
-    Group* groups = reinterpret_cast<Group*>(b + w.groups);
-    Slot* tiles = reinterpret_cast<Slot*>(b + w.tiles);
-    Slot* pieces = reinterpret_cast<Slot*>(b + w.pieces);
-    float* part = reinterpret_cast<float*>(b + w.grad);
-    const int RB = w.R16 / 16;
+    const LoraMem m(w, ws);
     hipError_t r;
-    hipLaunchKernelGGL(k_lora_plan, dim3(n + 2), dim3(1024), 0, s, tab.ids, T, n, perm, groups, tiles, pieces, w.piece);
+    hipLaunchKernelGGL(k_lora_plan, dim3(n + 2), dim3(1024), 0, s, tab.ids, T, n, m.perm, m.groups, m.tiles, m.pieces,
+                       w.piece, m.tickets, w.slots);
     if ((r = hipGetLastError()) != hipSuccess) return r;
     if (T > 0) {
-        const DownJob jv = {dy, lddy, N, tab.b, v}, ju = {x, ldx, K, tab.a, u};  // the larger side first
-        const bool both = db != nullptr;
-        r = down<ACT>(RB, dim3(w.slots, w.ks, both ? 2 : 1), s, jv, ju, n, R, tab, perm, tiles, T);
+        const DownJob jv = {dy, lddy, N, tab.b, m.part, dx ? m.vt : nullptr, da ? m.vr : nullptr};
+        const DownJob ju = {x, ldx, K, tab.a, m.part + (size_t)w.ks * T * w.R16, nullptr, m.ur};
+        const bool nv = dx || da;  // v: for dx and dA; u: for dB
+        r = down<ACT>(w, nv && db ? 2 : 1, s, nv ? jv : ju, ju, n, R, tab, m.perm, m.tiles, T, m.tickets);
         if (r != hipSuccess) return r;
         if (dx) {
-            r = up<ACT>(RB, dim3(w.slots, (K + kUpCols - 1) / kUpCols), s, v, T, w.ks, K, n, R, tab.a, tab, perm,
-                        tiles, dxb, lddxb, dx, lddx);
+            r = up<ACT>(w, s, m.vt, T, K, n, R, tab.a, tab, m.perm, m.tiles, dxb, lddxb, dx, lddx);
             if (r != hipSuccess) return r;
         }
     }
     if (!da && !db) return hipSuccess;
     if (T > 0) {
-        const GradSide ga = {v, x, ldx, K, da}, gb = {u, dy, lddy, N, db};
-        const dim3 grid(w.pslots, (K + kUpCols - 1) / kUpCols + (N + kUpCols - 1) / kUpCols);
-#define GR(B)                                                                                                     \
-    hipLaunchKernelGGL((k_lora_grad<ACT, B>), grid, dim3(256), 0, s, ga, gb, T, w.ks, n, R, w.piece, tab.ranks, perm, \
-                       groups, pieces, accumulate, part)
-        if (RB == 1) GR(1); else if (RB == 2) GR(2); else if (RB == 4) GR(4); else GR(8);
+        const GradSide ga = {m.vr, x, ldx, K, da}, gb = {m.ur, dy, lddy, N, db};
+        const dim3 grid(w.pslots, col_blocks(K) + col_blocks(N));
+#define GR(B)                                                                                                       \
+    hipLaunchKernelGGL((k_lora_grad<ACT, B>), grid, dim3(256), 0, s, ga, gb, n, R, w.piece, tab.ranks, m.perm, m.groups, \
+                       m.pieces, accumulate, m.grad)
+        if (w.R16 == 16) GR(1); else if (w.R16 == 32) GR(2); else if (w.R16 == 64) GR(4); else GR(8);
 #undef GR
         if ((r = hipGetLastError()) != hipSuccess) return r;
     }
     hipLaunchKernelGGL(k_lora_grad_reduce, dim3((K + 1023) / 1024 + (N + 1023) / 1024, R, n), dim3(256), 0, s, K, N, da,
-                       db, n, R, w.R16, w.piece, tab.ranks, groups, accumulate, part);
+                       db, n, R, w.R16, w.piece, tab.ranks, m.groups, accumulate, m.grad);
     return hipGetLastError();
 }
 
