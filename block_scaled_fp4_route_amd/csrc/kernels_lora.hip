@@ -183,7 +183,7 @@ struct Group {
 // parts (chunks of 8 values of one part):
 //   by token  [3][T][R32 / 8]             grouped rows, for "up" (R32: at least 32)
 //   by rank   [tile slot][3][R16][8]      chunk c (tokens 8 c .. of the tile) of
-//             rank k at place c ^ (k & 7), so that neighbouring ranks' reads
+//             rank k at place c ^ (k / 2 % 8), so that neighbouring ranks' reads
 //             from LDS fall on different banks, for "grad"
 struct LoraWs {
     int R16, R32, slots, piece, pslots, ks;
@@ -202,14 +202,14 @@ LoraWs lora_ws(int K, int N, int n, int R, int T, bool backward) {
     const int64_t piece = ((int64_t)T * (col_blocks(K) + col_blocks(N)) / 512 + kTile - 1) / kTile * kTile;
     w.piece = (int)(piece < 2 * kTile ? 2 * kTile : (piece > 4096 ? 4096 : piece));
     w.pslots = T / w.piece + n + 3;
-    // parts of the long axis of "down", so that short batches fill the chip
-    // (about 512 workgroups), at most 8 and at least four steps of 64 a wave
+    // parts of the long axis of "down": about 512 workgroups, at most 8 parts,
+    // of four steps at least on the longer side
     const int tiles = T / kTile + 1 + (n < T ? n : T) / 2;
-    const int steps = ((backward && N < K ? N : K) + 63) / 64;
+    const int steps = ((backward && N > K ? N : K) + 127) / 128;
     int ks = (512 + tiles - 1) / tiles;
     if (ks > 8) ks = 8;
-    while (ks > 1 && steps / ks < 16) ks--;
-    w.ks = ks;
+    if (ks > steps / 4) ks = steps / 4;
+    w.ks = ks < 1 ? 1 : ks;
     size_t o = kCounterBytes;
     auto take = [&o](size_t bytes) {
         const size_t at = o;
@@ -363,166 +363,167 @@ struct DownJob {
     u4v* by_rank;
 };
 
-// Sixteen consecutive activations of a row, as loaded.
-template <int ACT>
-struct Raw {
-    static constexpr int W = ACT == kActF32 ? 4 : 2;
-    u4v w[W];
+// A step of the long axis: 256 bytes of every activation row (128 above 32
+// ranks) and as many elements of every factor row. LDS holds a ring of RING
+// steps in at most 80 KB (two workgroups a compute unit), each as 16-byte
+// chunks, [64 tokens][XC] of activations and [ranks][FC] of the factor; chunk
+// c of row p is at place c ^ swizzle(p), so that the 16 rows that a matrix
+// operand reads at once lie on different banks.
+template <int ACT, int RB>
+struct DownStep {
+    static constexpr int XC = RB >= 4 ? 8 : 16;                  // chunks of an activation row
+    static constexpr int KE = XC * (ACT == kActF32 ? 4 : 8);     // elements
+    static constexpr int FC = KE / 8;                            // chunks of a factor row
+    static constexpr int XI = XC / 4;                            // 1 KB loads of a wave: its 16 tokens
+    static constexpr int FI = RB * 16 * FC / 64;                 // of the factor, all waves
+    static constexpr int FW = (FI + 3) / 4;                      // a wave's (each one twice where there are two)
+    static constexpr int CHUNKS = kTile * XC + RB * 16 * FC;
+    static constexpr int FIT = 81920 / (16 * CHUNKS), RING = FIT > 6 ? 6 : FIT;
+    static_assert(RING >= 3, "a step being read, one arriving, one to come");
 };
-// c += the product of half h (eight values) of x rows and w rows.
-template <int ACT>
-__device__ __forceinline__ f4v down_mma(const Raw<ACT>& x, int h, u4v w, f4v c) {
-    if constexpr (ACT == kActF32) {
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = __uint_as_float(x.w[2 * h + i / 4][i % 4]);
-        u4v p[3];
-        parts8<3>(v, p);
-#pragma unroll
-        for (int i = 2; i >= 0; i--) c = mma_bf16(p[i], w, c);
-        return c;
-    } else if constexpr (ACT == kActBf16) {
-        return mma_bf16(x.w[h], w, c);
-    } else {
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8v, x.w[h]), __builtin_bit_cast(h8v, w), c, 0, 0, 0);
-    }
-}
-__device__ __forceinline__ u4v ld_b128(rsrc_t r, uint32_t off) {
-    return __builtin_bit_cast(u4v, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+// Rows of C chunks: 16 / C of them span the banks, the next ones are shifted.
+template <int C>
+__device__ __forceinline__ int swizzle(int row) {
+    return row / (16 / C) % C;
 }
 
-// Steps s0 .. s1 - 1 of 64 of the long axis for NB x 16 tokens and RW x 16
-// ranks: lane (i = lane % 16, q = lane / 16) holds the elements 64 s + 16 q ..
-// + 15 of rows i, so a row's 128 bytes (16-bit types) arrive by neighbouring
-// lanes; which elements a matrix instruction pairs does not matter as long as
-// both operands agree. The loads of step s + 1 are under way during step s.
-// The elements of the last step that lie behind K are set to 0.
-template <int ACT, int NB, int RW>
-__device__ __forceinline__ void down_steps(f4v (&acc)[4][RW], const typename Act<ACT>::T* const (&xr)[4], int b0,
-                                           rsrc_t rf, const uint32_t (&wo)[RW], int s0, int s1, int K) {
-    const int lq = (threadIdx.x & 63) >> 4;
-    struct Set {
-        Raw<ACT> x[NB];
-        u4v w[RW][2];
-    } p, q;
-    auto load = [&](int s, Set& t) {
-        // pieces of eight behind K read the row's first ones
-        const int k = 64 * s + 16 * lq;
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const int o = k + 8 * h < K ? 64 * s + 8 * h : -16 * lq;
-#pragma unroll
-            for (int b = 0; b < NB; b++)
-#pragma unroll
-                for (int i = 0; i < Raw<ACT>::W / 2; i++)
-                    t.x[b].w[h * Raw<ACT>::W / 2 + i] = reinterpret_cast<const u4v*>(xr[b0 + b] + o)[i];
-#pragma unroll
-            for (int j = 0; j < RW; j++) t.w[j][h] = ld_b128(rf, wo[j] + (uint32_t)o * 2u);
-        }
-    };
-    auto multiply = [&](int s, Set& t) {
-        if (64 * s + 64 > K) {  // uniform: the last step only
-            const int k = 64 * s + 16 * lq;
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const bool in = k + 8 * h < K;
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-#pragma unroll
-                    for (int b = 0; b < NB; b++)
-#pragma unroll
-                        for (int i = 0; i < Raw<ACT>::W / 2; i++)
-                            t.x[b].w[h * Raw<ACT>::W / 2 + i][e] = in ? t.x[b].w[h * Raw<ACT>::W / 2 + i][e] : 0u;
-#pragma unroll
-                    for (int j = 0; j < RW; j++) t.w[j][h][e] = in ? t.w[j][h][e] : 0u;
-                }
-            }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; h++)
-#pragma unroll
-            for (int b = 0; b < NB; b++)
-#pragma unroll
-                for (int j = 0; j < RW; j++) acc[b0 + b][j] = down_mma<ACT>(t.x[b], h, t.w[j][h], acc[b0 + b][j]);
-    };
-    if (s0 >= s1) return;
-    load(s0, p);
-    for (int s = s0; s < s1; s += 2) {
-        load(min(s + 1, s1 - 1), q);
-        __builtin_amdgcn_sched_barrier(0);  // the loads stay before the products
-        multiply(s, p);
-        if (s + 1 >= s1) break;
-        load(min(s + 2, s1 - 1), p);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(s + 1, q);
-    }
+// A load of 16 bytes a lane from p straight into LDS: lane l writes lds + l.
+__device__ __forceinline__ void load_lds(const void* p, u4v* lds) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(uintptr_t)p,
+                                     (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+}
+// Wait until at most N vector memory operations of this wave are outstanding
+// (they complete in issue order) and its LDS accesses are done, then a
+// workgroup barrier.
+template <int N>
+__device__ __forceinline__ void ring_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 // grid (slots, parts of the long axis, sides): the low values of one tile over
-// one part. Four waves: each takes a quarter of the part's steps and all
-// ranks, or above 64 ranks a half of the steps and 64 ranks; operands go from
-// memory to registers, and the waves' sums are added in order through LDS.
-// Where the axis is in several parts, every workgroup leaves its own with
-// device-coherent stores, and the last one of a tile to finish (by a ticket)
-// adds them in order. Out go the bf16 parts of the scaled values.
+// one part. Wave w has the tokens 16 w .. + 15 and all ranks; the step after
+// next is on its way from memory while one is multiplied. (Operands loaded
+// straight into registers kept too little in flight: 90 us against ... for
+// both sides at 8192 tokens, 2560 and 8192 wide, rank 64.) Where the axis is
+// in several parts, every workgroup leaves its own with device-coherent
+// stores, and the last one of a tile to finish (by a ticket) adds them in
+// order. Out go the bf16 parts of the scaled values.
 template <int ACT, int RB>
 __global__ __launch_bounds__(256) void k_lora_down(DownJob ja, DownJob jb, int n, int R,
                                                    const int32_t* __restrict__ ranks, const float* __restrict__ scales,
                                                    const int32_t* __restrict__ perm, const Slot* __restrict__ tiles,
                                                    int T, uint32_t* __restrict__ tickets) {
-    constexpr int RW = RB > 4 ? 4 : RB, KW = 4 * RW / RB;  // rank blocks of a wave, waves along the long axis
-    constexpr int R16 = RB * 16, CH = (R16 < 32 ? 32 : R16) / 8;
-    __shared__ float red[kTile][R16 + 1];
-    __shared__ uint32_t ticket;
+    typedef DownStep<ACT, RB> S;
+    typedef typename Act<ACT>::T E;
+    constexpr int R16 = RB * 16, CH = (R16 < 32 ? 32 : R16) / 8, RING = S::RING;
+    // one array for everything (with several the compiler waits for every load
+    // in flight before each LDS read): the ring, later the tile's sums and a ticket
+    constexpr int SUMS = (kTile * (R16 + 1) * 4 + 15) / 16;
+    static_assert(RING * S::CHUNKS > SUMS, "the sums take the ring's place");
+    __shared__ u4v lds[RING * S::CHUNKS];
     const Slot sl = tiles[blockIdx.x];
     if (sl.rows == 0 || sl.g >= n) return;
     const DownJob j = blockIdx.z ? jb : ja;
     const int r = rank_of(ranks, sl.g, R);
     if (r < 0) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), li = lane & 15, lq = lane >> 4;
-    const int kw = wave % KW, r0 = wave / KW * RW;
-    const typename Act<ACT>::T* xr[4];
-    // rows behind the tile's tokens repeat the last one; their sums are not used
+    const int steps = (j.K + S::KE - 1) / S::KE;
+    const int s0 = (int)((int64_t)steps * blockIdx.y / gridDim.y), s1 = (int)((int64_t)steps * (blockIdx.y + 1) / gridDim.y);
+    // activations: load i of wave w has 64 / XC rows from 16 w + 64 i / XC;
+    // rows behind the tile's tokens repeat the last one, their sums are not used
+    const E* xp[S::XI];
+    int xk[S::XI];
 #pragma unroll
-    for (int b = 0; b < 4; b++)
-        xr[b] = reinterpret_cast<const typename Act<ACT>::T*>(j.x) +
-                (size_t)perm[sl.row + min(16 * b + li, sl.rows - 1)] * j.ldx + 16 * lq;
-    const rsrc_t rf = make_rsrc(j.fac[sl.g], (uint32_t)r * (uint32_t)j.K * 2u);  // rows behind the rank read 0
-    uint32_t wo[RW];
-#pragma unroll
-    for (int i = 0; i < RW; i++) wo[i] = ((uint32_t)(16 * (r0 + i) + li) * (uint32_t)j.K + (uint32_t)(16 * lq)) * 2u;
-    f4v acc[4][RW];
-#pragma unroll
-    for (int b = 0; b < 4; b++)
-#pragma unroll
-        for (int i = 0; i < RW; i++) acc[b][i] = f4v{0.f, 0.f, 0.f, 0.f};
-    const int steps = (j.K + 63) / 64, parts = gridDim.y * KW, part = blockIdx.y * KW + kw;
-    const int s0 = (int)((int64_t)steps * part / parts), s1 = (int)((int64_t)steps * (part + 1) / parts);
-    if (16 * r0 < r) {
-        if (sl.rows <= 16) {
-            down_steps<ACT, 1, RW>(acc, xr, 0, rf, wo, s0, s1, j.K);
-        } else if (sl.rows <= 32) {
-            down_steps<ACT, 2, RW>(acc, xr, 0, rf, wo, s0, s1, j.K);
-        } else if constexpr (ACT == kActF32) {  // fp32 rows take twice the registers
-            down_steps<ACT, 2, RW>(acc, xr, 0, rf, wo, s0, s1, j.K);
-            down_steps<ACT, 2, RW>(acc, xr, 2, rf, wo, s0, s1, j.K);
-        } else {
-            down_steps<ACT, 4, RW>(acc, xr, 0, rf, wo, s0, s1, j.K);
-        }
+    for (int i = 0; i < S::XI; i++) {
+        const int row = 16 * wave + (64 * i + lane) / S::XC, c = lane % S::XC ^ swizzle<S::XC>(row);
+        xk[i] = c * (S::KE / S::XC);
+        xp[i] = reinterpret_cast<const E*>(j.x) + (size_t)perm[sl.row + min(row, sl.rows - 1)] * j.ldx + xk[i];
     }
-    for (int w = 0; w < KW; w++) {
-        if (kw == w)
+    // factor: load i of wave w has the chunks 64 (w + 4 i) .. + 63; rows behind
+    // the rank repeat the last one, their sums are replaced by 0
+    const uint16_t* F = reinterpret_cast<const uint16_t*>(uniform_ptr(j.fac[sl.g]));
+    const uint16_t* fp[S::FW];
+    int fk[S::FW], fd[S::FW];
 #pragma unroll
-            for (int b = 0; b < 4; b++)
+    for (int i = 0; i < S::FW; i++) {
+        fd[i] = (wave + 4 * i) % S::FI * 64;
+        const int q = fd[i] + lane, row = q / S::FC, c = q % S::FC ^ swizzle<S::FC>(row);
+        fk[i] = c * 8;
+        fp[i] = F + (size_t)max(min(row, r - 1), 0) * j.K + fk[i];
+    }
+    // elements behind K read the row's first ones and are set to 0 when used
+    auto issue = [&](int s, u4v* to) {
+        const int k = min(s, s1 - 1) * S::KE;
 #pragma unroll
-                for (int i = 0; i < RW; i++)
+        for (int i = 0; i < S::XI; i++) load_lds(xp[i] + (k + xk[i] < j.K ? k : -xk[i]), to + 64 * (S::XI * wave + i));
+#pragma unroll
+        for (int i = 0; i < S::FW; i++) load_lds(fp[i] + (k + fk[i] < j.K ? k : -fk[i]), to + kTile * S::XC + fd[i]);
+    };
+    f4v acc[RB];
+#pragma unroll
+    for (int i = 0; i < RB; i++) acc[i] = f4v{0.f, 0.f, 0.f, 0.f};
+    if (r > 0 && s0 < s1) {
+        constexpr int NI = S::XI + S::FW;
+#pragma unroll
+        for (int i = 0; i < RING - 1; i++) issue(s0 + i, lds + i * S::CHUNKS);
+        int cur = 0, put = RING - 1;
+        const bool rows = 16 * wave < sl.rows;  // of this wave
+        for (int s = s0; s < s1; s++) {
+            ring_barrier<(RING - 2) * NI>();  // step s is there, and every wave is done with step s - 1
+            issue(s + RING - 1, lds + put * S::CHUNKS);
+            const u4v* x = lds + cur * S::CHUNKS + S::XC * (16 * wave + li);
+            const u4v* f = lds + cur * S::CHUNKS + kTile * S::XC + li * S::FC;
+            const int sx = swizzle<S::XC>(li), sf = swizzle<S::FC>(li);  // (rows 16 further have the same)
+            cur = cur + 1 == RING ? 0 : cur + 1;
+            put = put + 1 == RING ? 0 : put + 1;
+            if (!rows) continue;
+            const bool tail = (s + 1) * S::KE > j.K;
+#pragma unroll
+            for (int m = 0; m < S::KE / 32; m++) {
+                const int c = 4 * m + lq;  // the chunk of eight elements
+                const bool in = !tail || s * S::KE + 8 * c < j.K;
+                u4v a[ACT == kActF32 ? 3 : 1];
+                if constexpr (ACT == kActF32) {
+                    const u4v u = x[(2 * c) ^ sx], v = x[(2 * c + 1) ^ sx];
+                    float e[8];
 #pragma unroll
                     for (int q = 0; q < 4; q++) {
-                        float* p = &red[16 * b + 4 * lq + q][16 * (r0 + i) + li];
-                        *p = w ? *p + acc[b][i][q] : acc[b][i][q];
+                        e[q] = in ? __uint_as_float(u[q]) : 0.0f;
+                        e[4 + q] = in ? __uint_as_float(v[q]) : 0.0f;
                     }
-        __syncthreads();
+                    parts8<3>(e, a);
+                } else {
+                    a[0] = x[c ^ sx];
+#pragma unroll
+                    for (int q = 0; q < 4; q++) a[0][q] = in ? a[0][q] : 0u;
+                }
+#pragma unroll
+                for (int i = 0; i < RB; i++) {
+                    u4v w = f[16 * i * S::FC + (c ^ sf)];
+                    if (tail)
+#pragma unroll
+                        for (int q = 0; q < 4; q++) w[q] = in ? w[q] : 0u;
+                    if constexpr (ACT == kActF32) {
+#pragma unroll
+                        for (int q = 2; q >= 0; q--) acc[i] = mma_bf16(a[q], w, acc[i]);
+                    } else if constexpr (ACT == kActBf16) {
+                        acc[i] = mma_bf16(a[0], w, acc[i]);
+                    } else {
+                        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8v, a[0]),
+                                                                        __builtin_bit_cast(h8v, w), acc[i], 0, 0, 0);
+                    }
+                }
+            }
+        }
+        ring_barrier<0>();  // nothing is on its way into LDS any more, nobody reads the ring
     }
+    float(*red)[R16 + 1] = reinterpret_cast<float(*)[R16 + 1]>(lds);
+    uint32_t* ticket = reinterpret_cast<uint32_t*>(lds + SUMS);
+#pragma unroll
+    for (int i = 0; i < RB; i++)
+#pragma unroll
+        for (int q = 0; q < 4; q++) red[16 * wave + 4 * lq + q][16 * i + li] = acc[i][q];
+    __syncthreads();
     const int ks = gridDim.y, cells = sl.rows * R16;
     if (ks > 1) {
         float* mine = j.part + ((size_t)blockIdx.y * T + sl.row) * R16;
@@ -532,10 +533,10 @@ __global__ __launch_bounds__(256) void k_lora_down(DownJob ja, DownJob jb, int n
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
         if (tid == 0)
-            ticket = __hip_atomic_fetch_add(tickets + blockIdx.z * gridDim.x + blockIdx.x, 1u, __ATOMIC_RELAXED,
+            *ticket = __hip_atomic_fetch_add(tickets + blockIdx.z * gridDim.x + blockIdx.x, 1u, __ATOMIC_RELAXED,
                                             __HIP_MEMORY_SCOPE_AGENT);
         __syncthreads();
-        if (ticket + 1 != (uint32_t)ks) return;
+        if (*ticket + 1 != (uint32_t)ks) return;
         for (int i = tid; i < cells; i += 256) {
             float v[8];
 #pragma unroll
@@ -570,7 +571,7 @@ __global__ __launch_bounds__(256) void k_lora_down(DownJob ja, DownJob jb, int n
             u4v o[3];
             parts8<3>(v, o);
 #pragma unroll
-            for (int h = 0; h < 3; h++) j.by_rank[(((size_t)blockIdx.x * 3 + h) * R16 + k) * 8 + (c ^ (k & 7))] = o[h];
+            for (int h = 0; h < 3; h++) j.by_rank[(((size_t)blockIdx.x * 3 + h) * R16 + k) * 8 + (c ^ swizzle<8>(k))] = o[h];
         }
 }
 
@@ -639,7 +640,7 @@ __global__ __launch_bounds__(256) void k_lora_up(const u4v* __restrict__ u, int 
                                                  const int32_t* __restrict__ ranks, const int32_t* __restrict__ perm,
                                                  const Slot* __restrict__ tiles, const typename Act<ACT>::T* base,
                                                  size_t ldb, typename Act<ACT>::T* y, size_t ldy) {
-    constexpr int R16 = RB * 16, R32 = R16 < 32 ? 32 : R16, CH = R32 / 8;
+    constexpr int R32 = RB < 2 ? 32 : RB * 16, CH = R32 / 8;
     constexpr bool F16 = ACT == kActF16;
     const Slot sl = tiles[blockIdx.x];
     if (sl.rows == 0) return;
@@ -663,62 +664,73 @@ __global__ __launch_bounds__(256) void k_lora_up(const u4v* __restrict__ u, int 
             for (int q = 0; q < 4; q++) old[b][q] = *reinterpret_cast<const wv*>(base + (size_t)t[b][q] * ldb + cl);
     }
     const int r = none ? 0 : (sl.g == n ? -1 : rank_of(ranks, sl.g, R));
-    f4v acc[4][4];
+    constexpr int NG = R32 / 32, P = Cols16<F16>::P;
+    u4v f[NG][P][4];
+    u4v a[NG][3];
+    const u4v* ub = u + (size_t)(sl.row + li) * CH + lq;
+    auto load_u = [&](int b) {  // rows behind the tile repeat the last one
+        const int back = max(16 * b + li - (sl.rows - 1), 0);
 #pragma unroll
-    for (int b = 0; b < 4; b++)
+        for (int g = 0; g < NG; g++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) acc[b][j] = f4v{0.f, 0.f, 0.f, 0.f};
+            for (int h = 0; h < 3; h++) a[g][h] = ub[((size_t)h * T + 16 * b - back) * CH + 4 * g];
+    };
     if (r > 0) {
         const rsrc_t rf = make_rsrc(fac[sl.g], (uint32_t)r * (uint32_t)N * 2u);  // rows behind the rank read 0
-        const int nb = (sl.rows + 15) / 16;
+        u2v w[NG][8];
 #pragma unroll
-        for (int g = 0; g < R32 / 32; g++) {
-            if (32 * g >= r) break;
-            u2v w[8];
-            u4v a[4][3];
+        for (int g = 0; g < NG; g++)
 #pragma unroll
             for (int i = 0; i < 8; i++) {
                 const uint2 x = ld_b64(rf, ((uint32_t)(32 * g + 8 * lq + i) * (uint32_t)N + (uint32_t)cl) * 2u);
-                w[i] = u2v{x.x, x.y};
+                w[g][i] = u2v{x.x, x.y};
             }
+        load_u(0);
 #pragma unroll
-            for (int b = 0; b < 4; b++)
+        for (int g = 0; g < NG; g++) {
+            Cols16<F16> c;
+            cols16<F16>(w[g], c);
 #pragma unroll
-                for (int h = 0; h < 3; h++)
-                    a[b][h] = u[((size_t)h * T + sl.row + min(16 * b + li, sl.rows - 1)) * CH + 4 * g + lq];
-            Cols16<F16> f;
-            cols16<F16>(w, f);
+            for (int h = 0; h < P; h++)
 #pragma unroll
-            for (int b = 0; b < 4; b++) {
-                if (b >= nb) break;
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    u4v p[Cols16<F16>::P];
-#pragma unroll
-                    for (int h = 0; h < Cols16<F16>::P; h++) p[h] = f.c[h][j];
-                    acc[b][j] = mma_parts<Cols16<F16>::P>(a[b], p, acc[b][j]);
-                }
-            }
+                for (int j = 0; j < 4; j++) f[g][h][j] = c.c[h][j];
         }
     }
-    if (c0 >= N) return;
 #pragma unroll
-    for (int b = 0; b < 4; b++)
+    for (int b = 0; b < 4; b++) {
+        if (16 * b >= sl.rows) break;
+        f4v acc[4];
 #pragma unroll
-        for (int q = 0; q < 4; q++) {
-            f4v v = {acc[b][0][q], acc[b][1][q], acc[b][2][q], acc[b][3][q]};
-            if (base) {
-                if constexpr (ACT == kActF32) {
-                    v += __builtin_bit_cast(f4v, old[b][q]);
-                } else {
-                    float e, f;
-                    cvt2<ACT>(old[b][q][0], e, f); v.x += e; v.y += f;
-                    cvt2<ACT>(old[b][q][1], e, f); v.z += e; v.w += f;
+        for (int j = 0; j < 4; j++) acc[j] = f4v{0.f, 0.f, 0.f, 0.f};
+        if (r > 0) {
+#pragma unroll
+            for (int g = 0; g < NG; g++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    u4v p[P];
+#pragma unroll
+                    for (int h = 0; h < P; h++) p[h] = f[g][h][j];
+                    acc[j] = mma_parts<P>(a[g], p, acc[j]);
                 }
-            }
-            if (r < 0) v.x = v.y = v.z = v.w = __builtin_nanf("");
-            if (16 * b + 4 * lq + q < sl.rows) st4<ACT>(y + (size_t)t[b][q] * ldy + c0, v);
+            if (b < 3 && 16 * (b + 1) < sl.rows) load_u(b + 1);
         }
+        if (c0 < N)
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                f4v v = {acc[0][q], acc[1][q], acc[2][q], acc[3][q]};
+                if (base) {
+                    if constexpr (ACT == kActF32) {
+                        v += __builtin_bit_cast(f4v, old[b][q]);
+                    } else {
+                        float e, o;
+                        cvt2<ACT>(old[b][q][0], e, o); v.x += e; v.y += o;
+                        cvt2<ACT>(old[b][q][1], e, o); v.z += e; v.w += o;
+                    }
+                }
+                if (r < 0) v.x = v.y = v.z = v.w = __builtin_nanf("");
+                if (16 * b + 4 * lq + q < sl.rows) st4<ACT>(y + (size_t)t[b][q] * ldy + c0, v);
+            }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -833,7 +845,7 @@ __global__ __launch_bounds__(256) void k_lora_grad(GradSide ga, GradSide gb, int
             for (int b = 0; b < RB; b++) {
                 u4v a[3];
 #pragma unroll
-                for (int q = 0; q < 3; q++) a[q] = us_k[(q * R16 + 16 * b + li) * 8 + ((4 * h + lq) ^ (li & 7))];
+                for (int q = 0; q < 3; q++) a[q] = us_k[(q * R16 + 16 * b + li) * 8 + ((4 * h + lq) ^ swizzle<8>(li))];
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     u4v o[PX];
