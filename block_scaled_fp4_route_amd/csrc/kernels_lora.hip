@@ -186,7 +186,8 @@ struct Group {
 //             rank k at place c ^ (k / 2 % 8), so that neighbouring ranks' reads
 //             from LDS fall on different banks, for "grad"
 struct LoraWs {
-    int R16, R32, slots, piece, pslots, ks;
+    int R16, R32, slots, piece, pslots;
+    int ku, kv;  // parts of the long axis of "down": x with A, dy with B
     size_t perm, groups, tiles, pieces, tickets, part, ut, vt, ur, vr, grad, total;
 };
 
@@ -202,14 +203,18 @@ LoraWs lora_ws(int K, int N, int n, int R, int T, bool backward) {
     const int64_t piece = ((int64_t)T * (col_blocks(K) + col_blocks(N)) / 512 + kTile - 1) / kTile * kTile;
     w.piece = (int)(piece < 2 * kTile ? 2 * kTile : (piece > 4096 ? 4096 : piece));
     w.pslots = T / w.piece + n + 3;
-    // parts of the long axis of "down": about 512 workgroups, at most 8 parts,
-    // of four steps at least on the longer side
+    // parts of the long axes of "down": two workgroups per compute unit in all
+    // (what runs at once), shared out by the sides' lengths, at most 8 parts of
+    // a side, of four steps of 128 at least
     const int tiles = T / kTile + 1 + (n < T ? n : T) / 2;
-    const int steps = ((backward && N > K ? N : K) + 127) / 128;
-    int ks = (512 + tiles - 1) / tiles;
-    if (ks > 8) ks = 8;
-    if (ks > steps / 4) ks = steps / 4;
-    w.ks = ks < 1 ? 1 : ks;
+    auto parts = [tiles](int len, int all) {
+        int64_t k = (512 / tiles * (int64_t)len + all / 2) / all;
+        if (k > 8) k = 8;
+        if (k > len / 512) k = len / 512;
+        return (int)(k < 1 ? 1 : k);
+    };
+    w.ku = parts(K, backward ? K + N : K);
+    w.kv = backward ? parts(N, K + N) : 0;
     size_t o = kCounterBytes;
     auto take = [&o](size_t bytes) {
         const size_t at = o;
@@ -221,13 +226,12 @@ LoraWs lora_ws(int K, int N, int n, int R, int T, bool backward) {
         w.total = o;
         return w;
     }
-    const int sides = backward ? 2 : 1;
     w.perm = take((size_t)T * 4);
     w.groups = take((size_t)(n + 2) * sizeof(Group));
     w.tiles = take((size_t)w.slots * sizeof(Slot));
     w.pieces = take(backward ? (size_t)w.pslots * sizeof(Slot) : 0);
     w.tickets = take((size_t)w.slots * 2 * 4);
-    w.part = take(ks > 1 ? (size_t)sides * ks * T * w.R16 * 4 : 0);
+    w.part = take((size_t)((w.ku > 1 ? w.ku : 0) + (w.kv > 1 ? w.kv : 0)) * T * w.R16 * 4);
     const size_t by_token = (size_t)T * w.R32 * 6, by_rank = (size_t)w.slots * w.R16 * kTile * 6;
     w.ut = take(backward ? 0 : by_token);
     w.vt = take(backward ? by_token : 0);
@@ -262,17 +266,19 @@ __global__ __launch_bounds__(1024) void k_lora_plan(const int32_t* __restrict__ 
     };
     if (tid < 2) acc[tid] = 0;
     __syncthreads();
-    int less = 0, own = 0;
+    int less = 0, own = 0;  // of the wave
     for (int t0 = 0; t0 < T; t0 += SPAN) {
         load(t0);
 #pragma unroll
         for (int i = 0; i < kPlanIds; i++) {
-            less += key[i] >= 0 && key[i] < g;
-            own += key[i] == g;
+            less += __popcll(__ballot(key[i] >= 0 && key[i] < g));
+            own += __popcll(__ballot(key[i] == g));
         }
     }
-    if (less) atomicAdd(&acc[0], less);
-    if (own) atomicAdd(&acc[1], own);
+    if (lane == 0) {
+        atomicAdd(&acc[0], less);
+        atomicAdd(&acc[1], own);
+    }
     __syncthreads();
     const int first = acc[0], count = acc[1];
     int at = first;
@@ -358,7 +364,8 @@ struct DownJob {
     size_t ldx;
     int K;
     const void* const* fac;
-    float* part;    // [parts][T][R16]
+    int ks;         // parts of the long axis
+    float* part;    // [ks][T][R16]
     u4v* by_token;  // either may be null
     u4v* by_rank;
 };
@@ -400,8 +407,8 @@ __device__ __forceinline__ void ring_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// grid (slots, parts of the long axis, sides): the low values of one tile over
-// one part. Wave w has the tokens 16 w .. + 15 and all ranks; the step after
+// grid (slots, parts of side a, then of side b): the low values of one tile
+// over one part of one side's long axis. Wave w has the tokens 16 w .. + 15 and all ranks; the step after
 // next is on its way from memory while one is multiplied. (Operands loaded
 // straight into registers kept too little in flight: 90 us against ... for
 // both sides at 8192 tokens, 2560 and 8192 wide, rank 64.) Where the axis is
@@ -423,12 +430,14 @@ __global__ __launch_bounds__(256) void k_lora_down(DownJob ja, DownJob jb, int n
     __shared__ u4v lds[RING * S::CHUNKS];
     const Slot sl = tiles[blockIdx.x];
     if (sl.rows == 0 || sl.g >= n) return;
-    const DownJob j = blockIdx.z ? jb : ja;
+    const bool second = (int)blockIdx.y >= ja.ks;
+    const DownJob j = second ? jb : ja;
+    const int ks = j.ks, ky = (int)blockIdx.y - (second ? ja.ks : 0);
     const int r = rank_of(ranks, sl.g, R);
     if (r < 0) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), li = lane & 15, lq = lane >> 4;
     const int steps = (j.K + S::KE - 1) / S::KE;
-    const int s0 = (int)((int64_t)steps * blockIdx.y / gridDim.y), s1 = (int)((int64_t)steps * (blockIdx.y + 1) / gridDim.y);
+    const int s0 = (int)((int64_t)steps * ky / ks), s1 = (int)((int64_t)steps * (ky + 1) / ks);
     // activations: load i of wave w has 64 / XC rows from 16 w + 64 i / XC;
     // rows behind the tile's tokens repeat the last one, their sums are not used
     const E* xp[S::XI];
@@ -524,16 +533,16 @@ __global__ __launch_bounds__(256) void k_lora_down(DownJob ja, DownJob jb, int n
 #pragma unroll
         for (int q = 0; q < 4; q++) red[16 * wave + 4 * lq + q][16 * i + li] = acc[i][q];
     __syncthreads();
-    const int ks = gridDim.y, cells = sl.rows * R16;
+    const int cells = sl.rows * R16;
     if (ks > 1) {
-        float* mine = j.part + ((size_t)blockIdx.y * T + sl.row) * R16;
+        float* mine = j.part + ((size_t)ky * T + sl.row) * R16;
         for (int i = tid; i < cells; i += 256)
             __hip_atomic_store(mine + i, red[i / R16][i % R16], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         // each wave waits for its own stores, then one ticket for all of them
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
         if (tid == 0)
-            *ticket = __hip_atomic_fetch_add(tickets + blockIdx.z * gridDim.x + blockIdx.x, 1u, __ATOMIC_RELAXED,
+            *ticket = __hip_atomic_fetch_add(tickets + (second ? gridDim.x : 0) + blockIdx.x, 1u, __ATOMIC_RELAXED,
                                             __HIP_MEMORY_SCOPE_AGENT);
         __syncthreads();
         if (*ticket + 1 != (uint32_t)ks) return;
@@ -907,7 +916,7 @@ __global__ __launch_bounds__(256) void k_lora_grad_reduce(int ca, int cb, float*
 template <int ACT>
 hipError_t down(const LoraWs& w, int sides, hipStream_t s, const DownJob& a, const DownJob& b, int n, int R,
                 const LoraTable& tab, const int32_t* perm, const Slot* tiles, int T, uint32_t* tickets) {
-    const dim3 grid(w.slots, w.ks, sides);
+    const dim3 grid(w.slots, a.ks + (sides > 1 ? b.ks : 0));
 #define DN(B)                                                                                                       \
     hipLaunchKernelGGL((k_lora_down<ACT, B>), grid, dim3(256), 0, s, a, b, n, R, tab.ranks, tab.scales, perm, tiles, T, \
                        tickets)
@@ -972,7 +981,7 @@ hipError_t apply(int K, int N, int n, int R, const void* x, size_t ldx, int T, c
     hipLaunchKernelGGL(k_lora_plan, dim3(n + 2), dim3(1024), 0, s, tab.ids, T, n, m.perm, m.groups, m.tiles,
                        (Slot*)nullptr, w.piece, m.tickets, w.slots);
     if ((r = hipGetLastError()) != hipSuccess) return r;
-    const DownJob j = {x, ldx, K, tab.a, m.part, m.ut, nullptr};
+    const DownJob j = {x, ldx, K, tab.a, w.ku, m.part, m.ut, nullptr};
     if ((r = down<ACT>(w, 1, s, j, j, n, R, tab, m.perm, m.tiles, T, m.tickets)) != hipSuccess) return r;
     return up<ACT>(w, s, m.ut, T, N, n, R, tab.b, tab, m.perm, m.tiles, base, ldb, y, ldy);
 }
@@ -988,8 +997,8 @@ hipError_t backward(int K, int N, int n, int R, const void* x, size_t ldx, const
                        w.piece, m.tickets, w.slots);
     if ((r = hipGetLastError()) != hipSuccess) return r;
     if (T > 0) {
-        const DownJob jv = {dy, lddy, N, tab.b, m.part, dx ? m.vt : nullptr, da ? m.vr : nullptr};
-        const DownJob ju = {x, ldx, K, tab.a, m.part + (size_t)w.ks * T * w.R16, nullptr, m.ur};
+        const DownJob jv = {dy, lddy, N, tab.b, w.kv, m.part, dx ? m.vt : nullptr, da ? m.vr : nullptr};
+        const DownJob ju = {x, ldx, K, tab.a, w.ku, m.part + (w.kv > 1 ? (size_t)w.kv * T * w.R16 : 0), nullptr, m.ur};
         const bool nv = dx || da;  // v: for dx and dA; u: for dB
         r = down<ACT>(w, nv && db ? 2 : 1, s, nv ? jv : ju, ju, n, R, tab, m.perm, m.tiles, T, m.tickets);
         if (r != hipSuccess) return r;
