@@ -287,30 +287,42 @@ def moe_expert_prefetch(d, expert_ptrs, idx, n, sink, stream=None):
 
 # --- training the router, low-rank adapters ---------------------------------
 
-def _run(fn, head, stream, tensors, *args):
-    """fn(head, *args, stream) with the device of the tensors current (they
-    may lie on another one than the caller's) and, without a stream, on that
-    device's current stream."""
+def _run(fn, head, stream, *args):
+    """fn(head, *args, stream), tensors as their addresses, with the tensors'
+    device current (it may be another one than the caller's) and, without a
+    stream, on that device's current stream."""
     import torch
-    dev = None
-    for t in tensors:
-        if t is None or isinstance(t, int):
-            continue
-        if not t.is_cuda:
-            raise MoeError(MOE_ERR_ARG, "a tensor is not on the GPU")
-        if dev is None:
-            dev = t.get_device()
-        elif t.get_device() != dev:
-            raise MoeError(MOE_ERR_ARG, "tensors on different devices")
+    Tensor, dev, out = torch.Tensor, None, []
+    for a in args:
+        if isinstance(a, Tensor):
+            d = a.get_device()
+            if d != dev:
+                if d < 0:
+                    raise MoeError(MOE_ERR_ARG, "a tensor is not on the GPU")
+                if dev is not None:
+                    raise MoeError(MOE_ERR_ARG, "tensors on different devices")
+                dev = d
+            a = a.data_ptr()
+        out.append(a)
+    if stream is None and dev is not None:
+        stream = _current_stream(dev)
     if dev is None or dev == torch.cuda.current_device():
-        _check(fn(C.byref(head), *args, _stream(stream)))
+        _check(fn(C.byref(head), *out, _stream(stream)))
     else:
         with torch.cuda.device(dev):
-            _check(fn(C.byref(head), *args, _stream(stream)))
+            _check(fn(C.byref(head), *out, _stream(stream)))
+
+
+def _current_stream(dev: int) -> int:
+    """Handle of the device's current stream: what torch.cuda.current_stream()
+    makes a Stream object of (2.8 us against 0.1)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if raw else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _ws_bytes(ws, ws_bytes):
-    return ws.numel() * ws.element_size() if ws_bytes is None and ws is not None else (ws_bytes or 0)
+    return ws.nbytes if ws_bytes is None and ws is not None else (ws_bytes or 0)
 
 
 def moe_balance_workspace_bytes(d, T: int, S: int = 1) -> int:
@@ -319,9 +331,8 @@ def moe_balance_workspace_bytes(d, T: int, S: int = 1) -> int:
 
 def moe_balance_loss(d, logits, T, idx, mask, seq_off, S, balance_coef, z_coef, dloss, loss, counts, probs, dlogits,
                      ws, ws_bytes=None, stream=None):
-    _run(lib.moe_balance_loss, d, stream, (loss, logits, idx, mask, seq_off, dloss, counts, probs, dlogits, ws),
-         _ptr(logits), T, _ptr(idx), _ptr(mask), _ptr(seq_off), S, balance_coef, z_coef, _ptr(dloss), _ptr(loss),
-         _ptr(counts), _ptr(probs), _ptr(dlogits), _ptr(ws), _ws_bytes(ws, ws_bytes))
+    _run(lib.moe_balance_loss, d, stream, logits, T, idx, mask, seq_off, S, balance_coef, z_coef, dloss, loss, counts,
+         probs, dlogits, ws, _ws_bytes(ws, ws_bytes))
 
 
 def moe_route_backward_workspace_bytes(d, T: int) -> int:
@@ -330,9 +341,8 @@ def moe_route_backward_workspace_bytes(d, T: int) -> int:
 
 def moe_route_backward(d, x, T, Wr, idx, w, dw, mask, dlogits_in, dlogits_out, dx, dWr, accumulate, ws, ws_bytes=None,
                        stream=None):
-    _run(lib.moe_route_backward, d, stream, (x, Wr, idx, w, dw, mask, dlogits_in, dlogits_out, dx, dWr, ws),
-         _ptr(x), T, _ptr(Wr), _ptr(idx), _ptr(w), _ptr(dw), _ptr(mask), _ptr(dlogits_in), _ptr(dlogits_out), _ptr(dx),
-         _ptr(dWr), accumulate, _ptr(ws), _ws_bytes(ws, ws_bytes))
+    _run(lib.moe_route_backward, d, stream, x, T, Wr, idx, w, dw, mask, dlogits_in, dlogits_out, dx, dWr, accumulate,
+         ws, _ws_bytes(ws, ws_bytes))
 
 
 def lora_desc(K: int, N: int, n: int, max_rank: int, dtype) -> moe_lora_desc:
@@ -349,14 +359,11 @@ def moe_lora_workspace_bytes(l, T: int, backward) -> int:
 
 def moe_lora_apply(l, x, ldx, T, ids, a_ptrs, b_ptrs, ranks, scales, base, ldbase, y, ldy, ws, ws_bytes=None,
                    stream=None):
-    _run(lib.moe_lora_apply, l, stream, (y, x, ids, a_ptrs, b_ptrs, ranks, scales, base, ws),
-         _ptr(x), ldx, T, _ptr(ids), _ptr(a_ptrs), _ptr(b_ptrs), _ptr(ranks), _ptr(scales), _ptr(base), ldbase,
-         _ptr(y), ldy, _ptr(ws), _ws_bytes(ws, ws_bytes))
+    _run(lib.moe_lora_apply, l, stream, x, ldx, T, ids, a_ptrs, b_ptrs, ranks, scales, base, ldbase, y, ldy, ws,
+         _ws_bytes(ws, ws_bytes))
 
 
 def moe_lora_backward(l, x, ldx, dy, lddy, T, ids, a_ptrs, b_ptrs, ranks, scales, dx_base, lddx_base, dx, lddx,
                       da_ptrs, db_ptrs, accumulate, ws, ws_bytes=None, stream=None):
-    _run(lib.moe_lora_backward, l, stream, (x, dy, ids, a_ptrs, b_ptrs, ranks, scales, dx_base, dx, da_ptrs, db_ptrs, ws),
-         _ptr(x), ldx, _ptr(dy), lddy, T, _ptr(ids), _ptr(a_ptrs), _ptr(b_ptrs), _ptr(ranks), _ptr(scales),
-         _ptr(dx_base), lddx_base, _ptr(dx), lddx, _ptr(da_ptrs), _ptr(db_ptrs), accumulate, _ptr(ws),
-         _ws_bytes(ws, ws_bytes))
+    _run(lib.moe_lora_backward, l, stream, x, ldx, dy, lddy, T, ids, a_ptrs, b_ptrs, ranks, scales, dx_base, lddx_base,
+         dx, lddx, da_ptrs, db_ptrs, accumulate, ws, _ws_bytes(ws, ws_bytes))

@@ -109,7 +109,9 @@ class Case:
 SHAPES = [(1, 8, 8, [1], "one"), (1, 2560, 8192, [16, 8], "one"), (2, 16, 2560, [3, 1, 0], "mixed"),
           (17, 264, 40, [5, 16, 7], "mixed"), (64, 2560, 640, [16] * 8, "mixed"), (65, 2560, 640, [16] * 8, "mixed"),
           (65, 8, 8, [128], "one"), (130, 520, 1032, [33, 64, 1, 17], "mixed"), (300, 640, 2560, [8, 3], "runs"),
-          (257, 1000, 264, [128, 100], "mixed"), (700, 256, 512, [20, 31, 48], "runs"), (1500, 136, 24, [2] * 40, "mixed")]
+          (257, 1000, 264, [128, 100], "mixed"), (700, 256, 512, [20, 31, 48], "runs"), (1500, 136, 24, [2] * 40, "mixed"),
+          (512, 72, 520, [16, 9], "mixed"), (513, 72, 520, [16, 9], "mixed"), (64, 72, 520, [128, 1, 40], "mixed"), (8, 4096, 2560, [16], "one"),
+          (40, 8192, 256, [32, 8, 31], "mixed")]
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
@@ -126,7 +128,7 @@ def test_backward(m, dt, T, K, N, ranks, order):
     c.check_backward(c.backward())
 
 
-@pytest.mark.parametrize("T", [5, 200])
+@pytest.mark.parametrize("T", [5, 200, 600])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_bases_places_and_strides(m, dt, T):
     c = Case(m, dt, T, 264, 520, [16, 5, 9])
@@ -157,7 +159,7 @@ def test_max_rank_above_the_ranks(m, T):
         c.check_backward(c.backward())
 
 
-@pytest.mark.parametrize("T", [6, 90])
+@pytest.mark.parametrize("T", [6, 90, 600])
 def test_no_adapter_at_all(m, T):
     c = Case(m, "bf16", T, 264, 520, [16, 5])
     c.ids.fill_(-3)
@@ -168,7 +170,7 @@ def test_no_adapter_at_all(m, T):
     assert torch.equal(dx, c.dxb) and all(not t.any() for t in c.dA + c.dB)
 
 
-@pytest.mark.parametrize("T", [8, 150])
+@pytest.mark.parametrize("T", [8, 150, 700])
 def test_bad_ids(m, T):
     c = Case(m, "f32", T, 64, 72, [4, 4])
     c.ids[3], c.ids[T - 1] = 2, 1 << 30
@@ -177,7 +179,7 @@ def test_bad_ids(m, T):
     c.check_backward(c.backward())
 
 
-@pytest.mark.parametrize("T", [8, 150])
+@pytest.mark.parametrize("T", [8, 150, 700])
 @pytest.mark.parametrize("bad", [-1, 17, 1 << 30])
 def test_bad_rank(m, T, bad):
     c = Case(m, "f32", T, 64, 72, [16, 4, 16])
@@ -240,7 +242,7 @@ def test_no_tokens(m):
 def test_infinite_activations(m):
     """An infinity reaches its own row as fp32 arithmetic has it, and no other row."""
     for dt in DT:
-        for T in (9, 100):
+        for T in (9, 100, 600):
             c = Case(m, dt, T, 64, 72, [4], "one")
             y = c.apply()
             c.x[2, 5], c.x[4, 9] = float("inf"), float("nan")
@@ -253,7 +255,7 @@ def test_infinite_activations(m):
 def test_fp32_activations_keep_all_bits(m):
     """x = 1 + 2^-23 against a factor row that cancels the ones: what is left
     is the last bit, which a rounded activation would lose."""
-    for T in (3, 70):
+    for T in (3, 70, 600):
         c = Case(m, "f32", T, 16, 8, [1], "one")
         c.x[:] = 1.0 + 2.0 ** -23
         c.x[:, 8:] = 1.0
@@ -280,7 +282,7 @@ def test_strides_past_32_bits(m):
     assert torch.equal(out.as_strided((3, 64), (ld, 1)), dx)
     # and through the grouped kernels
     T = 70
-    c = Case(m, "bf16", T, 64, 72, [4], "one")
+    c = Case(m, "bf16", T, 64, 72, [128], "one")
     y = c.apply()
     ld = (1 << 31) // 64 + 64
     wide = torch.empty((T - 1) * ld + 128, dtype=torch.bfloat16, device="cuda")
