@@ -468,6 +468,10 @@ __device__ __forceinline__ int swizzle(int row) {
     return row / (16 / C) % C;
 }
 
+// Cache policy of loads and stores that other XCDs' workgroups take part in
+// (sc1: device scope).
+constexpr int kCoherent = 16;
+
 // A load of 16 bytes a lane from p straight into LDS: lane l writes lds + l.
 __device__ __forceinline__ void load_lds(const void* p, u4v* lds) {
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(uintptr_t)p,
@@ -607,30 +611,45 @@ __global__ __launch_bounds__(256) void k_lora_down(DownJob ja, DownJob jb, int n
 #pragma unroll
         for (int q = 0; q < 4; q++) red[16 * wave + 4 * lq + q][16 * i + li] = acc[i][q];
     __syncthreads();
-    const int cells = sl.rows * R16;
     if (ks > 1) {
-        float* mine = j.part + ((size_t)ky * T + sl.row) * R16;
-        for (int i = tid; i < cells; i += 256)
-            __hip_atomic_store(mine + i, red[i / R16][i % R16], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        // 16 bytes a thread at a time, kCoherent: past this XCD's L2
+        constexpr int PER = R16 / 16;  // of a thread: 64 tokens x R16 / 4 / 256
+        const rsrc_t rp = make_rsrc(j.part + (size_t)sl.row * R16, (uint32_t)sl.rows * (uint32_t)(R16 * 4));
+        auto cell = [&](int i) { return (tid + 256 * i) * 4; };  // rows behind the tile's store nothing, read 0
+        const size_t stride = (size_t)T * R16;
+        const rsrc_t mine = make_rsrc(j.part + ky * stride + (size_t)sl.row * R16, (uint32_t)sl.rows * (uint32_t)(R16 * 4));
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
+            const int c = cell(i);
+            const float* q = &red[c / R16][c % R16];
+            const u4v v = {__float_as_uint(q[0]), __float_as_uint(q[1]), __float_as_uint(q[2]), __float_as_uint(q[3])};
+            __builtin_amdgcn_raw_buffer_store_b128(v, mine, (uint32_t)c * 4u, 0, kCoherent);
+        }
         // each wave waits for its own stores, then one ticket for all of them
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
         if (tid == 0)
             *ticket = __hip_atomic_fetch_add(tickets + (second ? gridDim.x : 0) + blockIdx.x, 1u, __ATOMIC_RELAXED,
-                                            __HIP_MEMORY_SCOPE_AGENT);
+                                             __HIP_MEMORY_SCOPE_AGENT);
         __syncthreads();
         if (*ticket + 1 != (uint32_t)ks) return;
-        for (int i = tid; i < cells; i += 256) {
-            float v[8];
+        f4v sum[PER];
 #pragma unroll
-            for (int q = 0; q < 8; q++)
-                v[q] = __hip_atomic_load(j.part + ((size_t)min(q, ks - 1) * T + sl.row) * R16 + i, __ATOMIC_RELAXED,
-                                         __HIP_MEMORY_SCOPE_AGENT);
-            float a = v[0];
+        for (int i = 0; i < PER; i++)
+            sum[i] = __builtin_bit_cast(f4v, __builtin_amdgcn_raw_buffer_load_b128(rp, (uint32_t)cell(i) * 4u, 0, kCoherent));
+        for (int q = 1; q < ks; q++) {
+            const rsrc_t rq = make_rsrc(j.part + q * stride + (size_t)sl.row * R16, (uint32_t)sl.rows * (uint32_t)(R16 * 4));
+            f4v v[PER];
 #pragma unroll
-            for (int q = 1; q < 8; q++) a += q < ks ? v[q] : 0.0f;
-            red[i / R16][i % R16] = a;
+            for (int i = 0; i < PER; i++)
+                v[i] = __builtin_bit_cast(f4v, __builtin_amdgcn_raw_buffer_load_b128(rq, (uint32_t)cell(i) * 4u, 0, kCoherent));
+#pragma unroll
+            for (int i = 0; i < PER; i++) sum[i] += v[i];
         }
+#pragma unroll
+        for (int i = 0; i < PER; i++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) red[cell(i) / R16][cell(i) % R16 + q] = sum[i][q];
         __syncthreads();
     }
     const float sc = scales[sl.g];
