@@ -24,7 +24,8 @@ FLAGS = [
 # per-source additions: the grouped GEMMs keep their MFMA accumulators in the
 # ordinary vector registers, which saves the copies between register files
 # that the K loops otherwise carry (same results, 2-4% less time)
-EXTRA = {"kernels_prefill.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+EXTRA = {"kernels_prefill.hip": VGPR_FORM, "kernels_lora.hip": VGPR_FORM}
 
 
 def _compile(src: str) -> str:

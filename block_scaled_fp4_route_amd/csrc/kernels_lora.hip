@@ -16,6 +16,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "moe_device.h"
 #include "moe_internal.h"
 #include "moe_learn.h"
@@ -563,44 +565,46 @@ __global__ __launch_bounds__(256) void k_lora_down(DownJob ja, DownJob jb, int n
             const int sx = swizzle<S::XC>(li), sf = swizzle<S::FC>(li);  // (rows 16 further have the same)
             cur = cur + 1 == RING ? 0 : cur + 1;
             put = put + 1 == RING ? 0 : put + 1;
-            if (!rows) continue;
-            const bool tail = (s + 1) * S::KE > j.K;
+            // TAIL: the axis's last step, whose missing elements count as 0
+            auto multiply = [&](auto TAIL) {
 #pragma unroll
-            for (int m = 0; m < S::KE / 32; m++) {
-                const int c = 4 * m + lq;  // the chunk of eight elements
-                const bool in = !tail || s * S::KE + 8 * c < j.K;
-                u4v a[ACT == kActF32 ? 3 : 1];
-                if constexpr (ACT == kActF32) {
-                    const u4v u = x[(2 * c) ^ sx], v = x[(2 * c + 1) ^ sx];
-                    float e[8];
+                for (int m = 0; m < S::KE / 32; m++) {
+                    const int c = 4 * m + lq;  // the chunk of eight elements
+                    const bool in = !TAIL || s * S::KE + 8 * c < j.K;
+                    u4v a[ACT == kActF32 ? 3 : 1];
+                    if constexpr (ACT == kActF32) {
+                        const u4v u = x[(2 * c) ^ sx], v = x[(2 * c + 1) ^ sx];
+                        float e[8];
 #pragma unroll
-                    for (int q = 0; q < 4; q++) {
-                        e[q] = in ? __uint_as_float(u[q]) : 0.0f;
-                        e[4 + q] = in ? __uint_as_float(v[q]) : 0.0f;
+                        for (int q = 0; q < 4; q++) {
+                            e[q] = in ? __uint_as_float(u[q]) : 0.0f;
+                            e[4 + q] = in ? __uint_as_float(v[q]) : 0.0f;
+                        }
+                        parts8<3>(e, a);
+                    } else {
+                        a[0] = x[c ^ sx];
+#pragma unroll
+                        for (int q = 0; q < 4; q++) a[0][q] = in ? a[0][q] : 0u;
                     }
-                    parts8<3>(e, a);
-                } else {
-                    a[0] = x[c ^ sx];
 #pragma unroll
-                    for (int q = 0; q < 4; q++) a[0][q] = in ? a[0][q] : 0u;
-                }
-#pragma unroll
-                for (int i = 0; i < RB; i++) {
-                    u4v w = f[16 * i * S::FC + (c ^ sf)];
-                    if (tail)
+                    for (int i = 0; i < RB; i++) {
+                        u4v w = f[16 * i * S::FC + (c ^ sf)];
 #pragma unroll
                         for (int q = 0; q < 4; q++) w[q] = in ? w[q] : 0u;
-                    if constexpr (ACT == kActF32) {
+                        if constexpr (ACT == kActF32) {
 #pragma unroll
-                        for (int q = 2; q >= 0; q--) acc[i] = mma_bf16(a[q], w, acc[i]);
-                    } else if constexpr (ACT == kActBf16) {
-                        acc[i] = mma_bf16(a[0], w, acc[i]);
-                    } else {
-                        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8v, a[0]),
-                                                                        __builtin_bit_cast(h8v, w), acc[i], 0, 0, 0);
+                            for (int q = 2; q >= 0; q--) acc[i] = mma_bf16(a[q], w, acc[i]);
+                        } else if constexpr (ACT == kActBf16) {
+                            acc[i] = mma_bf16(a[0], w, acc[i]);
+                        } else {
+                            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8v, a[0]),
+                                                                            __builtin_bit_cast(h8v, w), acc[i], 0, 0, 0);
+                        }
                     }
                 }
-            }
+            };
+            if (rows && (s + 1) * S::KE <= j.K) multiply(std::false_type());
+            else if (rows) multiply(std::true_type());
         }
         ring_barrier<0>();  // nothing is on its way into LDS any more, nobody reads the ring
     }
