@@ -24,11 +24,16 @@ namespace moe {
 
 namespace {
 
-constexpr int kTM = 128, kTN = 128, kTK = 32;  // tile of the products (fp32 form; pair form: see k_rg_pair)
+constexpr int kTM = 64, kTN = 64, kTK = 32;  // tile of the products in fp32 form
+constexpr int kPairCols = 128;                 // columns of a tile in pair form
 constexpr int kMaxPart = 1024;                 // rows of a part of a product's long axis
 
 // Multiplications (T E H) from which the products run by pairs of fp16 parts.
-constexpr int64_t kPairFrom = (int64_t)1 << 24;
+// The parts cost a fixed 25 us or so (their panels written and read, two more
+// launches): all kernels together, fp32 against pairs, E = 512, H = 2560:
+// T = 64 18 against 33 us, 311 33 against 40, 700 50 against 44, 1200 98
+// against 65, 2451 157 against 89; E = 384, H = 4096, T = 311: 32 against 40.
+constexpr int64_t kPairFrom = (int64_t)1 << 29;
 
 typedef _Float16 h2v __attribute__((ext_vector_type(2)));
 typedef _Float16 h8v __attribute__((ext_vector_type(8)));
@@ -48,12 +53,15 @@ struct RgPlan {
 RgPlan rg_plan(int H, int E, int T) {
     RgPlan p = {};
     p.Ep = (E + kTK - 1) / kTK * kTK;
-    p.nt = (H + kTN - 1) / kTN;
     if ((int64_t)T * E * H >= kPairFrom) {
+        p.nt = H / kPairCols;
         // 256-row tiles read less per product; 128-row ones where the larger
-        // would leave compute units idle
+        // would leave compute units idle (E = 512, H = 2560: 240 larger tiles
+        // 62 us against 52 for T = 2451, 360 larger ones 71 against 78 for T = 4096)
         const int64_t large = ((int64_t)(T + 255) / 256 + (E + 255) / 256) * p.nt;
-        p.BM = large >= 512 ? 256 : 128;
+        p.BM = large >= 320 ? 256 : 128;
+    } else {
+        p.nt = H / kTN;
     }
     const int tm = p.BM ? p.BM : kTM;
     p.mt = (T + tm - 1) / tm;
@@ -158,13 +166,6 @@ __global__ __launch_bounds__(256) void k_rg_logits(const float* __restrict__ din
     }
 }
 
-// One tile of C[M][H] = A B over [k0, k1). A(m, k) is G[m][k] (dx: KMAJ
-// false) or G[k][m] (dWr: KMAJ true); B rows are rows of Wr (dx) or x (dWr).
-// Both operands go through LDS as [k][m] and [k][n]. In every wave lane
-// (i = lane % 16, q = lane / 16) reads 4 consecutive m (n) of row k + q in
-// one 16-byte read: MFMA (a, b) then covers the rows 4 i + a and columns
-// 4 i + b of the wave's 64 x 64 square, and a lane ends with 4 consecutive
-// columns of each of its rows.
 struct RgArgs {
     const float* G;
     int Ep;
@@ -177,7 +178,17 @@ struct RgArgs {
     int sx, sw, kx, kw, mt, nt, et, nx;  // nx: workgroups of dx
 };
 
+// One 64 x 64 tile of C[M][H] = A B over [k0, k1). A(m, k) is G[m][k] (dx: KMAJ
+// false) or G[k][m] (dWr: KMAJ true); B rows are rows of Wr (dx) or x (dWr).
+// Both operands go through LDS as [k][m] and [k][n], two steps of 32 k in turn.
+// In every wave lane (i = lane % 16, q = lane / 16) reads 2 consecutive m (n) of
+// row k + q at once: MFMA (a, b) then covers the rows 2 i + a and columns 2 i +
+// b of the wave's 32 x 32 square. Small tiles: what runs in this form has few
+// of them, and splitting the sums instead costs their parts' traffic. Bound by
+// latency at few tokens (8 us at T = 1), then by the fp32 matrix rate: 311 x 384
+// x 4096 27 us, 73 TFLOP/s; 2451 x 512 x 2560 (not run so) 146 us, 88 TFLOP/s.
 constexpr int kLdsRow = kTM + 4;
+constexpr int kLdsStep = 2 * kTK * kLdsRow;
 
 template <bool KMAJ>
 __device__ __forceinline__ void rg_tile(const RgArgs& a, int tile, int part, float* lds) {
@@ -186,84 +197,100 @@ __device__ __forceinline__ void rg_tile(const RgArgs& a, int tile, int part, flo
     const int klen = KMAJ ? a.T : a.E;              // length of the sum
     const int m0 = tile / a.nt * kTM, n0 = tile % a.nt * kTN;
     const int per = KMAJ ? a.kw : a.kx;
-    const int k0 = part * per, k1 = min(klen, k0 + per);
+    const int k0 = part * per, k1 = max(k0, min(klen, k0 + per)), len = k1 - k0;
     const float* B = KMAJ ? a.x : a.Wr;
-    const uint8_t* mask = KMAJ ? a.mask : nullptr;
-    float* As = lds;
-    float* Bs = lds + kTK * kLdsRow;
-    const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64, li = lane & 15, lq = lane >> 4;
-    f4v acc[4][4];
+    const bool masked = KMAJ && a.mask;
+    const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32, li = lane & 15, lq = lane >> 4;
+    f4v acc[2][2];
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < 2; i++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) acc[i][j] = f4v{0.f, 0.f, 0.f, 0.f};
-    const f4v zero = {0.f, 0.f, 0.f, 0.f};
-    f4v ra[4], rb[4];
-    auto fetch = [&](int k) {
+        for (int j = 0; j < 2; j++) acc[i][j] = f4v{0.f, 0.f, 0.f, 0.f};
+    // Loads through buffer resources over this part's rows: what lies behind
+    // them reads 0 and no load waits for a branch. (H is a multiple of 64, G's
+    // rows are padded to whole steps.)
+    const rsrc_t rB = make_rsrc(B + (size_t)k0 * a.H, (uint32_t)len * (uint32_t)a.H * 4u);
+    const rsrc_t rA = KMAJ ? make_rsrc(a.G + (size_t)k0 * a.Ep, (uint32_t)len * (uint32_t)a.Ep * 4u)
+                           : make_rsrc(a.G + (size_t)m0 * a.Ep, (uint32_t)min(kTM, M - m0) * (uint32_t)a.Ep * 4u);
+    const rsrc_t rm = make_rsrc(masked ? a.mask + k0 : nullptr, masked ? (uint32_t)len : 0u);
+    const int br = tid / 16, bc = tid % 16 * 4;  // B (and A by rows of k): rows br + 16 i, columns bc
+    const int ar = tid / 8, ac = tid % 8 * 4;    // A by rows of m: rows ar + 32 i, columns ac
+    const uint32_t oa = KMAJ ? (m0 + bc < a.Ep ? (uint32_t)(m0 + bc) * 4u : kOOB) : (uint32_t)(ar * a.Ep + ac) * 4u;
+    f4v ra[2], rb[2];
+    uint32_t keep[2];
+    auto fetch = [&](int k) {  // k from the part's start
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int p = tid + 256 * i;
-            // B: 32 float4 per row of 128
-            const int kr = k + p / 32, n = n0 + p % 32 * 4;
-            rb[i] = kr < k1 && n < a.H && (!mask || mask[kr])
-                        ? *reinterpret_cast<const f4v*>(B + (size_t)kr * a.H + n)
-                        : zero;
-            if (KMAJ) {  // G rows are tokens: 32 float4 per row of 128 experts
-                const int m = m0 + p % 32 * 4;
-                ra[i] = kr < k1 && m < a.Ep ? *reinterpret_cast<const f4v*>(a.G + (size_t)kr * a.Ep + m) : zero;
-            } else {     // 8 float4 per row of 32 experts
-                const int m = m0 + p / 8, kk = k + p % 8 * 4;
-                ra[i] = m < M && kk < a.Ep ? *reinterpret_cast<const f4v*>(a.G + (size_t)m * a.Ep + kk) : zero;
+        for (int i = 0; i < 2; i++) {
+            const uint32_t row = (uint32_t)(k + br + 16 * i);
+            rb[i] = __builtin_bit_cast(f4v, __builtin_amdgcn_raw_buffer_load_b128(
+                                                rB, row * (uint32_t)a.H * 4u + (uint32_t)(n0 + bc) * 4u, 0, 0));
+            keep[i] = masked ? ld_b8(rm, row) : 1u;
+            const uint32_t q = KMAJ ? row * (uint32_t)a.Ep * 4u + oa
+                                    : oa + (uint32_t)(32 * i * a.Ep + k0 + k) * 4u;
+            ra[i] = __builtin_bit_cast(f4v, __builtin_amdgcn_raw_buffer_load_b128(rA, q, 0, 0));
+        }
+    };
+    auto put = [&](float* As) {
+        float* Bs = As + kTK * kLdsRow;
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+#pragma unroll
+            for (int j = 0; j < 4; j++) rb[i][j] = keep[i] ? rb[i][j] : 0.0f;
+            *reinterpret_cast<f4v*>(Bs + (br + 16 * i) * kLdsRow + bc) = rb[i];
+            if (KMAJ) {
+                *reinterpret_cast<f4v*>(As + (br + 16 * i) * kLdsRow + bc) = ra[i];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; j++) As[(ac + j) * kLdsRow + ar + 32 * i] = ra[i][j];
             }
         }
     };
-    fetch(k0);
-    for (int k = k0; k < k1; k += kTK) {
-        __syncthreads();
+    if (len > 0) {
+        fetch(0);
+        put(lds);
+        if (kTK < len) fetch(kTK);
+        int cur = 0;
+        for (int k = 0; k < len; k += kTK, cur ^= 1) {
+            __syncthreads();  // step k is in LDS, and everybody is done with the step before
+            const float *As = lds + cur * kLdsStep, *Bs = As + kTK * kLdsRow;
+            if (k + kTK < len) put(lds + (cur ^ 1) * kLdsStep);
+            if (k + 2 * kTK < len) fetch(k + 2 * kTK);
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int p = tid + 256 * i;
-            *reinterpret_cast<f4v*>(Bs + p / 32 * kLdsRow + p % 32 * 4) = rb[i];
-            if (KMAJ) {
-                *reinterpret_cast<f4v*>(As + p / 32 * kLdsRow + p % 32 * 4) = ra[i];
-            } else {
+            for (int kk = 0; kk < kTK; kk += 4) {
+                const f2v fa = *reinterpret_cast<const f2v*>(As + (kk + lq) * kLdsRow + wm + 2 * li);
+                const f2v fb = *reinterpret_cast<const f2v*>(Bs + (kk + lq) * kLdsRow + wn + 2 * li);
 #pragma unroll
-                for (int j = 0; j < 4; j++) As[(p % 8 * 4 + j) * kLdsRow + p / 8] = ra[i][j];
+                for (int i = 0; i < 2; i++)
+#pragma unroll
+                    for (int j = 0; j < 2; j++)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[i], fb[j], acc[i][j], 0, 0, 0);
             }
-        }
-        __syncthreads();
-        if (k + kTK < k1) fetch(k + kTK);
-#pragma unroll
-        for (int kk = 0; kk < kTK; kk += 4) {
-            const f4v fa = *reinterpret_cast<const f4v*>(As + (kk + lq) * kLdsRow + wm + 4 * li);
-            const f4v fb = *reinterpret_cast<const f4v*>(Bs + (kk + lq) * kLdsRow + wn + 4 * li);
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-#pragma unroll
-                for (int j = 0; j < 4; j++)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[i], fb[j], acc[i][j], 0, 0, 0);
         }
     }
     const int parts = KMAJ ? a.sw : a.sx;
     float* C = (KMAJ ? a.dWr : a.dx) + (parts > 1 ? (size_t)part * M * a.H : 0);
     const bool add = parts == 1 && (KMAJ ? a.acc_w : a.acc_x);
-    const int n = n0 + wn + 4 * li;
+    const int n = n0 + wn + 2 * li;
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < 2; i++)
 #pragma unroll
         for (int q = 0; q < 4; q++) {
-            const int m = m0 + wm + 4 * (lq * 4 + q) + i;
-            if (m < M && n < a.H) {
-                f4v* c = reinterpret_cast<f4v*>(C + (size_t)m * a.H + n);
-                f4v v = {acc[i][0][q], acc[i][1][q], acc[i][2][q], acc[i][3][q]};
-                if (add) v += *c;
+            const int m = m0 + wm + 2 * (lq * 4 + q) + i;
+            if (m < M) {
+                f2v* c = reinterpret_cast<f2v*>(C + (size_t)m * a.H + n);
+                f2v v = {acc[i][0][q], acc[i][1][q]};
+                if (add) {
+                    const f2v o = *c;
+                    v.x += o.x;
+                    v.y += o.y;
+                }
                 *c = v;
             }
         }
 }
 
 __global__ __launch_bounds__(256) void k_rg_gemm(RgArgs a) {
-    __shared__ __align__(16) float lds[2 * kTK * kLdsRow];
+    __shared__ __align__(16) float lds[2 * kLdsStep];
     const int b = blockIdx.x;
     if (b < a.nx)
         rg_tile<false>(a, b % (a.mt * a.nt), b / (a.mt * a.nt), lds);

@@ -134,7 +134,7 @@ def route_backward(x, Wr, idx, w, dw, mask, din, T, E, k):
         off = ~mask
         G[off], eG[off] = 0.0, 0.0
     out = {"dlogits": (G, eG + 2.0 ** -140)}
-    pairs = Wr is not None and T * E * Wr.shape[1] >= 1 << 24  # the sizes that multiply pairs of fp16 parts
+    pairs = Wr is not None and T * E * Wr.shape[1] >= 1 << 29  # the sizes that multiply pairs of fp16 parts
     if Wr is not None:
         v, e = mm(G, cpu64(Wr), ea=eG, pairs=pairs)
         out["dx"] = (v, e + 2.0 ** -140)

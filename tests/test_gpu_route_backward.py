@@ -60,7 +60,8 @@ class Case:
 @pytest.mark.parametrize("T,E,k,H", [(1, 1, 1, 256), (1, 512, 10, 2560), (2, 5, 5, 256), (17, 384, 6, 4096), (33, 33, 3, 512),
                                      (64, 64, 8, 768), (127, 129, 2, 256), (129, 130, 32, 1280), (311, 384, 6, 512),
                                      (600, 512, 10, 256), (70, 1023, 7, 256), (40, 1024, 32, 8192), (5000, 9, 2, 256),
-                                     (1100, 513, 10, 2560), (33, 260, 6, 4096), (4100, 130, 4, 1280), (40000, 20, 3, 256)])
+                                     (1100, 513, 10, 2560), (33, 260, 6, 4096), (4100, 130, 4, 1280), (40000, 20, 3, 256),
+                                     (70, 1023, 7, 8192), (100000, 33, 3, 256), (4100, 300, 4, 2560), (600, 1024, 9, 1024)])
 def test_shapes(m, T, E, k, H):
     c = Case(m, T, E, k, H)
     c.check(c.run())
@@ -85,8 +86,9 @@ def test_norm_of_the_error(m):
         assert off <= 4 * (K ** 0.5 * ref.EPS + 3 ** 0.5 * 2.0 ** -22), (name, off)
 
 
-def test_masked_rows_hold_anything(m):
-    a, b = Case(m, 200, 96, 5, 512, 0.4), Case(m, 200, 96, 5, 512, 0.4)
+@pytest.mark.parametrize("T,H", [(200, 512), (2300, 2560)])
+def test_masked_rows_hold_anything(m, T, H):
+    a, b = Case(m, T, 96, 5, H, 0.4), Case(m, T, 96, 5, H, 0.4)
     off = (~b.mask).nonzero()[:, 0]
     b.x[off] = float("nan")
     b.dw[off] = float("inf")
@@ -100,9 +102,10 @@ def test_masked_rows_hold_anything(m):
     assert not x["dx"][off.cuda()].any()
 
 
-def test_all_masked(m):
-    c = Case(m, 30, 24, 3, 256)
-    c.mask = torch.zeros(30, dtype=torch.bool)
+@pytest.mark.parametrize("T,E,H", [(30, 24, 256), (1100, 130, 4096)])
+def test_all_masked(m, T, E, H):
+    c = Case(m, T, E, 3, H)
+    c.mask = torch.zeros(T, dtype=torch.bool)
     out = c.run()
     assert all(not v.any() for v in out.values())
 
@@ -130,7 +133,7 @@ def test_bad_expert(m, bad):
     c.check(c.run(dw=False), dw=False)
 
 
-@pytest.mark.parametrize("T,H", [(30, 256), (700, 1024), (9000, 256)])
+@pytest.mark.parametrize("T,H", [(30, 256), (700, 1024), (9000, 256), (9000, 2560)])
 def test_accumulate(m, T, H):
     c = Case(m, T, 40, 4, H)
     g = torch.Generator().manual_seed(1)
@@ -145,8 +148,9 @@ def test_accumulate(m, T, H):
             ref.close(out[name], v, e, name)
 
 
-def test_in_place_on_dlogits(m):
-    c = Case(m, 90, 60, 4, 512, 0.2)
+@pytest.mark.parametrize("T,E,H", [(90, 60, 512), (1100, 513, 1024)])
+def test_in_place_on_dlogits(m, T, E, H):
+    c = Case(m, T, E, 4, H, 0.2)
     a, b = c.run(), c.run(inplace=True)
     for name in a:
         assert torch.equal(a[name], b[name]), name
@@ -177,7 +181,7 @@ def test_against_autograd(m):
         ref.close(out[name], g, want[name][1] + more, name)
 
 
-@pytest.mark.parametrize("T,H", [(150, 512), (700, 1024)])
+@pytest.mark.parametrize("T,H", [(150, 512), (700, 1024), (1500, 4096)])
 @pytest.mark.parametrize("far", [30, 110])
 def test_large_and_small_values(m, T, H, far):
     """Tokens, experts and columns of very unlike sizes keep their relative
@@ -194,13 +198,14 @@ def test_large_and_small_values(m, T, H, far):
     c.check(c.run(dw=False, dx=False), dw=False)
 
 
-def test_zero_rows_and_columns(m):
-    c = Case(m, 700, 96, 5, 1024)
+@pytest.mark.parametrize("T,H", [(700, 1024), (1500, 4096)])
+def test_zero_rows_and_columns(m, T, H):
+    c = Case(m, T, 96, 5, H)
     c.din[3:200], c.din[:, 7], c.Wr[:, 100:300], c.Wr[9], c.x[:, 5] = 0.0, 0.0, 0.0, 0.0, 0.0
     c.check(c.run(dw=False), dw=False)
 
 
-@pytest.mark.parametrize("T,H", [(40, 256), (700, 1024)])
+@pytest.mark.parametrize("T,H", [(40, 256), (700, 1024), (4100, 4096)])
 def test_infinite_and_nan_values(m, T, H):
     c = Case(m, T, 33, 3, H)
     c.din[5, 3] = float("inf")
@@ -215,8 +220,9 @@ def test_infinite_and_nan_values(m, T, H):
     assert not torch.isfinite(out["dWr"][3]).any() and torch.isnan(out["dWr"][8]).all()
 
 
-def test_repeats_streams_and_graphs(m):
-    a, b = Case(m, 700, 130, 6, 512, 0.1), Case(m, 300, 256, 8, 256)
+@pytest.mark.parametrize("T,E,H", [(700, 130, 512), (1100, 513, 1024)])
+def test_repeats_streams_and_graphs(m, T, E, H):
+    a, b = Case(m, T, E, 6, H, 0.1), Case(m, 300, 256, 8, 256)
     want = []
     graphs = []
     ws = torch.zeros(max(m.moe_route_backward_workspace_bytes(m.desc(c.H, 64, c.E, c.k, "nvfp4"), c.T) for c in (a, b)),
