@@ -66,12 +66,15 @@ BalWs bal_ws(int T, int E, int S) {
         return at;
     };
     const size_t row = (size_t)E * 4;
+    // Sized so that fewer tokens never need more: JM and chunks fall where the
+    // parts or the tokens of a chunk grow.
+    const size_t jm = b.J < kMaxParts ? b.J : kMaxParts, most = T < 4096 ? ((size_t)T + 3) / 4 : 1024;
     b.part = take(b.J > b.JM ? (size_t)S * b.J * (row + 4) : 0);
-    b.cnt = take((size_t)S * b.JM * row);
-    b.n = take((size_t)S * b.JM * 4);
+    b.cnt = take((size_t)S * jm * row);
+    b.n = take((size_t)S * jm * 4);
     b.ticket = take(4);
-    b.psum = take(((size_t)b.chunks + S) * row);
-    b.zsum = take(((size_t)b.chunks + S) * 4);
+    b.psum = take((most + S) * row);
+    b.zsum = take((most + S) * 4);
     b.q = take((size_t)S * (((size_t)E + 15) / 16 + 1) * 4);
     b.total = o;
     return b;

@@ -114,9 +114,15 @@ __device__ __forceinline__ float dot8(const typename Act<ACT>::T* x, u4v w, floa
 }
 
 // The rank of adapter a, or -1 where the table's rank is not in [0, R].
-__device__ __forceinline__ int rank_of(const int32_t* __restrict__ ranks, int a, int R) {
-    const int r = ranks[a];
+__device__ __forceinline__ int table_rank(const LoraTable& tab, int a, int R) {
+    const int r = tab.ranks[a];
     return r < 0 || r > R ? -1 : r;
+}
+// The same, -1 also where a factor that it needs is NULL.
+__device__ __forceinline__ int rank_of(const LoraTable& tab, int a, int R) {
+    const int r = table_rank(tab, a, R);
+    const bool none = (tab.a[a] == nullptr) | (tab.b[a] == nullptr);
+    return r > 0 && none ? -1 : r;
 }
 
 // ---------------------------------------------------------------------------
@@ -129,7 +135,7 @@ __global__ __launch_bounds__(256) void k_lora_down_tok(const typename Act<ACT>::
     const int lane = threadIdx.x & 63, t = blockIdx.x, i = blockIdx.y * 4 + wave_id();
     const int a = tab.ids[t];
     if (a < 0 || a >= n) return;
-    const int r = rank_of(tab.ranks, a, R);
+    const int r = rank_of(tab, a, R);
     if (i >= r) return;
     const uint16_t* row = reinterpret_cast<const uint16_t*>(tab.a[a]) + (size_t)i * K;
     const typename Act<ACT>::T* xt = x + (size_t)t * ldx;
@@ -151,7 +157,7 @@ __global__ __launch_bounds__(256) void k_lora_up_tok(const float* __restrict__ u
     f4v v = {0.f, 0.f, 0.f, 0.f};
     if (base) v = ld4<ACT>(base + (size_t)t * ldb + c);
     if (a >= 0) {
-        const int r = a < n ? rank_of(tab.ranks, a, R) : -1;
+        const int r = a < n ? rank_of(tab, a, R) : -1;
         if (r < 0) {
             v.x = v.y = v.z = v.w = __builtin_nanf("");
         } else {
@@ -192,7 +198,7 @@ __global__ __launch_bounds__(1024) void k_lora_tok(const typename Act<ACT>::T* _
     const int a = tab.ids[t];
     f4v v = {0.f, 0.f, 0.f, 0.f};
     if (mine && base) v = ld4<ACT>(base + (size_t)t * ldb + c);
-    const int r = a < 0 ? 0 : (a < n ? rank_of(tab.ranks, a, R) : -1);
+    const int r = a < 0 ? 0 : (a < n ? rank_of(tab, a, R) : -1);
     if (r > 0) {
         const rsrc_t rb = make_rsrc(tab.b[a], (uint32_t)r * (uint32_t)N * 2u);  // rows behind the rank read 0
         const rsrc_t ra = make_rsrc(tab.a[a], (uint32_t)r * (uint32_t)K * 2u);
@@ -279,6 +285,10 @@ LoraWs lora_ws(int K, int N, int n, int R, int T, bool backward) {
     const int64_t piece = ((int64_t)T * (col_blocks(K) + col_blocks(N)) / 512 + kTile - 1) / kTile * kTile;
     w.piece = (int)(piece < 2 * kTile ? 2 * kTile : (piece > 4096 ? 4096 : piece));
     w.pslots = T / w.piece + n + 3;
+    // T / piece at most (512 / 128 (128 + 1) because the quotient is rounded
+    // down), growing with T: fewer tokens never need more workspace
+    const int in128 = T / 128, in512 = 516 / (col_blocks(K) + col_blocks(N)), least = in128 < in512 ? in128 : in512;
+    const size_t pslots = (size_t)(T / 4096 > least ? T / 4096 : least) + n + 3;
     // parts of the long axes of "down": two workgroups per compute unit in all
     // (what runs at once), shared out by the sides' lengths, at most 8 parts of
     // a side, of four steps of 128 at least
@@ -305,15 +315,18 @@ LoraWs lora_ws(int K, int N, int n, int R, int T, bool backward) {
     w.perm = take((size_t)T * 4);
     w.groups = take((size_t)(n + 2) * sizeof(Group));
     w.tiles = take((size_t)w.slots * sizeof(Slot));
-    w.pieces = take(backward ? (size_t)w.pslots * sizeof(Slot) : 0);
+    w.pieces = take(backward ? pslots * sizeof(Slot) : 0);
     w.tickets = take((size_t)w.slots * 2 * 4);
-    w.part = take((size_t)((w.ku > 1 ? w.ku : 0) + (w.kv > 1 ? w.kv : 0)) * T * w.R16 * 4);
+    // parts x tokens: 8 of a side at most, and 512 / (T / 64) rounded up by no
+    // more than a third
+    const size_t rows = (size_t)T * (backward ? 16 : 8), most = 512 * kTile * 4 / 3 + 1;
+    w.part = take((rows < most ? rows : most) * w.R16 * 4);
     const size_t by_token = (size_t)T * w.R32 * 6, by_rank = (size_t)w.slots * w.R16 * kTile * 6;
     w.ut = take(backward ? 0 : by_token);
     w.vt = take(backward ? by_token : 0);
     w.ur = take(backward ? by_rank : 0);
     w.vr = take(backward ? by_rank : 0);
-    w.grad = take(backward ? (size_t)w.pslots * w.R16 * ((size_t)K + N) * 4 : 0);
+    w.grad = take(backward ? pslots * w.R16 * ((size_t)K + N) * 4 : 0);
     w.total = o;
     return w;
 }
@@ -497,7 +510,7 @@ __device__ __forceinline__ void ring_barrier() {
 // order. Out go the bf16 parts of the scaled values.
 template <int ACT, int RB>
 __global__ __launch_bounds__(256) void k_lora_down(DownJob ja, DownJob jb, int n, int R,
-                                                   const int32_t* __restrict__ ranks, const float* __restrict__ scales,
+                                                   LoraTable tab,
                                                    const int32_t* __restrict__ perm, const Slot* __restrict__ tiles,
                                                    int T, uint32_t* __restrict__ tickets) {
     typedef DownStep<ACT, RB> S;
@@ -513,7 +526,7 @@ __global__ __launch_bounds__(256) void k_lora_down(DownJob ja, DownJob jb, int n
     const bool second = (int)blockIdx.y >= ja.ks;
     const DownJob j = second ? jb : ja;
     const int ks = j.ks, ky = (int)blockIdx.y - (second ? ja.ks : 0);
-    const int r = rank_of(ranks, sl.g, R);
+    const int r = rank_of(tab, sl.g, R);
     if (r < 0) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), li = lane & 15, lq = lane >> 4;
     const int steps = (j.K + S::KE - 1) / S::KE;
@@ -656,7 +669,7 @@ __global__ __launch_bounds__(256) void k_lora_down(DownJob ja, DownJob jb, int n
             for (int q = 0; q < 4; q++) red[cell(i) / R16][cell(i) % R16 + q] = sum[i][q];
         __syncthreads();
     }
-    const float sc = scales[sl.g];
+    const float sc = tab.scales[sl.g];
     if (j.by_token)
         for (int i = tid; i < sl.rows * CH; i += 256) {
             const int p = i / CH, c = i % CH;
@@ -744,7 +757,7 @@ __device__ __forceinline__ f4v mma_parts(const u4v (&a)[3], const u4v (&b)[PB], 
 template <int ACT, int RB>
 __global__ __launch_bounds__(256) void k_lora_up(const u4v* __restrict__ u, int T, int N, int n, int R,
                                                  const void* const* __restrict__ fac,
-                                                 const int32_t* __restrict__ ranks, const int32_t* __restrict__ perm,
+                                                 LoraTable tab, const int32_t* __restrict__ perm,
                                                  const Slot* __restrict__ tiles, const typename Act<ACT>::T* base,
                                                  size_t ldb, typename Act<ACT>::T* y, size_t ldy) {
     constexpr int R32 = RB < 2 ? 32 : RB * 16, CH = R32 / 8;
@@ -770,7 +783,7 @@ __global__ __launch_bounds__(256) void k_lora_up(const u4v* __restrict__ u, int 
 #pragma unroll
             for (int q = 0; q < 4; q++) old[b][q] = *reinterpret_cast<const wv*>(base + (size_t)t[b][q] * ldb + cl);
     }
-    const int r = none ? 0 : (sl.g == n ? -1 : rank_of(ranks, sl.g, R));
+    const int r = none ? 0 : (sl.g == n ? -1 : rank_of(tab, sl.g, R));
     constexpr int NG = R32 / 32, P = Cols16<F16>::P;
     u4v f[NG][P][4];
     u4v a[NG][3];
@@ -859,7 +872,7 @@ struct GradSide {
 // writes its gradient, others the piece's part for k_lora_grad_reduce.
 template <int ACT, int RB>
 __global__ __launch_bounds__(256) void k_lora_grad(GradSide ga, GradSide gb, int n, int R, int piece,
-                                                   const int32_t* __restrict__ ranks, const int32_t* __restrict__ perm,
+                                                   LoraTable tab, const int32_t* __restrict__ perm,
                                                    const Group* __restrict__ groups, const Slot* __restrict__ pieces,
                                                    int accumulate, float* __restrict__ part) {
     constexpr int R16 = RB * 16, TILE = 3 * R16 * 8;  // chunks of a tile's low values
@@ -868,7 +881,7 @@ __global__ __launch_bounds__(256) void k_lora_grad(GradSide ga, GradSide gb, int
     __shared__ u4v us[2 * TILE];
     const Slot sl = pieces[blockIdx.y];
     if (sl.rows == 0 || sl.g >= n) return;
-    const int r = rank_of(ranks, sl.g, R);
+    const int r = rank_of(tab, sl.g, R);
     if (r <= 0) return;
     const int nba = (ga.cols + kUpCols - 1) / kUpCols;
     const bool second = (int)blockIdx.x >= nba;
@@ -985,12 +998,12 @@ __global__ __launch_bounds__(256) void k_lora_grad(GradSide ga, GradSide gb, int
 // (zeros) and with several pieces (the parts, in increasing order); an
 // adapter whose rank is not usable gets nothing.
 __global__ __launch_bounds__(256) void k_lora_grad_reduce(int ca, int cb, float* const* da, float* const* db, int n,
-                                                          int R, int R16, int piece, const int32_t* __restrict__ ranks,
+                                                          int R, int R16, int piece, LoraTable tab,
                                                           const Group* __restrict__ groups, int accumulate,
                                                           const float* __restrict__ part) {
     const int a = blockIdx.z, m = blockIdx.y;
     const Group g = groups[a];
-    const int r = rank_of(ranks, a, R);
+    const int r = g.rows ? rank_of(tab, a, R) : table_rank(tab, a, R);  // without tokens there may be no factors
     if (m >= r) return;
     if (g.rows == 0 ? accumulate != 0 : g.rows <= piece) return;
     const int nba = (ca + 1023) / 1024;
@@ -1016,7 +1029,7 @@ hipError_t down(const LoraWs& w, int sides, hipStream_t s, const DownJob& a, con
                 const LoraTable& tab, const int32_t* perm, const Slot* tiles, int T, uint32_t* tickets) {
     const dim3 grid(w.slots, a.ks + (sides > 1 ? b.ks : 0));
 #define DN(B)                                                                                                       \
-    hipLaunchKernelGGL((k_lora_down<ACT, B>), grid, dim3(256), 0, s, a, b, n, R, tab.ranks, tab.scales, perm, tiles, T, \
+    hipLaunchKernelGGL((k_lora_down<ACT, B>), grid, dim3(256), 0, s, a, b, n, R, tab, perm, tiles, T, \
                        tickets)
     if (w.R16 == 16) DN(1); else if (w.R16 == 32) DN(2); else if (w.R16 == 64) DN(4); else DN(8);
 #undef DN
@@ -1030,7 +1043,7 @@ hipError_t up(const LoraWs& w, hipStream_t s, const u4v* u, int T, int N, int n,
     typedef typename Act<ACT>::T E;
     const dim3 grid(col_blocks(N), w.slots);
 #define UP(B)                                                                                                      \
-    hipLaunchKernelGGL((k_lora_up<ACT, B>), grid, dim3(256), 0, s, u, T, N, n, R, fac, tab.ranks, perm, tiles, (const E*)base, \
+    hipLaunchKernelGGL((k_lora_up<ACT, B>), grid, dim3(256), 0, s, u, T, N, n, R, fac, tab, perm, tiles, (const E*)base, \
                        ldb, (E*)y, ldy)
     if (w.R16 == 16) UP(1); else if (w.R16 == 32) UP(2); else if (w.R16 == 64) UP(4); else UP(8);
 #undef UP
@@ -1115,14 +1128,14 @@ hipError_t backward(int K, int N, int n, int R, const void* x, size_t ldx, const
         const GradSide ga = {m.vr, x, ldx, K, da}, gb = {m.ur, dy, lddy, N, db};
         const dim3 grid(col_blocks(K) + col_blocks(N), w.pslots);
 #define GR(B)                                                                                                       \
-    hipLaunchKernelGGL((k_lora_grad<ACT, B>), grid, dim3(256), 0, s, ga, gb, n, R, w.piece, tab.ranks, m.perm, m.groups, \
+    hipLaunchKernelGGL((k_lora_grad<ACT, B>), grid, dim3(256), 0, s, ga, gb, n, R, w.piece, tab, m.perm, m.groups, \
                        m.pieces, accumulate, m.grad)
         if (w.R16 == 16) GR(1); else if (w.R16 == 32) GR(2); else if (w.R16 == 64) GR(4); else GR(8);
 #undef GR
         if ((r = hipGetLastError()) != hipSuccess) return r;
     }
     hipLaunchKernelGGL(k_lora_grad_reduce, dim3((K + 1023) / 1024 + (N + 1023) / 1024, R, n), dim3(256), 0, s, K, N, da,
-                       db, n, R, w.R16, w.piece, tab.ranks, m.groups, accumulate, m.grad);
+                       db, n, R, w.R16, w.piece, tab, m.groups, accumulate, m.grad);
     return hipGetLastError();
 }
 

@@ -100,19 +100,30 @@ RgPlan rg_plan(int H, int E, int T) {
         o += align256(bytes);
         return at;
     };
+    // The regions grow with T, so that fewer tokens never need more (parts and
+    // tiles do not: a sum in fewer parts, a larger tile). Tokens x parts of dx:
+    // a sum is split only below 512 tiles x parts of 64 x 64, or 128 of 128 x
+    // 128, in parts of 64 at least; parts of dWr: likewise, or 1024 tokens each.
+    auto up = [](size_t a, size_t b) { return (a + b - 1) / b; };
+    const size_t tall = up(T, 1024) * 1024, ke = up(E, 64), most = ((size_t)1 << 21) / H;
+    const size_t px = ke > 1 ? (ke * T < most ? ke * T : most) : 0;
+    size_t pw = up(256, ke * (H / 64));
+    if ((1 << 14) / (up(E, 256) * H) > pw) pw = (1 << 14) / (up(E, 256) * H);
+    if (up(T, 1024) > pw) pw = up(T, 1024);
+    if (up(T, 64) < pw) pw = up(T, 64);
     p.g = take((size_t)T * p.Ep * 4);
     if (p.BM) {
         p.egr = take((size_t)T * 4);
-        p.egc = take((size_t)p.sw * p.Ep * 4);
-        p.ex = take((size_t)p.sw * H * 4);
-        p.ew = take((size_t)p.sx * H * 4);
-        p.ga = take((size_t)p.mt * p.BM * p.Ep * 4);
-        p.gt = take((size_t)p.sw * p.kw * p.et * p.BM * 4);
-        p.xb = take((size_t)p.sw * p.kw * H * 4);
-        p.wb = take((size_t)p.sx * p.kx * H * 4);
+        p.egc = take(pw * p.Ep * 4);
+        p.ex = take(pw * H * 4);
+        p.ew = take(ke * H * 4);
+        p.ga = take(up(T, 256) * 256 * p.Ep * 4);
+        p.gt = take(tall * up(E, 256) * 256 * 4);
+        p.xb = take(tall * H * 4);
+        p.wb = take(up(E, 1024) * 1024 * H * 4);
     }
-    p.px = take(p.sx > 1 ? (size_t)p.sx * T * H * 4 : 0);
-    p.pw = take(p.sw > 1 ? (size_t)p.sw * E * H * 4 : 0);
+    p.px = take(px * H * 4);
+    p.pw = take(pw > 1 ? pw * E * H * 4 : 0);
     p.total = o;
     return p;
 }

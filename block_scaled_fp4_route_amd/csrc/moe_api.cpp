@@ -432,6 +432,13 @@ int moe_route_backward(const moe_desc* d, const float* x, int32_t T, const float
         if (dlogits_out && (r = check_ptr(dlogits_out, 4, "dlogits_out"))) return r;
         if (dx && ((r = check_ptr(dx, 16, "dx")) || (r = check_ptr(Wr, 16, "Wr")))) return r;
         if (dWr && (r = check_ptr(x, 16, "x"))) return r;
+        // G, dx and dWr are written while the inputs are still read
+        const float* in[] = {x, Wr, w, dw, dlogits_in};
+        for (int i = 0; i < 5; i++)
+            if (in[i] && (in[i] == dx || in[i] == dWr || (in[i] == dlogits_out && in[i] != dlogits_in)))
+                return fail(MOE_ERR_ARG, "an output is an input");
+        if ((dx && dx == dWr) || (dlogits_out && (dlogits_out == dx || dlogits_out == dWr)))
+            return fail(MOE_ERR_ARG, "two outputs are the same");
     }
     if (dWr && (r = check_ptr(dWr, 16, "dWr"))) return r;
     if ((r = check_ws(ws, ws_bytes, moe::route_backward_ws_bytes(d->H, d->E, T)))) return r;
@@ -473,6 +480,7 @@ int moe_lora_backward(const moe_lora_desc* l, const void* x, int64_t ldx, const 
     if (T == 0 && !da_ptrs && !db_ptrs) return ok();
     if (da_ptrs && (r = check_ptr(da_ptrs, 8, "da_ptrs"))) return r;
     if (db_ptrs && (r = check_ptr(db_ptrs, 8, "db_ptrs"))) return r;
+    if (da_ptrs && da_ptrs == db_ptrs) return fail(MOE_ERR_ARG, "da_ptrs is db_ptrs");
     if (T > 0) {
         if ((r = check_rows(x, ldx, l->K, "x")) || (r = check_rows(dy, lddy, l->N, "dy")) ||
             (r = lora_table_checks(ids, a_ptrs, b_ptrs, ranks, scales)))

@@ -273,8 +273,9 @@ int moe_gemv_fp8(const uint8_t *W, const float *row_scale, const float *x, int32
  * gradient of the logits. A batch is T tokens in S sequences: sequence s
  * holds the tokens seq_off[s] <= t < seq_off[s + 1] with mask[t] != 0 (its
  * counted tokens, n_s of them); tokens before seq_off[0], behind seq_off[S]
- * or with mask[t] == 0 are not counted, and their values do not matter. With p_t = softmax(logits[t]) over all E, lse_t its log-sum-exp,
- * live = the sequences with n_s > 0 and N = sum n_s:
+ * or with mask[t] == 0 are not counted, and their values do not matter. With
+ * p_t = softmax(logits[t]) over all E, lse_t its log-sum-exp, live = the
+ * sequences with n_s > 0 and N = sum n_s:
  *   counts[s][e] = #{(t, j): t counted in s, idx[t][j] = e}
  *   probs[s][e]  = mean of p_t[e] over the counted tokens of s (0 if none)
  *   balance = 1/live sum_s E sum_e counts[s][e] / (n_s k) * probs[s][e]
@@ -297,8 +298,9 @@ int moe_gemv_fp8(const uint8_t *W, const float *row_scale, const float *x, int32
  *   dlogits [T][E] fp32 (out), 16-B aligned, or NULL; not logits itself
  * If seq_off decreases or leaves [0, T], or a counted token names an expert
  * outside [0, E), every fp32 output is NaN and every count -1. T = 0 gives
- * the loss 0 (logits, idx and dlogits are not used). Workspace:
- * moe_balance_workspace_bytes(d, T, S). Errors: MOE_ERR_ARG (descriptor,
+ * the loss 0 (logits, idx and dlogits are not used). Outputs overlap neither
+ * inputs nor each other. Workspace: moe_balance_workspace_bytes(d, T, S),
+ * which never falls as T grows. Errors: MOE_ERR_ARG (descriptor,
  * pointers, T < 0, S < 1, coefficients that are not finite);
  * MOE_ERR_UNSUPPORTED unless E <= 1024, k <= 32, S <= 65535 and T <= 2^24;
  * MOE_ERR_WORKSPACE. d->H, d->I and d->format only have to be valid. */
@@ -317,9 +319,15 @@ int moe_balance_loss(const moe_desc *d, const float *logits, int32_t T, const in
  *   ds[t][j] = w[t][j] * (dw[t][j] - sum_i w[t][i] dw[t][i])
  *   G[t][e]  = dlogits_in[t][e] + sum_{j: idx[t][j] = e} ds[t][j]
  *   dx = G Wr ([T][H]),  dWr = G^T x ([E][H])
- * Tokens with mask[t] == 0 have G = 0, and their values do not matter. A token with an index outside [0, E) (dw given) has G = NaN in its
- * whole row. fp32 operands, products and sums; results are bit-identical
- * from run to run.
+ * Tokens with mask[t] == 0 have G = 0, and their values do not matter. A token
+ * with an index outside [0, E) (dw given) has G = NaN in its whole row. Sums in
+ * fp32; results are bit-identical from run to run. Below 2^29 multiplications
+ * (T E H) the products have fp32 operands. From there on each operand is a
+ * pair of fp16 values under a power of two for its row or column, h + l with h
+ * = fp16(v), l = fp16(v - h), and the product of the two l is left out: off by
+ * at most 3 * 2^-22 of each product, and for values below 2^-17 of their row's
+ * (Wr, x: column's) largest by 2^-39 of that largest, whatever the exponents.
+ * An infinity or a NaN there makes every sum that it enters infinite or NaN.
  *   x [T][H], Wr [E][H] fp32, 16-B aligned (x may be NULL without dWr, Wr
  *   without dx);  idx [T][k] int32, w [T][k], dw [T][k] fp32 (dw NULL: only
  *   dlogits_in; idx and w are then not used);  mask [T] uint8 or NULL;
@@ -327,8 +335,10 @@ int moe_balance_loss(const moe_desc *d, const float *logits, int32_t T, const in
  *   dlogits_out [T][E] fp32 (out): G, or NULL; may be dlogits_in;
  *   dx [T][H], dWr [E][H] fp32 (out), 16-B aligned, or NULL
  *   accumulate  a sum of MOE_ACC_*
- * T = 0 writes zeros to dWr (unless it accumulates). Workspace:
- * moe_route_backward_workspace_bytes(d, T). Errors: MOE_ERR_ARG;
+ * Outputs overlap neither inputs nor each other, but for dlogits_out ==
+ * dlogits_in. T = 0 writes zeros to dWr (unless it accumulates). Workspace:
+ * moe_route_backward_workspace_bytes(d, T), which never falls as T grows.
+ * Errors: MOE_ERR_ARG (also where an output is an input or another output);
  * MOE_ERR_UNSUPPORTED unless moe_route supports the descriptor and
  * T <= 2^20; MOE_ERR_WORKSPACE. */
 size_t moe_route_backward_workspace_bytes(const moe_desc *d, int32_t T);
@@ -370,9 +380,10 @@ typedef struct moe_lora_desc {
  *         usual [N][r]), dense
  *   ranks [n] int32, 0 .. max_rank;  scales [n] fp32
  * A token whose id is n or more, or whose adapter's rank is not in
- * 0 .. max_rank, gets NaN in its row. Only rows of x whose tokens have an
- * adapter are read. T = 0 enqueues nothing. Workspace:
- * moe_lora_workspace_bytes(l, T, 0). Errors: MOE_ERR_ARG (descriptor: sizes
+ * 0 .. max_rank or has a NULL factor beside a rank above 0, gets NaN in its
+ * row. Only rows of x whose tokens have an adapter are read. T = 0 enqueues
+ * nothing. y overlaps no input, but for y == base. Workspace:
+ * moe_lora_workspace_bytes(l, T, 0), which never falls as T grows. Errors: MOE_ERR_ARG (descriptor: sizes
  * not positive, K or N not a multiple of 8, unknown dtype; pointers, strides,
  * T < 0); MOE_ERR_UNSUPPORTED unless K, N <= 65536, n <= 1024,
  * max_rank <= 128 and T <= 2^20; MOE_ERR_WORKSPACE. */
@@ -392,12 +403,14 @@ int moe_lora_apply(const moe_lora_desc *l, const void *x, int64_t ldx, int32_t T
  * aligned each, no two the same), or NULL; an entry that is NULL skips that
  * adapter's factor (an adapter that is served but not trained). An adapter
  * without tokens gets zeros. accumulate != 0 adds to dA and dB instead of
- * writing them. A token whose id is n or more, or whose adapter's rank is
- * not in 0 .. max_rank, gets NaN in its row of dx and enters no gradient; the
- * gradients of an adapter with such a rank are left as they are. Sums over
- * tokens run in a fixed order: results are bit-identical from run to run.
- * Workspace: moe_lora_workspace_bytes(l, T, 1). Errors as for
- * moe_lora_apply. */
+ * writing them. A token whose id is n or more, or whose adapter has no usable
+ * rank (not in 0 .. max_rank, or above 0 beside a NULL factor), gets NaN in
+ * its row of dx and enters no gradient; the gradients of an adapter with such
+ * a rank are left as they are (one without tokens may have NULL factors). Sums
+ * over tokens run in a fixed order: results are bit-identical from run to run.
+ * Outputs overlap neither inputs nor each other, but for dx == dx_base.
+ * Workspace: moe_lora_workspace_bytes(l, T, 1), which never falls as T grows.
+ * Errors as for moe_lora_apply. */
 int moe_lora_backward(const moe_lora_desc *l, const void *x, int64_t ldx, const void *dy, int64_t lddy, int32_t T,
                       const int32_t *ids, const void *const *a_ptrs, const void *const *b_ptrs, const int32_t *ranks,
                       const float *scales, const void *dx_base, int64_t lddx_base, void *dx, int64_t lddx,

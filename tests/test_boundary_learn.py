@@ -6,6 +6,7 @@ import block_scaled_fp4_route_amd as m
 
 FAKE = 1 << 20          # an aligned, never dereferenced address
 OTHER = 1 << 21
+THIRD = 3 << 20
 ODD = FAKE + 4          # misaligned for 16-byte arguments
 BIG = 1 << 42
 
@@ -54,7 +55,7 @@ def test_balance_errors():
 
 
 def route_backward(d=D, x=FAKE, T=100, Wr=FAKE, idx=FAKE, w=FAKE, dw=FAKE, mask=None, din=FAKE, dout=None, dx=OTHER,
-                   dWr=OTHER, acc=0, ws=FAKE, wsb=BIG):
+                   dWr=THIRD, acc=0, ws=FAKE, wsb=BIG):
     return status(m.moe_route_backward, d, x, T, Wr, idx, w, dw, mask, din, dout, dx, dWr, acc, ws, wsb, 0)
 
 
@@ -80,6 +81,35 @@ def test_route_backward_errors():
     assert need >= 100 * 512 * 4
     assert route_backward(ws=None, wsb=0) == m.MOE_ERR_WORKSPACE
     assert route_backward(wsb=need - 1) == m.MOE_ERR_WORKSPACE
+    # outputs that are inputs, or each other
+    own = dict(x=4 << 20, Wr=5 << 20, w=6 << 20, dw=7 << 20, din=8 << 20, dout=9 << 20)
+    assert route_backward(**own, wsb=0) == m.MOE_ERR_WORKSPACE
+    for out in ("dx", "dWr", "dout"):
+        for name in ("x", "Wr", "w", "dw", "din"):
+            if (out, name) != ("dout", "din"):
+                assert route_backward(**{**own, out: own[name]}) == m.MOE_ERR_ARG, (out, name)
+    assert route_backward(**{**own, "dout": own["din"]}, wsb=0) == m.MOE_ERR_WORKSPACE
+    assert route_backward(dx=THIRD) == m.MOE_ERR_ARG
+    assert route_backward(dout=OTHER) == m.MOE_ERR_ARG
+    assert route_backward(dout=THIRD) == m.MOE_ERR_ARG
+
+
+def test_fewer_tokens_never_need_more_workspace():
+    """A workspace made for the longest batch serves the shorter ones."""
+    Ts = [*range(0, 700), *range(700, 9000, 37), 8191, 8192, 8193, 16384, 32768, 40000, 1 << 17, 1 << 20]
+    Ts.sort()
+    for H, E in ((256, 8), (256, 1024), (1024, 64), (2560, 512), (4096, 384), (8192, 129)):
+        d = m.desc(H, 64, E, 4, "nvfp4")
+        sizes = [m.moe_route_backward_workspace_bytes(d, T) for T in Ts]
+        assert sizes == sorted(sizes), (H, E)
+        for S in (1, 7, 1000):
+            sizes = [m.moe_balance_workspace_bytes(d, T, S) for T in Ts]
+            assert sizes == sorted(sizes), (E, S)
+    for K, N in ((256, 256), (2560, 8192), (4096, 2880), (8192, 512)):
+        for n, R in ((1, 1), (4, 64), (8, 16), (300, 8), (2, 128)):
+            for back in (False, True):
+                sizes = [m.moe_lora_workspace_bytes(m.lora_desc(K, N, n, R, m.MOE_ACT_BF16), T, back) for T in Ts]
+                assert sizes == sorted(sizes), (K, N, n, R, back)
 
 
 L = m.lora_desc(2560, 8192, 4, 16, m.MOE_ACT_BF16)
@@ -122,7 +152,7 @@ def test_lora_errors():
 
 
 def lora_backward(l=L, x=FAKE, ldx=2560, dy=FAKE, lddy=8192, T=100, ids=FAKE, a=FAKE, b=FAKE, ranks=FAKE, scales=FAKE,
-                  dxb=None, lddxb=2560, dx=OTHER, lddx=2560, da=FAKE, db=FAKE, acc=0, ws=FAKE, wsb=BIG):
+                  dxb=None, lddxb=2560, dx=OTHER, lddx=2560, da=FAKE, db=OTHER, acc=0, ws=FAKE, wsb=BIG):
     return status(m.moe_lora_backward, l, x, ldx, dy, lddy, T, ids, a, b, ranks, scales, dxb, lddxb, dx, lddx, da, db,
                   acc, ws, wsb, 0)
 
@@ -144,6 +174,7 @@ def test_lora_backward_errors():
     assert lora_backward(lddx=2564) == m.MOE_ERR_ARG
     assert lora_backward(dxb=OTHER, lddxb=2568) == m.MOE_ERR_ARG
     assert lora_backward(dx=FAKE) == m.MOE_ERR_ARG        # dx is an input
+    assert lora_backward(db=FAKE) == m.MOE_ERR_ARG        # the tables of dA and dB are one
     need = m.moe_lora_workspace_bytes(L, 100, True)
     assert need > m.moe_lora_workspace_bytes(L, 100, False)
     assert lora_backward(wsb=need - 1) == m.MOE_ERR_WORKSPACE

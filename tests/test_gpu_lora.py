@@ -197,6 +197,25 @@ def test_bad_rank(m, T, bad):
     ref.close(y, *v, "y")
 
 
+@pytest.mark.parametrize("T,R", [(8, 16), (8, 128), (150, 16), (700, 16)])
+@pytest.mark.parametrize("side", [0, 1])
+def test_null_factors(m, T, R, side):
+    """As a rank that is not usable; not looked at beside a rank of 0 or without tokens."""
+    c = Case(m, "bf16", T, 264, 1032, [16, 4, 0, 7], R=R)
+    c.ids[c.ids == 3] = 2
+    c.ids[:4] = torch.tensor([1, 0, 2, 1], device="cuda")
+    y, dx = c.apply(), c.backward()
+    good = [t.clone() for t in c.dA + c.dB]
+    rows = c.ids == 1
+    c.tabs = tuple(ptrs([None if i in (2, 3) or (i == 1 and s == side) else f for i, f in enumerate(t)])
+                   for s, t in enumerate((c.A, c.B)))
+    y2, dx2 = c.apply(), c.backward()
+    assert torch.isnan(y2[rows]).all() and torch.equal(y2[~rows], y[~rows])
+    assert torch.isnan(dx2[rows]).all() and torch.equal(dx2[~rows], dx[~rows])
+    for i, (a, b) in enumerate(zip(good, c.dA + c.dB)):
+        assert (b == 7.0).all() if i % 4 == 1 else torch.equal(a, b)
+
+
 @pytest.mark.parametrize("T", [20, 900])
 def test_accumulate_and_untrained(m, T):
     c = Case(m, "bf16", T, 264, 136, [8, 3, 5, 2])
@@ -290,6 +309,26 @@ def test_strides_past_32_bits(m):
     out = torch.empty((T - 1) * ld + 128, dtype=torch.bfloat16, device="cuda")
     m.moe_lora_apply(c.l, wide, ld, T, *c.table(), c.base, 72, out, ld, c.ws(False))
     assert torch.equal(out.as_strided((T, 72), (ld, 1)), y)
+    dx = c.backward()
+    old = [t.clone() for t in c.dA + c.dB]
+    m.moe_lora_backward(c.l, wide, ld, c.dy, 72, T, *c.table(), c.dxb, 64, out, ld, *c.gp, 0, c.ws(True))
+    assert torch.equal(out.as_strided((T, 64), (ld, 1)), dx)
+    assert all(torch.equal(a, b) for a, b in zip(old, c.dA + c.dB))
+    wide.as_strided((T, 72), (ld, 1)).copy_(c.dy)
+    m.moe_lora_backward(c.l, c.x, 64, wide, ld, T, *c.table(), c.dxb, 64, out, ld, *c.gp, 0, c.ws(True))
+    assert torch.equal(out.as_strided((T, 64), (ld, 1)), dx)
+    assert all(torch.equal(a, b) for a, b in zip(old, c.dA + c.dB))
+
+
+def test_a_workspace_for_the_longest_batch(m):
+    ws = None
+    for T in (3000, 700, 65, 64, 3):
+        c = Case(m, "bf16", T, 264, 520, [16, 64, 3], R=64)
+        y, dx = c.apply(), c.backward()
+        grads = c.dA + c.dB
+        ws = c.ws(True) if ws is None else ws
+        assert torch.equal(y, c.apply(ws=ws)) and torch.equal(dx, c.backward(ws=ws))
+        assert all(torch.equal(a, b) for a, b in zip(grads, c.dA + c.dB))
 
 
 def test_gradients_against_differences(m):
