@@ -258,3 +258,25 @@ def test_repeats_streams_and_graphs(m, T, E, H):
     s.synchronize()
     for k, v in a.out.items():
         assert torch.equal(v, want[0][k])
+
+
+def test_long_batch_offsets_past_32_bits(m):
+    """2^20 tokens of 2560: more than 2^31 elements of x and dx."""
+    T, E, k, H = 1 << 20, 8, 2, 2560
+    dev = "cuda"
+    g = torch.Generator(device=dev).manual_seed(3)
+    x = torch.empty((T, H), device=dev)
+    for part in x.split(1 << 17):
+        part.normal_(generator=g)
+    Wr, din = torch.randn((E, H), device=dev, generator=g), torch.randn((T, E), device=dev, generator=g)
+    d = m.desc(H, 64, E, k, "nvfp4")
+    dx, dWr = torch.empty((T, H), device=dev), torch.empty((E, H), device=dev)
+    ws = torch.empty(m.moe_route_backward_workspace_bytes(d, T), dtype=torch.uint8, device=dev)
+    m.moe_route_backward(d, x, T, Wr, None, None, None, None, din, None, dx, dWr, 0, ws)
+    torch.cuda.synchronize()
+    t = torch.cat([torch.arange(8), torch.randint(0, T, (200,), generator=torch.Generator().manual_seed(1)), torch.arange(T - 8, T)])
+    G = din.cpu().double()
+    ref.close(dx[t.to(dev)], *ref.mm(G[t], ref.cpu64(Wr), pairs=True), "dx")
+    # some columns of dWr over all tokens
+    c = torch.tensor([0, 1, 777, 1280, 2559])
+    ref.close(dWr[:, c.to(dev)], *ref.mm(G.t().contiguous(), x[:, c.to(dev)].cpu().double(), pairs=True), "dWr")
