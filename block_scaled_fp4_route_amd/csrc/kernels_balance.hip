@@ -288,7 +288,9 @@ __device__ __forceinline__ void row_store(float* __restrict__ row, int E, int la
 // Each wave takes every fourth token of a piece, a lane NV columns, the next
 // token's row in flight while one is worked on.
 // SELF (one sequence, few tokens): every workgroup counts the whole routing
-// itself, the first one also for k_bal_reduce, and no counting launch runs.
+// itself, the first one also for k_bal_reduce, and no counting launch runs
+// (see kSelfCount). Bound by memory at length: logits read and written once, 134 MB of 32768 x
+// 512 in 34 us, 4.0 TB/s.
 template <int NV, bool VEC, bool SELF>
 __global__ __launch_bounds__(256) void k_bal_main(const float* __restrict__ logits, const uint8_t* __restrict__ mask,
                                                   const int32_t* __restrict__ off, int T, int E, int k, int S, int TB,
@@ -517,7 +519,10 @@ __global__ __launch_bounds__(256) void k_bal_main(const float* __restrict__ logi
 // the pieces of sequence s; the last workgroup to finish adds the sequences
 // up. Every workgroup takes a ticket from one counter, about 15 ns each, so
 // many sequences get wide blocks (22 us against 8 with 16 columns at 32768 x
-// 512 in 37 sequences), and few get narrow ones, many pieces at a time.
+// 512 in 37 sequences, 9.3 with the coherent join below), and few get narrow
+// ones, many pieces at a time. Bound by latency: 6 to 7 us for one sequence of
+// 311 or 2451 tokens, of which the ticket and the last workgroup's part are
+// about 2.
 template <int CB>
 __global__ __launch_bounds__(1024) void k_bal_reduce(const int32_t* __restrict__ off, int T, int E, int k, int S,
                                                      int TB, int J, const int32_t* __restrict__ cnt,

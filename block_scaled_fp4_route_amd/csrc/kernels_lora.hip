@@ -501,13 +501,18 @@ __device__ __forceinline__ void ring_barrier() {
 }
 
 // grid (slots, parts of side a, then of side b): the low values of one tile
-// over one part of one side's long axis. Wave w has the tokens 16 w .. + 15 and all ranks; the step after
-// next is on its way from memory while one is multiplied. (Operands loaded
-// straight into registers kept too little in flight: 90 us against ... for
-// both sides at 8192 tokens, 2560 and 8192 wide, rank 64.) Where the axis is
-// in several parts, every workgroup leaves its own with device-coherent
-// stores, and the last one of a tile to finish (by a ticket) adds them in
-// order. Out go the bf16 parts of the scaled values.
+// over one part of one side's long axis. Wave w has the tokens 16 w .. + 15
+// and all ranks; the step after next is on its way from memory while one is
+// multiplied. (Operands loaded straight into registers kept too little in
+// flight: the backward pass of 8192 tokens, 2560 and 8192 wide, rank 64 took
+// 214 us with them and 187 with the ring.) Where the axis is in several parts,
+// every workgroup leaves its own with device-coherent stores, and the last one
+// of a tile to finish (by a ticket) adds them in order. Out go the bf16 parts
+// of the scaled values. Bound by memory: one side of 8192 x 2560 bf16, rank
+// 16, 18 us (42 MB, 2.3 TB/s); both sides of 8192 x (2560 + 8192), rank 64, 65
+// us (176 MB, 2.7 TB/s, where a kernel that only reads the same 134 MB side in
+// such row pieces takes 26 to 33 us). Few tokens: one round of loads and the
+// join, 13 us at 300 x (2560 + 640) fp32.
 template <int ACT, int RB>
 __global__ __launch_bounds__(256) void k_lora_down(DownJob ja, DownJob jb, int n, int R,
                                                    LoraTable tab,
@@ -750,10 +755,13 @@ __device__ __forceinline__ f4v mma_parts(const u4v (&a)[3], const u4v (&b)[PB], 
 // ---------------------------------------------------------------------------
 // "up": grid (ceil(N / 256), slots): y of one tile and 256 columns, 64 a wave,
 // everything from memory to registers. Workgroups that run together write whole
-// rows (the tiles first: 68 us against 59 at 8192 x 8192, rank 16). The base rows are requested first. Of
-// the factor, lane (i, q) loads ranks 8 q .. + 7 of 4 neighbouring columns
-// 4 i + j and turns them into one operand for each column, so that a lane ends
-// with 4 neighbouring columns of its rows.
+// rows (the tiles first: 68 us against 59 at 8192 x 8192, rank 16). The base
+// rows are requested first. Of the factor, lane (i, q) loads ranks 8 q .. + 7
+// of 4 neighbouring columns 4 i + j and turns them into one operand for each
+// column, so that a lane ends with 4 neighbouring columns of its rows. Bound by
+// memory: base read and y written, 268 MB at 8192 x 8192 bf16 in 59 us, 4.5
+// TB/s (a large copy: 5.1); 2451 x 2560 fp16, rank 64: 16 us, 1.6 TB/s, where
+// the launch, the factor's loads and their turning count.
 template <int ACT, int RB>
 __global__ __launch_bounds__(256) void k_lora_up(const u4v* __restrict__ u, int T, int N, int n, int R,
                                                  const void* const* __restrict__ fac,
@@ -865,8 +873,10 @@ struct GradSide {
 };
 
 // grid (column blocks of A then of B, piece slots; the pieces first: 62 us
-// against 46 at 8192 tokens, rank 64): 256 columns, 64 a wave, over one piece, a tile of 64 tokens at a time: low's parts go from memory
-// straight into LDS, the rows' values into registers, by lane (i, q) as tokens
+// against 46 at 8192 tokens, rank 64: 3.8 TB/s of x and dy read): 256 columns,
+// 64 a wave, over one piece, a tile of 64 tokens at a time. One workgroup
+// reads each row piece once for all ranks, so the rows pass by once and the
+// sums stay in registers. low's parts go from memory straight into LDS, the rows' values into registers, by lane (i, q) as tokens
 // 8 q .. + 7 (and 32 more) of 4 neighbouring columns, both a tile ahead; the
 // values are turned into an operand for each column. An adapter of one piece
 // writes its gradient, others the piece's part for k_lora_grad_reduce.
