@@ -348,8 +348,14 @@ __device__ __forceinline__ void pair8(const float (&v)[8], float scale, u4v& h, 
 }
 
 // Position of column n in its operand: within 64, even columns first, so that
-// a lane of a product ends with two neighbouring columns.
-__device__ __forceinline__ int place(int n) { return n / 64 * 64 + n % 2 * 32 + n / 2 % 32; }
+// a lane of a product ends with two neighbouring columns; the pairs in an order
+// in which the eight threads of make_panel that share a row of chunks write 128
+// bytes in a row at once. Lane i of a product has pair pair_of(i).
+__device__ __forceinline__ int place(int n) {
+    const int p = n / 2 % 32;
+    return n / 64 * 64 + n % 2 * 32 + p / 16 * 16 + p % 2 * 8 + p / 2 % 8;
+}
+__device__ __forceinline__ int pair_of(int i) { return i / 16 * 16 + i % 8 * 2 + i / 8 % 2; }
 
 // The parts of a matrix whose rows run along the sum: out[part][2][kw / 8][W]
 // chunks from p [rows][cols]. A workgroup of NT = 2^ntl threads (at least
@@ -372,19 +378,21 @@ __device__ __forceinline__ void make_panel(const Panel& j, int b, f4v (*red)[8])
     const int col = ((b % j.cb << (j.ntl - j.kwl)) + sub) * 32 + 4 * c4, r0 = part * kw + 8 * r8;
     const bool in = col < j.cols;
     f4v v[8];
-    bool on[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         const int r = min(r0 + i, j.rows - 1);
         v[i] = *reinterpret_cast<const f4v*>(j.p + (size_t)r * j.cols + (in ? col : 0));
-        on[i] = r0 + i < j.rows && (!j.mask || j.mask[r]);
     }
+    // a wave has 64 rows: each lane looks at one of them
+    const int mr = r0 - 8 * (tid / 8 % 8) + (tid & 63);
+    const unsigned long long on = __ballot(mr < j.rows && (!j.mask || j.mask[min(mr, j.rows - 1)]));
+    const uint32_t mine = (uint32_t)(on >> (tid / 8 % 8 * 8)) & 0xFFu;
     f4v m = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 8; i++)
 #pragma unroll
         for (int q = 0; q < 4; q++) {
-            if (!on[i]) v[i][q] = 0.0f;
+            if (!(mine >> i & 1)) v[i][q] = 0.0f;
             m[q] = fmaxf(m[q], finite_mag(v[i][q]));
         }
 #pragma unroll
@@ -658,10 +666,10 @@ __device__ __forceinline__ void pair_tile(const PairIn& A, const PairIn& B, int 
         turn(s + 1, f1, f0);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    const int nl = 64 * wn + 2 * (lane & 31), n = n0 + nl, e0 = exps[BM + nl], e1 = exps[BM + nl + 1];
+    const int nl = 64 * wn + 2 * pair_of(lane & 31), n = n0 + nl, e0 = exps[BM + nl], e1 = exps[BM + nl + 1];
     auto row = [&](int i, int r) {  // of the workgroup's tile
         const int q = 8 * (r / 4) + 4 * (lane >> 5) + r % 4;  // of the MFMA tile
-        return 32 * MI * wm + (permuted ? i / 2 * 64 + 2 * q + i % 2 : 32 * i + q);
+        return 32 * MI * wm + (permuted ? i / 2 * 64 + 2 * pair_of(q) + i % 2 : 32 * i + q);
     };
     C += (size_t)m0 * H + n;
     const int rows = M - m0;

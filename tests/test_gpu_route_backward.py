@@ -69,8 +69,9 @@ def test_shapes(m, T, E, k, H):
 
 @pytest.mark.parametrize("dw,din,dx,dWr", [(True, False, True, True), (False, True, True, True), (True, True, False, True),
                                            (True, True, True, False), (True, True, False, False)])
-def test_parts_left_out(m, dw, din, dx, dWr):
-    c = Case(m, 90, 60, 4, 512, 0.2)
+@pytest.mark.parametrize("T,E,H", [(90, 60, 512), (1100, 512, 1024)])
+def test_parts_left_out(m, dw, din, dx, dWr, T, E, H):
+    c = Case(m, T, E, 4, H, 0.2)
     c.check(c.run(dw, din, dx, dWr), dw, din)
 
 
@@ -154,6 +155,23 @@ def test_in_place_on_dlogits(m, T, E, H):
     a, b = c.run(), c.run(inplace=True)
     for name in a:
         assert torch.equal(a[name], b[name]), name
+
+
+@pytest.mark.parametrize("T,E,H", [(90, 60, 512), (1100, 512, 1024)])
+def test_logits_gradients_at_any_float(m, T, E, H):
+    """dlogits_in and dlogits_out need no more than a float's alignment."""
+    c = Case(m, T, E, 4, H, 0.2)
+    want = c.run()
+    wide = torch.full((2, T * E + 8), 7.0, device="cuda")
+    wide[0, 1:1 + T * E] = c.dev[5].view(-1)
+    args = list(c.args)
+    for at in (1, 2):
+        wide[1] = 7.0
+        args[8], args[9] = wide[0, 1:], wide[1, at:]
+        m.moe_route_backward(*args)
+        assert torch.equal(wide[1, at:at + T * E].view(T, E), want["dlogits"])
+        assert (wide[1, :at] == 7).all() and (wide[1, at + T * E:] == 7).all()
+        assert torch.equal(args[10], want["dx"]) and torch.equal(args[11], want["dWr"])
 
 
 def test_no_tokens(m):
