@@ -275,7 +275,7 @@ struct LoraWs {
 
 int col_blocks(int cols) { return (cols + kUpCols - 1) / kUpCols; }
 
-LoraWs lora_ws(int K, int N, int n, int R, int T, bool backward) {
+LoraWs lora_ws(int K, int N, int n, int R, int T, bool backward, bool f32) {
     LoraWs w = {};
     w.R16 = R <= 16 ? 16 : (R <= 32 ? 32 : (R <= 64 ? 64 : 128));
     w.R32 = w.R16 < 32 ? 32 : w.R16;
@@ -289,14 +289,19 @@ LoraWs lora_ws(int K, int N, int n, int R, int T, bool backward) {
     // down), growing with T: fewer tokens never need more workspace
     const int in128 = T / 128, in512 = 516 / (col_blocks(K) + col_blocks(N)), least = in128 < in512 ? in128 : in512;
     const size_t pslots = (size_t)(T / 4096 > least ? T / 4096 : least) + n + 3;
-    // parts of the long axes of "down": two workgroups per compute unit in all
-    // (what runs at once), shared out by the sides' lengths, at most 8 parts of
-    // a side, of four steps of 128 at least
+    // parts of the long axes of "down": one workgroup per compute unit, or two
+    // (what runs at once) for two sides, whose lengths share them out; at most 8
+    // parts of a side, of four steps at least. One side, one against two a unit:
+    // 16000 x 1024 12 us against 15, 4000 x 4096 14 against 16; two sides: 8192 x
+    // (2560 + 8192), rank 64, 81 against 64 (bf16). Four steps against two: 2451 x
+    // 2560 fp16 14 us against 16, against eight: 22 at 300 x (2560 + 640) fp32,
+    // where four take 12.
     const int tiles = T / kTile + 1 + (n < T ? n : T) / 2;
-    auto parts = [tiles](int len, int all) {
-        int64_t k = (512 / tiles * (int64_t)len + all / 2) / all;
+    auto parts = [=](int len, int all) {
+        int64_t k = ((backward ? 512 : 256) / tiles * (int64_t)len + (all - 1) / 2) / all;
         if (k > 8) k = 8;
-        if (k > len / 512) k = len / 512;
+        const int step = f32 ? 64 : 128;
+        if (k > len / (4 * step)) k = len / (4 * step);
         return (int)(k < 1 ? 1 : k);
     };
     w.ku = parts(K, backward ? K + N : K);
@@ -317,9 +322,8 @@ LoraWs lora_ws(int K, int N, int n, int R, int T, bool backward) {
     w.tiles = take((size_t)w.slots * sizeof(Slot));
     w.pieces = take(backward ? pslots * sizeof(Slot) : 0);
     w.tickets = take((size_t)w.slots * 2 * 4);
-    // parts x tokens: 8 of a side at most, and 512 / (T / 64) rounded up by no
-    // more than a third
-    const size_t rows = (size_t)T * (backward ? 16 : 8), most = 512 * kTile * 4 / 3 + 1;
+    // parts x tokens: 8 of a side at most, and 512 / (T / 64) in all
+    const size_t rows = (size_t)T * (backward ? 16 : 8), most = 512 * kTile;
     w.part = take((rows < most ? rows : most) * w.R16 * 4);
     const size_t by_token = (size_t)T * w.R32 * 6, by_rank = (size_t)w.slots * w.R16 * kTile * 6;
     w.ut = take(backward ? 0 : by_token);
@@ -1088,7 +1092,7 @@ template <int ACT>
 hipError_t apply(int K, int N, int n, int R, const void* x, size_t ldx, int T, const LoraTable& tab, const void* base,
                  size_t ldb, void* y, size_t ldy, void* ws, hipStream_t s) {
     typedef typename Act<ACT>::T E;
-    const LoraWs w = lora_ws(K, N, n, R, T, false);
+    const LoraWs w = lora_ws(K, N, n, R, T, false, ACT == kActF32);
     const LoraMem m(w, ws);
     hipError_t r;
     if (direct(T, R)) {
@@ -1116,7 +1120,7 @@ template <int ACT>
 hipError_t backward(int K, int N, int n, int R, const void* x, size_t ldx, const void* dy, size_t lddy, int T,
                     const LoraTable& tab, const void* dxb, size_t lddxb, void* dx, size_t lddx, float* const* da,
                     float* const* db, int accumulate, void* ws, hipStream_t s) {
-    const LoraWs w = lora_ws(K, N, n, R, T, true);
+    const LoraWs w = lora_ws(K, N, n, R, T, true, ACT == kActF32);
     const LoraMem m(w, ws);
     hipError_t r;
     hipLaunchKernelGGL(k_lora_plan, dim3(n + 2), dim3(1024), 0, s, tab.ids, T, n, m.perm, m.groups, m.tiles, m.pieces,
@@ -1151,7 +1155,7 @@ hipError_t backward(int K, int N, int n, int R, const void* x, size_t ldx, const
 
 }  // namespace
 
-size_t lora_ws_bytes(int K, int N, int n, int R, int T, bool back) { return lora_ws(K, N, n, R, T, back).total; }
+size_t lora_ws_bytes(int K, int N, int n, int R, int T, bool back) { return lora_ws(K, N, n, R, T, back, false).total; }
 
 hipError_t launch_lora_apply(int dtype, int K, int N, int n, int R, const void* x, size_t ldx, int T,
                              const LoraTable& tab, const void* base, size_t ldbase, void* y, size_t ldy, void* ws,
