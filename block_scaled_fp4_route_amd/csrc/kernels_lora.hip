@@ -513,10 +513,10 @@ __device__ __forceinline__ void ring_barrier() {
 // every workgroup leaves its own with device-coherent stores, and the last one
 // of a tile to finish (by a ticket) adds them in order. Out go the bf16 parts
 // of the scaled values. Bound by memory: one side of 8192 x 2560 bf16, rank
-// 16, 18 us (42 MB, 2.3 TB/s); both sides of 8192 x (2560 + 8192), rank 64, 65
+// 16, 17 us (42 MB, 2.5 TB/s); both sides of 8192 x (2560 + 8192), rank 64, 65
 // us (176 MB, 2.7 TB/s, where a kernel that only reads the same 134 MB side in
 // such row pieces takes 26 to 33 us). Few tokens: one round of loads and the
-// join, 13 us at 300 x (2560 + 640) fp32.
+// join, 12 us at 300 x (2560 + 640) fp32.
 template <int ACT, int RB>
 __global__ __launch_bounds__(256) void k_lora_down(DownJob ja, DownJob jb, int n, int R,
                                                    LoraTable tab,
@@ -880,9 +880,10 @@ struct GradSide {
 // against 46 at 8192 tokens, rank 64: 3.8 TB/s of x and dy read): 256 columns,
 // 64 a wave, over one piece, a tile of 64 tokens at a time. One workgroup
 // reads each row piece once for all ranks, so the rows pass by once and the
-// sums stay in registers. low's parts go from memory straight into LDS, the rows' values into registers, by lane (i, q) as tokens
-// 8 q .. + 7 (and 32 more) of 4 neighbouring columns, both a tile ahead; the
-// values are turned into an operand for each column. An adapter of one piece
+// sums stay in registers. low's parts go from memory straight into LDS, the
+// rows' values into registers, by lane (i, q) as tokens 8 q .. + 7 (and 32
+// more) of 4 neighbouring columns, both a tile ahead; the values are turned
+// into an operand for each column. An adapter of one piece
 // writes its gradient, others the piece's part for k_lora_grad_reduce.
 template <int ACT, int RB>
 __global__ __launch_bounds__(256) void k_lora_grad(GradSide ga, GradSide gb, int n, int R, int piece,
