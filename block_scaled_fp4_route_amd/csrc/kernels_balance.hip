@@ -292,8 +292,8 @@ __device__ __forceinline__ void row_store(float* __restrict__ row, int E, int la
 // token's row in flight while one is worked on.
 // SELF (one sequence, few tokens): every workgroup counts the whole routing
 // itself, the first one also for k_bal_reduce, and no counting launch runs
-// (see kSelfCount). Bound by memory at length: logits read and written once, 134 MB of 32768 x
-// 512 in 34 us, 4.0 TB/s.
+// (see kSelfCount). Bound by memory at length: logits read and gradient written
+// once, 134 MB of 32768 x 512 in 34 us, 4.0 TB/s.
 template <int NV, bool VEC, bool SELF>
 __global__ __launch_bounds__(256) void k_bal_main(const float* __restrict__ logits, const uint8_t* __restrict__ mask,
                                                   const int32_t* __restrict__ off, int T, int E, int k, int S, int TB,
@@ -518,14 +518,18 @@ __global__ __launch_bounds__(256) void k_bal_main(const float* __restrict__ logi
     }
 }
 
-// grid (ceil(E / CB), S), 1024 threads: CB columns x 1024 / CB row groups over
-// the pieces of sequence s; the last workgroup to finish adds the sequences
-// up. Every workgroup takes a ticket from one counter, about 15 ns each, so
-// many sequences get wide blocks (22 us against 8 with 16 columns at 32768 x
-// 512 in 37 sequences, 9.3 with the coherent join below), and few get narrow
-// ones, many pieces at a time. Bound by latency: 6 to 7 us for one sequence of
+// grid (ceil(E / CB), rows), 1024 threads: CB columns x 1024 / CB row groups
+// over the pieces of a sequence, every gridDim.y-th sequence; the last
+// workgroup to finish adds the sequences up. Every workgroup takes a ticket
+// from one counter, about 15 ns each, and looks at all sequences' numbers, so
+// up to 4 sequences get narrow blocks, many pieces at a time, and more get
+// wide ones (22 us against 8 with 16 columns at 32768 x 512 in 37 sequences,
+// 9.3 with the coherent join below), about kReduceGroups of them in all
+// (32768 x 512 in 200 sequences: 17 us against 35 with one for each, in 1000:
+// 42 against 164, 99 with 2048 in all). Bound by latency: 6 to 7 us for one sequence of
 // 311 or 2451 tokens, of which the ticket and the last workgroup's part are
 // about 2.
+constexpr int kNarrow = 16, kWide = 128, kReduceGroups = 256;
 template <int CB>
 __global__ __launch_bounds__(1024) void k_bal_reduce(const int32_t* __restrict__ off, int T, int E, int k, int S,
                                                      int TB, int J, const int32_t* __restrict__ cnt,
@@ -538,76 +542,81 @@ __global__ __launch_bounds__(1024) void k_bal_reduce(const int32_t* __restrict__
     __shared__ float red[RG][CB + 1];
     __shared__ float wr[2][NW];
     __shared__ uint32_t last;
-    const int tid = threadIdx.x, col = tid % CB, g = tid / CB, s = blockIdx.y;
+    const int tid = threadIdx.x, col = tid % CB, g = tid / CB;
     const int EB = gridDim.x, e = blockIdx.x * CB + col;
     __shared__ int sn[kSeqLds], so[2 * kSeqLds];
-    const int ns = seq_n(n, s, J);
-    int lo, hi, c = 0;
-    const bool mine = seq_bounds(off, s, T, lo, hi);
-    if (tid < CB && e < E) {
-        int h[kMaxParts];
+    Seqs all;
+    for (int s = blockIdx.y; s < S; s += gridDim.y) {
+        const int ns = seq_n(n, s, J);
+        int lo, hi, c = 0;
+        const bool mine = seq_bounds(off, s, T, lo, hi);
+        if (tid < CB && e < E) {
+            int h[kMaxParts];
 #pragma unroll
-        for (int j = 0; j < kMaxParts; j++) h[j] = cnt[((size_t)s * J + min(j, J - 1)) * E + e];
+            for (int j = 0; j < kMaxParts; j++) h[j] = cnt[((size_t)s * J + min(j, J - 1)) * E + e];
 #pragma unroll
-        for (int j = 0; j < kMaxParts; j++) c += j < J ? h[j] : 0;
-    }
-    const Seqs all = bal_totals<NT>(n, off, T, 0, S, J, sn, so);
-    const int live = all.live, total = all.total;
-    const bool fine = all.fine, any = fine && mine && hi > lo;
-    const int r0 = any ? lo / TB + s : 0, r1 = any ? (hi - 1) / TB + s + 1 : 0;
-    float a = 0.0f;
-    if (e < E)
-#pragma unroll 4
-        for (int r = r0 + g; r < r1; r += RG) a += psum[(size_t)r * E + e];
-    float z = 0.0f;  // this sequence's sum of lse^2, by the first column block
-    if (blockIdx.x == 0)
-        for (int r = r0 + tid; r < r1; r += NT) z += zsum[r];
-    red[g][col] = a;
-    __syncthreads();
-#pragma unroll
-    for (int h = RG / 2; h >= 1; h >>= 1) {
-        if (g < h) red[g][col] += red[g + h][col];
-        __syncthreads();
-    }
-    float v = 0.0f;
-    if (tid < CB && e < E) {
-        float p = ns > 0 ? red[0][col] / (float)ns : 0.0f;
-        if (!fine) p = __builtin_nanf("");
-        if (probs) probs[(size_t)s * E + e] = p;
-        if (counts) counts[(size_t)s * E + e] = fine ? c : -1;
-        v = (float)c * p;
-    }
-    v = wave_sum(v);
-    z = wave_sum(z);
-    if ((tid & 63) == 0) {
-        wr[0][tid >> 6] = v;
-        wr[1][tid >> 6] = z;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        v = z = 0.0f;
-        for (int i = 0; i < NW; i++) {
-            v += wr[0][i];
-            z += wr[1][i];
+            for (int j = 0; j < kMaxParts; j++) c += j < J ? h[j] : 0;
         }
-        if (ns > 0) v *= (float)E / ((float)live * (float)k * (float)ns);
-        __hip_atomic_store(&q[(size_t)s * (EB + 1) + blockIdx.x], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (s == (int)blockIdx.y) all = bal_totals<NT>(n, off, T, 0, S, J, sn, so);
+        const bool any = all.fine && mine && hi > lo;
+        const int r0 = any ? lo / TB + s : 0, r1 = any ? (hi - 1) / TB + s + 1 : 0;
+        float a = 0.0f;
+        if (e < E)
+#pragma unroll 4
+            for (int r = r0 + g; r < r1; r += RG) a += psum[(size_t)r * E + e];
+        float z = 0.0f;  // this sequence's sum of lse^2, by the first column block
         if (blockIdx.x == 0)
-            __hip_atomic_store(&q[(size_t)s * (EB + 1) + EB], z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            for (int r = r0 + tid; r < r1; r += NT) z += zsum[r];
+        red[g][col] = a;
+        __syncthreads();
+#pragma unroll
+        for (int h = RG / 2; h >= 1; h >>= 1) {
+            if (g < h) red[g][col] += red[g + h][col];
+            __syncthreads();
+        }
+        float v = 0.0f;
+        if (tid < CB && e < E) {
+            float p = ns > 0 ? red[0][col] / (float)ns : 0.0f;
+            if (!all.fine) p = __builtin_nanf("");
+            if (probs) probs[(size_t)s * E + e] = p;
+            if (counts) counts[(size_t)s * E + e] = all.fine ? c : -1;
+            v = (float)c * p;
+        }
+        v = wave_sum(v);
+        z = wave_sum(z);
+        if ((tid & 63) == 0) {
+            wr[0][tid >> 6] = v;
+            wr[1][tid >> 6] = z;
+        }
+        __syncthreads();
+        if (tid == 0) {
+            v = z = 0.0f;
+            for (int i = 0; i < NW; i++) {
+                v += wr[0][i];
+                z += wr[1][i];
+            }
+            if (ns > 0) v *= (float)E / ((float)all.live * (float)k * (float)ns);
+            __hip_atomic_store(&q[(size_t)s * (EB + 1) + blockIdx.x], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (blockIdx.x == 0)
+                __hip_atomic_store(&q[(size_t)s * (EB + 1) + EB], z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        if constexpr (CB == kNarrow) break;  // a workgroup for each of the few sequences
+        // (wr is written again only behind the next sequence's barriers)
     }
-    // Thread 0 made this workgroup's one or two stores of q itself, with
+    const int total = all.total;
+    const bool fine = all.fine;
+    // Thread 0 made this workgroup's stores of q itself, with
     // device-coherent stores: it waits for them, then takes the ticket. (A
     // release fence would write back the XCD's whole L2, here full of the
     // gradient just written: 65 us against 7 at 32768 x 512 in 37 sequences.)
     if (tid == 0) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u ==
-               (uint32_t)EB * (uint32_t)S;
+               (uint32_t)EB * gridDim.y;
     }
     __syncthreads();
     if (!last) return;
-    float bal = 0.0f;
-    z = 0.0f;
+    float bal = 0.0f, z = 0.0f;
     const size_t cells = (size_t)S * (EB + 1);
     for (size_t i = tid; i < cells; i += NT) {
         const float x = __hip_atomic_load(&q[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -680,9 +689,10 @@ hipError_t launch_balance(int E, int k, const float* logits, int T, const int32_
         if ((r = hipGetLastError()) != hipSuccess) return r;
     }
 #define BR(CB)                                                                                                         \
-    hipLaunchKernelGGL((k_bal_reduce<CB>), dim3((E + CB - 1) / CB, S), dim3(1024), 0, s, seq_off, T, E, k, S, b.TB, J, cnt, \
+    hipLaunchKernelGGL((k_bal_reduce<CB>), dim3((E + CB - 1) / CB, rows), dim3(1024), 0, s, seq_off, T, E, k, S, b.TB, J, cnt, \
                        n, cb, cz, psum, zsum, q, ticket, loss, counts, probs)
-    if (S <= 4) BR(16); else BR(128);
+    const int most = kReduceGroups / ((E + kWide - 1) / kWide), rows = S <= 4 || S < most ? S : most;
+    if (S <= 4) BR(kNarrow); else BR(kWide);
 #undef BR
     return hipGetLastError();
 }

@@ -66,7 +66,7 @@ def test_one_sequence(m, T, E, k):
     c.check(c.run(up=0.75, whole=True), up=0.75)
 
 
-@pytest.mark.parametrize("T,E,k,S,masked", [(1, 16, 2, 3, 0.0), (100, 60, 4, 5, 0.3), (777, 512, 10, 9, 0.0),
+@pytest.mark.parametrize("T,E,k,S,masked", [(1, 16, 2, 3, 0.0), (900, 1023, 2, 300, 0.1), (500, 40, 3, 1000, 0.2), (200, 64, 3, 65535, 0.0), (100, 60, 4, 5, 0.3), (777, 512, 10, 9, 0.0),
                                             (777, 130, 10, 64, 0.5), (4500, 384, 6, 2, 0.1), (33, 33, 3, 40, 0.9)])
 def test_sequences_and_masks(m, T, E, k, S, masked):
     c = Case(m, T, E, k, S, masked)
