@@ -10,9 +10,10 @@
 // (an outer product summed over an adapter's tokens). u, v and every sum are
 // fp32. The products run on the 16-bit matrix instructions: 16-bit operands
 // as they are, and fp32 ones as three bf16 parts, each the truncation of what
-// the ones before left, which hold all 24 bits over the whole fp32 range (the
-// fp32 instructions run at a sixteenth of the rate; against fp32 u and v an
-// fp16 operand enters as two bf16 parts, exactly).
+// the ones before left, which hold all 24 bits of values above 2^-110 (bits
+// below 2^-133, bf16's smallest step, are cut off; the fp32 instructions run at
+// a sixteenth of the rate; against fp32 u and v an fp16 operand enters as two
+// bf16 parts, exactly).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -449,6 +450,35 @@ __device__ __forceinline__ void parts8(const float (&v)[8], u4v (&p)[P]) {
 __device__ __forceinline__ f4v mma_bf16(u4v a, u4v b, f4v c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8v, a), __builtin_bit_cast(bf8v, b), c, 0, 0, 0);
 }
+// Infinities. An infinity has the parts (inf, 0, 0), and a finite value of few
+// bits has low parts of 0 too, so an infinite product of two values becomes NaN
+// where the infinity meets such a part. The product of the two first parts
+// alone has the class of the whole product (infinite with its sign, NaN or
+// finite; values below 2^-133 have no parts and count as 0). So a sum that
+// comes out as NaN is formed once more from the first parts, and is infinite
+// if that one is. Other sums cost a comparison each.
+__device__ __forceinline__ bool is_nan(float v) { return v != v; }
+__device__ __forceinline__ int has_nan(f4v v) {
+    return __builtin_isunordered(v.x, v.y) | __builtin_isunordered(v.z, v.w);
+}
+// What a NaN among the sums is, from the sum of the first parts.
+__device__ __forceinline__ float nan_or_inf(float first) {
+    return fabsf(first) == INFINITY ? first : __builtin_nanf("");
+}
+// The bf16 truncations of a and b, NaN also where the truncation cuts off all
+// bits that make one.
+__device__ __forceinline__ uint32_t pack_first(float a, float b) {
+    return pack_hi(is_nan(a) ? __builtin_nanf("") : a, is_nan(b) ? __builtin_nanf("") : b);
+}
+// (for a product beside the first ones' in a second run over the same data)
+__device__ __forceinline__ u4v without_inf(u4v p) {
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+        if ((p[q] & 0x7FFFu) == 0x7F80u) p[q] &= 0xFFFF0000u;
+        if ((p[q] & 0x7FFF0000u) == 0x7F800000u) p[q] &= 0xFFFFu;
+    }
+    return p;
+}
 
 // ---------------------------------------------------------------------------
 // "down": the two sides of a pass (x with A; dy with B) in one launch.
@@ -571,67 +601,81 @@ __global__ __launch_bounds__(256) void k_lora_down(DownJob ja, DownJob jb, int n
         for (int i = 0; i < S::FW; i++) load_lds(fp[i] + (k + fk[i] < j.K ? k : -fk[i]), to + kTile * S::XC + fd[i]);
     };
     f4v acc[RB];
+    auto sums = [&](auto INF) {
 #pragma unroll
-    for (int i = 0; i < RB; i++) acc[i] = f4v{0.f, 0.f, 0.f, 0.f};
-    if (r > 0 && s0 < s1) {
-        constexpr int NI = S::XI + S::FW;
+        for (int i = 0; i < RB; i++) acc[i] = f4v{0.f, 0.f, 0.f, 0.f};
+        if (r > 0 && s0 < s1) {
+            constexpr int NI = S::XI + S::FW;
 #pragma unroll
-        for (int i = 0; i < RING - 1; i++) issue(s0 + i, lds + i * S::CHUNKS);
-        int cur = 0, put = RING - 1;
-        const bool rows = 16 * wave < sl.rows;  // of this wave
-        for (int s = s0; s < s1; s++) {
-            ring_barrier<(RING - 2) * NI>();  // step s is there, and every wave is done with step s - 1
-            issue(s + RING - 1, lds + put * S::CHUNKS);
-            const u4v* x = lds + cur * S::CHUNKS + S::XC * (16 * wave + li);
-            const u4v* f = lds + cur * S::CHUNKS + kTile * S::XC + li * S::FC;
-            const int sx = swizzle<S::XC>(li), sf = swizzle<S::FC>(li);  // (rows 16 further have the same)
-            cur = cur + 1 == RING ? 0 : cur + 1;
-            put = put + 1 == RING ? 0 : put + 1;
-            // TAIL: the axis's last step, whose missing elements count as 0
-            auto multiply = [&](auto TAIL) {
+            for (int i = 0; i < RING - 1; i++) issue(s0 + i, lds + i * S::CHUNKS);
+            int cur = 0, put = RING - 1;
+            const bool rows = 16 * wave < sl.rows;  // of this wave
+            for (int s = s0; s < s1; s++) {
+                ring_barrier<(RING - 2) * NI>();  // step s is there, and every wave is done with step s - 1
+                issue(s + RING - 1, lds + put * S::CHUNKS);
+                const u4v* x = lds + cur * S::CHUNKS + S::XC * (16 * wave + li);
+                const u4v* f = lds + cur * S::CHUNKS + kTile * S::XC + li * S::FC;
+                const int sx = swizzle<S::XC>(li), sf = swizzle<S::FC>(li);  // (rows 16 further have the same)
+                cur = cur + 1 == RING ? 0 : cur + 1;
+                put = put + 1 == RING ? 0 : put + 1;
+                // TAIL: the axis's last step, whose missing elements count as 0
+                auto multiply = [&](auto TAIL) {
 #pragma unroll
-                for (int m = 0; m < S::KE / 32; m++) {
-                    const int c = 4 * m + lq;  // the chunk of eight elements
-                    const bool in = !TAIL || s * S::KE + 8 * c < j.K;
-                    u4v a[ACT == kActF32 ? 3 : 1];
-                    if constexpr (ACT == kActF32) {
-                        const u4v u = x[(2 * c) ^ sx], v = x[(2 * c + 1) ^ sx];
-                        float e[8];
-#pragma unroll
-                        for (int q = 0; q < 4; q++) {
-                            e[q] = in ? __uint_as_float(u[q]) : 0.0f;
-                            e[4 + q] = in ? __uint_as_float(v[q]) : 0.0f;
-                        }
-                        parts8<3>(e, a);
-                    } else {
-                        a[0] = x[c ^ sx];
-#pragma unroll
-                        for (int q = 0; q < 4; q++) a[0][q] = in ? a[0][q] : 0u;
-                    }
-#pragma unroll
-                    for (int i = 0; i < RB; i++) {
-                        u4v w = f[16 * i * S::FC + (c ^ sf)];
-#pragma unroll
-                        for (int q = 0; q < 4; q++) w[q] = in ? w[q] : 0u;
+                    for (int m = 0; m < S::KE / 32; m++) {
+                        const int c = 4 * m + lq;  // the chunk of eight elements
+                        const bool in = !TAIL || s * S::KE + 8 * c < j.K;
+                        u4v a[ACT == kActF32 ? 3 : 1];
                         if constexpr (ACT == kActF32) {
+                            const u4v u = x[(2 * c) ^ sx], v = x[(2 * c + 1) ^ sx];
+                            float e[8];
 #pragma unroll
-                            for (int q = 2; q >= 0; q--) acc[i] = mma_bf16(a[q], w, acc[i]);
-                        } else if constexpr (ACT == kActBf16) {
-                            acc[i] = mma_bf16(a[0], w, acc[i]);
+                            for (int q = 0; q < 4; q++) {
+                                e[q] = in ? __uint_as_float(u[q]) : 0.0f;
+                                e[4 + q] = in ? __uint_as_float(v[q]) : 0.0f;
+                            }
+                            parts8<3>(e, a);
                         } else {
-                            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8v, a[0]),
-                                                                            __builtin_bit_cast(h8v, w), acc[i], 0, 0, 0);
+                            a[0] = x[c ^ sx];
+#pragma unroll
+                            for (int q = 0; q < 4; q++) a[0][q] = in ? a[0][q] : 0u;
+                        }
+#pragma unroll
+                        for (int i = 0; i < RB; i++) {
+                            u4v w = f[16 * i * S::FC + (c ^ sf)];
+#pragma unroll
+                            for (int q = 0; q < 4; q++) w[q] = in ? w[q] : 0u;
+                            if constexpr (ACT == kActF32) {
+#pragma unroll
+                                for (int q = 2; q >= 0; q--) acc[i] = mma_bf16(a[q], INF && q ? without_inf(w) : w, acc[i]);
+                            } else if constexpr (ACT == kActBf16) {
+                                acc[i] = mma_bf16(a[0], w, acc[i]);
+                            } else {
+                                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8v, a[0]),
+                                                                                __builtin_bit_cast(h8v, w), acc[i], 0, 0, 0);
+                            }
                         }
                     }
-                }
-            };
-            if (rows && (s + 1) * S::KE <= j.K) multiply(std::false_type());
-            else if (rows) multiply(std::true_type());
+                };
+                if (rows && (s + 1) * S::KE <= j.K) multiply(std::false_type());
+                else if (rows) multiply(std::true_type());
+            }
+            ring_barrier<0>();  // nothing is on its way into LDS any more, nobody reads the ring
         }
-        ring_barrier<0>();  // nothing is on its way into LDS any more, nobody reads the ring
-    }
+    };
+    sums(std::false_type());
     float(*red)[R16 + 1] = reinterpret_cast<float(*)[R16 + 1]>(lds);
     uint32_t* ticket = reinterpret_cast<uint32_t*>(lds + SUMS);
+    if constexpr (ACT == kActF32) {  // operands in parts: all waves once more, by one's NaN
+        int nan = 0;
+#pragma unroll
+        for (int i = 0; i < RB; i++) nan |= has_nan(acc[i]);
+        const bool any = __ballot(nan) != 0;
+        if (lane == 0) ticket[wave] = any;
+        __syncthreads();
+        const bool again = ticket[0] | ticket[1] | ticket[2] | ticket[3];
+        __syncthreads();
+        if (again) sums(std::true_type());
+    }
 #pragma unroll
     for (int i = 0; i < RB; i++)
 #pragma unroll
@@ -828,10 +872,24 @@ __global__ __launch_bounds__(256) void k_lora_up(const u4v* __restrict__ u, int 
                 for (int j = 0; j < 4; j++) f[g][h][j] = c.c[h][j];
         }
     }
+    f4v acc[4];
+    auto value = [&](int q, wv o4) {  // of row q of acc
+        f4v v = {acc[0][q], acc[1][q], acc[2][q], acc[3][q]};
+        if (base) {
+            if constexpr (ACT == kActF32) {
+                v += __builtin_bit_cast(f4v, o4);
+            } else {
+                float e, o;
+                cvt2<ACT>(o4[0], e, o); v.x += e; v.y += o;
+                cvt2<ACT>(o4[1], e, o); v.z += e; v.w += o;
+            }
+        }
+        return v;
+    };
+    uint32_t todo = 0;  // blocks of 16 rows, not written yet for a NaN
 #pragma unroll
     for (int b = 0; b < 4; b++) {
         if (16 * b >= sl.rows) break;
-        f4v acc[4];
 #pragma unroll
         for (int j = 0; j < 4; j++) acc[j] = f4v{0.f, 0.f, 0.f, 0.f};
         if (r > 0) {
@@ -845,23 +903,69 @@ __global__ __launch_bounds__(256) void k_lora_up(const u4v* __restrict__ u, int 
                     acc[j] = mma_parts<P>(a[g], p, acc[j]);
                 }
             if (b < 3 && 16 * (b + 1) < sl.rows) load_u(b + 1);
+            if (__ballot(has_nan(acc[0]) | has_nan(acc[1]) | has_nan(acc[2]) | has_nan(acc[3]))) {
+                todo |= 1u << b;
+                continue;
+            }
         }
         if (c0 < N)
 #pragma unroll
             for (int q = 0; q < 4; q++) {
-                f4v v = {acc[0][q], acc[1][q], acc[2][q], acc[3][q]};
-                if (base) {
-                    if constexpr (ACT == kActF32) {
-                        v += __builtin_bit_cast(f4v, old[b][q]);
-                    } else {
-                        float e, o;
-                        cvt2<ACT>(old[b][q][0], e, o); v.x += e; v.y += o;
-                        cvt2<ACT>(old[b][q][1], e, o); v.z += e; v.w += o;
-                    }
-                }
+                f4v v = value(q, old[b][q]);
                 if (r < 0) v.x = v.y = v.z = v.w = __builtin_nanf("");
                 if (16 * b + 4 * lq + q < sl.rows) st4<ACT>(y + (size_t)t[b][q] * ldy + c0, v);
             }
+    }
+    if (!todo) return;
+    // See nan_or_inf. Everything is loaded again, from places that the compiler
+    // does not know to be the same: kept for this, they take the registers of a
+    // workgroup above.
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    const int i2 = ln & 15, q2 = ln >> 4, c2 = blockIdx.x * kUpCols + wave * 64 + 4 * i2, cl2 = min(c2, N - 4);
+    const int tok = perm[sl.row + min(ln, sl.rows - 1)];
+    const rsrc_t rf = make_rsrc(fac[sl.g], (uint32_t)r * (uint32_t)N * 2u);
+#pragma unroll 1
+    for (int b = 0; b < 4; b++) {
+        if (!(todo >> b & 1u)) continue;
+        f4v first[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) acc[j] = first[j] = f4v{0.f, 0.f, 0.f, 0.f};
+        const int row = sl.row + min(16 * b + i2, sl.rows - 1);
+#pragma unroll 1
+        for (int g = 0; g < NG; g++) {
+            u2v w[8];
+            u4v au[3];
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const uint2 x = ld_b64(rf, ((uint32_t)(32 * g + 8 * q2 + i) * (uint32_t)N + (uint32_t)cl2) * 2u);
+                w[i] = u2v{x.x, x.y};
+            }
+#pragma unroll
+            for (int h = 0; h < 3; h++) au[h] = u[((size_t)h * T + row) * CH + 4 * g + q2];
+            Cols16<F16> c;
+            cols16<F16>(w, c);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                u4v p[P];
+#pragma unroll
+                for (int h = 0; h < P; h++) p[h] = c.c[h][j];
+                acc[j] = mma_parts<P>(au, p, acc[j]);
+                first[j] = mma_bf16(au[0], p[0], first[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) acc[j][q] = is_nan(acc[j][q]) ? nan_or_inf(first[j][q]) : acc[j][q];
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const int tq = __shfl(tok, 16 * b + 4 * q2 + q, 64);
+            if (16 * b + 4 * q2 + q >= sl.rows || c2 >= N) continue;
+            wv o = {};
+            if (base) o = *reinterpret_cast<const wv*>(base + (size_t)tq * ldb + c2);
+            st4<ACT>(y + (size_t)tq * ldy + c2, value(q, o));
+        }
     }
 }
 
@@ -991,22 +1095,83 @@ __global__ __launch_bounds__(256) void k_lora_grad(GradSide ga, GradSide gb, int
             }
         }
     }
-    if (c0 >= cols) return;
     const bool whole = grp.rows <= piece;
     typedef __attribute__((address_space(1))) f4v* gp;  // the table's pointers are to global memory
     float* to = whole ? out : part + (size_t)blockIdx.y * R16 * ((size_t)ga.cols + gb.cols) +
                                   (second ? (size_t)R16 * ga.cols : 0);
+    int nan = 0;
 #pragma unroll
     for (int b = 0; b < RB; b++)
 #pragma unroll
-        for (int q = 0; q < 4; q++) {
-            const int m = 16 * b + 4 * lq + q;
-            if (m >= r) continue;
-            gp p = (gp)(uintptr_t)(to + (size_t)m * cols + c0);
-            f4v v = {acc[b][0][q], acc[b][1][q], acc[b][2][q], acc[b][3][q]};
-            if (whole && accumulate) v += *p;
-            *p = v;
+        for (int j = 0; j < 4; j++) nan |= has_nan(acc[b][j]);
+    if (!__ballot(nan)) {
+        if (c0 >= cols) return;
+#pragma unroll
+        for (int b = 0; b < RB; b++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const int m = 16 * b + 4 * lq + q;
+                if (m >= r) continue;
+                gp p = (gp)(uintptr_t)(to + (size_t)m * cols + c0);
+                f4v v = {acc[b][0][q], acc[b][1][q], acc[b][2][q], acc[b][3][q]};
+                if (whole && accumulate) v += *p;
+                *p = v;
+            }
+        return;
+    }
+    // see nan_or_inf: the other sums are written as they are
+    uint32_t todo[4] = {0, 0, 0, 0};  // of column j: bit 4 b + q
+    auto place = [&](int b, int q, int j) { return to + (size_t)(16 * b + 4 * lq + q) * cols + c0 + j; };
+    auto write = [&](float* p, float v) { *p = whole && accumulate ? *p + v : v; };
+#pragma unroll
+    for (int b = 0; b < RB; b++)
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                if (c0 >= cols || 16 * b + 4 * lq + q >= r) continue;
+                if (is_nan(acc[b][j][q])) todo[j] |= 1u << (4 * b + q);
+                else write(place(b, q, j), acc[b][j][q]);
+            }
+#pragma unroll 1
+    for (int b = 0; b < RB; b++) {
+        if (!__ballot((todo[0] | todo[1] | todo[2] | todo[3]) >> (4 * b) & 15u)) continue;
+        f4v first[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) first[j] = f4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int k = 0; k < 2 * tiles; k++) {  // 32 tokens
+            const int tk = perm[sl.row + min(32 * k + (lane & 31), sl.rows - 1)];
+            const u4v a = low[(k / 2) * TILE + (16 * b + li) * 8 + ((4 * (k % 2) + lq) ^ swizzle<8>(li))];
+            wv w[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const wv v = *reinterpret_cast<const wv*>(X + (size_t)__shfl(tk, 8 * lq + i, 64) * side.ld);
+#pragma unroll
+                for (int d = 0; d < WB; d++) w[i][d] = 32 * k + 8 * lq + i < sl.rows ? v[d] : 0u;
+            }
+            u4v f[4];
+            if constexpr (ACT == kActF32) {
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+#pragma unroll
+                    for (int q = 0; q < 4; q++)
+                        f[j][q] = pack_first(__uint_as_float(w[2 * q][j]), __uint_as_float(w[2 * q + 1][j]));
+            } else {
+                Cols16<ACT == kActF16> c;
+                cols16<ACT == kActF16>(w, c);
+#pragma unroll
+                for (int j = 0; j < 4; j++) f[j] = c.c[0][j];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j++) first[j] = mma_bf16(a, f[j], first[j]);
         }
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                if (todo[j] >> (4 * b + q) & 1u) write(place(b, q, j), nan_or_inf(first[j][q]));
+    }
 }
 
 // grid (column blocks of 1024, R, n): gradients of adapters with no token

@@ -370,7 +370,9 @@ typedef struct moe_lora_desc {
  * where base is the projection's output. y may be base (the same rows and
  * stride). Products and sums in fp32 (16-bit operands multiply exactly, fp32
  * activations enter with all their bits); the intermediate A_a x stays fp32;
- * y is rounded once. Results are bit-identical from run to run.
+ * y is rounded once. Infinities and NaN enter the sums as in fp32 arithmetic;
+ * an fp32 value's bits below 2^-133 may count as 0. Results are bit-identical
+ * from run to run.
  *   x     [T] rows of K, stride ldx elements;  base (or NULL: zeros) and y
  *         [T] rows of N, strides ldbase and ldy. 16-B aligned, strides
  *         multiples of 8 and at least the row.
@@ -398,8 +400,8 @@ int moe_lora_apply(const moe_lora_desc *l, const void *x, int64_t ldx, int32_t T
  *           gradient of x, or NULL: zeros; dx may be dx_base; dx may be NULL)
  *   dA_a  = sum_{t: ids[t] = a} v_t x[t]^T   ([r_a][K] fp32)
  *   dB_a  = sum_{t: ids[t] = a} u_t dy[t]^T  ([r_a][N] fp32)
- * Tables, types, alignment and strides as for moe_lora_apply; dy [T] rows of
- * N. da_ptrs and db_ptrs are DEVICE arrays of n pointers to fp32 memory (16-B
+ * Tables, types, arithmetic, alignment and strides as for moe_lora_apply; dy
+ * [T] rows of N. da_ptrs and db_ptrs are DEVICE arrays of n pointers to fp32 memory (16-B
  * aligned each, no two the same), or NULL; an entry that is NULL skips that
  * adapter's factor (an adapter that is served but not trained). An adapter
  * without tokens gets zeros. accumulate != 0 adds to dA and dB instead of

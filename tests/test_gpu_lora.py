@@ -395,3 +395,35 @@ def test_repeats_streams_and_graphs(m):
     m.moe_lora_apply(*b[6][:-1], wb, stream=sb)
     torch.cuda.synchronize()
     assert torch.equal(a[1], a[4][0]) and torch.equal(b[1], b[4][0])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,R,K,N", [(9, 1, 64, 72), (9, 1, 2560, 8192), (70, 128, 64, 72), (600, 17, 264, 520), (600, 64, 1032, 72),
+                                     (9000, 33, 64, 72)])
+def test_infinities_keep_their_class(m, dt, T, R, K, N):
+    """Infinite activations and factors beside values of few bits: an infinite
+    product stays infinite, with its sign, and only 0 times an infinity or
+    opposite infinities make a NaN, whatever the batch and the rank that
+    choose the kernels. The formula in 64 bits says which."""
+    c = Case(m, dt, T, K, N, [1, 1, 1], "mixed", R=R)
+    inf, nan = float("inf"), float("nan")
+    few = torch.tensor([1.0, -0.5, 1.0 + 2.0 ** -7, -3.0, 0.0, 2.0 ** -3, 1.0 + 2.0 ** -10, 0.40625])  # and one of 11 bits
+    for t in (c.x, c.dy, *c.A, *c.B):
+        t.copy_(few[torch.arange(t.numel()) * 5 % 8].view(t.shape))
+    c.scales[:] = torch.tensor([1.0, -2.0, 0.0])
+    c.ids[:8] = torch.tensor([0, 0, 1, 1, 2, -1, 0, 1], device="cuda")
+    c.x[0, 0], c.x[1, 3], c.x[2, K - 1], c.x[4, 8], c.x[6, 9] = inf, -inf, inf, inf, nan
+    c.dy[3, 5], c.dy[7, N - 1], c.dy[6, 2] = inf, -inf, nan
+    c.A[1][0, 7], c.B[0][0, 3], c.B[0][0, 8], c.B[1][0, N - 2], c.B[1][0, 10] = inf, inf, -inf, -inf, nan
+    y, want = c.apply(), c.want()
+    assert torch.isinf(want[0]).any() and torch.isnan(want[0]).any() and torch.isfinite(want[0]).any()
+    ref.close(y, *want, "y")
+    c.check_backward(c.backward())
+    # and where nothing but the activations is infinite
+    c = Case(m, dt, T, K, N, [1, 1], "mixed", R=R)
+    for t in (c.x, c.dy, *c.A, *c.B):
+        t.copy_(few[torch.arange(t.numel()) * 5 % 8].view(t.shape))
+    c.ids[:4] = torch.tensor([0, 1, 0, 1], device="cuda")
+    c.x[0, 1], c.x[1, 2], c.dy[2, 3], c.dy[3, 1] = inf, -inf, inf, -inf
+    ref.close(c.apply(), *c.want(), "y")
+    c.check_backward(c.backward())
