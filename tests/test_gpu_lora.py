@@ -427,3 +427,22 @@ def test_infinities_keep_their_class(m, dt, T, R, K, N):
     c.x[0, 1], c.x[1, 2], c.dy[2, 3], c.dy[3, 1] = inf, -inf, inf, -inf
     ref.close(c.apply(), *c.want(), "y")
     c.check_backward(c.backward())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,K,N,ranks,order", [
+    (8193, 64, 72, [5, 16, 1], "mixed"), (16500, 64, 72, [17, 3], "mixed"),  # ids in more than one span of 8192
+    (13500, 264, 520, [16, 9, 33], "runs"),  # pieces of three tiles, several an adapter, the last ones ragged
+    (9000, 1032, 2056, [64, 7], "mixed"),    # pieces of four tiles
+    (1 << 20, 8, 16, [3, 1], "mixed")])      # the longest batch: pieces of 64 tiles
+def test_long_batches(m, dt, T, K, N, ranks, order):
+    c = Case(m, dt, T, K, N, ranks, order)
+    ref.close(c.apply(), *c.want(), "y")
+    c.check_backward(c.backward())
+
+
+@pytest.mark.parametrize("T,dt", [(1, "bf16"), (300, "f16"), (3000, "f32"), (3000, "bf16")])
+def test_as_many_adapters_as_the_tables_hold(m, T, dt):
+    c = Case(m, dt, T, 64, 72, [a % 4 for a in range(1024)], "mixed")
+    ref.close(c.apply(), *c.want(), "y")
+    c.check_backward(c.backward())
