@@ -446,3 +446,26 @@ def test_as_many_adapters_as_the_tables_hold(m, T, dt):
     c = Case(m, dt, T, 64, 72, [a % 4 for a in range(1024)], "mixed")
     ref.close(c.apply(), *c.want(), "y")
     c.check_backward(c.backward())
+
+
+@pytest.mark.parametrize("T,K,N,r", [(40, 2560, 640, 16), (600, 64, 2560, 16), (600, 2560, 64, 64), (2500, 264, 520, 128), (4000, 520, 264, 17)])
+def test_norm_of_the_error(m, T, K, N, r):
+    """Beside the elementwise worst case: over random values the roundings of a
+    sum of L products add up like a random walk. The i-th partial sum is about
+    sqrt(i / L) of the root S of the sum of squared products, and one rounding
+    has a variance of EPS^2 / 3 of its square, so the error is about
+    sqrt(L / 6) EPS S. A product of parts has up to eight terms, sqrt(8) at
+    most; four times the walk is allowed. Leaving out the third part of an
+    operand, 2^-16.4 of it by the root mean square, is more at every size here."""
+    c = Case(m, "f32", T, K, N, [r], "one")
+    walk = lambda L, a, b: (L / 6) ** 0.5 * ref.EPS * torch.sqrt((a ** 2) @ (b ** 2))  # noqa: E731
+    thru = lambda e, b: torch.sqrt((e ** 2) @ (b ** 2))  # noqa: E731
+    x, dy, A, B, s = c.x.cpu().double(), c.dy.cpu().double(), c.A[0].cpu().double(), c.B[0].cpu().double(), float(c.scales[0])
+    u, v = s * (x @ A.t()), s * (dy @ B.t())
+    eu, ev = walk(K, s * x, A.t()), walk(N, s * dy, B.t())
+    out = {"y": c.apply(base=None), "dx": c.backward(base=False), "dA": c.dA[0], "dB": c.dB[0]}
+    want = {"y": (u @ B, walk(r, u, B) + thru(eu, B)), "dx": (v @ A, walk(r, v, A) + thru(ev, A)),
+            "dA": (v.t() @ x, walk(T, v.t(), x) + thru(ev.t(), x)), "dB": (u.t() @ dy, walk(T, u.t(), dy) + thru(eu.t(), dy))}
+    for name, (value, walked) in want.items():
+        off = (out[name].cpu().double() - value).norm() / (4 * walked.norm())
+        assert off <= 1, (name, off)
