@@ -152,9 +152,10 @@ __device__ __forceinline__ void add_routing(float (&v)[NV], COL col, int E, int 
 // fp32 form
 
 // grid ceil(T / 4), 256 threads: one wave per token; lane owns columns
-// lane + 64 i (i < NV).
+// lane + 64 i (i < NV). dout may be din: a wave loads its row before it writes
+// it, and no other wave touches it.
 template <int NV>
-__global__ __launch_bounds__(256) void k_rg_logits(const float* __restrict__ din, const int32_t* __restrict__ idx,
+__global__ __launch_bounds__(256) void k_rg_logits(const float* din, const int32_t* __restrict__ idx,
                                                    const float* __restrict__ w, const float* __restrict__ dw,
                                                    const uint8_t* __restrict__ mask, int T, int E, int Ep, int k,
                                                    float* __restrict__ G, float* dout) {
@@ -426,9 +427,10 @@ __device__ __forceinline__ void make_panel(const Panel& j, int b, f4v (*red)[8])
 // grid ng + panels of x + panels of Wr, 1024 threads or fewer. The first ng
 // workgroups make G (a wave two tokens, a lane the columns 8 lane + 512 c + i):
 // in fp32 for k_rg_gt (unless dout serves), and its rows' parts ga [tile][2][Ep / 8][BM].
-// Everything a wave needs is loaded before its mask bytes are looked at.
+// Everything a wave needs is loaded before its mask bytes are looked at, and
+// before it writes (dout may be din; no other wave uses its two rows' values).
 template <int NC>
-__global__ __launch_bounds__(1024) void k_rg_prep(const float* __restrict__ din, const int32_t* __restrict__ idx,
+__global__ __launch_bounds__(1024) void k_rg_prep(const float* din, const int32_t* __restrict__ idx,
                                                   const float* __restrict__ w, const float* __restrict__ dw,
                                                   const uint8_t* __restrict__ mask, int T, int E, int Ep, int k,
                                                   int vec, float* __restrict__ G, float* dout, u4v* __restrict__ ga,

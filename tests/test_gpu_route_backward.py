@@ -298,3 +298,14 @@ def test_long_batch_offsets_past_32_bits(m):
     # some columns of dWr over all tokens
     c = torch.tensor([0, 1, 777, 1280, 2559])
     ref.close(dWr[:, c.to(dev)], *ref.mm(G.t().contiguous(), x[:, c.to(dev)].cpu().double(), pairs=True), "dWr")
+
+
+@pytest.mark.parametrize("T,E,H", [(91, 64, 512), (1101, 512, 1024), (1023, 520, 1280), (8191, 32, 2560)])
+@pytest.mark.parametrize("dw", [True, False])
+def test_in_place_on_whole_vectors(m, T, E, H, dw):
+    """dlogits_out is dlogits_in where rows are loaded and written 16 bytes at a time, in batches of odd length."""
+    c = Case(m, T, E, 4, H, 0.2)
+    a, b = c.run(dw=dw), c.run(dw=dw, inplace=True)
+    for name in a:
+        assert torch.equal(a[name], b[name]), name
+    c.check(b, dw=dw)
