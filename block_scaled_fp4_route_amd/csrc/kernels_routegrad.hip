@@ -82,7 +82,7 @@ RgPlan rg_plan(int H, int E, int T) {
             per = kTK;
             if (tiles < 1 || len < 1) return;  // no tokens
             int64_t n = (256 + tiles - 1) / tiles;
-            if (len / kMaxPart > n) n = len / kMaxPart;
+            if ((len + kMaxPart - 1) / kMaxPart > n) n = (len + kMaxPart - 1) / kMaxPart;
             const int64_t most = (len + 2 * kTK - 1) / (2 * kTK);
             if (n > most) n = most;
             if (n < 1) n = 1;

@@ -309,3 +309,17 @@ def test_in_place_on_whole_vectors(m, T, E, H, dw):
     for name in a:
         assert torch.equal(a[name], b[name]), name
     c.check(b, dw=dw)
+
+
+@pytest.mark.parametrize("T,E,H", [(3000, 1, 8192), (2047, 3, 8192), (5000, 9, 256), (1500, 2, 2560)])
+def test_parts_of_long_sums_are_bounded(m, T, E, H):
+    """Below 2^29 multiplications dWr is summed over parts of at most 1024
+    tokens. Beside 2^26 a 1, or a few ones added together, is half a step at
+    most and lost, so of T - 1 ones no more than those of the first token's own
+    part may be missing (and one step where the parts are added)."""
+    c = Case(m, T, E, 1, H)
+    c.din.fill_(1.0)
+    c.x.fill_(1.0)
+    c.x[0] = 2.0 ** 26
+    out = c.run(dw=False, dx=False)["dWr"].double().cpu()
+    assert (out <= 2.0 ** 26 + T + 8).all() and (out >= 2.0 ** 26 + T - 1 - 1024 - 8).all(), (out.min() - 2.0 ** 26).item()
