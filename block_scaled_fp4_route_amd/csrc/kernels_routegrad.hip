@@ -4,7 +4,7 @@
 //   G        = dlogits_in + ds scattered to the chosen experts (masked tokens: 0)
 //   dx       = G Wr        [T][H], over E
 //   dWr      = G^T x       [E][H], over T
-// Two forms of the two products, chosen by their size (kPairFrom):
+// Two forms of the two products, chosen by their size (pair_form):
 //   fp32  k_rg_logits writes G, k_rg_gemm runs both products as one launch on
 //         v_mfma_f32_16x16x4_f32.
 //   pair  operands as pairs of fp16 parts (see pair_exp): k_rg_prep writes G
@@ -33,7 +33,17 @@ constexpr int kMaxPart = 1024;                 // rows of a part of a product's 
 // launches): all kernels together, fp32 against pairs, E = 512, H = 2560:
 // T = 64 18 against 33 us, 311 33 against 40, 700 50 against 44, 1200 98
 // against 65, 2451 157 against 89; E = 384, H = 4096, T = 311: 32 against 40.
+// And only above 64 experts: up to there one fp32 tile holds all of them, so
+// that x passes through the product once, and making its parts costs more than
+// they save. Calls of T x E x H, fp32 against pairs: 8191 x 8 x 4096 112
+// against 157 us, x 32 113 against 158, x 64 132 against 164; 8191 x 64 x 1024
+// 54 against 57; 2048 x 64 x 8192 92 against 94; 32768 x 8 x 4096 322 against
+// 538; 2^20 x 64 x 256 1222 against 2021. Above, pairs are from 17% slower to
+// 1.8 times as fast: 8191 x 66 x 4096 150 against 170, 2^20 x 96 x 512 2779
+// against 3259, 8191 x 128 x 4096 167 against 178, x 2560 134 against 119, x
+// 1024 87 against 60, 8191 x 256 x 4096 306 against 205.
 constexpr int64_t kPairFrom = (int64_t)1 << 29;
+bool pair_form(int H, int E, int T) { return E > kTM && (int64_t)T * E * H >= kPairFrom; }
 
 typedef _Float16 h2v __attribute__((ext_vector_type(2)));
 typedef _Float16 h8v __attribute__((ext_vector_type(8)));
@@ -53,7 +63,7 @@ struct RgPlan {
 RgPlan rg_plan(int H, int E, int T) {
     RgPlan p = {};
     p.Ep = (E + kTK - 1) / kTK * kTK;
-    if ((int64_t)T * E * H >= kPairFrom) {
+    if (pair_form(H, E, T)) {
         p.nt = H / kPairCols;
         // 256-row tiles read less per product; 128-row ones where the larger
         // would leave compute units idle (E = 512, H = 2560: 240 larger tiles

@@ -322,12 +322,13 @@ int moe_balance_loss(const moe_desc *d, const float *logits, int32_t T, const in
  * Tokens with mask[t] == 0 have G = 0, and their values do not matter. A token
  * with an index outside [0, E) (dw given) has G = NaN in its whole row. Sums in
  * fp32; results are bit-identical from run to run. Below 2^29 multiplications
- * (T E H) the products have fp32 operands. From there on each operand is a
- * pair of fp16 values under a power of two for its row or column, h + l with h
- * = fp16(v), l = fp16(v - h), and the product of the two l is left out: off by
- * at most 3 * 2^-22 of each product, and for values below 2^-17 of their row's
- * (Wr, x: column's) largest by 2^-39 of that largest, whatever the exponents.
- * An infinity or a NaN there makes every sum that it enters infinite or NaN.
+ * (T E H), and with up to 64 experts, the products have fp32 operands.
+ * Otherwise each operand is a pair of fp16 values under a power of two for its
+ * row or column, h + l with h = fp16(v), l = fp16(v - h), and the product of
+ * the two l is left out: off by at most 3 * 2^-22 of each product, and for
+ * values below 2^-17 of their row's (Wr, x: column's) largest by 2^-39 of that
+ * largest, whatever the exponents. An infinity or a NaN there makes every sum
+ * that it enters infinite or NaN.
  *   x [T][H], Wr [E][H] fp32, 16-B aligned (x may be NULL without dWr, Wr
  *   without dx);  idx [T][k] int32, w [T][k], dw [T][k] fp32 (dw NULL: only
  *   dlogits_in; idx and w are then not used);  mask [T] uint8 or NULL;

@@ -323,3 +323,70 @@ def test_parts_of_long_sums_are_bounded(m, T, E, H):
     c.x[0] = 2.0 ** 26
     out = c.run(dw=False, dx=False)["dWr"].double().cpu()
     assert (out <= 2.0 ** 26 + T + 8).all() and (out >= 2.0 ** 26 + T - 1 - 1024 - 8).all(), (out.min() - 2.0 ** 26).item()
+
+
+@pytest.mark.parametrize("T,E,H", [(8191, 8, 4096), (8191, 33, 2560), (2100, 64, 4096), (16500, 64, 768)])
+def test_few_experts_multiply_in_fp32(m, T, E, H):
+    """Up to 64 experts, batches of any length have fp32 products: operands
+    2^30 apart within a row, whose products are alike, keep fp32's accuracy."""
+    c = Case(m, T, E, min(E, 4), H, 0.1)
+    for s in range(2):
+        c.din = torch.randn(T, E, generator=torch.Generator().manual_seed(T + s))
+        if s == 0:  # along the experts
+            c.din[:, 1:] *= 2.0 ** -30
+            c.Wr[0] *= 2.0 ** -30
+        else:       # along the tokens
+            c.din[2:] *= 2.0 ** -30
+            c.x[:2] *= 2.0 ** -30
+        out = c.run(dw=False)
+        G = c.din.double() * c.mask[:, None]
+        if s == 0:
+            ref.close(out["dx"], *ref.mm(G, c.Wr.double()), "dx")
+        else:
+            ref.close(out["dWr"], *ref.mm(G.t().contiguous(), c.x.double()), "dWr")
+
+
+@pytest.mark.parametrize("T,E,H", [(3000, 72, 2560), (9000, 65, 1024)])
+@pytest.mark.parametrize("acc", [1, 2, 3])
+def test_accumulate_in_pairs(m, T, E, H, acc):
+    c = Case(m, T, E, 4, H)
+    g = torch.Generator().manual_seed(1)
+    old = {"dx": torch.randn((T, H), generator=g), "dWr": torch.randn((E, H), generator=g)}
+    want, out = c.want(), c.run(acc=acc, before=old)
+    for bit, name in ((1, "dx"), (2, "dWr")):
+        v, e = want[name]
+        if acc & bit:
+            v, e = v + old[name].double(), e + ref.EPS * (v.abs() + old[name].double().abs()) * 2
+        ref.close(out[name], v, e, name)
+
+
+def test_infinite_and_nan_values_in_pairs(m):
+    c = Case(m, 4100, 72, 3, 2560)
+    c.din[5, 3], c.din[9, 8], c.Wr[3, 17] = float("inf"), float("nan"), 0.0
+    out, want = c.run(dw=False), c.want(dw=False)
+    ok = [t for t in range(4100) if t not in (5, 9)]
+    ref.close(out["dx"][ok], want["dx"][0][ok], want["dx"][1][ok], "dx")
+    assert not torch.isfinite(out["dx"][5]).any() and torch.isnan(out["dx"][9]).all()
+    ok = [e for e in range(72) if e not in (3, 8)]
+    ref.close(out["dWr"][ok], want["dWr"][0][ok], want["dWr"][1][ok], "dWr")
+    assert not torch.isfinite(out["dWr"][3]).any() and torch.isnan(out["dWr"][8]).all()
+
+
+def test_long_batch_of_pairs_past_32_bits(m):
+    """2^20 tokens of 2304 with 72 experts: more than 2^31 elements of x, dx and the pairs."""
+    T, E, H, dev = 1 << 20, 72, 2304, "cuda"
+    g = torch.Generator(device=dev).manual_seed(3)
+    x = torch.empty((T, H), device=dev)
+    for part in x.split(1 << 17):
+        part.normal_(generator=g)
+    Wr, din = torch.randn((E, H), device=dev, generator=g), torch.randn((T, E), device=dev, generator=g)
+    d = m.desc(H, 64, E, 2, "nvfp4")
+    dx, dWr = torch.empty((T, H), device=dev), torch.empty((E, H), device=dev)
+    ws = torch.empty(m.moe_route_backward_workspace_bytes(d, T), dtype=torch.uint8, device=dev)
+    m.moe_route_backward(d, x, T, Wr, None, None, None, None, din, None, dx, dWr, 0, ws)
+    torch.cuda.synchronize()
+    t = torch.cat([torch.arange(8), torch.randint(0, T, (200,), generator=torch.Generator().manual_seed(1)), torch.arange(T - 8, T)])
+    G = din.cpu().double()
+    ref.close(dx[t.to(dev)], *ref.mm(G[t], ref.cpu64(Wr), pairs=True), "dx")
+    c = torch.tensor([0, 1, 777, 1280, H - 1])
+    ref.close(dWr[:, c.to(dev)], *ref.mm(G.t().contiguous(), x[:, c.to(dev)].cpu().double(), pairs=True), "dWr")
