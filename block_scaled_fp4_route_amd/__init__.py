@@ -10,7 +10,7 @@ from .binding import (  # noqa: F401
     alloc_workspace, desc, expert_ptr_table, lib, moe_block_bytes, moe_block_layout, moe_dequant_block,
     moe_act_quant_fp8, moe_expert_decode, moe_expert_prefetch, moe_prefetch_sink_bytes, moe_expert_prefill, moe_gemv_fp8, moe_layer_decode, moe_layer_decode_noalloc, moe_route,
     moe_workspace_bytes,
-    MOE_ACC_DWR, MOE_ACC_DX, MOE_ACT_BF16, MOE_ACT_F16, MOE_ACT_F32, lora_desc, moe_balance_loss,
+    MOE_ACC_DWR, MOE_ACC_DX, MOE_ACT_BF16, MOE_ACT_F16, MOE_ACT_F32, MOE_FP32_PRODUCTS, lora_desc, moe_balance_loss,
     moe_balance_workspace_bytes, moe_lora_apply, moe_lora_backward, moe_lora_workspace_bytes, moe_route_backward,
     moe_route_backward_workspace_bytes,
 )

@@ -19,7 +19,7 @@ MOE_OK, MOE_ERR_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_HIP, MOE_ERR_WORKSPACE = 0, -1
 MOE_MODE_ROUTE, MOE_MODE_DECODE, MOE_MODE_PREFILL = 0, 1, 2
 MOE_OUT_F32, MOE_OUT_BF16 = 0, 1
 MOE_NOALLOC_SCRATCH_BYTES = 1 << 20
-MOE_ACC_DX, MOE_ACC_DWR = 1, 2
+MOE_ACC_DX, MOE_ACC_DWR, MOE_FP32_PRODUCTS = 1, 2, 8
 MOE_ACT_F32, MOE_ACT_BF16, MOE_ACT_F16 = 0, 1, 2
 FORMATS = {"nvfp4": MOE_FMT_NVFP4, "mxfp4": MOE_FMT_MXFP4}
 

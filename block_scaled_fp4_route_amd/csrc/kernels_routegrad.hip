@@ -4,7 +4,8 @@
 //   G        = dlogits_in + ds scattered to the chosen experts (masked tokens: 0)
 //   dx       = G Wr        [T][H], over E
 //   dWr      = G^T x       [E][H], over T
-// Two forms of the two products, chosen by their size (pair_form):
+// Two forms of the two products, chosen by their size (pair_form), the first
+// also by the caller (accumulate's bit 8, MOE_FP32_PRODUCTS):
 //   fp32  k_rg_logits writes G, k_rg_gemm runs both products as one launch on
 //         v_mfma_f32_16x16x4_f32.
 //   pair  operands as pairs of fp16 parts (see pair_exp): k_rg_prep writes G
@@ -29,19 +30,20 @@ constexpr int kPairCols = 128;                 // columns of a tile in pair form
 constexpr int kMaxPart = 1024;                 // rows of a part of a product's long axis
 
 // Multiplications (T E H) from which the products run by pairs of fp16 parts.
-// The parts cost a fixed 25 us or so (their panels written and read, two more
-// launches): all kernels together, fp32 against pairs, E = 512, H = 2560:
-// T = 64 18 against 33 us, 311 33 against 40, 700 50 against 44, 1200 98
-// against 65, 2451 157 against 89; E = 384, H = 4096, T = 311: 32 against 40.
+// The parts cost a fixed 15 us or so (their panels written and read, two more
+// launches). Whole calls, fp32 against pairs, E = 512, H = 2560: T = 64 15
+// against 29 us, 311 31 against 35, 409 (the limit) 35 against 37, 700 45
+// against 42, 1200 74 against 63, 2451 124 against 82, 8191 376 against 201;
+// E = 384, H = 4096: T = 311 27 against 42, 450 39 against 44.
 // And only above 64 experts: up to there one fp32 tile holds all of them, so
 // that x passes through the product once, and making its parts costs more than
-// they save. Calls of T x E x H, fp32 against pairs: 8191 x 8 x 4096 112
-// against 157 us, x 32 113 against 158, x 64 132 against 164; 8191 x 64 x 1024
-// 54 against 57; 2048 x 64 x 8192 92 against 94; 32768 x 8 x 4096 322 against
-// 538; 2^20 x 64 x 256 1222 against 2021. Above, pairs are from 17% slower to
-// 1.8 times as fast: 8191 x 66 x 4096 150 against 170, 2^20 x 96 x 512 2779
-// against 3259, 8191 x 128 x 4096 167 against 178, x 2560 134 against 119, x
-// 1024 87 against 60, 8191 x 256 x 4096 306 against 205.
+// they save. T x E x H, fp32 against pairs: 8191 x 8 x 4096 112 against 157 us,
+// x 32 113 against 158, x 64 132 against 164; 8191 x 64 x 1024 54 against 57;
+// 2048 x 64 x 8192 92 against 94; 32768 x 8 x 4096 322 against 538; 2^20 x 64
+// x 256 1222 against 2021. Above, pairs are from 17% slower to 1.9 times as
+// fast: 8191 x 66 x 4096 150 against 170, 2^20 x 96 x 512 2779 against 3259,
+// 8191 x 128 x 4096 167 against 178, x 2560 134 against 119, x 1024 87 against
+// 60, 8191 x 256 x 4096 306 against 205.
 constexpr int64_t kPairFrom = (int64_t)1 << 29;
 bool pair_form(int H, int E, int T) { return E > kTM && (int64_t)T * E * H >= kPairFrom; }
 
@@ -60,10 +62,11 @@ struct RgPlan {
     size_t g, egr, egc, ex, ew, ga, gt, xb, wb, px, pw, total;
 };
 
-RgPlan rg_plan(int H, int E, int T) {
+// fp32: the fp32 form at every size (its regions are a part of the other one's).
+RgPlan rg_plan(int H, int E, int T, bool fp32 = false) {
     RgPlan p = {};
     p.Ep = (E + kTK - 1) / kTK * kTK;
-    if (pair_form(H, E, T)) {
+    if (!fp32 && pair_form(H, E, T)) {
         p.nt = H / kPairCols;
         // 256-row tiles read less per product; 128-row ones where the larger
         // would leave compute units idle (E = 512, H = 2560: 240 larger tiles
@@ -208,7 +211,7 @@ struct RgArgs {
 // b of the wave's 32 x 32 square. Small tiles: what runs in this form has few
 // of them, and splitting the sums instead costs their parts' traffic. Bound by
 // latency at few tokens (8 us at T = 1), then by the fp32 matrix rate: 311 x 384
-// x 4096 27 us, 73 TFLOP/s; 2451 x 512 x 2560 (not run so) 146 us, 88 TFLOP/s.
+// x 4096 27 us, 73 TFLOP/s; 2451 x 512 x 2560 (on request) 124 us, 104 TFLOP/s.
 constexpr int kLdsRow = kTM + 4;
 constexpr int kLdsStep = 2 * kTK * kLdsRow;
 
@@ -770,7 +773,7 @@ hipError_t launch_route_backward(int H, int E, int k, const float* x, int T, con
                                  const float* w, const float* dw, const uint8_t* mask, const float* dlogits_in,
                                  float* dlogits_out, float* dx, float* dWr, int accumulate, void* ws, hipStream_t s) {
     if (T == 0 && (!dWr || accumulate & 2)) return hipSuccess;  // no tokens: zeros for dWr at most
-    const RgPlan p = rg_plan(H, E, T);
+    const RgPlan p = rg_plan(H, E, T, accumulate & 8);
     char* base = reinterpret_cast<char*>(ws);
     float* G = reinterpret_cast<float*>(base + p.g);
     const int nx = dx && T > 0 ? p.mt * p.nt * p.sx : 0, nw = dWr ? p.et * p.nt * p.sw : 0;

@@ -423,7 +423,7 @@ int moe_route_backward(const moe_desc* d, const float* x, int32_t T, const float
                        void* stream) {
     int r;
     if ((r = route_backward_checks(d, T))) return r;
-    if (accumulate & ~(MOE_ACC_DX | MOE_ACC_DWR)) return fail(MOE_ERR_ARG, "unknown accumulate bits %d", accumulate);
+    if (accumulate & ~(MOE_ACC_DX | MOE_ACC_DWR | MOE_FP32_PRODUCTS)) return fail(MOE_ERR_ARG, "unknown accumulate bits %d", accumulate);
     if (T > 0) {
         if (!dw && !dlogits_in) return fail(MOE_ERR_ARG, "neither dw nor dlogits_in");
         if (!dlogits_out && !dx && !dWr) return fail(MOE_ERR_ARG, "no output");

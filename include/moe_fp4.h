@@ -312,6 +312,7 @@ int moe_balance_loss(const moe_desc *d, const float *logits, int32_t T, const in
 
 #define MOE_ACC_DX 1  /* add to dx instead of writing it */
 #define MOE_ACC_DWR 2 /* add to dWr instead of writing it */
+#define MOE_FP32_PRODUCTS 8 /* fp32 operands in batches of any length */
 
 /* The backward pass of moe_route: from dw, the loss's gradient at the
  * routing weights w, and dlogits_in, a gradient that reaches the logits
@@ -322,8 +323,8 @@ int moe_balance_loss(const moe_desc *d, const float *logits, int32_t T, const in
  * Tokens with mask[t] == 0 have G = 0, and their values do not matter. A token
  * with an index outside [0, E) (dw given) has G = NaN in its whole row. Sums in
  * fp32; results are bit-identical from run to run. Below 2^29 multiplications
- * (T E H), and with up to 64 experts, the products have fp32 operands.
- * Otherwise each operand is a pair of fp16 values under a power of two for its
+ * (T E H), with up to 64 experts, and where the caller asks for it
+ * (MOE_FP32_PRODUCTS), the products have fp32 operands. Otherwise each operand is a pair of fp16 values under a power of two for its
  * row or column, h + l with h = fp16(v), l = fp16(v - h), and the product of
  * the two l is left out: off by at most 3 * 2^-22 of each product, and for
  * values below 2^-17 of their row's (Wr, x: column's) largest by 2^-39 of that
@@ -335,7 +336,7 @@ int moe_balance_loss(const moe_desc *d, const float *logits, int32_t T, const in
  *   dlogits_in [T][E] fp32 or NULL (one of dw and dlogits_in is needed);
  *   dlogits_out [T][E] fp32 (out): G, or NULL; may be dlogits_in;
  *   dx [T][H], dWr [E][H] fp32 (out), 16-B aligned, or NULL
- *   accumulate  a sum of MOE_ACC_*
+ *   accumulate  a sum of MOE_ACC_* and MOE_FP32_PRODUCTS
  * Outputs overlap neither inputs nor each other, but for dlogits_out ==
  * dlogits_in. T = 0 writes zeros to dWr (unless it accumulates). Workspace:
  * moe_route_backward_workspace_bytes(d, T), which never falls as T grows.

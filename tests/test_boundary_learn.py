@@ -192,3 +192,11 @@ def test_descs_by_dtype():
     assert m.lora_desc(8, 8, 1, 1, torch.float32).dtype == m.MOE_ACT_F32
     assert m.lora_desc(8, 8, 1, 1, torch.bfloat16).dtype == m.MOE_ACT_BF16
     assert m.lora_desc(8, 8, 1, 1, torch.float16).dtype == m.MOE_ACT_F16
+
+
+def test_fp32_products_is_a_flag_of_its_own():
+    assert m.MOE_FP32_PRODUCTS not in (m.MOE_ACC_DX, m.MOE_ACC_DWR, 4)
+    for acc in range(4):  # accepted up to the workspace
+        assert route_backward(acc=acc + m.MOE_FP32_PRODUCTS, wsb=0) == m.MOE_ERR_WORKSPACE
+    assert route_backward(acc=2 * m.MOE_FP32_PRODUCTS) == m.MOE_ERR_ARG
+    assert route_backward(acc=-1) == m.MOE_ERR_ARG

@@ -390,3 +390,45 @@ def test_long_batch_of_pairs_past_32_bits(m):
     ref.close(dx[t.to(dev)], *ref.mm(G[t], ref.cpu64(Wr), pairs=True), "dx")
     c = torch.tensor([0, 1, 777, 1280, H - 1])
     ref.close(dWr[:, c.to(dev)], *ref.mm(G.t().contiguous(), x[:, c.to(dev)].cpu().double(), pairs=True), "dWr")
+
+
+@pytest.mark.parametrize("T,E,H", [(1100, 512, 1024), (4100, 130, 1280), (2451, 384, 4096)])
+def test_fp32_products_on_request(m, T, E, H):
+    """Operands 2^30 apart within a row, whose products are alike: pairs keep
+    2^-39 of the row's largest, fp32 products all of it."""
+    for along in range(2):
+        c = Case(m, T, E, 4, H, 0.1)
+        c.din = torch.randn(T, E, generator=torch.Generator().manual_seed(T + along))
+        if along == 0:
+            c.din[:, 1:] *= 2.0 ** -30
+            c.Wr[0] *= 2.0 ** -30
+        else:
+            c.din[2:] *= 2.0 ** -30
+            c.x[:2] *= 2.0 ** -30
+        G = c.din.double() * c.mask[:, None]
+        want = ref.mm(G, c.Wr.double()) if along == 0 else ref.mm(G.t().contiguous(), c.x.double())
+        name = "dWr" if along else "dx"
+        ref.close(c.run(dw=False, acc=m.MOE_FP32_PRODUCTS)[name], *want, name)
+        if along == 0:  # (over the tokens each part of the sum has its own power of two)
+            d = (c.run(dw=False)[name].cpu().double() - want[0]).abs()
+            assert (d > want[1]).any()  # the sizes do tell the forms apart
+
+
+def test_fp32_products_with_all_else(m):
+    c = Case(m, 1101, 512, 6, 1024, 0.2)
+    g = torch.Generator().manual_seed(1)
+    old = {"dx": torch.randn((1101, 1024), generator=g), "dWr": torch.randn((512, 1024), generator=g)}
+    G, eG = c.want()["dlogits"]
+    x = c.x.double() * c.mask[:, None]
+    want = {"dx": ref.mm(G, c.Wr.double(), ea=eG), "dWr": ref.mm(G.t().contiguous(), x, ea=eG.t().contiguous())}
+    for acc in range(4):
+        out = c.run(acc=acc + m.MOE_FP32_PRODUCTS, before=old, inplace=acc == 1)
+        for bit, name in ((1, "dx"), (2, "dWr")):
+            v, e = want[name]
+            if acc & bit:
+                v, e = v + old[name].double(), e + ref.EPS * (v.abs() + old[name].double().abs()) * 2
+            ref.close(out[name], v, e, name)
+        ref.close(out["dlogits"], G, eG, "dlogits")
+    few = Case(m, 90, 60, 4, 512)
+    a, b = few.run(), few.run(acc=m.MOE_FP32_PRODUCTS)
+    assert all(torch.equal(a[k], b[k]) for k in a)
