@@ -522,14 +522,19 @@ __global__ __launch_bounds__(256) void k_bal_main(const float* __restrict__ logi
 // over the pieces of a sequence, every gridDim.y-th sequence; the last
 // workgroup to finish adds the sequences up. Every workgroup takes a ticket
 // from one counter, about 15 ns each, and looks at all sequences' numbers, so
-// up to 4 sequences get narrow blocks, many pieces at a time, and more get
-// wide ones (22 us against 8 with 16 columns at 32768 x 512 in 37 sequences,
-// 9.3 with the coherent join below), about kReduceGroups of them in all
-// (32768 x 512 in 200 sequences: 17 us against 35 with one for each, in 1000:
-// 42 against 164, 99 with 2048 in all). Bound by latency: 6 to 7 us for one sequence of
-// 311 or 2451 tokens, of which the ticket and the last workgroup's part are
-// about 2.
-constexpr int kNarrow = 16, kWide = 128, kReduceGroups = 256;
+// up to kFewSeqs sequences get narrow blocks, many pieces at a time, and more
+// get wide ones, about kReduceGroups of them in all. Whole calls, narrow
+// against wide: 2451 x 512 in 1 sequence 18 against 23 us, in 4 19 against 21,
+// in 8 21 against 21, in 16 27 against 21; 32768 x 512 in 1 45 against 54, in 4
+// 44 against 48, in 8 45 against 47, in 16 49 against 43, in 37 70 against 45;
+// 32768 x 64 in 8 28 against 31. (This launch alone, 32768 x 512 in 200
+// sequences: 17 us against 35 with a workgroup for each sequence and block, in
+// 1000: 42 against 164, 99 with 2048 in all.) Bound by latency: 6 to 7 us for
+// one sequence of 311 or 2451 tokens, of which the ticket and the last
+// workgroup's part are about 2. Very many sequences stay slow, since each
+// chunk and each workgroup here looks at all of them: calls of 32768 x 512
+// take 58 us in 200, 94 in 1000, 364 in 8000, 2357 in 65535.
+constexpr int kNarrow = 16, kWide = 128, kFewSeqs = 8, kReduceGroups = 256;
 template <int CB>
 __global__ __launch_bounds__(1024) void k_bal_reduce(const int32_t* __restrict__ off, int T, int E, int k, int S,
                                                      int TB, int J, const int32_t* __restrict__ cnt,
@@ -691,8 +696,8 @@ hipError_t launch_balance(int E, int k, const float* logits, int T, const int32_
 #define BR(CB)                                                                                                         \
     hipLaunchKernelGGL((k_bal_reduce<CB>), dim3((E + CB - 1) / CB, rows), dim3(1024), 0, s, seq_off, T, E, k, S, b.TB, J, cnt, \
                        n, cb, cz, psum, zsum, q, ticket, loss, counts, probs)
-    const int most = kReduceGroups / ((E + kWide - 1) / kWide), rows = S <= 4 || S < most ? S : most;
-    if (S <= 4) BR(kNarrow); else BR(kWide);
+    const int most = kReduceGroups / ((E + kWide - 1) / kWide), rows = S <= kFewSeqs || S < most ? S : most;
+    if (S <= kFewSeqs) BR(kNarrow); else BR(kWide);
 #undef BR
     return hipGetLastError();
 }

@@ -260,3 +260,10 @@ def test_graphs_that_share_a_workspace(m):
                 assert torch.equal(v, w[k]), (turn, k)
         a.ld.add_(0)
         m.moe_balance_loss(*a.args)
+
+
+@pytest.mark.parametrize("T,E,k", [(37, 20, 2), (1900, 512, 10), (700, 1023, 3)])
+@pytest.mark.parametrize("S", [4, 5, 7, 8, 9, 10])
+def test_few_and_many_sequences(m, T, E, k, S):
+    """Both sides of the number of sequences that the reducing launch is shaped by."""
+    test_sequences_and_masks(m, T, E, k, S, 0.1)
