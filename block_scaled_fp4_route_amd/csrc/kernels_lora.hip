@@ -542,11 +542,12 @@ __device__ __forceinline__ void ring_barrier() {
 // 214 us with them and 187 with the ring.) Where the axis is in several parts,
 // every workgroup leaves its own with device-coherent stores, and the last one
 // of a tile to finish (by a ticket) adds them in order. Out go the bf16 parts
-// of the scaled values. Bound by memory: one side of 8192 x 2560 bf16, rank
-// 16, 17 us (42 MB, 2.5 TB/s); both sides of 8192 x (2560 + 8192), rank 64, 65
-// us (176 MB, 2.7 TB/s, where a kernel that only reads the same 134 MB side in
-// such row pieces takes 26 to 33 us). Few tokens: one round of loads and the
-// join, 12 us at 300 x (2560 + 640) fp32.
+// of the scaled values. One side of 8192 x 2560 bf16, rank 16: 17 us (42 MB, 2.5
+// TB/s). Both sides of 8192 x (2560 + 8192), rank 64: 64 us; 176 MB come from
+// memory, as much again of the factors from L2 (64 tokens stand against 64
+// ranks), and 384 workgroups of 40 or 64 steps share 256 compute units, where a
+// kernel that only reads the 134 MB side in such row pieces takes 26 to 33 us.
+// Few tokens: one round of loads and the join, 12 us at 300 x (2560 + 640) fp32.
 template <int ACT, int RB>
 __global__ __launch_bounds__(256) void k_lora_down(DownJob ja, DownJob jb, int n, int R,
                                                    LoraTable tab,

@@ -210,8 +210,10 @@ struct RgArgs {
 // row k + q at once: MFMA (a, b) then covers the rows 2 i + a and columns 2 i +
 // b of the wave's 32 x 32 square. Small tiles: what runs in this form has few
 // of them, and splitting the sums instead costs their parts' traffic. Bound by
-// latency at few tokens (8 us at T = 1), then by the fp32 matrix rate: 311 x 384
-// x 4096 27 us, 73 TFLOP/s; 2451 x 512 x 2560 (on request) 124 us, 104 TFLOP/s.
+// latency at few tokens (8 us at T = 1). 311 x 384 x 4096 26 us, 75 TFLOP/s,
+// half of the fp32 matrix rate: its 704 tiles all run at once, in 10 to 12 steps
+// each, so that their starts and ends count. Then by that rate: 2451 x 512 x
+// 2560 (on request) 124 us a call, 104 TFLOP/s.
 constexpr int kLdsRow = kTM + 4;
 constexpr int kLdsStep = 2 * kTK * kLdsRow;
 
