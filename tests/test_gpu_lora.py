@@ -469,3 +469,45 @@ def test_norm_of_the_error(m, T, K, N, r):
     for name, (value, walked) in want.items():
         off = (out[name].cpu().double() - value).norm() / (4 * walked.norm())
         assert off <= 1, (name, off)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T", [60, 900])
+def test_infinities_beside_old_values(m, dt, T):
+    """In place on the base, and added to gradients that are there: what is
+    beside an infinity keeps its value, and an infinity meets what it is added to."""
+    inf, nan = float("inf"), float("nan")
+    c = Case(m, dt, T, 72, 136, [2, 3], "mixed", R=40)
+    c.A[0][0], c.A[0][1] = 1.0, 0.0
+    c.ids[:6] = torch.tensor([0, 0, 1, 0, -1, 0], device="cuda")
+    c.x[1, 5], c.dy[3, 7], c.x[4] = inf, -inf, nan
+    c.base[1, 3], c.base[1, 4], c.base[1, 6] = nan, inf, -inf
+    c.dxb[3, 3], c.dxb[3, 4], c.dxb[3, 6] = nan, inf, -inf
+    y = c.apply()
+    ref.close(y, *c.want(), "y")
+    ok = torch.isfinite(y)
+    assert torch.equal(torch.where(ok, y, 0), torch.where(ok, c.apply(inplace=True), 0)) and ok.any() and not ok.all()
+    ref.close(c.apply(inplace=True), *c.want(), "y in place")
+    c.check_backward(c.backward(inplace=True))
+    g = torch.Generator().manual_seed(2)
+    old = ([torch.randn(a.shape, generator=g).cuda() for a in c.A], [torch.randn(b.shape, generator=g).cuda() for b in c.B])
+    old[0][0][0, 5], old[0][0][1, 5], old[1][0][0, 7], old[1][0][0, 8] = inf, -inf, nan, inf
+    c.backward(acc=1, old=old)
+    want = ref.lora_grads(c.x, c.dy, c.ids, c.A, c.B, c.scales, c.n)
+    for a in range(2):
+        for name, got, o, (v, e) in (("A", c.dA[a], old[0][a], want[a][0]), ("B", c.dB[a], old[1][a], want[a][1])):
+            o = o.cpu().double()
+            ref.close(got, v + o, e + 2 * ref.EPS * (v.abs() + o.abs()), (name, a))
+
+
+@pytest.mark.parametrize("T", [9, 600])
+def test_nan_of_any_bits(m, T):
+    """A NaN whose bits are all in the low half of an fp32 value is one in every sum that it enters."""
+    c = Case(m, "f32", T, 72, 136, [3], "one", R=40)
+    c.x.view(torch.int32)[2, 9] = 0x7F800001
+    c.dy.view(torch.int32)[5, 11] = -0x7FFFFF  # 0xFF800001
+    assert torch.isnan(c.x[2, 9]) and torch.isnan(c.dy[5, 11])
+    y, dx = c.apply(), c.backward()
+    ref.close(y, *c.want(), "y")
+    c.check_backward(dx)
+    assert torch.isnan(y[2]).all() and torch.isnan(dx[5]).all() and torch.isnan(c.dA[0][:, 9]).all() and torch.isnan(c.dB[0][:, 11]).all()
