@@ -742,7 +742,9 @@ __global__ __launch_bounds__(256, 2) void k_rg_pair(PairArgs a) {
     }
 }
 
-// out (+)= the parts, in increasing order.
+// out (+)= the parts, in increasing order. A thread adds all parts of its four
+// outputs: 9 us at 512 x 2560 outputs of 8 parts; 117 us where 256 outputs have
+// 1024 (2^20 tokens of one expert, 995 us in all).
 __global__ __launch_bounds__(256) void k_rg_reduce(const f4v* __restrict__ px, int sx, size_t nx, f4v* dx, int acc_x,
                                                    const f4v* __restrict__ pw, int sw, size_t nw, f4v* dWr,
                                                    int acc_w) {
