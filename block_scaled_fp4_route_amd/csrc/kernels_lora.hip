@@ -470,7 +470,9 @@ __device__ __forceinline__ float nan_or_inf(float first) {
 __device__ __forceinline__ uint32_t pack_first(float a, float b) {
     return pack_hi(is_nan(a) ? __builtin_nanf("") : a, is_nan(b) ? __builtin_nanf("") : b);
 }
-// (for a product beside the first ones' in a second run over the same data)
+// Infinities taken out. "down", where only the activations are in parts and
+// there are many steps, runs all of them again instead, with the low parts
+// beside a factor without its infinities.
 __device__ __forceinline__ u4v without_inf(u4v p) {
 #pragma unroll
     for (int q = 0; q < 4; q++) {
