@@ -13,4 +13,7 @@ from .binding import (  # noqa: F401
     MOE_ACC_DWR, MOE_ACC_DX, MOE_ACT_BF16, MOE_ACT_F16, MOE_ACT_F32, MOE_FP32_PRODUCTS, lora_desc, moe_balance_loss,
     moe_balance_workspace_bytes, moe_lora_apply, moe_lora_backward, moe_lora_workspace_bytes, moe_route_backward,
     moe_route_backward_workspace_bytes,
+    MOE_GATE_CHANNEL, MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_MODE_DECODE_BATCH, MOE_SCALE_NEAREST, fp4_desc, moe_block_norm,
+    moe_block_norm_backward, moe_block_norm_workspace_bytes, moe_fp4_apply, moe_fp4_backward, moe_fp4_quant,
+    moe_fp4_workspace_bytes, moe_layer_decode_batch, norm_desc,
 )

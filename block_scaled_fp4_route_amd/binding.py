@@ -16,11 +16,13 @@ LIB_PATH = os.path.join(HERE, "libmoe_fp4.so")
 
 MOE_FMT_NVFP4, MOE_FMT_MXFP4 = 1, 2
 MOE_OK, MOE_ERR_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_HIP, MOE_ERR_WORKSPACE = 0, -1, -2, -3, -4
-MOE_MODE_ROUTE, MOE_MODE_DECODE, MOE_MODE_PREFILL = 0, 1, 2
+MOE_MODE_ROUTE, MOE_MODE_DECODE, MOE_MODE_PREFILL, MOE_MODE_DECODE_BATCH = 0, 1, 2, 3
 MOE_OUT_F32, MOE_OUT_BF16 = 0, 1
 MOE_NOALLOC_SCRATCH_BYTES = 1 << 20
 MOE_ACC_DX, MOE_ACC_DWR, MOE_FP32_PRODUCTS = 1, 2, 8
 MOE_ACT_F32, MOE_ACT_BF16, MOE_ACT_F16 = 0, 1, 2
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN = 0, 1, 2
+GATES = {"none": MOE_GATE_NONE, "channel": MOE_GATE_CHANNEL, "token": MOE_GATE_TOKEN}
 FORMATS = {"nvfp4": MOE_FMT_NVFP4, "mxfp4": MOE_FMT_MXFP4}
 
 # every symbol declared in include/moe_fp4.h
@@ -28,7 +30,9 @@ EXPORTS = ("moe_block_bytes", "moe_block_layout", "moe_workspace_bytes", "moe_ro
            "moe_layer_decode", "moe_layer_decode_noalloc", "moe_expert_prefill", "moe_dequant_block", "moe_act_quant_fp8", "moe_gemv_fp8",
            "moe_prefetch_sink_bytes", "moe_expert_prefetch", "moe_tier_create", "moe_tier_destroy", "moe_tier_update", "moe_tier_get_stats", "moe_tier_slot_of",
            "moe_balance_workspace_bytes", "moe_balance_loss", "moe_route_backward_workspace_bytes", "moe_route_backward",
-           "moe_lora_workspace_bytes", "moe_lora_apply", "moe_lora_backward", "moe_status_string", "moe_last_error")
+           "moe_lora_workspace_bytes", "moe_lora_apply", "moe_lora_backward", "moe_layer_decode_batch",
+           "moe_fp4_quant", "moe_fp4_workspace_bytes", "moe_fp4_apply", "moe_fp4_backward", "moe_block_norm", "moe_block_norm_workspace_bytes", "moe_block_norm_backward",
+           "moe_status_string", "moe_last_error")
 
 
 class MoeError(RuntimeError):
@@ -58,6 +62,15 @@ class moe_tier_stats(C.Structure):
 
 class moe_lora_desc(C.Structure):
     _fields_ = [("K", C.c_int32), ("N", C.c_int32), ("n", C.c_int32), ("max_rank", C.c_int32), ("dtype", C.c_int32)]
+
+
+class moe_fp4_desc(C.Structure):
+    _fields_ = [("K", C.c_int32), ("N", C.c_int32), ("format", C.c_int32), ("dtype", C.c_int32)]
+
+
+class moe_norm_desc(C.Structure):
+    _fields_ = [("H", C.c_int32), ("r_dtype", C.c_int32), ("y_dtype", C.c_int32), ("x_dtype", C.c_int32), ("gate", C.c_int32),
+                ("scale", C.c_float), ("eps", C.c_float)]
 
 
 def _load():
@@ -107,6 +120,21 @@ def _load():
     L.moe_lora_apply.argtypes = [LD, P, I64, I32, P, P, P, P, P, P, I64, P, I64, P, SZ, P]
     L.moe_lora_backward.restype = C.c_int
     L.moe_lora_backward.argtypes = [LD, P, I64, P, I64, I32, P, P, P, P, P, P, I64, P, I64, P, P, I32, P, SZ, P]
+    L.moe_layer_decode_batch.restype = C.c_int
+    L.moe_layer_decode_batch.argtypes = [D, P, I32, P, P, P, C.POINTER(moe_shared), P, P, P, P, SZ, P]
+    FD, ND = C.POINTER(moe_fp4_desc), C.POINTER(moe_norm_desc)
+    L.moe_fp4_quant.restype = C.c_int; L.moe_fp4_quant.argtypes = [P, I64, I32, I32, I32, I32, I32, P, P, P, P, I64, P]
+    L.moe_fp4_workspace_bytes.restype = SZ; L.moe_fp4_workspace_bytes.argtypes = [FD, I32, I32]
+    L.moe_fp4_apply.restype = C.c_int
+    L.moe_fp4_apply.argtypes = [FD, P, I64, I32, P, P, P, I32, P, I64, P, I64, P, SZ, P]
+    L.moe_fp4_backward.restype = C.c_int
+    L.moe_fp4_backward.argtypes = [FD, P, I64, I32, P, P, P, P, I64, P, I64, P, SZ, P]
+    L.moe_block_norm.restype = C.c_int
+    L.moe_block_norm.argtypes = [ND, P, I64, P, I64, I32, P, P, P, P, P, I64, P, I64, P]
+    L.moe_block_norm_workspace_bytes.restype = SZ; L.moe_block_norm_workspace_bytes.argtypes = [ND, I32]
+    L.moe_block_norm_backward.restype = C.c_int
+    L.moe_block_norm_backward.argtypes = [ND, P, I64, P, I64, I32, P, P, P, P, P, I64, P, I64, P, I64, P, I64, P, P, P, I32,
+                                          P, SZ, P]
     L.moe_status_string.restype = C.c_char_p; L.moe_status_string.argtypes = [C.c_int]
     L.moe_last_error.restype = C.c_char_p; L.moe_last_error.argtypes = []
     return L
@@ -229,7 +257,7 @@ def expert_ptr_table(blocks, block_bytes: int | None = None):
     return torch.tensor(ptrs, dtype=torch.int64, device=dev)
 
 
-MOE_SCALE_FLOOR, MOE_SCALE_CEIL = 0, 1
+MOE_SCALE_FLOOR, MOE_SCALE_CEIL, MOE_SCALE_NEAREST = 0, 1, 2
 
 
 def moe_act_quant_fp8(x, rows, cols, block, rule, codes, scales, stream=None):
@@ -290,7 +318,8 @@ def moe_expert_prefetch(d, expert_ptrs, idx, n, sink, stream=None):
 def _run(fn, head, stream, *args):
     """fn(head, *args, stream), tensors as their addresses, with the tensors'
     device current (it may be another one than the caller's) and, without a
-    stream, on that device's current stream."""
+    stream, on that device's current stream. head: a descriptor, or None for an
+    entry point without one."""
     import torch
     Tensor, dev, out = torch.Tensor, None, []
     for a in args:
@@ -307,10 +336,10 @@ def _run(fn, head, stream, *args):
     if stream is None and dev is not None:
         stream = _current_stream(dev)
     if dev is None or dev == torch.cuda.current_device():
-        _check(fn(C.byref(head), *out, _stream(stream)))
+        _check(fn(*((C.byref(head),) if head is not None else ()), *out, _stream(stream)))
     else:
         with torch.cuda.device(dev):
-            _check(fn(C.byref(head), *out, _stream(stream)))
+            _check(fn(*((C.byref(head),) if head is not None else ()), *out, _stream(stream)))
 
 
 def _current_stream(dev: int) -> int:
@@ -345,12 +374,16 @@ def moe_route_backward(d, x, T, Wr, idx, w, dw, mask, dlogits_in, dlogits_out, d
          ws, _ws_bytes(ws, ws_bytes))
 
 
+def _act(dtype) -> int:
+    if isinstance(dtype, int):
+        return dtype
+    import torch
+    return {torch.float32: MOE_ACT_F32, torch.bfloat16: MOE_ACT_BF16, torch.float16: MOE_ACT_F16}[dtype]
+
+
 def lora_desc(K: int, N: int, n: int, max_rank: int, dtype) -> moe_lora_desc:
     """dtype: the activations' torch dtype (float32, bfloat16, float16) or MOE_ACT_*."""
-    if not isinstance(dtype, int):
-        import torch
-        dtype = {torch.float32: MOE_ACT_F32, torch.bfloat16: MOE_ACT_BF16, torch.float16: MOE_ACT_F16}[dtype]
-    return moe_lora_desc(K, N, n, max_rank, dtype)
+    return moe_lora_desc(K, N, n, max_rank, _act(dtype))
 
 
 def moe_lora_workspace_bytes(l, T: int, backward) -> int:
@@ -367,3 +400,58 @@ def moe_lora_backward(l, x, ldx, dy, lddy, T, ids, a_ptrs, b_ptrs, ranks, scales
                       da_ptrs, db_ptrs, accumulate, ws, ws_bytes=None, stream=None):
     _run(lib.moe_lora_backward, l, stream, x, ldx, dy, lddy, T, ids, a_ptrs, b_ptrs, ranks, scales, dx_base, lddx_base,
          dx, lddx, da_ptrs, db_ptrs, accumulate, ws, _ws_bytes(ws, ws_bytes))
+
+
+# --- a layer for a few tokens, 4-bit matrices, norms around a block ----------
+
+def moe_layer_decode_batch(d, x, T, mask, Wr, expert_ptrs, shared, y, idx_out, w_out, ws, ws_bytes=None, stream=None):
+    """shared: None or (gate, up, down) bf16 tensors."""
+    sh = None
+    if shared is not None:
+        sh = C.byref(moe_shared(_ptr(shared[0]), _ptr(shared[1]), _ptr(shared[2])))
+    _run(lib.moe_layer_decode_batch, d, stream, x, T, mask, Wr, expert_ptrs, sh, y, idx_out, w_out, ws,
+         _ws_bytes(ws, ws_bytes))
+
+
+def moe_fp4_quant(x, ldx, rows, cols, dtype, fmt, rule, row_exp, codes, scales, values, ldv, stream=None):
+    """dtype: x's torch dtype or MOE_ACT_*; fmt: "nvfp4", "mxfp4" or MOE_FMT_*."""
+    _run(lib.moe_fp4_quant, None, stream, x, ldx, rows, cols, _act(dtype), FORMATS[fmt] if isinstance(fmt, str) else int(fmt), rule,
+         row_exp, codes, scales, values, ldv)
+
+
+def fp4_desc(K: int, N: int, fmt, dtype) -> moe_fp4_desc:
+    """dtype: the activations' torch dtype (float32, bfloat16, float16) or MOE_ACT_*."""
+    return moe_fp4_desc(K, N, FORMATS[fmt] if isinstance(fmt, str) else int(fmt), _act(dtype))
+
+
+def moe_fp4_workspace_bytes(f, T: int, backward) -> int:
+    return int(lib.moe_fp4_workspace_bytes(C.byref(f), T, 1 if backward else 0))
+
+
+def moe_fp4_apply(f, x, ldx, T, codes, scales, row_exp, round_x, base, ldbase, y, ldy, ws, ws_bytes=None, stream=None):
+    _run(lib.moe_fp4_apply, f, stream, x, ldx, T, codes, scales, row_exp, 1 if round_x else 0, base, ldbase, y, ldy, ws,
+         _ws_bytes(ws, ws_bytes))
+
+
+def moe_fp4_backward(f, dy, lddy, T, codes, scales, row_exp, dx_base, lddx_base, dx, lddx, ws, ws_bytes=None, stream=None):
+    _run(lib.moe_fp4_backward, f, stream, dy, lddy, T, codes, scales, row_exp, dx_base, lddx_base, dx, lddx, ws,
+         _ws_bytes(ws, ws_bytes))
+
+
+def norm_desc(H: int, r_dtype, y_dtype, x_dtype, gate, scale: float, eps: float) -> moe_norm_desc:
+    """dtypes: torch dtypes or MOE_ACT_*; gate: "none", "channel", "token" or MOE_GATE_*."""
+    return moe_norm_desc(H, _act(r_dtype), _act(y_dtype), _act(x_dtype), GATES[gate] if isinstance(gate, str) else int(gate), scale, eps)
+
+
+def moe_block_norm(n, r, ldr, y, ldy, T, mask, post, gate, pre, r_out, ldr_out, x, ldx, stream=None):
+    _run(lib.moe_block_norm, n, stream, r, ldr, y, ldy, T, mask, post, gate, pre, r_out, ldr_out, x, ldx)
+
+
+def moe_block_norm_workspace_bytes(n, T: int) -> int:
+    return int(lib.moe_block_norm_workspace_bytes(C.byref(n), T))
+
+
+def moe_block_norm_backward(n, r_out, ldr_out, y, ldy, T, mask, post, gate, pre, dr_out, lddr_out, dx, lddx, dr, lddr, dy, lddy,
+                            dpost, dgate, dpre, accumulate, ws, ws_bytes=None, stream=None):
+    _run(lib.moe_block_norm_backward, n, stream, r_out, ldr_out, y, ldy, T, mask, post, gate, pre, dr_out, lddr_out, dx, lddx,
+         dr, lddr, dy, lddy, dpost, dgate, dpre, accumulate, ws, _ws_bytes(ws, ws_bytes))

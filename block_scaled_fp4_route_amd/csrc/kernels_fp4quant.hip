@@ -1,0 +1,223 @@
+// Quantisation to block-scaled e2m1 codes (gfx950): a matrix of fp32, bf16 or
+// fp16 values to NVFP4 (an E4M3 scale for 16 codes, and a power of two for
+// each row if the caller wants one) or MXFP4 (a UE8M0 scale for 32 codes), and
+// the values that the codes stand for.
+//
+// Nothing is divided. A block's exponent comes from the bits of its largest
+// magnitude. A magnitude m goes to code c where the borders between codes
+// (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5) times the scale s lie on the right
+// sides of m: a border has at most 3 significant bits, an E4M3 scale 4, so
+// the product is exact in fp32 and so is m times a power of two. The E4M3
+// scale nearest to amax / 6 is found the same way: 6 times the border between
+// two E4M3 values has 7 bits. The result is therefore the definition's, bit
+// for bit, with no case that a rounded quotient would decide.
+//
+// Memory bounds it: every value read once (a row with an exponent of its own
+// stays in registers between its two uses), codes, scales and values written
+// once.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "moe_device.h"
+#include "moe_internal.h"
+#include "moe_rows.h"
+#include "moe_serve.h"
+
+namespace moe {
+namespace {
+
+constexpr uint32_t kInfBits = 0x7F800000u;
+constexpr int kRowExpMin = -100, kRowExpMax = 116;  // so that every decoded value is a normal bf16, and finite
+
+struct QuantArgs {
+    const char* x;
+    size_t ldx;  // bytes
+    uint32_t rows, c8;  // c8: pieces of 8 in a row
+    int8_t* row_exp;
+    uint8_t *codes, *scales;
+    char* values;
+    size_t ldv;  // bytes
+    int rule;
+};
+
+// The E4M3 byte nearest to a / 6 (ties to even, at most 448), a >= 0 finite.
+__device__ __forceinline__ uint32_t e4m3_sixth(float a) {
+    // near the result: a * fp32(1/6) is off by 2^-23 of a at most, so the byte
+    // it rounds to is the nearest one or its neighbour; which one is decided
+    // by comparing a with 6 times the borders, exactly
+    const float q = fminf(a * 0.16666667f, 448.0f);
+    uint32_t b = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q, q, 0, false) & 0x7Fu;
+    const float v = e4m3_to_f32(b);
+    const float up = e4m3_to_f32(min(b + 1u, 0x7Eu)), down = e4m3_to_f32(b ? b - 1u : 0u);
+    const float hi = 3.0f * (v + up), lo = 3.0f * (v + down);  // 6 times the middle: exact
+    const bool odd = b & 1u;
+    if (b < 0x7Eu && (a > hi || (a == hi && odd))) b++;
+    else if (b > 0u && (a < lo || (a == lo && odd))) b--;
+    return b;
+}
+
+// Codes of eight values (times the exact power of two p) under the scale s,
+// as one word, and the values they stand for (without p).
+__device__ __forceinline__ uint32_t codes8(const float (&v)[8], float p, float s, float (&q)[8]) {
+    const float b0 = 0.25f * s, b1 = 0.75f * s, b2 = 1.25f * s, b3 = 1.75f * s, b4 = 2.5f * s, b5 = 3.5f * s, b6 = 5.0f * s;
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const float m = fabsf(v[i]) * p;
+        const uint32_t c = (uint32_t)(m > b0) + (m >= b1) + (m > b2) + (m >= b3) + (m > b4) + (m >= b5) + (m > b6);
+        w |= (c | (__float_as_uint(v[i]) >> 31 << 3)) << (4 * i);
+    }
+    const f2v d0 = fp4x2<0>(w), d1 = fp4x2<1>(w), d2 = fp4x2<2>(w), d3 = fp4x2<3>(w);
+    q[0] = d0.x; q[1] = d0.y; q[2] = d1.x; q[3] = d1.y;
+    q[4] = d2.x; q[5] = d2.y; q[6] = d3.x; q[7] = d3.y;
+    return w;
+}
+
+__device__ __forceinline__ uint32_t max_mag(const float (&v)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    return m;
+}
+
+// One piece of 8 values, its block's lanes beside it (2 of NVFP4, 4 of MXFP4;
+// all of them active). re: the row's exponent.
+template <int DT, int FMT>
+__device__ __forceinline__ void quant_piece(const QuantArgs& a, uint32_t row, uint32_t c, const float (&v)[8], int re) {
+    constexpr int L = Fmt<FMT>::G / 8;
+    uint32_t top = max_mag(v);
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o, 64));
+    const bool bad = top >= kInfBits;  // an infinity or a NaN: the whole block decodes to NaN
+    uint32_t byte;
+    float p, s, back;  // magnitudes times p against s; decoded times s times back
+    if constexpr (FMT == kFmtNvfp4) {
+        p = exp2i(-re);
+        back = exp2i(re);
+        byte = bad ? 0x7Fu : e4m3_sixth(__uint_as_float(top) * p);
+        s = e4m3_to_f32(byte);
+    } else {
+        int X = (int)(top >> 23) - 129 + (a.rule == kScaleCeil && (top & 0x7FFFFFu) > 0x400000u ? 1 : 0);
+        X = max(-127, min(125, X));
+        byte = bad ? 0xFFu : top == 0u ? 0u : (uint32_t)(X + 127);
+        p = exp2i(-X);
+        s = 1.0f;
+        back = ue8m0_to_f32(byte);
+    }
+    float q[8];
+    uint32_t w = codes8(v, p, s, q);
+    if (bad || (FMT == kFmtNvfp4 && byte == 0u)) {  // all codes zero (under a scale of 0, every border is 0)
+        w = 0;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            w |= bad ? 0u : __float_as_uint(v[i]) >> 31 << (4 * i + 3);
+            q[i] = bad ? __uint_as_float(0x7FC00000u) : copysignf(0.0f, v[i]);
+        }
+    }
+    const size_t at = (size_t)row * a.c8 + c;
+    if (a.codes) reinterpret_cast<uint32_t*>(a.codes)[at] = w;
+    if (a.scales && (c & (L - 1)) == 0) a.scales[at / L] = (uint8_t)byte;
+    if (a.values) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            q[i] = q[i] * s * back;
+            if (DT == kActF16) q[i] = q[i] > 65504.f ? 65504.f : q[i] < -65504.f ? -65504.f : q[i];
+        }
+        store8<DT>(a.values + (size_t)row * a.ldv, 8 * (size_t)c, pack8<DT>(q));
+    }
+}
+
+// Blocks on their own: a lane a piece, whole blocks in or out of the matrix.
+template <int DT, int FMT>
+__global__ __launch_bounds__(256) void k_fp4_quant(QuantArgs a) {
+    const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+    const uint32_t row = i / a.c8, c = i - row * a.c8;
+    if (row >= a.rows) return;
+    float v[8];
+    unpack8<DT>(load8<DT>(a.x + (size_t)row * a.ldx, 8 * (size_t)c), v);
+    quant_piece<DT, FMT>(a, row, c, v, 0);
+}
+
+// NVFP4 with row exponents: NT threads take a row (64: four rows a workgroup,
+// 256: one). The first kHeld pieces of a lane stay in registers, further ones
+// are read again (longer rows: out of the cache).
+constexpr int kHeld = 4;
+template <int DT, int NT>
+__global__ __launch_bounds__(256) void k_fp4_quant_rows(QuantArgs a) {
+    __shared__ uint32_t tops[4];
+    const uint32_t t = threadIdx.x & (NT - 1), row = NT == 64 ? blockIdx.x * 4u + wave_id() : blockIdx.x;
+    if (NT == 64 && row >= a.rows) return;
+    const char* xr = a.x + (size_t)row * a.ldx;
+    float v[kHeld][8];
+    uint32_t top = 0;
+    auto look = [&](const float (&u)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const uint32_t m = __float_as_uint(u[i]) & 0x7FFFFFFFu;
+            top = max(top, m < kInfBits ? m : 0u);
+        }
+    };
+    Raw8<DT> raw[kHeld];
+#pragma unroll
+    for (int j = 0; j < kHeld; j++)
+        if (t + NT * j < a.c8) raw[j] = load8<DT>(xr, 8 * (size_t)(t + NT * j));
+#pragma unroll
+    for (int j = 0; j < kHeld; j++)
+        if (t + NT * j < a.c8) {
+            unpack8<DT>(raw[j], v[j]);
+            look(v[j]);
+        }
+    for (uint32_t c = t + NT * kHeld; c < a.c8; c += NT) {
+        float u[8];
+        unpack8<DT>(load8<DT>(xr, 8 * (size_t)c), u);
+        look(u);
+    }
+    top = wave_max_u32(top);
+    if (NT == 256) {
+        if ((threadIdx.x & 63) == 0) tops[wave_id()] = top;
+        __syncthreads();
+        top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+    }
+    // the smallest e with top <= 2688 2^e = 1.3125 2^(11 + e)
+    int e = (int)(top >> 23) - 138 + ((top & 0x7FFFFFu) > 0x280000u ? 1 : 0);
+    e = top == 0u ? 0 : max(kRowExpMin, min(kRowExpMax, e));
+    if (t == 0) a.row_exp[row] = (int8_t)e;
+#pragma unroll
+    for (int j = 0; j < kHeld; j++)
+        if (t + NT * j < a.c8) quant_piece<DT, kFmtNvfp4>(a, row, t + NT * j, v[j], e);
+    for (uint32_t c = t + NT * kHeld; c < a.c8; c += NT) {
+        float u[8];
+        unpack8<DT>(load8<DT>(xr, 8 * (size_t)c), u);
+        quant_piece<DT, kFmtNvfp4>(a, row, c, u, e);
+    }
+}
+
+template <int DT>
+hipError_t quant(int fmt, const QuantArgs& a, hipStream_t s) {
+    if (a.row_exp) {
+        if (a.c8 <= 64 * kHeld)
+            hipLaunchKernelGGL((k_fp4_quant_rows<DT, 64>), dim3((a.rows + 3) / 4), dim3(256), 0, s, a);
+        else
+            hipLaunchKernelGGL((k_fp4_quant_rows<DT, 256>), dim3(a.rows), dim3(256), 0, s, a);
+    } else {
+        const dim3 grid((unsigned)(((size_t)a.rows * a.c8 + 255) / 256));
+        if (fmt == kFmtNvfp4)
+            hipLaunchKernelGGL((k_fp4_quant<DT, kFmtNvfp4>), grid, dim3(256), 0, s, a);
+        else
+            hipLaunchKernelGGL((k_fp4_quant<DT, kFmtMxfp4>), grid, dim3(256), 0, s, a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_fp4_quant(int dtype, int fmt, int rule, const void* x, size_t ldx, int rows, int cols,
+                            int8_t* row_exp, uint8_t* codes, uint8_t* scales, void* values, size_t ldv, hipStream_t s) {
+    const size_t es = dtype == kActF32 ? 4 : 2;
+    const QuantArgs a = {static_cast<const char*>(x), ldx * es, (uint32_t)rows, (uint32_t)cols / 8, row_exp, codes, scales,
+                         static_cast<char*>(values), ldv * es, rule};
+    if (dtype == kActF32) return quant<kActF32>(fmt, a, s);
+    return dtype == kActBf16 ? quant<kActBf16>(fmt, a, s) : quant<kActF16>(fmt, a, s);
+}
+
+}  // namespace moe

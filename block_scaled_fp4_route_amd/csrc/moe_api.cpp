@@ -10,9 +10,11 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 
 #include "moe_internal.h"
 #include "moe_learn.h"
+#include "moe_serve.h"
 
 namespace {
 
@@ -95,6 +97,7 @@ size_t moe_workspace_bytes(const moe_desc* d, int32_t T, int32_t mode) {
         case MOE_MODE_ROUTE: return moe::route_ws_bytes(T, d->E);
         case MOE_MODE_DECODE: return moe::decode_ws_bytes(d->H, d->I, d->k, d->E);
         case MOE_MODE_PREFILL: return moe::prefill_ws_bytes(d->format, d->H, d->I, d->E, d->k, T);
+        case MOE_MODE_DECODE_BATCH: return T > moe::kBatchMaxT ? 0 : moe::batch_ws_bytes(d->format, d->H, d->I, d->E, d->k, T);
         default: return 0;
     }
 }
@@ -234,6 +237,28 @@ int moe_layer_decode_noalloc(const moe_desc* d, const float* x, const float* Wr,
     void* ws = nullptr;
     if ((r = scratch_address(&ws))) return r;
     return layer_decode_launch(d, plan, x, Wr, expert_ptrs, shared, y, idx_out, w_out, ws, stream);
+}
+
+int moe_layer_decode_batch(const moe_desc* d, const float* x, int32_t T, const uint8_t* mask, const float* Wr,
+                           const void* const* expert_ptrs, const moe_shared* shared, float* y, int32_t* idx_out,
+                           float* w_out, void* ws, size_t ws_bytes, void* stream) {
+    int r;
+    moe::DecodePlan plan;
+    if ((r = check_desc(d))) return r;
+    if (T < 0) return fail(MOE_ERR_ARG, "T=%d is negative", T);
+    if (T > moe::kBatchMaxT) return fail(MOE_ERR_UNSUPPORTED, "T=%d exceeds %d", T, moe::kBatchMaxT);
+    if (T == 0) return ok();
+    if ((r = layer_decode_checks(d, x, Wr, expert_ptrs, shared, y, idx_out, w_out, &plan))) return r;
+    if (static_cast<const void*>(y) == x || y == w_out || static_cast<const void*>(y) == idx_out ||
+        static_cast<const void*>(w_out) == idx_out || static_cast<const void*>(w_out) == x ||
+        static_cast<const void*>(idx_out) == x)
+        return fail(MOE_ERR_ARG, "an output is an input or another output");
+    if ((r = check_ws(ws, ws_bytes, moe::batch_ws_bytes(d->format, d->H, d->I, d->E, d->k, T)))) return r;
+    return hip_status(moe::launch_layer_batch(d->format, d->H, d->I, d->E, d->k, x, T, mask, Wr, expert_ptrs,
+                                              shared ? shared->gate : nullptr, shared ? shared->up : nullptr,
+                                              shared ? shared->down : nullptr, y, idx_out, w_out, ws,
+                                              reinterpret_cast<hipStream_t>(stream)),
+                      "batched decode launch");
 }
 
 int moe_expert_prefill(const moe_desc* d, const float* x, int32_t T, const void* const* expert_ptrs,
@@ -498,6 +523,221 @@ int moe_lora_backward(const moe_lora_desc* l, const void* x, int64_t ldx, const 
                                                 (size_t)lddy, T, tab, dx_base, (size_t)lddx_base, dx, (size_t)lddx,
                                                 da_ptrs, db_ptrs, accumulate, ws, reinterpret_cast<hipStream_t>(stream)),
                       "adapter gradient launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+bool act_known(int32_t dtype) { return dtype == MOE_ACT_F32 || dtype == MOE_ACT_BF16 || dtype == MOE_ACT_F16; }
+
+int fp4_checks(const moe_fp4_desc* f, int32_t T) {
+    if (!f) return fail(MOE_ERR_ARG, "fp4 desc is NULL");
+    if (!group_size(f->format)) return fail(MOE_ERR_ARG, "unknown format %d", f->format);
+    if (!act_known(f->dtype)) return fail(MOE_ERR_ARG, "unknown dtype %d", f->dtype);
+    if (f->K <= 0 || f->N <= 0 || f->K % 32 || f->N % 8)
+        return fail(MOE_ERR_ARG, "K=%d must be a positive multiple of 32, N=%d of 8", f->K, f->N);
+    if (T < 0) return fail(MOE_ERR_ARG, "T=%d is negative", T);
+    if (f->K > moe::kFp4MaxDim || f->N > moe::kFp4MaxDim || T > moe::kFp4MaxT)
+        return fail(MOE_ERR_UNSUPPORTED, "4-bit products need K, N <= %d, T <= %d (K=%d N=%d T=%d)", moe::kFp4MaxDim,
+                    moe::kFp4MaxT, f->K, f->N, T);
+    return MOE_OK;
+}
+
+int fp4_rows(const void* p, int64_t ld, int32_t cols, const char* name) {
+    int r;
+    if ((r = check_rows(p, ld, cols, name))) return r;
+    if (ld > moe::kFp4MaxLd)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: stride %lld exceeds %lld", name, (long long)ld, (long long)moe::kFp4MaxLd);
+    return MOE_OK;
+}
+
+int fp4_matrix(const moe_fp4_desc* f, const uint8_t* codes, const uint8_t* scales, const int8_t* row_exp) {
+    int r;
+    if ((r = check_ptr(codes, 16, "codes")) || (r = check_ptr(scales, 1, "scales"))) return r;
+    if (row_exp && f->format != MOE_FMT_NVFP4) return fail(MOE_ERR_ARG, "row_exp beside a format without row exponents");
+    return MOE_OK;
+}
+
+int norm_checks(const moe_norm_desc* n, int32_t T) {
+    if (!n) return fail(MOE_ERR_ARG, "norm desc is NULL");
+    if (n->H <= 0 || n->H % 8) return fail(MOE_ERR_ARG, "H=%d must be a positive multiple of 8", n->H);
+    if (!act_known(n->r_dtype) || !act_known(n->y_dtype) || !act_known(n->x_dtype))
+        return fail(MOE_ERR_ARG, "unknown dtype (r %d y %d x %d)", n->r_dtype, n->y_dtype, n->x_dtype);
+    if (n->gate != MOE_GATE_NONE && n->gate != MOE_GATE_CHANNEL && n->gate != MOE_GATE_TOKEN)
+        return fail(MOE_ERR_ARG, "unknown gate %d", n->gate);
+    if (!(n->eps > 0.0f) || !std::isfinite(n->eps) || !std::isfinite(n->scale))
+        return fail(MOE_ERR_ARG, "eps=%g must be above 0 and scale=%g finite", (double)n->eps, (double)n->scale);
+    if (T < 0) return fail(MOE_ERR_ARG, "T=%d is negative", T);
+    if (n->H > moe::kNormMaxH || T > moe::kNormMaxT)
+        return fail(MOE_ERR_UNSUPPORTED, "norms need H <= %d, T <= %d (H=%d T=%d)", moe::kNormMaxH, moe::kNormMaxT, n->H, T);
+    return MOE_OK;
+}
+
+// The vectors of a norm: post and gate only matter beside y. The rows of an
+// empty batch may have no address.
+int norm_vectors(const moe_norm_desc* n, int32_t T, const void* y, const float* post, const float* gate, const float* pre) {
+    int r;
+    if (post && (r = check_ptr(post, 16, "post"))) return r;
+    if (pre && (r = check_ptr(pre, 16, "pre"))) return r;
+    if (post && !y && T > 0) return fail(MOE_ERR_ARG, "post without y");
+    if (n->gate == MOE_GATE_NONE && gate) return fail(MOE_ERR_ARG, "a gate beside MOE_GATE_NONE");
+    if (n->gate != MOE_GATE_NONE && y && (r = check_ptr(gate, n->gate == MOE_GATE_CHANNEL ? 16 : 4, "gate"))) return r;
+    return MOE_OK;
+}
+
+// Whether an output is an input or another output, but for the pairs that may be.
+bool shared_memory(std::initializer_list<const void*> out, std::initializer_list<const void*> in, const void* ok_out,
+                   const void* ok_in) {
+    int i = 0;
+    for (const void* o : out) {
+        int j = 0;
+        for (const void* p : out)
+            if (j++ > i && o && o == p) return true;
+        for (const void* p : in)
+            if (o && o == p && !(o == ok_out && p == ok_in)) return true;
+        i++;
+    }
+    return false;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_fp4_quant(const void* x, int64_t ldx, int32_t rows, int32_t cols, int32_t dtype, int32_t format, int32_t rule,
+                  int8_t* row_exp, uint8_t* codes, uint8_t* scales, void* values, int64_t ldv, void* stream) {
+    const int G = group_size(format);
+    int r;
+    if (!G) return fail(MOE_ERR_ARG, "unknown format %d", format);
+    if (!act_known(dtype)) return fail(MOE_ERR_ARG, "unknown dtype %d", dtype);
+    if (rows < 0) return fail(MOE_ERR_ARG, "rows=%d is negative", rows);
+    if (cols <= 0 || cols % G) return fail(MOE_ERR_ARG, "cols=%d must be a positive multiple of %d", cols, G);
+    if (format == MOE_FMT_NVFP4 ? rule != MOE_SCALE_NEAREST : rule != MOE_SCALE_FLOOR && rule != MOE_SCALE_CEIL)
+        return fail(MOE_ERR_ARG, "scale rule %d does not go with format %d", rule, format);
+    if (row_exp && format != MOE_FMT_NVFP4) return fail(MOE_ERR_ARG, "row_exp beside a format without row exponents");
+    if (!codes && !scales && !values && !row_exp) return fail(MOE_ERR_ARG, "no output");
+    if ((size_t)rows * cols > ((size_t)1 << 33)) return fail(MOE_ERR_UNSUPPORTED, "rows*cols exceeds 2^33");
+    if (rows == 0) return ok();
+    if ((r = check_rows(x, ldx, cols, "x"))) return r;
+    if (codes && (r = check_ptr(codes, 4, "codes"))) return r;
+    if (values && (r = check_rows(values, ldv, cols, "values"))) return r;
+    if (values == x && ldv != ldx) return fail(MOE_ERR_ARG, "values is x with another stride");
+    if (shared_memory({codes, scales, row_exp, values}, {x}, values, x))
+        return fail(MOE_ERR_ARG, "an output is an input or another output");
+    return hip_status(moe::launch_fp4_quant(dtype, format, rule, x, (size_t)ldx, rows, cols, row_exp, codes, scales, values,
+                                            (size_t)ldv, reinterpret_cast<hipStream_t>(stream)),
+                      "fp4 quantisation launch");
+}
+
+size_t moe_fp4_workspace_bytes(const moe_fp4_desc* f, int32_t T, int32_t backward) {
+    return fp4_checks(f, T) == MOE_OK ? moe::fp4_ws_bytes(f->K, f->N, f->format, f->dtype, T, backward != 0) : 0;
+}
+
+int moe_fp4_apply(const moe_fp4_desc* f, const void* x, int64_t ldx, int32_t T, const uint8_t* codes,
+                  const uint8_t* scales, const int8_t* row_exp, int32_t round_x, const void* base, int64_t ldbase,
+                  void* y, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+    int r;
+    if ((r = fp4_checks(f, T))) return r;
+    if (round_x && f->format != MOE_FMT_MXFP4) return fail(MOE_ERR_ARG, "round_x needs an MXFP4 matrix");
+    if (T == 0) return ok();
+    if ((r = fp4_rows(x, ldx, f->K, "x")) || (r = fp4_matrix(f, codes, scales, row_exp)) ||
+        (r = fp4_rows(y, ldy, f->N, "y")) || (base && (r = fp4_rows(base, ldbase, f->N, "base"))))
+        return r;
+    if (base == y && ldbase != ldy) return fail(MOE_ERR_ARG, "base is y with another stride");
+    if (shared_memory({y}, {x, codes, scales, row_exp}, nullptr, nullptr)) return fail(MOE_ERR_ARG, "y is an input");
+    if ((r = check_ws(ws, ws_bytes, moe::fp4_ws_bytes(f->K, f->N, f->format, f->dtype, T, false)))) return r;
+    return hip_status(moe::launch_fp4_apply(f->K, f->N, f->format, f->dtype, x, (size_t)ldx, T, {codes, scales, row_exp},
+                                            round_x != 0, base, (size_t)ldbase, y, (size_t)ldy, ws,
+                                            reinterpret_cast<hipStream_t>(stream)),
+                      "fp4 product launch");
+}
+
+int moe_fp4_backward(const moe_fp4_desc* f, const void* dy, int64_t lddy, int32_t T, const uint8_t* codes,
+                     const uint8_t* scales, const int8_t* row_exp, const void* dx_base, int64_t lddx_base, void* dx,
+                     int64_t lddx, void* ws, size_t ws_bytes, void* stream) {
+    int r;
+    if ((r = fp4_checks(f, T))) return r;
+    if (T == 0) return ok();
+    if ((r = fp4_rows(dy, lddy, f->N, "dy")) || (r = fp4_matrix(f, codes, scales, row_exp)) ||
+        (r = fp4_rows(dx, lddx, f->K, "dx")) || (dx_base && (r = fp4_rows(dx_base, lddx_base, f->K, "dx_base"))))
+        return r;
+    if (dx_base == dx && lddx_base != lddx) return fail(MOE_ERR_ARG, "dx_base is dx with another stride");
+    if (shared_memory({dx}, {dy, codes, scales, row_exp}, nullptr, nullptr)) return fail(MOE_ERR_ARG, "dx is an input");
+    if ((r = check_ws(ws, ws_bytes, moe::fp4_ws_bytes(f->K, f->N, f->format, f->dtype, T, true)))) return r;
+    return hip_status(moe::launch_fp4_backward(f->K, f->N, f->format, f->dtype, dy, (size_t)lddy, T,
+                                               {codes, scales, row_exp}, dx_base, (size_t)lddx_base, dx, (size_t)lddx, ws,
+                                               reinterpret_cast<hipStream_t>(stream)),
+                      "fp4 gradient launch");
+}
+
+int moe_block_norm(const moe_norm_desc* n, const void* r, int64_t ldr, const void* y, int64_t ldy, int32_t T,
+                   const uint8_t* mask, const float* post, const float* gate, const float* pre, void* r_out,
+                   int64_t ldr_out, void* x, int64_t ldx, void* stream) {
+    int e;
+    if ((e = norm_checks(n, T))) return e;
+    if ((e = norm_vectors(n, T, y, post, gate, pre))) return e;
+    if (T == 0) return ok();
+    if ((pre != nullptr) != (x != nullptr)) return fail(MOE_ERR_ARG, "x and pre go together");
+    if (!r_out && !x) return fail(MOE_ERR_ARG, "no output");
+    if ((e = check_rows(r, ldr, n->H, "r")) || (y && (e = check_rows(y, ldy, n->H, "y"))) ||
+        (r_out && (e = check_rows(r_out, ldr_out, n->H, "r_out"))) || (x && (e = check_rows(x, ldx, n->H, "x"))))
+        return e;
+    if (r_out == r && ldr_out != ldr) return fail(MOE_ERR_ARG, "r_out is r with another stride");
+    if (shared_memory({r_out, x}, {r, y, mask, post, gate, pre}, r_out, r))
+        return fail(MOE_ERR_ARG, "an output is an input or another output");
+    moe::NormArgs a = {};
+    a.H = n->H; a.T = T; a.rt = n->r_dtype; a.yt = n->y_dtype; a.xt = n->x_dtype; a.gate_kind = n->gate;
+    a.scale = n->scale; a.eps = n->eps;
+    a.r = r; a.y = y; a.mask = mask; a.post = post; a.gate = gate; a.pre = pre;
+    a.ldr = (size_t)ldr; a.ldy = (size_t)ldy; a.r_out = r_out; a.x = x; a.ldro = (size_t)ldr_out; a.ldx = (size_t)ldx;
+    return hip_status(moe::launch_block_norm(a, reinterpret_cast<hipStream_t>(stream)), "norm launch");
+}
+
+size_t moe_block_norm_workspace_bytes(const moe_norm_desc* n, int32_t T) {
+    return norm_checks(n, T) == MOE_OK ? moe::norm_ws_bytes(n->H, n->gate, T) : 0;
+}
+
+int moe_block_norm_backward(const moe_norm_desc* n, const void* r_out, int64_t ldr_out, const void* y, int64_t ldy,
+                            int32_t T, const uint8_t* mask, const float* post, const float* gate, const float* pre,
+                            const void* dr_out, int64_t lddr_out, const void* dx, int64_t lddx, void* dr, int64_t lddr,
+                            void* dy, int64_t lddy, float* dpost, float* dgate, float* dpre, int32_t accumulate,
+                            void* ws, size_t ws_bytes, void* stream) {
+    int e;
+    if ((e = norm_checks(n, T))) return e;
+    if ((e = norm_vectors(n, T, y, post, gate, pre))) return e;
+    if (T > 0 && !dr && !dy && !dpost && !dgate && !dpre) return fail(MOE_ERR_ARG, "no output");
+    if (T > 0 && !y && (dy || dgate)) return fail(MOE_ERR_ARG, "a gradient of y or its gate without y");
+    if (dpost && !post) return fail(MOE_ERR_ARG, "dpost without post");
+    if (dpre && !pre) return fail(MOE_ERR_ARG, "dpre without pre");
+    if (dx && !pre) return fail(MOE_ERR_ARG, "dx without pre");
+    if (dpre && !dx && T > 0) return fail(MOE_ERR_ARG, "dpre without dx");
+    if (dgate && n->gate == MOE_GATE_NONE) return fail(MOE_ERR_ARG, "dgate beside MOE_GATE_NONE");
+    if ((dpost && (e = check_ptr(dpost, 16, "dpost"))) || (dpre && (e = check_ptr(dpre, 16, "dpre"))) ||
+        (dgate && (e = check_ptr(dgate, n->gate == MOE_GATE_CHANNEL ? 16 : 4, "dgate"))))
+        return e;
+    if (T > 0) {
+        if ((dx && (e = check_rows(r_out, ldr_out, n->H, "r_out"))) || (y && (e = check_rows(y, ldy, n->H, "y"))) ||
+            (dr_out && (e = check_rows(dr_out, lddr_out, n->H, "dr_out"))) ||
+            (dx && (e = check_rows(dx, lddx, n->H, "dx"))) || (dr && (e = check_rows(dr, lddr, n->H, "dr"))) ||
+            (dy && (e = check_rows(dy, lddy, n->H, "dy"))))
+            return e;
+        if (dr && dr == dr_out && lddr != lddr_out) return fail(MOE_ERR_ARG, "dr is dr_out with another stride");
+        if (shared_memory({dr, dy, dpost, dgate, dpre}, {r_out, y, mask, post, gate, pre, dr_out, dx}, dr, dr_out))
+            return fail(MOE_ERR_ARG, "an output is an input or another output");
+    } else if (shared_memory({dpost, dgate, dpre}, {post, gate, pre}, nullptr, nullptr)) {
+        return fail(MOE_ERR_ARG, "an output is an input or another output");
+    }
+    if ((e = check_ws(ws, ws_bytes, moe::norm_ws_bytes(n->H, n->gate, T)))) return e;
+    moe::NormArgs a = {};
+    a.H = n->H; a.T = T; a.rt = n->r_dtype; a.yt = n->y_dtype; a.xt = n->x_dtype; a.gate_kind = n->gate;
+    a.scale = n->scale; a.eps = n->eps;
+    a.r = r_out; a.y = y; a.mask = mask; a.post = post; a.gate = gate; a.pre = pre;
+    a.ldr = (size_t)ldr_out; a.ldy = (size_t)ldy;
+    a.dr_out = dr_out; a.dx = dx; a.dr = dr; a.dy = dy;
+    a.lddro = (size_t)lddr_out; a.lddx = (size_t)lddx; a.lddr = (size_t)lddr; a.lddy = (size_t)lddy;
+    a.dpost = dpost; a.dgate = dgate; a.dpre = dpre; a.accumulate = accumulate != 0;
+    return hip_status(moe::launch_block_norm_backward(a, ws, reinterpret_cast<hipStream_t>(stream)), "norm gradient launch");
 }
 
 size_t moe_prefetch_sink_bytes(const moe_desc* d, int32_t n) {

@@ -62,6 +62,7 @@ extern "C" {
 #define MOE_MODE_ROUTE 0
 #define MOE_MODE_DECODE 1
 #define MOE_MODE_PREFILL 2
+#define MOE_MODE_DECODE_BATCH 3
 
 #define MOE_OUT_F32 0
 #define MOE_OUT_BF16 1
@@ -180,6 +181,30 @@ int moe_expert_decode(const moe_desc *d, const float *x, const void *const *expe
 int moe_layer_decode(const moe_desc *d, const float *x, const float *Wr, const void *const *expert_ptrs,
                      const moe_shared *shared, float *y, int32_t *idx_out, float *w_out, void *ws, size_t ws_bytes,
                      void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* Decode: a few tokens                                                    */
+/* ---------------------------------------------------------------------- */
+
+/* One layer for T tokens at once (sequences decoded side by side, a draft of
+ * several tokens checked at once): for every token what moe_layer_decode
+ * computes for one, in fp32 with fp32 accumulation; each chosen expert's block
+ * is read once for all of its tokens. Results are bit-identical from run to
+ * run, but not to moe_layer_decode's (the sums run in another order; the
+ * chosen experts agree unless two logits differ by less than their rounding).
+ *   x    [T][H] fp32, 16-B aligned;  Wr [E][H] fp32
+ *   mask [T] uint8 or NULL: a token with mask[t] == 0 (an empty slot of a
+ *        serving batch) is left out: its rows of y, idx_out and w_out stay as
+ *        they were, and its row of x does not matter
+ *   y    [T][H] fp32 (out);  idx_out [T][k] int32 (out);  w_out [T][k] fp32 (out)
+ * expert_ptrs, shared and the supported shapes as for moe_layer_decode, and
+ * T <= 64 (MOE_ERR_UNSUPPORTED above; moe_expert_prefill takes longer
+ * batches). T = 0 enqueues nothing. Outputs overlap neither inputs nor each
+ * other. Workspace: moe_workspace_bytes(d, T, MOE_MODE_DECODE_BATCH), which
+ * never falls as T grows. */
+int moe_layer_decode_batch(const moe_desc *d, const float *x, int32_t T, const uint8_t *mask, const float *Wr,
+                           const void *const *expert_ptrs, const moe_shared *shared, float *y, int32_t *idx_out,
+                           float *w_out, void *ws, size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------------- */
 /* Decode without a workspace                                              */
@@ -420,6 +445,144 @@ int moe_lora_backward(const moe_lora_desc *l, const void *x, int64_t ldx, const 
                       const float *scales, const void *dx_base, int64_t lddx_base, void *dx, int64_t lddx,
                       float *const *da_ptrs, float *const *db_ptrs, int32_t accumulate, void *ws, size_t ws_bytes,
                       void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* 4-bit matrices: quantisation and products                               */
+/* ---------------------------------------------------------------------- */
+
+#define MOE_SCALE_NEAREST 2 /* NVFP4: the E4M3 value nearest to amax / 6 */
+
+/* A matrix to block-scaled e2m1 codes, laid out as in an expert block (codes
+ * [rows][cols / 2], element 2c in the low nibble of byte c; scales
+ * [rows][cols / G]): three calls fill the regions of one block.
+ *   MOE_FMT_MXFP4, rule MOE_SCALE_FLOOR: shared exponent X = floor(log2 amax) - 2
+ *     (OCP MX; quotients above 6 saturate); MOE_SCALE_CEIL: the smallest X with
+ *     amax <= 6 * 2^X. X is clamped to [-127, 125]; byte X + 127, 0 for an
+ *     all-zero block. row_exp must be NULL.
+ *   MOE_FMT_NVFP4, rule MOE_SCALE_NEAREST: scale = the E4M3 value nearest to
+ *     amax / 6 (ties to even, at most 448) of the row's values times 2^-e.
+ *     e = row_exp[r] (out) is the smallest with the row's largest finite
+ *     magnitude <= 2688 * 2^e, in [-100, 116], 0 for a row of zeros; with
+ *     row_exp NULL (expert blocks) e = 0.
+ *   codes: v / (scale 2^e) to the nearest e2m1 value, ties to the even code,
+ *     magnitudes above 6 saturate; a negative value that rounds to zero keeps
+ *     its sign. A block that holds an infinity or a NaN gets a NaN scale (0xFF;
+ *     E4M3 0x7F) and codes 0.
+ * Every step is exact: the codes and scales are those of the definition.
+ *   x      [rows] rows of cols elements of dtype (MOE_ACT_*), stride ldx
+ *          elements; 16-B aligned, strides multiples of 8
+ *   cols   a positive multiple of G
+ *   codes  (out) 4-B aligned, or NULL;  scales (out) or NULL
+ *   values (out) the values that the codes stand for, in dtype (in fp16 at most
+ *          65504 in magnitude), stride ldv; or NULL; may be x with its stride
+ * At least one output. rows == 0 enqueues nothing. No workspace. Errors:
+ * MOE_ERR_ARG; MOE_ERR_UNSUPPORTED above 2^33 elements. */
+int moe_fp4_quant(const void *x, int64_t ldx, int32_t rows, int32_t cols, int32_t dtype, int32_t format, int32_t rule,
+                  int8_t *row_exp, uint8_t *codes, uint8_t *scales, void *values, int64_t ldv, void *stream);
+
+/* K = input size, N = output size, format = MOE_FMT_*, dtype = MOE_ACT_* of
+ * the activations on both sides. */
+typedef struct moe_fp4_desc {
+    int32_t K, N, format, dtype;
+} moe_fp4_desc;
+
+/* y[t] = base[t] + W x[t] with W [N][K] stored as moe_fp4_quant writes it:
+ * W[n][k] = e2m1(code) * scale * 2^row_exp[n]. The activations keep all their
+ * bits (fp32 ones down to 2^-133), products are exact, sums are in fp32, y is
+ * rounded once. With round_x != 0 (MOE_FMT_MXFP4 only) the activations are
+ * first rounded to MXFP4 per 32 elements (MOE_SCALE_FLOOR) and multiplied as
+ * codes on the FP4 matrix units. Results are bit-identical from run to run.
+ *   x     [T] rows of K, stride ldx;  base (or NULL: zeros; may be y, with its
+ *         stride) and y [T] rows of N, strides ldbase and ldy. 16-B aligned,
+ *         strides multiples of 8, at least the row and at most 2^22 elements
+ *   codes [N][K / 2], 16-B aligned; scales [N][K / G];
+ *   row_exp [N] in [-100, 116], or NULL: zeros (MOE_FMT_MXFP4: must be NULL)
+ * An infinity or a NaN among the activations enters the sums as in fp32
+ * arithmetic; one in W (a NaN scale, a value above the largest fp32) makes
+ * every output that it enters infinite or NaN. T = 0 enqueues nothing. y
+ * overlaps no input, but for base. Workspace:
+ * moe_fp4_workspace_bytes(f, T, 0), which never falls as T grows. Errors:
+ * MOE_ERR_ARG (K not a multiple of 32, N not of 8, pointers, strides, round_x
+ * with NVFP4); MOE_ERR_UNSUPPORTED unless K, N <= 65536, T <= 2^20 and strides
+ * <= 2^22; MOE_ERR_WORKSPACE. */
+size_t moe_fp4_workspace_bytes(const moe_fp4_desc *f, int32_t T, int32_t backward);
+int moe_fp4_apply(const moe_fp4_desc *f, const void *x, int64_t ldx, int32_t T, const uint8_t *codes,
+                  const uint8_t *scales, const int8_t *row_exp, int32_t round_x, const void *base, int64_t ldbase,
+                  void *y, int64_t ldy, void *ws, size_t ws_bytes, void *stream);
+
+/* The activations' gradient: dx[t] = dx_base[t] + W^T dy[t] (W is frozen; a
+ * rounding of x counts as the identity). dy [T] rows of N, dx_base (or NULL)
+ * and dx [T] rows of K; dx may be dx_base, e.g. to add to what
+ * moe_lora_backward takes as its own dx_base. Arithmetic, alignment, strides,
+ * limits and errors as for moe_fp4_apply; workspace:
+ * moe_fp4_workspace_bytes(f, T, 1). */
+int moe_fp4_backward(const moe_fp4_desc *f, const void *dy, int64_t lddy, int32_t T, const uint8_t *codes,
+                     const uint8_t *scales, const int8_t *row_exp, const void *dx_base, int64_t lddx_base, void *dx,
+                     int64_t lddx, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* The norms around a block                                                */
+/* ---------------------------------------------------------------------- */
+
+#define MOE_GATE_NONE 0
+#define MOE_GATE_CHANNEL 1 /* gate [H]: one learned value a channel */
+#define MOE_GATE_TOKEN 2   /* gate [T]: one value a token */
+
+/* H = hidden size; r_dtype, y_dtype, x_dtype = MOE_ACT_* of the residual
+ * stream, the block's output and the next block's input; gate = MOE_GATE_*;
+ * scale = residual scale; eps > 0. */
+typedef struct moe_norm_desc {
+    int32_t H, r_dtype, y_dtype, x_dtype, gate;
+    float scale, eps;
+} moe_norm_desc;
+
+/* Behind a block and before the next one, in one pass: with
+ * rms(v) = v / sqrt(mean(v^2) + eps),
+ *   s     = r + scale * gate * (rms(y) * post)
+ *   r_out = s rounded to r_dtype
+ *   x     = rms(s) * pre rounded to x_dtype (from s before its rounding)
+ * in fp32. y NULL: s = r (the norm before the first block); post NULL: y
+ * enters without a norm; pre NULL: no x.
+ *   r, y  [T] rows of H with strides ldr, ldy;  r_out (or NULL; may be r, with
+ *         its stride) and x (NULL without pre) [T] rows of H. 16-B aligned,
+ *         strides multiples of 8 and at least H
+ *   mask  [T] uint8 or NULL: rows with mask[t] == 0 are not read, and their
+ *         rows of r_out and x stay as they were
+ *   post, pre [H] fp32, 16-B aligned;  gate [H] or [T] fp32 (channel: 16-B
+ *         aligned)
+ * T = 0 enqueues nothing. Outputs overlap neither inputs nor each other, but
+ * for r_out == r. Errors: MOE_ERR_ARG (H not a multiple of 8, eps not above 0,
+ * scale not finite, pointers, strides); MOE_ERR_UNSUPPORTED unless H <= 16384
+ * and T <= 2^20. */
+int moe_block_norm(const moe_norm_desc *n, const void *r, int64_t ldr, const void *y, int64_t ldy, int32_t T,
+                   const uint8_t *mask, const float *post, const float *gate, const float *pre, void *r_out,
+                   int64_t ldr_out, void *x, int64_t ldx, void *stream);
+
+/* Its backward pass, from the stored sum r_out (all of the forward pass that
+ * it needs beside y): dr_out is the gradient that reaches r_out from behind
+ * (NULL: zeros), dx the gradient of x (NULL: zeros; needed with dpre). With
+ * n = rms(r_out), q = rms(y) (y itself without post) and the root mean squares
+ * S and Y that they were divided by:
+ *   a = dx * pre,  d = dr_out + (a - n * mean(a n)) / S,  dr = d
+ *   dpre = sum_t dx * n;  u = scale * gate * d;  dpost = sum_t u * q
+ *   dgate = scale * d * q * post summed over the tokens (channel) or the
+ *           channels (token)
+ *   b = u * post,  dy = (b - q * mean(b q)) / Y   (without post: dy = u)
+ * A row with mask[t] == 0 has dr = dy = 0, dgate[t] = 0 and enters no sum.
+ *   dr [T] rows of H (r_dtype; may be dr_out, with its stride), dy [T] rows of
+ *   H (y_dtype), dpost, dpre [H], dgate [H] or [T] fp32 (out); any may be NULL.
+ *   accumulate != 0 adds to dpost, dpre and dgate instead of writing them.
+ * Sums over tokens run in a fixed order: results are bit-identical from run to
+ * run. T = 0 writes zeros to dpost, dpre and a channel's dgate (unless it
+ * accumulates). Outputs overlap neither inputs nor each other, but for
+ * dr == dr_out. Workspace: moe_block_norm_workspace_bytes(n, T), which never
+ * falls as T grows. Errors as for moe_block_norm; MOE_ERR_WORKSPACE. */
+size_t moe_block_norm_workspace_bytes(const moe_norm_desc *n, int32_t T);
+int moe_block_norm_backward(const moe_norm_desc *n, const void *r_out, int64_t ldr_out, const void *y, int64_t ldy,
+                            int32_t T, const uint8_t *mask, const float *post, const float *gate, const float *pre,
+                            const void *dr_out, int64_t lddr_out, const void *dx, int64_t lddx, void *dr, int64_t lddr,
+                            void *dy, int64_t lddy, float *dpost, float *dgate, float *dpre, int32_t accumulate,
+                            void *ws, size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------------- */
 /* Speculative expert prefetch                                             */
