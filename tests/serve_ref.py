@@ -113,14 +113,15 @@ def layer(x, mats, shared, idx, w):
 
     Products of 4-bit weights with fp32 values taken as parts are exact to 2^-22 of each product, and
     2^-39 of the row's largest value (parts of fp16 under one power of two); three bf16 parts are exact.
-    A sum of up to 3 K such products: (3 K + 2) EPS + 3 2^-22 of the magnitudes."""
+    A sum of up to 3 K such products: (3 K + 2) EPS + 3 2^-22 of the magnitudes. Below fp32's normal range
+    a result is off by half its smallest step, 2^-150, at most, whatever its size."""
     T, H = x.shape
     y, off = torch.zeros((T, H), dtype=torch.float64), torch.zeros((T, H), dtype=torch.float64)
 
     def dot(m, v, ev):
         K = m.shape[1]
         out, mag = m @ v, m.abs() @ v.abs()
-        return out, ((3 * K + 2) * EPS + 3 * 2.0 ** -22) * mag + 2.0 ** -39 * v.abs().max() * m.abs().sum(1) + m.abs() @ ev
+        return out, ((3 * K + 2) * EPS + 3 * 2.0 ** -22) * mag + 2.0 ** -39 * v.abs().max() * m.abs().sum(1) + m.abs() @ ev + 3 * K * 2.0 ** -149
 
     def ffn(g, u, d, v):
         zero = torch.zeros_like(v)
@@ -131,7 +132,7 @@ def layer(x, mats, shared, idx, w):
         slope = (sg * (1 + a * (1 - sg))).abs()  # of silu
         # silu in fp32: expf, an addition, a division and two products, each a few roundings; an e^-a that
         # overflows leaves 0 for a value below 1e-36
-        eh = slope * ea * b.abs() + (a * sg).abs() * eb + ea * eb + 16 * EPS * h.abs() * (1 + a.abs() * EPS) + 1e-36 * b.abs()
+        eh = slope * ea * b.abs() + (a * sg).abs() * eb + ea * eb + 16 * EPS * h.abs() * (1 + a.abs() * EPS) + 1e-36 * b.abs() + 2.0 ** -148
         return dot(d, h, eh)
 
     for t in range(T):
