@@ -12,10 +12,10 @@
 //   b = u post,  dy = rs_y (b - q mean(b q))
 //
 // Memory bounds both: every row is held in registers between its sums and its
-// outputs, so each value is read once and written once. A workgroup of 256
-// threads takes a row at a time; the sums over the tokens are kept in registers
-// by workgroups that run through rows, written out as one partial row for each
-// and added in a fixed order by a second launch.
+// outputs, so each value is read once and written once. A workgroup takes a row
+// at a time; the sums over the tokens are kept in registers by workgroups that
+// run through rows, written out as one partial row for each and added in a
+// fixed order by a second launch.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -27,278 +27,394 @@
 namespace moe {
 namespace {
 
-// Loads and stores of eight elements in a type known at run time (uniform).
-__device__ __forceinline__ void get8(int dt, const void* row, size_t at, float (&v)[8]) {
-    if (dt == kActF32) unpack8<kActF32>(load8<kActF32>(row, at), v);
-    else if (dt == kActBf16) unpack8<kActBf16>(load8<kActBf16>(row, at), v);
-    else unpack8<kActF16>(load8<kActF16>(row, at), v);
+// Eight elements of a row whose type's size S is known at compile time (the
+// loads of a row go out together and are waited for once) and whose kind, of
+// the 16-bit ones, at run time.
+template <int S>
+struct Piece {
+    u4w w[S / 2];
+};
+template <int S>
+__device__ __forceinline__ void fetch(Piece<S>& p, const void* row, uint32_t c) {
+    const u4w* q = reinterpret_cast<const u4w*>(row) + (size_t)c * (S / 2);
+#pragma unroll
+    for (int i = 0; i < S / 2; i++) p.w[i] = q[i];
 }
-__device__ __forceinline__ void put8(int dt, void* row, size_t at, const float (&v)[8]) {
-    if (dt == kActF32) store8<kActF32>(row, at, pack8<kActF32>(v));
-    else if (dt == kActBf16) store8<kActBf16>(row, at, pack8<kActBf16>(v));
-    else store8<kActF16>(row, at, pack8<kActF16>(v));
+template <int S>
+__device__ __forceinline__ void widen(const Piece<S>& p, int dt, float (&v)[8]) {
+    if constexpr (S == 4) {
+        unpack8<kActF32>(Raw8<kActF32>{{p.w[0], p.w[1]}}, v);
+    } else {
+        if (dt == kActBf16) unpack8<kActBf16>(Raw8<kActBf16>{{p.w[0]}}, v);
+        else unpack8<kActF16>(Raw8<kActF16>{{p.w[0]}}, v);
+    }
 }
-__device__ __forceinline__ size_t es(int dt) { return dt == kActF32 ? 4 : 2; }
+template <int S>
+__device__ __forceinline__ void put(int dt, void* row, uint32_t c, const float (&v)[8]) {
+    if constexpr (S == 4) store8<kActF32>(row, 8 * (size_t)c, pack8<kActF32>(v));
+    else store8<kActBf16>(row, 8 * (size_t)c, dt == kActBf16 ? pack8<kActBf16>(v) : Raw8<kActBf16>{{pack8<kActF16>(v).w[0]}});
+}
+template <int S>
+__device__ __forceinline__ auto row_of(const void* p, size_t ld, size_t t) {
+    return static_cast<const char*>(p) + t * ld * S;
+}
 
-// Sum over the workgroup's 256 threads, in a fixed order, for everybody. The
-// caller alternates between two places so that one barrier a sum is enough.
-__device__ __forceinline__ float block_sum(float v, float* place) {
-    v = wave_sum(v);
-    if ((threadIdx.x & 63) == 0) place[wave_id()] = v;
+// Sums over the workgroup's threads, in a fixed order, for everybody.
+template <int N>
+__device__ __forceinline__ void block_sums(float (&v)[N], float (*place)[16]) {
+#pragma unroll
+    for (int n = 0; n < N; n++) v[n] = wave_sum(v[n]);
+    const int waves = blockDim.x >> 6;
+    if (waves == 1) return;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+        for (int n = 0; n < N; n++) place[n][wave_id()] = v[n];
+    }
     __syncthreads();
-    return (place[0] + place[1]) + (place[2] + place[3]);
+#pragma unroll
+    for (int n = 0; n < N; n++) {
+        float s = 0.0f;
+        for (int w = 0; w < waves; w++) s += place[n][w];
+        v[n] = s;
+    }
 }
+__device__ __forceinline__ float rms_inv(float sum, const NormArgs& a) { return 1.0f / sqrtf(sum * (1.0f / (float)a.H) + a.eps); }
 
-// NI: pieces of 8 channels a thread, H <= 2048 NI.
-template <int NI>
-__global__ __launch_bounds__(256) void k_norm_fwd(NormArgs a) {
-    __shared__ float red[2][4];
-    const int t = blockIdx.x, tid = threadIdx.x, n8 = a.H / 8;
+// A workgroup a row. NI: pieces of 8 channels a thread (H <= 8 NI threads).
+template <int SR, int SY, int SX, int NI, int NT>
+__global__ __launch_bounds__(NT) void k_norm_fwd(NormArgs a) {
+    __shared__ float red[2][1][16];
+    const uint32_t t = blockIdx.x, n8 = a.H / 8;
     if (a.mask && !a.mask[t]) return;
-    const float inv = 1.0f / (float)a.H;
-    const char* r = static_cast<const char*>(a.r) + (size_t)t * a.ldr * es(a.rt);
-    float s[NI][8], y[NI][8];
-    float sum = 0.0f;
+    uint32_t c[NI];
+    Piece<SR> pr[NI];
+    Piece<SY> py[NI];
+    Piece<4> wpost[NI], wgate[NI], wpre[NI];
+    const bool ch = a.gate_kind == kGateChannel && a.y;
 #pragma unroll
     for (int i = 0; i < NI; i++) {
-        const int c = tid + 256 * i;
-        if (c < n8) {
-            get8(a.rt, r, 8 * (size_t)c, s[i]);
-            if (a.y) {
-                get8(a.yt, static_cast<const char*>(a.y) + (size_t)t * a.ldy * es(a.yt), 8 * (size_t)c, y[i]);
+        c[i] = threadIdx.x + blockDim.x * i;
+        const uint32_t l = min(c[i], n8 - 1);
+        fetch<SR>(pr[i], row_of<SR>(a.r, a.ldr, t), l);
+        if (a.y) fetch<SY>(py[i], row_of<SY>(a.y, a.ldy, t), l);
+        if (a.post) fetch<4>(wpost[i], a.post, l);
+        if (ch) fetch<4>(wgate[i], a.gate, l);
+        if (a.pre) fetch<4>(wpre[i], a.pre, l);
+    }
+    const float gt = a.scale * (a.y && a.gate_kind == kGateToken ? a.gate[t] : 1.0f);
+    float s[NI][8];
 #pragma unroll
-                for (int j = 0; j < 8; j++) sum = fmaf(y[i][j], y[i][j], sum);
+    for (int i = 0; i < NI; i++) widen<SR>(pr[i], a.rt, s[i]);
+    if (a.y) {
+        float y[NI][8], sum[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < NI; i++) {
+            widen<SY>(py[i], a.yt, y[i]);
+            if (c[i] < n8)
+#pragma unroll
+                for (int j = 0; j < 8; j++) sum[0] = fmaf(y[i][j], y[i][j], sum[0]);
+        }
+        float rs = 1.0f;
+        if (a.post) {
+            block_sums(sum, red[0]);
+            rs = rms_inv(sum[0], a);
+        }
+#pragma unroll
+        for (int i = 0; i < NI; i++) {
+            float w[8], g[8];
+            if (a.post) widen<4>(wpost[i], kActF32, w);
+            if (ch) widen<4>(wgate[i], kActF32, g);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                float v = y[i][j] * rs;
+                if (a.post) v *= w[j];
+                s[i][j] = fmaf(ch ? gt * g[j] : gt, v, s[i][j]);
             }
         }
     }
-    if (a.y) {
-        const float rs = a.post ? 1.0f / sqrtf(block_sum(sum, red[0]) * inv + a.eps) : 1.0f;
-        const float gt = a.scale * (a.gate_kind == kGateToken ? a.gate[t] : 1.0f);
+    float sum[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NI; i++)
+        if (c[i] < n8) {
+            if (a.r_out) put<SR>(a.rt, const_cast<char*>(row_of<SR>(a.r_out, a.ldro, t)), c[i], s[i]);
+#pragma unroll
+            for (int j = 0; j < 8; j++) sum[0] = fmaf(s[i][j], s[i][j], sum[0]);
+        }
+    if (!a.pre) return;
+    block_sums(sum, red[1]);
+    const float rs = rms_inv(sum[0], a);
+#pragma unroll
+    for (int i = 0; i < NI; i++)
+        if (c[i] < n8) {
+            float w[8];
+            widen<4>(wpre[i], kActF32, w);
+#pragma unroll
+            for (int j = 0; j < 8; j++) w[j] *= s[i][j] * rs;
+            put<SX>(a.xt, const_cast<char*>(row_of<SX>(a.x, a.ldx, t)), c[i], w);
+        }
+}
+
+// part: [3][groups][H] sums of dpost, dpre, dgate (channel).
+template <int SR, int SY, int SX, int NI, int NT>
+__global__ __launch_bounds__(NT) void k_norm_bwd(NormArgs a, float* __restrict__ part) {
+    __shared__ float red[2][3][16];
+    const uint32_t n8 = a.H / 8, groups = gridDim.x;
+    const float inv = 1.0f / (float)a.H;
+    const bool ch = a.gate_kind == kGateChannel && a.y, tok = a.gate_kind == kGateToken && a.y;
+    uint32_t c[NI], l[NI];
+    float spost[NI][8], spre[NI][8], sgate[NI][8];
+    struct Row {
+        Piece<SR> r[NI], dro[NI];
+        Piece<SX> dx[NI];
+        Piece<SY> y[NI];
+        float gate;
+        bool on;
+    };
+#pragma unroll
+    for (int i = 0; i < NI; i++) {
+        c[i] = threadIdx.x + blockDim.x * i;
+        l[i] = min(c[i], n8 - 1);
+#pragma unroll
+        for (int j = 0; j < 8; j++) spost[i][j] = spre[i][j] = sgate[i][j] = 0.0f;
+    }
+    Piece<4> wpre[NI], wpost[NI], wgate[NI];
+    auto weights = [&]() {
 #pragma unroll
         for (int i = 0; i < NI; i++) {
-            const int c = tid + 256 * i;
-            if (c < n8) {
-                float w[8], g[8];
-                if (a.post) get8(kActF32, a.post, 8 * (size_t)c, w);
-                if (a.gate_kind == kGateChannel) get8(kActF32, a.gate, 8 * (size_t)c, g);
+            if (a.dx) fetch<4>(wpre[i], a.pre, l[i]);
+            if (a.post) fetch<4>(wpost[i], a.post, l[i]);
+            if (ch) fetch<4>(wgate[i], a.gate, l[i]);
+        }
+    };
+    auto start = [&](uint32_t t, Row& q) {
+        q.on = !a.mask || a.mask[t];
+        q.gate = tok ? a.gate[t] : 1.0f;
+#pragma unroll
+        for (int i = 0; i < NI; i++) {
+            if (a.dx) {
+                fetch<SR>(q.r[i], row_of<SR>(a.r, a.ldr, t), l[i]);
+                fetch<SX>(q.dx[i], row_of<SX>(a.dx, a.lddx, t), l[i]);
+            }
+            if (a.dr_out) fetch<SR>(q.dro[i], row_of<SR>(a.dr_out, a.lddro, t), l[i]);
+            if (a.y) fetch<SY>(q.y[i], row_of<SY>(a.y, a.ldy, t), l[i]);
+        }
+    };
+    auto work = [&](uint32_t t, const Row& q) {
+        void* dr = a.dr ? const_cast<char*>(row_of<SR>(a.dr, a.lddr, t)) : nullptr;
+        void* dy = a.dy ? const_cast<char*>(row_of<SY>(a.dy, a.lddy, t)) : nullptr;
+        if (!q.on) {
+            const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < NI; i++)
+                if (c[i] < n8) {
+                    if (dr) put<SR>(a.rt, dr, c[i], z);
+                    if (dy) put<SY>(a.yt, dy, c[i], z);
+                }
+            if (tok && a.dgate && threadIdx.x == 0 && !a.accumulate) a.dgate[t] = 0.0f;
+            return;
+        }
+        if (NI > 1) weights();
+        float s[3] = {0.0f, 0.0f, 0.0f};  // r^2, dx pre r, y^2
+        float d[NI][8], y[NI][8], r[NI][8], av[NI][8];
+#pragma unroll
+        for (int i = 0; i < NI; i++) {
+            if (a.dx) {
+                float w[8];
+                widen<SR>(q.r[i], a.rt, r[i]);
+                widen<SX>(q.dx[i], a.xt, av[i]);
+                widen<4>(wpre[i], kActF32, w);
+                if (c[i] < n8)
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        s[0] = fmaf(r[i][j], r[i][j], s[0]);
+                        s[1] = fmaf(av[i][j] * w[j], r[i][j], s[1]);
+                    }
+            }
+            if (a.dr_out) widen<SR>(q.dro[i], a.rt, d[i]);
+            else
+#pragma unroll
+                for (int j = 0; j < 8; j++) d[i][j] = 0.0f;
+            if (a.y) {
+                widen<SY>(q.y[i], a.yt, y[i]);
+                if (c[i] < n8)
+#pragma unroll
+                    for (int j = 0; j < 8; j++) s[2] = fmaf(y[i][j], y[i][j], s[2]);
+            }
+        }
+        block_sums(s, red[0]);
+        if (a.dx) {
+            const float rs = rms_inv(s[0], a), m = s[1] * rs * inv;
+#pragma unroll
+            for (int i = 0; i < NI; i++) {
+                float w[8];
+                widen<4>(wpre[i], kActF32, w);
 #pragma unroll
                 for (int j = 0; j < 8; j++) {
-                    float v = y[i][j] * rs;
-                    if (a.post) v *= w[j];
-                    s[i][j] = fmaf(a.gate_kind == kGateChannel ? gt * g[j] : gt, v, s[i][j]);
+                    const float n = r[i][j] * rs;
+                    spre[i][j] = fmaf(av[i][j], n, spre[i][j]);
+                    d[i][j] = fmaf(rs, fmaf(-n, m, av[i][j] * w[j]), d[i][j]);
                 }
             }
         }
-    }
-    sum = 0.0f;
-    char* ro = static_cast<char*>(a.r_out) + (size_t)t * a.ldro * es(a.rt);
+        if (dr) {
 #pragma unroll
-    for (int i = 0; i < NI; i++) {
-        const int c = tid + 256 * i;
-        if (c < n8) {
-            if (a.r_out) put8(a.rt, ro, 8 * (size_t)c, s[i]);
-#pragma unroll
-            for (int j = 0; j < 8; j++) sum = fmaf(s[i][j], s[i][j], sum);
+            for (int i = 0; i < NI; i++)
+                if (c[i] < n8) put<SR>(a.rt, dr, c[i], d[i]);
         }
-    }
-    if (!a.pre) return;
-    const float rs = 1.0f / sqrtf(block_sum(sum, red[1]) * inv + a.eps);
-    char* x = static_cast<char*>(a.x) + (size_t)t * a.ldx * es(a.xt);
+        if (!a.y) return;
+        const float rs = a.post ? rms_inv(s[2], a) : 1.0f, gt = a.scale * q.gate;
+        float b[2] = {0.0f, 0.0f};  // d post y, and times the channel's gate
 #pragma unroll
-    for (int i = 0; i < NI; i++) {
-        const int c = tid + 256 * i;
-        if (c < n8) {
-            float w[8];
-            get8(kActF32, a.pre, 8 * (size_t)c, w);
+        for (int i = 0; i < NI; i++) {
+            float w[8], g[8];
+            if (a.post) widen<4>(wpost[i], kActF32, w);
+            if (ch) widen<4>(wgate[i], kActF32, g);
+            if (c[i] < n8)
 #pragma unroll
-            for (int j = 0; j < 8; j++) w[j] *= s[i][j] * rs;
-            put8(a.xt, x, 8 * (size_t)c, w);
+                for (int j = 0; j < 8; j++) {
+                    const float v = a.post ? d[i][j] * w[j] : d[i][j];
+                    b[0] = fmaf(v, y[i][j], b[0]);
+                    if (ch) b[1] = fmaf(v * g[j], y[i][j], b[1]);
+                }
         }
+        if (a.post || tok) block_sums(b, red[1]);
+        const float m = a.post ? (ch ? b[1] : b[0]) * gt * rs * inv : 0.0f;
+        if (tok && a.dgate && threadIdx.x == 0) {
+            const float v = b[0] * rs * a.scale;
+            a.dgate[t] = a.accumulate ? a.dgate[t] + v : v;
+        }
+#pragma unroll
+        for (int i = 0; i < NI; i++) {
+            float w[8], g[8], o[8];
+            if (a.post) widen<4>(wpost[i], kActF32, w);
+            if (ch) widen<4>(wgate[i], kActF32, g);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const float p = a.post ? w[j] : 1.0f, n = y[i][j] * rs;
+                const float u = (ch ? gt * g[j] : gt) * d[i][j];
+                spost[i][j] = fmaf(u, n, spost[i][j]);
+                if (ch) sgate[i][j] = fmaf(d[i][j] * p, n, sgate[i][j]);
+                o[j] = a.post ? rs * fmaf(-n, m, u * p) : u;
+            }
+            if (dy && c[i] < n8) put<SY>(a.yt, dy, c[i], o);
+        }
+    };
+    if (NI == 1) weights();
+    const uint32_t T = a.T;
+    for (uint32_t t = blockIdx.x; t < T; t += groups) {
+        Row q;
+        start(t, q);
+        work(t, q);
+        __syncthreads();  // red is free again
     }
+#pragma unroll
+    for (int i = 0; i < NI; i++)
+        if (c[i] < n8) {
+            const size_t at = (size_t)blockIdx.x * a.H, all = (size_t)groups * a.H;
+            if (a.dpost) store8<kActF32>(part + at, 8 * (size_t)c[i], pack8<kActF32>(spost[i]));
+            if (a.dpre) store8<kActF32>(part + all + at, 8 * (size_t)c[i], pack8<kActF32>(spre[i]));
+            if (ch && a.dgate) {
+#pragma unroll
+                for (int j = 0; j < 8; j++) sgate[i][j] *= a.scale;
+                store8<kActF32>(part + 2 * all + at, 8 * (size_t)c[i], pack8<kActF32>(sgate[i]));
+            }
+        }
+}
+
+// The partial rows of one output (blockIdx.y), added in a fixed order: 16
+// slices of consecutive rows, 16 quads of channels a workgroup, then the slices.
+__global__ __launch_bounds__(256) void k_norm_sum(const float* __restrict__ part, int groups, int H, float* dpost,
+                                                  float* dpre, float* dgate, int accumulate) {
+    __shared__ f4v slice[16][16];
+    float* out = blockIdx.y == 0 ? dpost : blockIdx.y == 1 ? dpre : dgate;
+    if (!out) return;
+    const int q = threadIdx.x & 15, sl = threadIdx.x >> 4, col = blockIdx.x * 16 + q, per = (groups + 15) / 16;
+    const int g0 = min(groups, sl * per), g1 = min(groups, g0 + per);
+    f4v v = {0.f, 0.f, 0.f, 0.f};
+    if (col < H / 4) {
+        const f4v* p = reinterpret_cast<const f4v*>(part + (size_t)blockIdx.y * groups * H) + col;
+#pragma unroll 8
+        for (int g = g0; g < g1; g++) v += p[(size_t)g * (H / 4)];
+    }
+    slice[sl][q] = v;
+    __syncthreads();
+    if (sl == 0 && col < H / 4) {
+        for (int i = 1; i < 16; i++) v += slice[i][q];
+        f4v* o = reinterpret_cast<f4v*>(out) + col;
+        *o = accumulate ? *o + v : v;
+    }
+}
+
+// Threads of a row and pieces of each: 64 to 1024 threads with one piece of 8
+// channels (a short row leaves no lanes idle, the sums over tokens take 24
+// registers a thread and the weights stay in as many), two above 8192 channels.
+struct NormShape {
+    int threads, ni;
+};
+NormShape norm_shape(int H) {
+    int t = 64;
+    while (t < 1024 && 8 * t < H) t *= 2;
+    return {t, 8 * t < H ? 2 : 1};
 }
 
 // Workgroups of the backward pass: each runs through the rows t, t + n, ...
-int norm_groups(int T) { return T < 512 ? T : 512; }
-
-// part: [3][groups][H] sums of dpost, dpre, dgate (channel).
-template <int NI>
-__global__ __launch_bounds__(256) void k_norm_bwd(NormArgs a, float* __restrict__ part) {
-    __shared__ float red[4][4];
-    const int tid = threadIdx.x, n8 = a.H / 8, groups = gridDim.x;
-    const float inv = 1.0f / (float)a.H;
-    float spost[NI][8], spre[NI][8], sgate[NI][8];
-#pragma unroll
-    for (int i = 0; i < NI; i++)
-#pragma unroll
-        for (int j = 0; j < 8; j++) spost[i][j] = spre[i][j] = sgate[i][j] = 0.0f;
-    for (int t = blockIdx.x; t < a.T; t += groups) {
-        const bool on = !a.mask || a.mask[t];
-        char* dr = a.dr ? static_cast<char*>(a.dr) + (size_t)t * a.lddr * es(a.rt) : nullptr;
-        char* dy = a.dy ? static_cast<char*>(a.dy) + (size_t)t * a.lddy * es(a.yt) : nullptr;
-        if (!on) {
-            const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < NI; i++) {
-                const int c = tid + 256 * i;
-                if (c < n8) {
-                    if (dr) put8(a.rt, dr, 8 * (size_t)c, z);
-                    if (dy) put8(a.yt, dy, 8 * (size_t)c, z);
-                }
-            }
-            if (a.gate_kind == kGateToken && a.dgate && tid == 0 && !a.accumulate) a.dgate[t] = 0.0f;
-            continue;
-        }
-        float d[NI][8], y[NI][8];
-        {
-            float r[NI][8], av[NI][8];
-            float sr = 0.0f, sar = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NI; i++) {
-                const int c = tid + 256 * i;
-                if (c < n8) {
-                    if (a.dr_out) get8(a.rt, static_cast<const char*>(a.dr_out) + (size_t)t * a.lddro * es(a.rt), 8 * (size_t)c, d[i]);
-                    else
-#pragma unroll
-                        for (int j = 0; j < 8; j++) d[i][j] = 0.0f;
-                    if (a.dx) {
-                        float w[8];
-                        get8(a.rt, static_cast<const char*>(a.r) + (size_t)t * a.ldr * es(a.rt), 8 * (size_t)c, r[i]);
-                        get8(a.xt, static_cast<const char*>(a.dx) + (size_t)t * a.lddx * es(a.xt), 8 * (size_t)c, av[i]);
-                        get8(kActF32, a.pre, 8 * (size_t)c, w);
-#pragma unroll
-                        for (int j = 0; j < 8; j++) {
-                            sr = fmaf(r[i][j], r[i][j], sr);
-                            sar = fmaf(av[i][j] * w[j], r[i][j], sar);
-                        }
-                    }
-                }
-            }
-            if (a.dx) {
-                const float rs = 1.0f / sqrtf(block_sum(sr, red[0]) * inv + a.eps);
-                const float m = block_sum(sar, red[1]) * rs * inv;
-#pragma unroll
-                for (int i = 0; i < NI; i++) {
-                    const int c = tid + 256 * i;
-                    if (c < n8) {
-                        float w[8];
-                        get8(kActF32, a.pre, 8 * (size_t)c, w);
-#pragma unroll
-                        for (int j = 0; j < 8; j++) {
-                            const float n = r[i][j] * rs;
-                            spre[i][j] = fmaf(av[i][j], n, spre[i][j]);
-                            d[i][j] = fmaf(rs, fmaf(-n, m, av[i][j] * w[j]), d[i][j]);
-                        }
-                    }
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < NI; i++)
-            if (dr && tid + 256 * i < n8) put8(a.rt, dr, 8 * (size_t)(tid + 256 * i), d[i]);
-        if (!a.y) {
-            __syncthreads();  // red is free again
-            continue;
-        }
-        float sy = 0.0f, sg = 0.0f, sby = 0.0f;
-        const float gt = a.scale * (a.gate_kind == kGateToken ? a.gate[t] : 1.0f);
-#pragma unroll
-        for (int i = 0; i < NI; i++) {
-            const int c = tid + 256 * i;
-            if (c < n8) {
-                get8(a.yt, static_cast<const char*>(a.y) + (size_t)t * a.ldy * es(a.yt), 8 * (size_t)c, y[i]);
-                float w[8], g[8];
-                if (a.post) get8(kActF32, a.post, 8 * (size_t)c, w);
-                if (a.gate_kind == kGateChannel) get8(kActF32, a.gate, 8 * (size_t)c, g);
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const float p = a.post ? w[j] : 1.0f;
-                    sy = fmaf(y[i][j], y[i][j], sy);
-                    sg = fmaf(d[i][j] * p, y[i][j], sg);
-                    sby = fmaf(d[i][j] * p * (a.gate_kind == kGateChannel ? g[j] : 1.0f), y[i][j], sby);
-                }
-            }
-        }
-        const float rs = a.post ? 1.0f / sqrtf(block_sum(sy, red[2]) * inv + a.eps) : 1.0f;
-        const float m = a.post ? block_sum(sby, red[3]) * gt * rs * inv : 0.0f;
-        if (a.gate_kind == kGateToken && a.dgate) {
-            const float v = block_sum(sg, red[0]) * rs * a.scale;
-            if (tid == 0) a.dgate[t] = a.accumulate ? a.dgate[t] + v : v;
-        }
-#pragma unroll
-        for (int i = 0; i < NI; i++) {
-            const int c = tid + 256 * i;
-            if (c < n8) {
-                float w[8], g[8], o[8];
-                if (a.post) get8(kActF32, a.post, 8 * (size_t)c, w);
-                if (a.gate_kind == kGateChannel) get8(kActF32, a.gate, 8 * (size_t)c, g);
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const float p = a.post ? w[j] : 1.0f, q = y[i][j] * rs;
-                    const float u = (a.gate_kind == kGateChannel ? gt * g[j] : gt) * d[i][j];
-                    spost[i][j] = fmaf(u, q, spost[i][j]);
-                    if (a.gate_kind == kGateChannel) sgate[i][j] = fmaf(d[i][j] * p, q, sgate[i][j]);
-                    o[j] = a.post ? rs * fmaf(-q, m, u * p) : u;
-                }
-                if (dy) put8(a.yt, dy, 8 * (size_t)c, o);
-            }
-        }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < NI; i++) {
-        const int c = tid + 256 * i;
-        if (c < n8) {
-            const size_t at = (size_t)blockIdx.x * a.H, all = (size_t)groups * a.H;
-            put8(kActF32, part + at, 8 * (size_t)c, spost[i]);
-            put8(kActF32, part + all + at, 8 * (size_t)c, spre[i]);
-#pragma unroll
-            for (int j = 0; j < 8; j++) sgate[i][j] *= a.scale;
-            put8(kActF32, part + 2 * all + at, 8 * (size_t)c, sgate[i]);
-        }
-    }
+// Two of 512 threads a compute unit fill the chip; shorter rows take more
+// workgroups, as long as each has 8 rows (a workgroup leaves three rows of fp32
+// sums).
+int norm_groups(int H, int T) {
+    const int most = 512 * 512 / norm_shape(H).threads;
+    int n = T / 8 < most ? T / 8 : most;
+    n = n > 512 ? n : 512;
+    return T < n ? T : n;
 }
 
-// The partial rows of one output (blockIdx.y) added in order.
-__global__ __launch_bounds__(256) void k_norm_sum(const float* __restrict__ part, int groups, int H, float* dpost,
-                                                  float* dpre, float* dgate, int accumulate) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    float* out = blockIdx.y == 0 ? dpost : blockIdx.y == 1 ? dpre : dgate;
-    if (c >= H || !out) return;
-    const float* p = part + (size_t)blockIdx.y * groups * H + c;
-    float v = 0.0f;
-    for (int g = 0; g < groups; g++) v += p[(size_t)g * H];
-    out[c] = accumulate ? out[c] + v : v;
+template <int SR, int SY, int SX>
+hipError_t norm_launch(const NormArgs& a, float* part, hipStream_t s) {
+    const NormShape n = norm_shape(a.H);
+    const dim3 block(n.threads);
+    if (!part) {
+        const dim3 grid(a.T);
+        if (n.ni == 2) hipLaunchKernelGGL((k_norm_fwd<SR, SY, SX, 2, 1024>), grid, block, 0, s, a);
+        else if (n.threads == 1024) hipLaunchKernelGGL((k_norm_fwd<SR, SY, SX, 1, 1024>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((k_norm_fwd<SR, SY, SX, 1, 512>), grid, block, 0, s, a);
+    } else {
+        const dim3 grid(norm_groups(a.H, a.T));
+        if (n.ni == 2) hipLaunchKernelGGL((k_norm_bwd<SR, SY, SX, 2, 1024>), grid, block, 0, s, a, part);
+        else if (n.threads == 1024) hipLaunchKernelGGL((k_norm_bwd<SR, SY, SX, 1, 1024>), grid, block, 0, s, a, part);
+        else hipLaunchKernelGGL((k_norm_bwd<SR, SY, SX, 1, 512>), grid, block, 0, s, a, part);
+    }
+    return hipGetLastError();
+}
+hipError_t norm_types(const NormArgs& a, float* part, hipStream_t s) {
+    const int k = (a.rt == kActF32) * 4 + (a.yt == kActF32) * 2 + (a.xt == kActF32);
+    switch (k) {
+        case 0: return norm_launch<2, 2, 2>(a, part, s);
+        case 1: return norm_launch<2, 2, 4>(a, part, s);
+        case 2: return norm_launch<2, 4, 2>(a, part, s);
+        case 3: return norm_launch<2, 4, 4>(a, part, s);
+        case 4: return norm_launch<4, 2, 2>(a, part, s);
+        case 5: return norm_launch<4, 2, 4>(a, part, s);
+        case 6: return norm_launch<4, 4, 2>(a, part, s);
+        default: return norm_launch<4, 4, 4>(a, part, s);
+    }
 }
 
 }  // namespace
 
-size_t norm_ws_bytes(int H, int gate_kind, int T) { return align256((size_t)3 * norm_groups(T) * H * sizeof(float)); }
+size_t norm_ws_bytes(int H, int gate_kind, int T) { return align256((size_t)3 * norm_groups(H, T) * H * sizeof(float)); }
 
-hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) {
-    const int ni = (a.H + 2047) / 2048;
-    const dim3 grid(a.T), block(256);
-    if (ni <= 1) hipLaunchKernelGGL(k_norm_fwd<1>, grid, block, 0, s, a);
-    else if (ni <= 2) hipLaunchKernelGGL(k_norm_fwd<2>, grid, block, 0, s, a);
-    else if (ni <= 4) hipLaunchKernelGGL(k_norm_fwd<4>, grid, block, 0, s, a);
-    else hipLaunchKernelGGL(k_norm_fwd<8>, grid, block, 0, s, a);
-    return hipGetLastError();
-}
+hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) { return norm_types(a, nullptr, s); }
 
 hipError_t launch_block_norm_backward(const NormArgs& a, void* ws, hipStream_t s) {
-    const int ni = (a.H + 2047) / 2048, groups = norm_groups(a.T);
-    const dim3 grid(groups), block(256);
+    const int groups = norm_groups(a.H, a.T);
     float* part = static_cast<float*>(ws);
     if (groups) {
-        if (ni <= 1) hipLaunchKernelGGL(k_norm_bwd<1>, grid, block, 0, s, a, part);
-        else if (ni <= 2) hipLaunchKernelGGL(k_norm_bwd<2>, grid, block, 0, s, a, part);
-        else if (ni <= 4) hipLaunchKernelGGL(k_norm_bwd<4>, grid, block, 0, s, a, part);
-        else hipLaunchKernelGGL(k_norm_bwd<8>, grid, block, 0, s, a, part);
-        const hipError_t r = hipGetLastError();
+        const hipError_t r = norm_types(a, part, s);
         if (r != hipSuccess) return r;
     }
     float* dg = a.gate_kind == kGateChannel ? a.dgate : nullptr;
     if (a.dpost || a.dpre || dg)
-        hipLaunchKernelGGL(k_norm_sum, dim3((a.H + 255) / 256, 3), block, 0, s, part, groups, a.H, a.dpost, a.dpre, dg,
+        hipLaunchKernelGGL(k_norm_sum, dim3((a.H / 4 + 15) / 16, 3), dim3(256), 0, s, part, groups, a.H, a.dpost, a.dpre, dg,
                            a.accumulate);
     return hipGetLastError();
 }
