@@ -14,7 +14,7 @@ BUILD = os.path.join(HERE, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["kernels_decode.hip", "kernels_route.hip", "kernels_prefill.hip", "kernels_fp8.hip", "kernels_prefetch.hip", "kernels_balance.hip",
-           "kernels_routegrad.hip", "kernels_lora.hip", "kernels_fp4quant.hip", "kernels_fp4mm.hip", "kernels_batch.hip", "kernels_norm.hip", "moe_api.cpp", "moe_tier.cpp"]
+           "kernels_routegrad.hip", "kernels_lora.hip", "kernels_fp4quant.hip", "kernels_fp4few.hip", "kernels_fp4mm.hip", "kernels_batch.hip", "kernels_norm.hip", "moe_api.cpp", "moe_tier.cpp"]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
     # packed-FP32 VALU forms are kept out of all device code

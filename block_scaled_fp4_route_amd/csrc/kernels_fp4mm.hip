@@ -339,6 +339,7 @@ hipError_t launch_fp4_apply(int K, int N, int fmt, int dtype, const void* x, siz
                             bool round_x, const void* base, size_t ldbase, void* y, size_t ldy, void* ws,
                             hipStream_t s) {
     const size_t es = dtype == kActF32 ? 4 : 2;
+    if (T <= kGemvMaxT) return launch_fp4_gemv(K, N, fmt, dtype, x, ldx, T, w, round_x, base, ldbase, y, ldy, s);
     char* p = static_cast<char*>(ws);
     MmArgs g = {};
     g.M = T;
@@ -357,6 +358,7 @@ hipError_t launch_fp4_apply(int K, int N, int fmt, int dtype, const void* x, siz
         uint8_t* sb = sa + steps * 8 * tile_rows(T);
         r = launch_fp4_quant(dtype, kFmtMxfp4, kScaleFloor, x, ldx, T, K, nullptr, codes, scales, nullptr, 0, s);
         if (r != hipSuccess) return r;
+        if (T <= kFewMaxT) return launch_fp4_few(K, N, fmt, dtype, codes, K / 2, scales, T, w, base, ldbase, y, ldy, s);
         hipLaunchKernelGGL(k_fp4_scale_panel, dim3((T + 255) / 256, steps), dim3(256), 0, s, scales, T, K / 32, sa);
         if ((r = hipGetLastError()) != hipSuccess) return r;
         hipLaunchKernelGGL(k_fp4_scale_panel, dim3((N + 255) / 256, steps), dim3(256), 0, s, w.scales, N, K / 32, sb);
@@ -370,6 +372,8 @@ hipError_t launch_fp4_apply(int K, int N, int fmt, int dtype, const void* x, siz
         return mm<kFp4>(dtype, g, s);
     }
     const int kind = act_kind(fmt, dtype, false), P = act_parts(dtype, kind);
+    if ((r = activations(dtype, P, x, ldx, T, K, p + align256((size_t)K * N * 2), g, s)) != hipSuccess) return r;
+    if (T <= kFewMaxT) return launch_fp4_few(K, N, fmt, dtype, g.a, g.lda, nullptr, T, w, base, ldbase, y, ldy, s);
     const size_t pieces = (size_t)N * (K / 8);
     const dim3 grid((unsigned)((pieces + 255) / 256));
     const uint32_t* codes = reinterpret_cast<const uint32_t*>(w.codes);
@@ -381,7 +385,6 @@ hipError_t launch_fp4_apply(int K, int N, int fmt, int dtype, const void* x, siz
     else
         hipLaunchKernelGGL((k_fp4_widen<kFmtMxfp4, kBf16>), grid, dim3(256), 0, s, codes, w.scales, pieces, wide);
     if ((r = hipGetLastError()) != hipSuccess) return r;
-    if ((r = activations(dtype, P, x, ldx, T, K, p + align256((size_t)K * N * 2), g, s)) != hipSuccess) return r;
     g.b = p;
     g.ldb = g.wb = (uint32_t)K * 2;
     g.steps = (int)((g.wa + kStepBytes - 1) / kStepBytes);

@@ -20,13 +20,13 @@
 
 #include "moe_device.h"
 #include "moe_internal.h"
+#include "moe_codes.h"
 #include "moe_rows.h"
 #include "moe_serve.h"
 
 namespace moe {
 namespace {
 
-constexpr uint32_t kInfBits = 0x7F800000u;
 constexpr int kRowExpMin = -100, kRowExpMax = 116;  // so that every decoded value is a normal bf16, and finite
 
 struct QuantArgs {
@@ -39,46 +39,6 @@ struct QuantArgs {
     size_t ldv;  // bytes
     int rule;
 };
-
-// The E4M3 byte nearest to a / 6 (ties to even, at most 448), a >= 0 finite.
-__device__ __forceinline__ uint32_t e4m3_sixth(float a) {
-    // near the result: a * fp32(1/6) is off by 2^-23 of a at most, so the byte
-    // it rounds to is the nearest one or its neighbour; which one is decided
-    // by comparing a with 6 times the borders, exactly
-    const float q = fminf(a * 0.16666667f, 448.0f);
-    uint32_t b = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q, q, 0, false) & 0x7Fu;
-    const float v = e4m3_to_f32(b);
-    const float up = e4m3_to_f32(min(b + 1u, 0x7Eu)), down = e4m3_to_f32(b ? b - 1u : 0u);
-    const float hi = 3.0f * (v + up), lo = 3.0f * (v + down);  // 6 times the middle: exact
-    const bool odd = b & 1u;
-    if (b < 0x7Eu && (a > hi || (a == hi && odd))) b++;
-    else if (b > 0u && (a < lo || (a == lo && odd))) b--;
-    return b;
-}
-
-// Codes of eight values (times the exact power of two p) under the scale s,
-// as one word, and the values they stand for (without p).
-__device__ __forceinline__ uint32_t codes8(const float (&v)[8], float p, float s, float (&q)[8]) {
-    const float b0 = 0.25f * s, b1 = 0.75f * s, b2 = 1.25f * s, b3 = 1.75f * s, b4 = 2.5f * s, b5 = 3.5f * s, b6 = 5.0f * s;
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const float m = fabsf(v[i]) * p;
-        const uint32_t c = (uint32_t)(m > b0) + (m >= b1) + (m > b2) + (m >= b3) + (m > b4) + (m >= b5) + (m > b6);
-        w |= (c | (__float_as_uint(v[i]) >> 31 << 3)) << (4 * i);
-    }
-    const f2v d0 = fp4x2<0>(w), d1 = fp4x2<1>(w), d2 = fp4x2<2>(w), d3 = fp4x2<3>(w);
-    q[0] = d0.x; q[1] = d0.y; q[2] = d1.x; q[3] = d1.y;
-    q[4] = d2.x; q[5] = d2.y; q[6] = d3.x; q[7] = d3.y;
-    return w;
-}
-
-__device__ __forceinline__ uint32_t max_mag(const float (&v)[8]) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; i++) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    return m;
-}
 
 // One piece of 8 values, its block's lanes beside it (2 of NVFP4, 4 of MXFP4;
 // all of them active). re: the row's exponent.
@@ -97,8 +57,7 @@ __device__ __forceinline__ void quant_piece(const QuantArgs& a, uint32_t row, ui
         byte = bad ? 0x7Fu : e4m3_sixth(__uint_as_float(top) * p);
         s = e4m3_to_f32(byte);
     } else {
-        int X = (int)(top >> 23) - 129 + (a.rule == kScaleCeil && (top & 0x7FFFFFu) > 0x400000u ? 1 : 0);
-        X = max(-127, min(125, X));
+        const int X = mx_exponent(top, a.rule == kScaleCeil);
         byte = bad ? 0xFFu : top == 0u ? 0u : (uint32_t)(X + 127);
         p = exp2i(-X);
         s = 1.0f;

@@ -25,6 +25,13 @@ struct Fp4Matrix {
     const uint8_t* scales;  // [N][K / G]
     const int8_t* row_exp;  // [N] or null
 };
+// Up to kGemvMaxT and kFewMaxT tokens (x of the second: the activations, their
+// parts, or codes beside x_scales).
+constexpr int kGemvMaxT = 4, kFewMaxT = 64;
+hipError_t launch_fp4_gemv(int K, int N, int fmt, int dtype, const void* x, size_t ldx, int T, const Fp4Matrix& w,
+                           bool round_x, const void* base, size_t ldbase, void* y, size_t ldy, hipStream_t s);
+hipError_t launch_fp4_few(int K, int N, int fmt, int dtype, const void* x, size_t ldx_bytes, const uint8_t* x_scales, int T,
+                          const Fp4Matrix& w, const void* base, size_t ldbase, void* y, size_t ldy, hipStream_t s);
 size_t fp4_ws_bytes(int K, int N, int fmt, int dtype, int T, bool backward);
 hipError_t launch_fp4_apply(int K, int N, int fmt, int dtype, const void* x, size_t ldx, int T, const Fp4Matrix& w,
                             bool round_x, const void* base, size_t ldbase, void* y, size_t ldy, void* ws,

@@ -149,7 +149,7 @@ def test_three_quantised_matrices_are_an_expert_block(m):
 
 def matrix(g, N, K, fmt, lo=None, hi=None, rows=True):
     codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, generator=g)
-    lo, hi = lo or (0x18 if fmt == "nvfp4" else 121), hi or (0x49 if fmt == "nvfp4" else 130)
+    lo, hi = lo if lo is not None else (0x18 if fmt == "nvfp4" else 121), hi or (0x49 if fmt == "nvfp4" else 130)
     scales = torch.randint(lo, hi, (N, K // ref.GROUP[fmt]), dtype=torch.uint8, generator=g)
     e = torch.randint(-9, 3, (N,), dtype=torch.int8, generator=g) if fmt == "nvfp4" and rows else None
     return codes.cuda(), scales.cuda(), None if e is None else e.cuda()
@@ -232,7 +232,7 @@ def test_product_long(m, T, K, N, fmt, dt, rnd, back):
     check_product(m, T, K, N, fmt, dt, rnd, back)
 
 
-@pytest.mark.parametrize("T", [3, 200])
+@pytest.mark.parametrize("T", [3, 20, 50, 200])
 @pytest.mark.parametrize("dt", sorted(DT))
 @pytest.mark.parametrize("back", [False, True])
 def test_product_far_scales(m, T, dt, back):
@@ -245,13 +245,13 @@ def test_product_far_scales(m, T, dt, back):
         x = x * 2.0 ** (100 if lo == 0 and dt != "f16" else -10 if lo == 240 else 0)
         if lo == 240 and dt == "f16":
             continue  # outside of fp16
-        check_product(m, T, K, N, "mxfp4", dt, back=back, w=matrix(g, N, K, "mxfp4", lo or 1, hi), x=x.to(DT[dt]), base="none")
+        check_product(m, T, K, N, "mxfp4", dt, back=back, w=matrix(g, N, K, "mxfp4", lo, hi), x=x.to(DT[dt]), base="none")
     c, s, _ = matrix(g, N, K, "nvfp4", 1, 9)
     e = torch.tensor([-100, 60, -3, 0, 7], dtype=torch.int8).repeat(8).cuda()
     check_product(m, T, K, N, "nvfp4", dt, back=back, w=(c, s, e if dt != "f16" else e.clamp(-8, 8)), base="none")
 
 
-@pytest.mark.parametrize("T", [2, 200])
+@pytest.mark.parametrize("T", [2, 20, 200])
 @pytest.mark.parametrize("fmt,rnd", [("nvfp4", False), ("mxfp4", False), ("mxfp4", True)])
 @pytest.mark.parametrize("dt", sorted(DT))
 def test_product_infinities_and_nan(m, T, dt, fmt, rnd):
@@ -276,7 +276,7 @@ def test_product_infinities_and_nan(m, T, dt, fmt, rnd):
     ref.close(y[2:], rest, off, "other tokens")
 
 
-@pytest.mark.parametrize("T", [2, 200])
+@pytest.mark.parametrize("T", [2, 20, 200])
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 @pytest.mark.parametrize("back", [False, True])
 def test_product_nan_scale(m, T, fmt, back):
@@ -339,7 +339,7 @@ def test_product_graphs_share_a_workspace(m, T, kind):
         assert all(torch.equal(a, b) for a, b in zip(ys, want))
 
 
-@pytest.mark.parametrize("T", [4, 300])
+@pytest.mark.parametrize("T", [4, 40, 300])
 def test_two_streams_at_once(m, T):
     g = torch.Generator().manual_seed(1)
     K, N = 1056, 264
