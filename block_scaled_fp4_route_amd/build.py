@@ -25,7 +25,7 @@ FLAGS = [
 # ordinary vector registers, which saves the copies between register files
 # that the K loops otherwise carry (same results, 2-4% less time)
 VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
-EXTRA = {"kernels_prefill.hip": VGPR_FORM, "kernels_lora.hip": VGPR_FORM}
+EXTRA = {f: VGPR_FORM for f in ("kernels_prefill.hip", "kernels_lora.hip", "kernels_fp4few.hip", "kernels_fp4mm.hip", "kernels_batch.hip")}
 
 
 def _compile(src: str) -> str:
