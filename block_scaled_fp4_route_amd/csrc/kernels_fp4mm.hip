@@ -12,6 +12,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
+#include "moe_codes.h"
 #include "moe_device.h"
 #include "moe_internal.h"
 #include "moe_rows.h"
@@ -20,10 +23,7 @@
 namespace moe {
 namespace {
 
-typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
-typedef _Float16 hf8 __attribute__((ext_vector_type(8)));
 typedef float f16v __attribute__((ext_vector_type(16)));
-typedef int i8v __attribute__((ext_vector_type(8)));
 
 constexpr int kBf16 = 0, kF16 = 1, kFp4 = 2;  // operands of the product
 constexpr int kStepBytes = 128;               // of a row in one step of the sum
@@ -116,12 +116,12 @@ __global__ __launch_bounds__(256) void k_fp4_parts(const char* __restrict__ x, s
     }
 }
 
-// Scale bytes for the scaled product: [K / 256 steps][rows up to a whole tile][8], within a step's
-// 8 blocks the even ones first (lanes 0-31 of a wave hold the even blocks of a
-// step, lanes 32-63 the odd ones: a lane's four bytes are one word). Blocks
-// behind the row's end are 0.
+// Scale bytes for the scaled product: [K / 256 steps][rows up to a whole
+// tile][8], within a step's eight blocks the even ones first (lanes 0-31 of a
+// wave hold the even blocks of a step, lanes 32-63 the odd ones: a lane's four
+// bytes are one word). Blocks behind the row's end are 0.
+__host__ __device__ constexpr size_t tile_rows(size_t rows) { return (rows + 255) / 256 * 256; }
 __device__ __forceinline__ int scale_place(int b) { return (b & 1) * 4 + (b >> 1 & 3); }
-constexpr size_t tile_rows(size_t rows) { return (rows + 127) / 128 * 128; }
 __global__ __launch_bounds__(256) void k_fp4_scale_panel(const uint8_t* __restrict__ scales, int rows, int nb,
                                                          uint8_t* __restrict__ out) {
     const int r = blockIdx.x * 256 + threadIdx.x, st = blockIdx.y;
@@ -132,32 +132,49 @@ __global__ __launch_bounds__(256) void k_fp4_scale_panel(const uint8_t* __restri
         const int b = 8 * st + j;
         if (b < nb) w[scale_place(j) / 4] |= (uint32_t)scales[(size_t)r * nb + b] << (8 * (scale_place(j) % 4));
     }
-    *reinterpret_cast<uint2*>(out + ((size_t)st * tile_rows(rows) + r) * 8) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(out + (st * tile_rows(rows) + r) * 8) = make_uint2(w[0], w[1]);
 }
 
 // ---------------------------------------------------------------------------
-// C = A B^T, both row-major along the sum. A workgroup of 4 waves has a tile of
-// 128 x 128; a step is 128 bytes of every row (64 16-bit values or 256 codes),
-// loaded from memory straight into one of two LDS buffers while the other is
-// multiplied. A row's eight 16-byte chunks sit in LDS at chunk ^ (row & 7), so
-// that the reads of eight neighbouring rows' same chunk hit all banks once; the
-// loads pick their chunk accordingly.
+// C = A B^T, both row-major along the sum. A step is 128 bytes of every row of
+// the tile (64 16-bit values or 256 codes), loaded from memory straight into a
+// ring of LDS buffers. A row's eight 16-byte chunks sit in LDS at chunk ^ (row /
+// 2 & 7), so that the reads of 16 neighbouring rows' same chunk hit all banks
+// once; the loads pick their chunk accordingly.
+//
+// Tiles: 256 x 256 by eight waves of 128 x 64 where they fill the chip. A
+// compute unit takes 64 bytes a cycle from memory and 128 from LDS: a step's
+// loads are half, its reads three quarters of its 2048 cycles of matrix
+// instructions (256 x 128 by four waves, two workgroups a compute unit, steps of
+// 64 bytes: loads three quarters; 415 us against 418 where the larger tiles
+// leave a quarter of the chip idle in the last round, 127 against 112 where they
+// do not). 128 x 128 and 64 x 64 where there are too few of those.
 struct MmArgs {
     const char *a, *b;
     size_t lda, ldb;        // bytes between rows
     uint32_t wa, wb;        // bytes of a row (A's parts together; B starts again at its end)
     int M, N, steps;
-    const uint8_t *sa, *sb; // kFp4: scale panels [steps][M or N][8]
+    const uint8_t *sa, *sb; // kFp4: scale panels [steps][rows up to a whole tile][8]
     const int8_t* row_exp;  // of B's rows, or null
     const char* base;
     char* y;
     size_t ldbase, ldy;     // bytes
-    int nt;                 // tiles along N
+    int mt, nt;             // tiles
+    int full, split;        // the first `full` are whole; each other one has `split` workgroups, a part of the sum each
+    float* part;            // their sums [tile - full][split][BM][BN]
 };
 
 template <int N>
 __device__ __forceinline__ void ring_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// 16 or 4 bytes a lane from memory straight into LDS, the lanes' side by side.
+__device__ __forceinline__ void to_lds16(rsrc_t r, uint8_t* to, uint32_t off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, off, 0, 0, 0);
+}
+__device__ __forceinline__ void to_lds4(rsrc_t r, uint8_t* to, uint32_t off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 4, off, 0, 0, 0);
 }
 
 template <int KIND>
@@ -174,45 +191,83 @@ __device__ __forceinline__ f16v mma4(u4w a, u4w b, f16v c, uint32_t sa, uint32_t
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, B, c, 4, 4, KS, (int)sa, KS, (int)sb);
 }
 
-template <int KIND, int DT>
-__global__ __launch_bounds__(256, 2) void k_fp4_mm(MmArgs g) {
-    constexpr int BM = 128, BN = 128, MI = 2, NI = 2;
-    constexpr int SC = KIND == kFp4 ? (BM + BN) * 8 : 0;       // scale bytes of a step
+// The place of tile number seq.
+__device__ __forceinline__ void tile_at(int seq, int mt, int nt, int& m, int& n) {
+    const int per = 4 * nt, grp = seq / per, gm = min(4, mt - 4 * grp), in = seq % per;
+    m = 4 * grp + in % gm;
+    n = in / gm;
+}
+
+// BM x BN by waves of 32 MI x 32 NI, a ring of R steps.
+template <int KIND, int DT, int BM, int BN, int MI, int NI, int R>
+__global__ __launch_bounds__(64 * (BM / (32 * MI)) * (BN / (32 * NI))) void k_fp4_mm(MmArgs g) {
+    constexpr int WN = BN / (32 * NI), WAVES = BM / (32 * MI) * WN;
+    constexpr int SC = KIND == kFp4 ? (BM + BN) * 8 : 0;                        // scale bytes of a step
+    constexpr int LA = BM / 8 / WAVES, LB = BN / 8 / WAVES, LS = SC / 256 / WAVES, LOADS = LA + LB + LS;  // loads of a wave and step
     constexpr int STEP = (BM + BN) * kStepBytes + SC;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STEP];
-    const int lane = threadIdx.x & 63, wave = wave_id(), wm = wave >> 1, wn = wave & 1;
-    const int m0 = blockIdx.x / g.nt * BM, n0 = blockIdx.x % g.nt * BN;
+    constexpr int OUT = 32 * (32 * NI * 4 + 16);                                // a wave's 32 rows on their way out, fp32
+    constexpr int LDS = R * STEP > WAVES * OUT ? R * STEP : WAVES * OUT;
+    static_assert(LA * 8 * WAVES == BM && LB * 8 * WAVES == BN && LS * 256 * WAVES == SC && LA % 2 == 0 && LB % 2 == 0 && LOADS * (R - 1) < 64, "tile");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[LDS];
+    const int lane = threadIdx.x & 63, wave = wave_id(), wm = wave / WN, wn = wave % WN;
+    // workgroups go to the eight XCDs in turn: each takes a run of the tiles, which
+    // go down four tiles of M before the next of N, so that the workgroups of an
+    // XCD share rows of both operands in its L2
+    int m0, n0, s0 = 0, s1 = g.steps, piece = -1;
+    {
+        const int b = blockIdx.x, x = b % 8, q = g.full / 8, r = g.full % 8;
+        int seq = x * q + min(x, r) + b / 8;
+        if (b >= g.full) {
+            piece = b - g.full;
+            seq = g.full + piece / g.split;
+            s0 = (int)((int64_t)(piece % g.split) * g.steps / g.split);
+            s1 = (int)((int64_t)(piece % g.split + 1) * g.steps / g.split);
+        }
+        tile_at(seq, g.mt, g.nt, m0, n0);
+        m0 *= BM;
+        n0 *= BN;
+    }
     const int am = min(BM, g.M - m0), bn = min(BN, g.N - n0);
     const rsrc_t rA = make_rsrc(g.a + (size_t)m0 * g.lda, (uint32_t)(am - 1) * (uint32_t)g.lda + g.wa);
     const rsrc_t rB = make_rsrc(g.b + (size_t)n0 * g.ldb, (uint32_t)(bn - 1) * (uint32_t)g.ldb + g.wb);
-    // this lane's loads: 4 of each operand, row 8 (4 wave + i) + lane / 8
-    const uint32_t ch = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16u;
-    uint32_t ka = ch, kb = ch;  // byte within the row
-    while (kb >= g.wb) kb -= g.wb;
-    uint32_t oa[4], ob[4];
+    // this lane's loads: row 8 (L wave + i) + lane / 8, chunk (lane ^ row / 2) % 8,
+    // which in every second load is another by 4
+    const uint32_t ch = (uint32_t)((lane & 7) ^ (lane >> 4)) * 16u;
+    const uint32_t k0 = (uint32_t)s0 * kStepBytes;
+    uint32_t ka[2] = {k0 + ch, k0 + (ch ^ 64u)}, kb[2] = {ka[0] % g.wb, ka[1] % g.wb};  // bytes within the row
+    uint32_t oa[LA], ob[LB];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int r = 8 * (4 * wave + i) + (lane >> 3);
+    for (int i = 0; i < LA; i++) {
+        const int r = 8 * (LA * wave + i) + (lane >> 3);
         oa[i] = r < am ? (uint32_t)r * (uint32_t)g.lda : kOOB;
+    }
+#pragma unroll
+    for (int i = 0; i < LB; i++) {
+        const int r = 8 * (LB * wave + i) + (lane >> 3);
         ob[i] = r < bn ? (uint32_t)r * (uint32_t)g.ldb : kOOB;
     }
-    auto to_lds = [](rsrc_t r, uint8_t* to, uint32_t off) {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, off, 0, 0, 0);
-    };
+    // every step issues the same loads; those behind the last one read nothing
     auto issue = [&](int s, uint8_t* to) {
-        const bool on = ka < g.wa;
 #pragma unroll
-        for (int i = 0; i < 4; i++) to_lds(rA, to + 1024 * (4 * wave + i), on && oa[i] != kOOB ? oa[i] + ka : kOOB);
+        for (int i = 0; i < LA; i++)
+            to_lds16(rA, to + 1024 * (LA * wave + i), ka[i & 1] < g.wa && oa[i] != kOOB ? oa[i] + ka[i & 1] : kOOB);
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-            to_lds(rB, to + BM * kStepBytes + 1024 * (4 * wave + i), on && ob[i] != kOOB ? ob[i] + kb : kOOB);
-        ka += kStepBytes;
-        kb += kStepBytes;
-        while (kb >= g.wb) kb -= g.wb;
-        if constexpr (KIND == kFp4) {
-            if (wave < 2) {  // 1 KB: 128 rows of 8 bytes
-                const uint8_t* p = wave ? g.sb + ((size_t)s * tile_rows(g.N) + n0) * 8 : g.sa + ((size_t)s * tile_rows(g.M) + m0) * 8;
-                to_lds(make_rsrc(p, 1024), to + (BM + BN) * kStepBytes + wave * BM * 8, 16u * lane);
+        for (int i = 0; i < LB; i++)
+            to_lds16(rB, to + BM * kStepBytes + 1024 * (LB * wave + i), ka[i & 1] < g.wa && ob[i] != kOOB ? ob[i] + kb[i & 1] : kOOB);
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            ka[h] += kStepBytes;
+            kb[h] += kStepBytes;
+            while (kb[h] >= g.wb) kb[h] -= g.wb;
+        }
+        if constexpr (KIND == kFp4) {  // rows of 8 bytes: A's, then B's
+            const size_t ss = min(s, g.steps - 1);
+#pragma unroll
+            for (int i = 0; i < LS; i++) {
+                const int q = LS * wave + i;  // 256 bytes, 32 rows, each
+                const bool ofa = q < BM / 32;
+                const uint8_t* p = ofa ? g.sa + (ss * tile_rows(g.M) + m0) * 8 : g.sb + (ss * tile_rows(g.N) + n0) * 8;
+                to_lds4(make_rsrc(p, (ofa ? BM : BN) * 8), to + (BM + BN) * kStepBytes + 256 * q, 256u * (ofa ? q : q - BM / 32) + 4u * lane);
             }
         }
     };
@@ -223,83 +278,195 @@ __global__ __launch_bounds__(256, 2) void k_fp4_mm(MmArgs g) {
         for (int j = 0; j < NI; j++)
 #pragma unroll
             for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
-    const int lr = lane & 31, lh = lane >> 5;
-    auto at = [&](int row, int c) { return (uint32_t)row * kStepBytes + (uint32_t)((c ^ (row & 7)) * 16); };
-    auto multiply = [&](const uint8_t* from) {
-        const uint8_t* fb = from + BM * kStepBytes;
-        uint32_t sa[MI], sb[NI];
-        if constexpr (KIND == kFp4) {
-            const uint8_t* fs = from + (BM + BN) * kStepBytes;
-#pragma unroll
-            for (int i = 0; i < MI; i++) sa[i] = *reinterpret_cast<const uint32_t*>(fs + (64 * wm + 32 * i + lr) * 8 + 4 * lh);
-#pragma unroll
-            for (int j = 0; j < NI; j++)
-                sb[j] = *reinterpret_cast<const uint32_t*>(fs + (BM + 64 * wn + 32 * j + lr) * 8 + 4 * lh);
-        }
-#pragma unroll
-        for (int ks = 0; ks < 4; ks++) {
-            u4w a[MI], b[NI];
-#pragma unroll
-            for (int i = 0; i < MI; i++) a[i] = *reinterpret_cast<const u4w*>(from + at(64 * wm + 32 * i + lr, 2 * ks + lh));
-#pragma unroll
-            for (int j = 0; j < NI; j++) b[j] = *reinterpret_cast<const u4w*>(fb + at(64 * wn + 32 * j + lr, 2 * ks + lh));
-#pragma unroll
-            for (int i = 0; i < MI; i++)
-#pragma unroll
-                for (int j = 0; j < NI; j++) {
-                    if constexpr (KIND == kFp4) {
-                        if (ks == 0) acc[i][j] = mma4<0>(a[i], b[j], acc[i][j], sa[i], sb[j]);
-                        if (ks == 1) acc[i][j] = mma4<1>(a[i], b[j], acc[i][j], sa[i], sb[j]);
-                        if (ks == 2) acc[i][j] = mma4<2>(a[i], b[j], acc[i][j], sa[i], sb[j]);
-                        if (ks == 3) acc[i][j] = mma4<3>(a[i], b[j], acc[i][j], sa[i], sb[j]);
-                    } else {
-                        acc[i][j] = mma<KIND>(a[i], b[j], acc[i][j]);
-                    }
-                }
-        }
+    const int lr = lane & 31, lh = lane >> 5, am0 = 32 * MI * wm, bn0 = 32 * NI * wn;
+    auto at = [&](int row, int c) { return (uint32_t)row * kStepBytes + (uint32_t)((c ^ (row >> 1 & 7)) * 16); };
+    struct Frags {
+        u4w a[MI], b[NI];
     };
-    issue(0, lds);
-    for (int s = 0; s < g.steps; s++) {
-        ring_barrier<0>();  // step s is there, and every wave is done with step s - 1
-        if (s + 1 < g.steps) issue(s + 1, lds + ((s + 1) & 1) * STEP);
-        multiply(lds + (s & 1) * STEP);
-    }
-    // acc[i][j][r]: row 8 (r / 4) + 4 lh + r % 4, column lr
+    struct Scales {
+        uint32_t a[MI], b[NI];
+    };
+    auto read = [&](const uint8_t* from, int ks, Frags& f) {
 #pragma unroll
-    for (int j = 0; j < NI; j++) {
-        const int n = n0 + 64 * wn + 32 * j + lr;
-        if (n >= g.N) continue;
-        const int e = g.row_exp ? g.row_exp[n] : 0;
+        for (int i = 0; i < MI; i++) f.a[i] = *reinterpret_cast<const u4w*>(from + at(am0 + 32 * i + lr, 2 * ks + lh));
+#pragma unroll
+        for (int j = 0; j < NI; j++) f.b[j] = *reinterpret_cast<const u4w*>(from + BM * kStepBytes + at(bn0 + 32 * j + lr, 2 * ks + lh));
+    };
+    auto read_scales = [&](const uint8_t* from, Scales& q) {
+        const uint8_t* fs = from + (BM + BN) * kStepBytes;
+#pragma unroll
+        for (int i = 0; i < MI; i++) q.a[i] = *reinterpret_cast<const uint32_t*>(fs + (am0 + 32 * i + lr) * 8 + 4 * lh);
+#pragma unroll
+        for (int j = 0; j < NI; j++) q.b[j] = *reinterpret_cast<const uint32_t*>(fs + (BM + bn0 + 32 * j + lr) * 8 + 4 * lh);
+    };
+    // B first: rows of the result are B's, a lane's column is a row of A
+    auto multiply = [&](auto KS, const Frags& f, const Scales& q) {
+        __builtin_amdgcn_sched_barrier(0);  // the next reads go out before the products
 #pragma unroll
         for (int i = 0; i < MI; i++)
 #pragma unroll
-            for (int r = 0; r < 16; r++) {
-                const int m = m0 + 64 * wm + 32 * i + 8 * (r / 4) + 4 * lh + r % 4;
-                if (m >= g.M) continue;
-                float v = ldexpf(acc[i][j][r], e);
-                const size_t es = Act<DT>::size;
-                if constexpr (DT == kActF32) {
-                    if (g.base) v += *reinterpret_cast<const float*>(g.base + (size_t)m * g.ldbase + n * es);
-                    *reinterpret_cast<float*>(g.y + (size_t)m * g.ldy + n * es) = v;
-                } else if constexpr (DT == kActBf16) {
-                    if (g.base) v += (float)*reinterpret_cast<const __bf16*>(g.base + (size_t)m * g.ldbase + n * es);
-                    *reinterpret_cast<__bf16*>(g.y + (size_t)m * g.ldy + n * es) = (__bf16)v;
-                } else {
-                    if (g.base) v += (float)*reinterpret_cast<const _Float16*>(g.base + (size_t)m * g.ldbase + n * es);
-                    *reinterpret_cast<_Float16*>(g.y + (size_t)m * g.ldy + n * es) = (_Float16)v;
-                }
+            for (int j = 0; j < NI; j++) {
+                if constexpr (KIND == kFp4) acc[i][j] = mma4<decltype(KS)::value>(f.b[j], f.a[i], acc[i][j], q.b[j], q.a[i]);
+                else acc[i][j] = mma<KIND>(f.b[j], f.a[i], acc[i][j]);
             }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+#pragma unroll
+    for (int s = 0; s < R; s++) issue(s0 + s, lds + s * STEP);
+    ring_barrier<(R - 1) * LOADS>();  // step 0 is there
+    Frags f0, f1;
+    Scales q0, q1;
+    read(lds, 0, f0);
+    if constexpr (KIND == kFp4) read_scales(lds, q0);
+    int cur = 0;  // s % R
+    // a step's four products, each with the fragments of the next on their way.
+    // Before the last, the next step is there, every wave has read all of this
+    // one, and its buffer takes step s + R.
+    auto step = [&](int s, const Scales& q, Scales& next) {
+        uint8_t* buf = lds + cur * STEP;
+        cur = cur + 1 == R ? 0 : cur + 1;
+        read(buf, 1, f1);
+        multiply(std::integral_constant<int, 0>{}, f0, q);
+        read(buf, 2, f0);
+        multiply(std::integral_constant<int, 1>{}, f1, q);
+        read(buf, 3, f1);
+        multiply(std::integral_constant<int, 2>{}, f0, q);
+        ring_barrier<(R - 2) * LOADS>();
+        issue(s + R, buf);
+        read(lds + cur * STEP, 0, f0);
+        if constexpr (KIND == kFp4) read_scales(lds + cur * STEP, next);
+        multiply(std::integral_constant<int, 3>{}, f1, q);
+    };
+    for (int s = s0; s < s1; s += 2) {
+        step(s, q0, q1);
+        if (s + 1 < s1) step(s + 1, q1, q0);
+    }
+    ring_barrier<0>();  // no load still writes LDS, and every wave has read its last step
+    // acc[i][j][r]: row m = lr of A's 32, column n = 8 (r / 4) + 4 lh + r % 4 of
+    // B's 32. Through LDS, so that a row's 32 NI columns leave side by side.
+    float* out = reinterpret_cast<float*>(lds + wave * OUT);
+    constexpr int ROW = 32 * NI + 4, PIECES = 4 * NI, PER = 64 / PIECES;  // floats of a row, its pieces of 8, rows at a time
+    const int pc = lane % PIECES, n = n0 + bn0 + 8 * pc;
+    float e[8];
+#pragma unroll
+    for (int q = 0; q < 8; q++) e[q] = g.row_exp && n < g.N ? exp2i(g.row_exp[n + q]) : 1.0f;
+#pragma unroll
+    for (int i = 0; i < MI; i++) {
+#pragma unroll
+        for (int j = 0; j < NI; j++)
+#pragma unroll
+            for (int q = 0; q < 4; q++)
+                *reinterpret_cast<f4v*>(out + lr * ROW + 32 * j + 8 * q + 4 * lh) =
+                    f4v{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // a wave's own region: its reads come behind its writes
+#pragma unroll
+        for (int u = 0; u < 32 / PER; u++) {
+            const int row = u * PER + lane / PIECES, m = m0 + am0 + 32 * i + row;
+            const f4v lo = *reinterpret_cast<const f4v*>(out + row * ROW + 8 * pc), hi = *reinterpret_cast<const f4v*>(out + row * ROW + 8 * pc + 4);
+            if (piece >= 0) {
+                float* to = g.part + ((size_t)piece * BM + am0 + 32 * i + row) * BN + bn0 + 8 * pc;
+                *reinterpret_cast<f4v*>(to) = lo;
+                *reinterpret_cast<f4v*>(to + 4) = hi;
+            } else if (m < g.M && n < g.N) {
+                float v[8];
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    v[q] = lo[q] * e[q];
+                    v[4 + q] = hi[q] * e[4 + q];
+                }
+                if (g.base) {
+                    float o[8];
+                    unpack8<DT>(load8<DT>(g.base + (size_t)m * g.ldbase, n), o);
+#pragma unroll
+                    for (int q = 0; q < 8; q++) v[q] += o[q];
+                }
+                store8<DT>(g.y + (size_t)m * g.ldy, n, pack8<DT>(v));
+            }
+        }
+        asm volatile("" ::: "memory");
     }
 }
 
+// The split tiles' parts, added in order: a thread 8 columns of a row.
+template <int DT>
+__global__ __launch_bounds__(256) void k_fp4_join(MmArgs g) {
+    constexpr int B = 256;
+    const int tile = blockIdx.x / (B * B / 8 / 256), at = blockIdx.x % (B * B / 8 / 256) * 256 + threadIdx.x, row = at / (B / 8), c = at % (B / 8) * 8;
+    int m, n;
+    tile_at(g.full + tile, g.mt, g.nt, m, n);
+    m = m * B + row;
+    n = n * B + c;
+    if (m >= g.M || n >= g.N) return;
+    const float* p = g.part + ((size_t)tile * g.split * B + row) * B + c;
+    f4v lo = *reinterpret_cast<const f4v*>(p), hi = *reinterpret_cast<const f4v*>(p + 4);
+    for (int i = 1; i < g.split; i++) {
+        lo += *reinterpret_cast<const f4v*>(p + (size_t)i * B * B);
+        hi += *reinterpret_cast<const f4v*>(p + (size_t)i * B * B + 4);
+    }
+    float v[8];
+#pragma unroll
+    for (int q = 0; q < 8; q++) v[q] = (q < 4 ? lo[q % 4] : hi[q % 4]) * (g.row_exp ? exp2i(g.row_exp[n + q]) : 1.0f);
+    if (g.base) {
+        float o[8];
+        unpack8<DT>(load8<DT>(g.base + (size_t)m * g.ldbase, n), o);
+#pragma unroll
+        for (int q = 0; q < 8; q++) v[q] += o[q];
+    }
+    store8<DT>(g.y + (size_t)m * g.ldy, n, pack8<DT>(v));
+}
+
+constexpr int kCus = 256;                       // workgroups of a round of the large tiles
+constexpr size_t kPart = 256 * 256 * 4;         // bytes of a part
+constexpr int kMaxSplit = 8;
+// Parts that a product may leave: those of one round, or of all its tiles.
+size_t part_bytes(int M, int N) {
+    const size_t all = (size_t)((M + 255) / 256) * ((N + 255) / 256) * kMaxSplit;
+    return (all < kCus ? all : kCus) * kPart;
+}
+
+template <int KIND, int DT>
+hipError_t mm_tiles(MmArgs& g, hipStream_t s) {
+    auto tiles = [&](int bm, int bn) {
+        g.mt = (g.M + bm - 1) / bm;
+        g.nt = (g.N + bn - 1) / bn;
+        return g.full = g.mt * g.nt;
+    };
+    g.split = 1;
+    if (tiles(256, 256) >= 192) {
+        // A last round of few tiles costs as much as a full one: each takes several
+        // workgroups, and their sums are joined by a launch of their own (8192 x
+        // 2560 of 8192: 320 tiles on 256 compute units, 415 us whole). Not where the
+        // round is short: the parts are written and read (30 us at most, some 20
+        // steps).
+        const int all = g.full, rest = all % kCus;
+        if (rest) {
+            int split = kCus / rest;
+            split = split < kMaxSplit ? split : kMaxSplit;
+            while (split > 1 && g.steps / split < 4) split--;
+            if (split > 1 && g.steps - g.steps / split >= 24) {
+                g.split = split;
+                g.full = all - rest;
+            }
+        }
+        const int cut = all - g.full;
+        hipLaunchKernelGGL((k_fp4_mm<KIND, DT, 256, 256, 4, 2, 2>), dim3(g.full + cut * g.split), dim3(512), 0, s, g);
+        if (cut) {
+            const hipError_t r = hipGetLastError();
+            if (r != hipSuccess) return r;
+            hipLaunchKernelGGL(k_fp4_join<DT>, dim3(cut * (256 * 256 / 8 / 256)), dim3(256), 0, s, g);
+        }
+    } else if (tiles(128, 128) >= 192) {
+        hipLaunchKernelGGL((k_fp4_mm<KIND, DT, 128, 128, 2, 2, 2>), dim3(g.full), dim3(256), 0, s, g);
+    } else {
+        tiles(64, 64);
+        hipLaunchKernelGGL((k_fp4_mm<KIND, DT, 64, 64, 1, 1, 4>), dim3(g.full), dim3(256), 0, s, g);
+    }
+    return hipGetLastError();
+}
 template <int KIND>
 hipError_t mm(int dtype, MmArgs& g, hipStream_t s) {
-    g.nt = (g.N + 127) / 128;
-    const dim3 grid((unsigned)((g.M + 127) / 128) * g.nt);
-    if (dtype == kActF32) hipLaunchKernelGGL((k_fp4_mm<KIND, kActF32>), grid, dim3(256), 0, s, g);
-    else if (dtype == kActBf16) hipLaunchKernelGGL((k_fp4_mm<KIND, kActBf16>), grid, dim3(256), 0, s, g);
-    else hipLaunchKernelGGL((k_fp4_mm<KIND, kActF16>), grid, dim3(256), 0, s, g);
-    return hipGetLastError();
+    if (dtype == kActF32) return mm_tiles<KIND, kActF32>(g, s);
+    return dtype == kActBf16 ? mm_tiles<KIND, kActBf16>(g, s) : mm_tiles<KIND, kActF16>(g, s);
 }
 
 // A's operand of a 16-bit product over K: the activations themselves, or their
@@ -328,10 +495,11 @@ hipError_t activations(int dtype, int P, const void* x, size_t ldx, int T, int K
 
 size_t fp4_ws_bytes(int K, int N, int fmt, int dtype, int T, bool backward) {
     const int sum = backward ? N : K, P = act_parts(dtype, act_kind(fmt, dtype, backward));
-    const size_t kept = align256((size_t)K * N * 2) + (P > 1 ? align256((size_t)T * P * sum * 2) : 0);
+    const size_t parts = T > kFewMaxT || backward ? part_bytes(T, backward ? K : N) : 0;
+    const size_t kept = parts + align256((size_t)K * N * 2) + (P > 1 ? align256((size_t)T * P * sum * 2) : 0);
     if (backward || fmt != kFmtMxfp4) return kept;
     const size_t steps = (K + 255) / 256;
-    const size_t rounded = align256((size_t)T * K / 2) + align256((size_t)T * K / 32) + steps * 8 * (tile_rows(T) + tile_rows(N));
+    const size_t rounded = parts + align256((size_t)T * K / 2) + align256((size_t)T * K / 32) + steps * 8 * (tile_rows(T) + tile_rows(N));
     return kept > rounded ? kept : rounded;
 }
 
@@ -344,6 +512,8 @@ hipError_t launch_fp4_apply(int K, int N, int fmt, int dtype, const void* x, siz
     MmArgs g = {};
     g.M = T;
     g.N = N;
+    g.part = reinterpret_cast<float*>(p);
+    if (T > kFewMaxT) p += part_bytes(T, N);
     g.row_exp = w.row_exp;
     g.base = static_cast<const char*>(base);
     g.y = static_cast<char*>(y);
@@ -399,6 +569,8 @@ hipError_t launch_fp4_backward(int K, int N, int fmt, int dtype, const void* dy,
     MmArgs g = {};
     g.M = T;
     g.N = K;
+    g.part = reinterpret_cast<float*>(p);
+    p += part_bytes(T, K);
     g.base = static_cast<const char*>(dx_base);
     g.y = static_cast<char*>(dx);
     g.ldbase = lddxb * es;
