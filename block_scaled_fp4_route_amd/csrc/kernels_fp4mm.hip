@@ -26,7 +26,6 @@ namespace {
 typedef float f16v __attribute__((ext_vector_type(16)));
 
 constexpr int kBf16 = 0, kF16 = 1, kFp4 = 2;  // operands of the product
-constexpr int kStepBytes = 128;               // of a row in one step of the sum
 
 // Parts of an activation on the way of `dtype`, W as 16-bit `kind`.
 int act_kind(int fmt, int dtype, bool backward) {
@@ -153,8 +152,8 @@ struct MmArgs {
     const char *a, *b;
     size_t lda, ldb;        // bytes between rows
     uint32_t wa, wb;        // bytes of a row (A's parts together; B starts again at its end)
-    int M, N, steps;
-    const uint8_t *sa, *sb; // kFp4: scale panels [steps][rows up to a whole tile][8]
+    int M, N, wide;         // wide: a row's bytes in the sum, all parts
+    const uint8_t *sa, *sb; // kFp4: scale panels [K / 256][rows up to a whole tile][8]
     const int8_t* row_exp;  // of B's rows, or null
     const char* base;
     char* y;
@@ -170,11 +169,11 @@ __device__ __forceinline__ void ring_barrier() {
 }
 
 // 16 or 4 bytes a lane from memory straight into LDS, the lanes' side by side.
-__device__ __forceinline__ void to_lds16(rsrc_t r, uint8_t* to, uint32_t off) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, off, 0, 0, 0);
+__device__ __forceinline__ void to_lds16(rsrc_t r, uint8_t* to, uint32_t off, uint32_t step) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, off, step, 0, 0);
 }
-__device__ __forceinline__ void to_lds4(rsrc_t r, uint8_t* to, uint32_t off) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 4, off, 0, 0, 0);
+__device__ __forceinline__ void to_lds4(rsrc_t r, uint8_t* to, uint32_t off, uint32_t step) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 4, off, step, 0, 0);
 }
 
 template <int KIND>
@@ -202,26 +201,28 @@ __device__ __forceinline__ void tile_at(int seq, int mt, int nt, int& m, int& n)
 template <int KIND, int DT, int BM, int BN, int MI, int NI, int R>
 __global__ __launch_bounds__(64 * (BM / (32 * MI)) * (BN / (32 * NI))) void k_fp4_mm(MmArgs g) {
     constexpr int WN = BN / (32 * NI), WAVES = BM / (32 * MI) * WN;
+    constexpr int SB = 128, CH = SB / 16, RP = 64 / CH;                         // bytes and chunks of a row in a step; rows of a load
     constexpr int SC = KIND == kFp4 ? (BM + BN) * 8 : 0;                        // scale bytes of a step
-    constexpr int LA = BM / 8 / WAVES, LB = BN / 8 / WAVES, LS = SC / 256 / WAVES, LOADS = LA + LB + LS;  // loads of a wave and step
-    constexpr int STEP = (BM + BN) * kStepBytes + SC;
+    constexpr int LA = BM / RP / WAVES, LB = BN / RP / WAVES, LS = SC / 256 / WAVES, LOADS = LA + LB + LS;  // loads of a wave and step
+    constexpr int STEP = (BM + BN) * SB + SC;
     constexpr int OUT = 32 * (32 * NI * 4 + 16);                                // a wave's 32 rows on their way out, fp32
     constexpr int LDS = R * STEP > WAVES * OUT ? R * STEP : WAVES * OUT;
-    static_assert(LA * 8 * WAVES == BM && LB * 8 * WAVES == BN && LS * 256 * WAVES == SC && LA % 2 == 0 && LB % 2 == 0 && LOADS * (R - 1) < 64, "tile");
+    static_assert(LA * RP * WAVES == BM && LB * RP * WAVES == BN && LS * 256 * WAVES == SC && LOADS * (R - 1) < 64, "tile");
     __shared__ __attribute__((aligned(16))) uint8_t lds[LDS];
+    const int steps = (g.wide + SB - 1) / SB;
     const int lane = threadIdx.x & 63, wave = wave_id(), wm = wave / WN, wn = wave % WN;
     // workgroups go to the eight XCDs in turn: each takes a run of the tiles, which
     // go down four tiles of M before the next of N, so that the workgroups of an
     // XCD share rows of both operands in its L2
-    int m0, n0, s0 = 0, s1 = g.steps, piece = -1;
+    int m0, n0, s0 = 0, s1 = steps, piece = -1;
     {
         const int b = blockIdx.x, x = b % 8, q = g.full / 8, r = g.full % 8;
         int seq = x * q + min(x, r) + b / 8;
         if (b >= g.full) {
             piece = b - g.full;
             seq = g.full + piece / g.split;
-            s0 = (int)((int64_t)(piece % g.split) * g.steps / g.split);
-            s1 = (int)((int64_t)(piece % g.split + 1) * g.steps / g.split);
+            s0 = (int)((int64_t)(piece % g.split) * steps / g.split);
+            s1 = (int)((int64_t)(piece % g.split + 1) * steps / g.split);
         }
         tile_at(seq, g.mt, g.nt, m0, n0);
         m0 *= BM;
@@ -230,44 +231,65 @@ __global__ __launch_bounds__(64 * (BM / (32 * MI)) * (BN / (32 * NI))) void k_fp
     const int am = min(BM, g.M - m0), bn = min(BN, g.N - n0);
     const rsrc_t rA = make_rsrc(g.a + (size_t)m0 * g.lda, (uint32_t)(am - 1) * (uint32_t)g.lda + g.wa);
     const rsrc_t rB = make_rsrc(g.b + (size_t)n0 * g.ldb, (uint32_t)(bn - 1) * (uint32_t)g.ldb + g.wb);
-    // this lane's loads: row 8 (L wave + i) + lane / 8, chunk (lane ^ row / 2) % 8,
-    // which in every second load is another by 4
-    const uint32_t ch = (uint32_t)((lane & 7) ^ (lane >> 4)) * 16u;
-    const uint32_t k0 = (uint32_t)s0 * kStepBytes;
-    uint32_t ka[2] = {k0 + ch, k0 + (ch ^ 64u)}, kb[2] = {ka[0] % g.wb, ka[1] % g.wb};  // bytes within the row
+    // this lane's loads: row RP (L wave + i) + lane / CH, chunk lane % CH ^ swizzle;
+    // with eight chunks, every second load's is another by 4
+    const uint32_t ch = (uint32_t)((lane % CH) ^ (lane >> 4)) * 16u;
     uint32_t oa[LA], ob[LB];
 #pragma unroll
     for (int i = 0; i < LA; i++) {
-        const int r = 8 * (LA * wave + i) + (lane >> 3);
-        oa[i] = r < am ? (uint32_t)r * (uint32_t)g.lda : kOOB;
+        const int r = RP * (LA * wave + i) + lane / CH;
+        oa[i] = r < am ? (uint32_t)r * (uint32_t)g.lda + ((LA * wave + i) & 1 ? ch ^ 64u : ch) : kOOB;
     }
 #pragma unroll
     for (int i = 0; i < LB; i++) {
-        const int r = 8 * (LB * wave + i) + (lane >> 3);
-        ob[i] = r < bn ? (uint32_t)r * (uint32_t)g.ldb : kOOB;
+        const int r = RP * (LB * wave + i) + lane / CH;
+        ob[i] = r < bn ? (uint32_t)r * (uint32_t)g.ldb + ((LB * wave + i) & 1 ? ch ^ 64u : ch) : kOOB;
     }
-    // every step issues the same loads; those behind the last one read nothing
+    uint32_t kb = (uint32_t)s0 * SB % g.wb;  // B's byte of the next step to be loaded
+    // Every step issues the same loads; those behind the last one read nothing.
+    // The step goes into the scalar offset, so that a load costs no arithmetic,
+    // unless a row of A ends within the step, or one of B.
     auto issue = [&](int s, uint8_t* to) {
+        const uint32_t ka = (uint32_t)s * SB;
+        if constexpr (KIND == kFp4) {  // both rows are as long (and with the second path its operands do not fit the registers)
 #pragma unroll
-        for (int i = 0; i < LA; i++)
-            to_lds16(rA, to + 1024 * (LA * wave + i), ka[i & 1] < g.wa && oa[i] != kOOB ? oa[i] + ka[i & 1] : kOOB);
+            for (int i = 0; i < LA; i++) {
+                const uint32_t c = (LA * wave + i) & 1 ? ch ^ 64u : ch;
+                to_lds16(rA, to + 1024 * (LA * wave + i), ka + c < g.wa && oa[i] != kOOB ? oa[i] + ka : kOOB, 0);
+            }
 #pragma unroll
-        for (int i = 0; i < LB; i++)
-            to_lds16(rB, to + BM * kStepBytes + 1024 * (LB * wave + i), ka[i & 1] < g.wa && ob[i] != kOOB ? ob[i] + kb[i & 1] : kOOB);
+            for (int i = 0; i < LB; i++) {
+                const uint32_t c = (LB * wave + i) & 1 ? ch ^ 64u : ch;
+                to_lds16(rB, to + BM * SB + 1024 * (LB * wave + i), ka + c < g.wa && ob[i] != kOOB ? ob[i] + ka : kOOB, 0);
+            }
+        } else if (ka + SB <= g.wa && kb + SB <= g.wb) {
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            ka[h] += kStepBytes;
-            kb[h] += kStepBytes;
-            while (kb[h] >= g.wb) kb[h] -= g.wb;
+            for (int i = 0; i < LA; i++) to_lds16(rA, to + 1024 * (LA * wave + i), oa[i], ka);
+#pragma unroll
+            for (int i = 0; i < LB; i++) to_lds16(rB, to + BM * SB + 1024 * (LB * wave + i), ob[i], kb);
+        } else {
+            int l = lane;
+            asm volatile("" : "+v"(l));  // nothing of this rare path is kept in registers over the loop
+            auto off = [&](int q, int rows, uint32_t ld, uint32_t at, uint32_t end) {
+                const int r = RP * q + l / CH;
+                const uint32_t c = (uint32_t)((l % CH) ^ (l >> 4) ^ (q & 1 ? 4 : 0)) * 16u;
+                return r < rows && ka + c < g.wa ? (uint32_t)r * ld + (at + c) % end : kOOB;
+            };
+#pragma unroll
+            for (int i = 0; i < LA; i++) to_lds16(rA, to + 1024 * (LA * wave + i), off(LA * wave + i, am, (uint32_t)g.lda, ka, g.wa), 0);
+#pragma unroll
+            for (int i = 0; i < LB; i++) to_lds16(rB, to + BM * SB + 1024 * (LB * wave + i), off(LB * wave + i, bn, (uint32_t)g.ldb, kb, g.wb), 0);
         }
+        kb += SB;
+        while (kb >= g.wb) kb -= g.wb;
         if constexpr (KIND == kFp4) {  // rows of 8 bytes: A's, then B's
-            const size_t ss = min(s, g.steps - 1);
+            const size_t ss = min(s, steps - 1);
 #pragma unroll
             for (int i = 0; i < LS; i++) {
                 const int q = LS * wave + i;  // 256 bytes, 32 rows, each
                 const bool ofa = q < BM / 32;
                 const uint8_t* p = ofa ? g.sa + (ss * tile_rows(g.M) + m0) * 8 : g.sb + (ss * tile_rows(g.N) + n0) * 8;
-                to_lds4(make_rsrc(p, (ofa ? BM : BN) * 8), to + (BM + BN) * kStepBytes + 256 * q, 256u * (ofa ? q : q - BM / 32) + 4u * lane);
+                to_lds4(make_rsrc(p, (ofa ? BM : BN) * 8), to + (BM + BN) * SB + 256 * q, 4u * lane, 256u * (ofa ? q : q - BM / 32));
             }
         }
     };
@@ -279,7 +301,7 @@ __global__ __launch_bounds__(64 * (BM / (32 * MI)) * (BN / (32 * NI))) void k_fp
 #pragma unroll
             for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
     const int lr = lane & 31, lh = lane >> 5, am0 = 32 * MI * wm, bn0 = 32 * NI * wn;
-    auto at = [&](int row, int c) { return (uint32_t)row * kStepBytes + (uint32_t)((c ^ (row >> 1 & 7)) * 16); };
+    auto at = [&](int row, int c) { return (uint32_t)row * SB + (uint32_t)((c ^ (row >> 1 & 7)) * 16); };
     struct Frags {
         u4w a[MI], b[NI];
     };
@@ -290,25 +312,29 @@ __global__ __launch_bounds__(64 * (BM / (32 * MI)) * (BN / (32 * NI))) void k_fp
 #pragma unroll
         for (int i = 0; i < MI; i++) f.a[i] = *reinterpret_cast<const u4w*>(from + at(am0 + 32 * i + lr, 2 * ks + lh));
 #pragma unroll
-        for (int j = 0; j < NI; j++) f.b[j] = *reinterpret_cast<const u4w*>(from + BM * kStepBytes + at(bn0 + 32 * j + lr, 2 * ks + lh));
+        for (int j = 0; j < NI; j++) f.b[j] = *reinterpret_cast<const u4w*>(from + BM * SB + at(bn0 + 32 * j + lr, 2 * ks + lh));
     };
     auto read_scales = [&](const uint8_t* from, Scales& q) {
-        const uint8_t* fs = from + (BM + BN) * kStepBytes;
+        const uint8_t* fs = from + (BM + BN) * SB + 4 * lh;
 #pragma unroll
-        for (int i = 0; i < MI; i++) q.a[i] = *reinterpret_cast<const uint32_t*>(fs + (am0 + 32 * i + lr) * 8 + 4 * lh);
+        for (int i = 0; i < MI; i++) q.a[i] = *reinterpret_cast<const uint32_t*>(fs + (am0 + 32 * i + lr) * 8);
 #pragma unroll
-        for (int j = 0; j < NI; j++) q.b[j] = *reinterpret_cast<const uint32_t*>(fs + (BM + bn0 + 32 * j + lr) * 8 + 4 * lh);
+        for (int j = 0; j < NI; j++) q.b[j] = *reinterpret_cast<const uint32_t*>(fs + (BM + bn0 + 32 * j + lr) * 8);
     };
     // B first: rows of the result are B's, a lane's column is a row of A
-    auto multiply = [&](auto KS, const Frags& f, const Scales& q) {
-        __builtin_amdgcn_sched_barrier(0);  // the next reads go out before the products
+    auto rows = [&](auto KS, int i0, int i1, const Frags& f, const Scales& q) {
+        constexpr int ks = decltype(KS)::value;
 #pragma unroll
-        for (int i = 0; i < MI; i++)
+        for (int i = i0; i < i1; i++)
 #pragma unroll
             for (int j = 0; j < NI; j++) {
-                if constexpr (KIND == kFp4) acc[i][j] = mma4<decltype(KS)::value>(f.b[j], f.a[i], acc[i][j], q.b[j], q.a[i]);
+                if constexpr (KIND == kFp4) acc[i][j] = mma4<ks>(f.b[j], f.a[i], acc[i][j], q.b[j], q.a[i]);
                 else acc[i][j] = mma<KIND>(f.b[j], f.a[i], acc[i][j]);
             }
+    };
+    auto multiply = [&](auto KS, const Frags& f, const Scales& q) {
+        __builtin_amdgcn_sched_barrier(0);  // the next reads go out before the products
+        rows(KS, 0, MI, f, q);
         __builtin_amdgcn_sched_barrier(0);
     };
 #pragma unroll
@@ -319,9 +345,9 @@ __global__ __launch_bounds__(64 * (BM / (32 * MI)) * (BN / (32 * NI))) void k_fp
     read(lds, 0, f0);
     if constexpr (KIND == kFp4) read_scales(lds, q0);
     int cur = 0;  // s % R
-    // a step's four products, each with the fragments of the next on their way.
-    // Before the last, the next step is there, every wave has read all of this
-    // one, and its buffer takes step s + R.
+    // a step's four products, each with the fragments of the next on their
+    // way. Before the last, the next step is there, every wave has read all of
+    // this one, and its buffer takes step s + R.
     auto step = [&](int s, const Scales& q, Scales& next) {
         uint8_t* buf = lds + cur * STEP;
         cur = cur + 1 == R ? 0 : cur + 1;
@@ -332,10 +358,21 @@ __global__ __launch_bounds__(64 * (BM / (32 * MI)) * (BN / (32 * NI))) void k_fp
         read(buf, 3, f1);
         multiply(std::integral_constant<int, 2>{}, f0, q);
         ring_barrier<(R - 2) * LOADS>();
-        issue(s + R, buf);
+        if constexpr (KIND == kFp4) {  // (in two parts its operands do not fit the registers)
+            issue(s + R, buf);
+            read(lds + cur * STEP, 0, f0);
+            read_scales(lds + cur * STEP, next);
+            multiply(std::integral_constant<int, 3>{}, f1, q);
+            return;
+        }
         read(lds + cur * STEP, 0, f0);
-        if constexpr (KIND == kFp4) read_scales(lds + cur * STEP, next);
-        multiply(std::integral_constant<int, 3>{}, f1, q);
+        __builtin_amdgcn_sched_barrier(0);
+        rows(std::integral_constant<int, 3>{}, 0, MI / 2, f1, q);
+        __builtin_amdgcn_sched_barrier(0);
+        issue(s + R, buf);  // between products, so that these do not wait for it
+        __builtin_amdgcn_sched_barrier(0);
+        rows(std::integral_constant<int, 3>{}, MI / 2, MI, f1, q);
+        __builtin_amdgcn_sched_barrier(0);
     };
     for (int s = s0; s < s1; s += 2) {
         step(s, q0, q1);
@@ -442,8 +479,8 @@ hipError_t mm_tiles(MmArgs& g, hipStream_t s) {
         if (rest) {
             int split = kCus / rest;
             split = split < kMaxSplit ? split : kMaxSplit;
-            while (split > 1 && g.steps / split < 4) split--;
-            if (split > 1 && g.steps - g.steps / split >= 24) {
+            const int steps = g.wide / 128;
+            if (split > 1 && steps - steps / split >= 24) {
                 g.split = split;
                 g.full = all - rest;
             }
@@ -538,7 +575,7 @@ hipError_t launch_fp4_apply(int K, int N, int fmt, int dtype, const void* x, siz
         g.lda = g.ldb = g.wa = g.wb = (uint32_t)K / 2;
         g.sa = sa;
         g.sb = sb;
-        g.steps = steps;
+        g.wide = K / 2;
         return mm<kFp4>(dtype, g, s);
     }
     const int kind = act_kind(fmt, dtype, false), P = act_parts(dtype, kind);
@@ -557,7 +594,7 @@ hipError_t launch_fp4_apply(int K, int N, int fmt, int dtype, const void* x, siz
     if ((r = hipGetLastError()) != hipSuccess) return r;
     g.b = p;
     g.ldb = g.wb = (uint32_t)K * 2;
-    g.steps = (int)((g.wa + kStepBytes - 1) / kStepBytes);
+    g.wide = (int)g.wa;
     return kind == kF16 ? mm<kF16>(dtype, g, s) : mm<kBf16>(dtype, g, s);
 }
 
@@ -586,7 +623,7 @@ hipError_t launch_fp4_backward(int K, int N, int fmt, int dtype, const void* dy,
     if ((r = activations(dtype, P, dy, lddy, T, N, p + align256((size_t)K * N * 2), g, s)) != hipSuccess) return r;
     g.b = p;
     g.ldb = g.wb = (uint32_t)N * 2;
-    g.steps = (int)((g.wa + kStepBytes - 1) / kStepBytes);
+    g.wide = (int)g.wa;
     return mm<kBf16>(dtype, g, s);
 }
 
