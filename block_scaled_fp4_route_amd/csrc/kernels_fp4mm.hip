@@ -425,9 +425,8 @@ __global__ __launch_bounds__(64 * (BM / (32 * MI)) * (BN / (32 * NI))) void k_fp
 }
 
 // The split tiles' parts, added in order: a thread 8 columns of a row.
-template <int DT>
+template <int DT, int B>
 __global__ __launch_bounds__(256) void k_fp4_join(MmArgs g) {
-    constexpr int B = 256;
     const int tile = blockIdx.x / (B * B / 8 / 256), at = blockIdx.x % (B * B / 8 / 256) * 256 + threadIdx.x, row = at / (B / 8), c = at % (B / 8) * 8;
     int m, n;
     tile_at(g.full + tile, g.mt, g.nt, m, n);
@@ -453,12 +452,15 @@ __global__ __launch_bounds__(256) void k_fp4_join(MmArgs g) {
 }
 
 constexpr int kCus = 256;                       // workgroups of a round of the large tiles
-constexpr size_t kPart = 256 * 256 * 4;         // bytes of a part
-constexpr int kMaxSplit = 8;
-// Parts that a product may leave: those of one round, or of all its tiles.
+constexpr int kLargeFrom = 192;                 // tiles of a size that is worth it
+constexpr int kSmallGroups = 512;               // workgroups of the small tiles, where the sum is split
+constexpr int kMaxSplit = 8, kMaxSmallSplit = 16;
+// Bytes of parts that a product may leave: one round of large tiles, or all the
+// small ones. Neither falls as M grows.
 size_t part_bytes(int M, int N) {
-    const size_t all = (size_t)((M + 255) / 256) * ((N + 255) / 256) * kMaxSplit;
-    return (all < kCus ? all : kCus) * kPart;
+    const size_t large = (size_t)((M + 255) / 256) * ((N + 255) / 256), small = (size_t)((M + 63) / 64) * ((N + 63) / 64) * kMaxSmallSplit;
+    const size_t a = large >= kLargeFrom ? (size_t)kCus * 256 * 256 * 4 : 0, b = (small < kSmallGroups ? small : kSmallGroups) * 64 * 64 * 4;
+    return a > b ? a : b;
 }
 
 template <int KIND, int DT>
@@ -468,35 +470,37 @@ hipError_t mm_tiles(MmArgs& g, hipStream_t s) {
         g.nt = (g.N + bn - 1) / bn;
         return g.full = g.mt * g.nt;
     };
+    // A last round of few tiles costs as much as a full one: each takes several
+    // workgroups, and their sums are joined by a launch of their own (8192 x 2560
+    // of 8192: 320 tiles on 256 compute units, 415 us whole, 305 split). Not where
+    // few steps are saved: the parts are written and read, and the launch costs 4 us.
+    auto cut = [&](int rest, int split, int least) {
+        const int steps = g.wide / 128;
+        while (split > 1 && steps / split < 4) split--;
+        if (rest && split > 1 && steps - steps / split >= least) {
+            g.split = split;
+            g.full -= rest;
+            return rest;
+        }
+        return 0;
+    };
     g.split = 1;
-    if (tiles(256, 256) >= 192) {
-        // A last round of few tiles costs as much as a full one: each takes several
-        // workgroups, and their sums are joined by a launch of their own (8192 x
-        // 2560 of 8192: 320 tiles on 256 compute units, 415 us whole). Not where the
-        // round is short: the parts are written and read (30 us at most, some 20
-        // steps).
-        const int all = g.full, rest = all % kCus;
-        if (rest) {
-            int split = kCus / rest;
-            split = split < kMaxSplit ? split : kMaxSplit;
-            const int steps = g.wide / 128;
-            if (split > 1 && steps - steps / split >= 24) {
-                g.split = split;
-                g.full = all - rest;
-            }
-        }
-        const int cut = all - g.full;
-        hipLaunchKernelGGL((k_fp4_mm<KIND, DT, 256, 256, 4, 2, 2>), dim3(g.full + cut * g.split), dim3(512), 0, s, g);
-        if (cut) {
-            const hipError_t r = hipGetLastError();
-            if (r != hipSuccess) return r;
-            hipLaunchKernelGGL(k_fp4_join<DT>, dim3(cut * (256 * 256 / 8 / 256)), dim3(256), 0, s, g);
-        }
-    } else if (tiles(128, 128) >= 192) {
+    int parts = 0;
+    hipError_t r;
+    if (tiles(256, 256) >= kLargeFrom) {
+        const int rest = g.full % kCus;
+        parts = cut(rest, rest ? (kCus / rest < kMaxSplit ? kCus / rest : kMaxSplit) : 1, 24);
+        hipLaunchKernelGGL((k_fp4_mm<KIND, DT, 256, 256, 4, 2, 2>), dim3(g.full + parts * g.split), dim3(512), 0, s, g);
+        if ((r = hipGetLastError()) != hipSuccess || !parts) return r;
+        hipLaunchKernelGGL((k_fp4_join<DT, 256>), dim3(parts * (256 * 256 / 8 / 256)), dim3(256), 0, s, g);
+    } else if (tiles(128, 128) >= kLargeFrom) {
         hipLaunchKernelGGL((k_fp4_mm<KIND, DT, 128, 128, 2, 2, 2>), dim3(g.full), dim3(256), 0, s, g);
     } else {
-        tiles(64, 64);
-        hipLaunchKernelGGL((k_fp4_mm<KIND, DT, 64, 64, 1, 1, 4>), dim3(g.full), dim3(256), 0, s, g);
+        const int all = tiles(64, 64), split = kSmallGroups / all;
+        parts = cut(all, split < kMaxSmallSplit ? split : kMaxSmallSplit, 20);
+        hipLaunchKernelGGL((k_fp4_mm<KIND, DT, 64, 64, 1, 1, 4>), dim3(g.full + parts * g.split), dim3(256), 0, s, g);
+        if ((r = hipGetLastError()) != hipSuccess || !parts) return r;
+        hipLaunchKernelGGL((k_fp4_join<DT, 64>), dim3(parts * (64 * 64 / 8 / 256)), dim3(256), 0, s, g);
     }
     return hipGetLastError();
 }

@@ -232,6 +232,42 @@ def test_product_long(m, T, K, N, fmt, dt, rnd, back):
     check_product(m, T, K, N, fmt, dt, rnd, back)
 
 
+@pytest.mark.parametrize("T,K,N,fmt,dt,rnd,back", [
+    (40, 64, 8192, "nvfp4", "f32", False, True),      # one tile, its sum over 16 workgroups
+    (1, 256, 4104, "mxfp4", "bf16", False, True),
+    (130, 5600, 72, "mxfp4", "f16", False, False),    # six tiles, a sum that ends within a step
+    (200, 12320, 136, "mxfp4", "bf16", True, False),
+    (257, 3200, 200, "nvfp4", "f32", False, False)])
+def test_product_split_sums(m, T, K, N, fmt, dt, rnd, back):
+    check_product(m, T, K, N, fmt, dt, rnd, back)
+
+
+@pytest.mark.parametrize("fmt,dt,rnd,back", [("mxfp4", "bf16", False, True), ("nvfp4", "f16", False, False), ("mxfp4", "bf16", True, False),
+                                             ("nvfp4", "f32", False, True)])
+def test_product_last_round_split(m, fmt, dt, rnd, back):
+    """17 x 16 tiles of 256 x 256 with ragged edges: one round of the chip and 16 tiles in several parts. Every row of the last
+    tiles and some of the others against the reference."""
+    T, ko, ki = 4200, 4096 - 24, 8192 if rnd else 3392
+    K, N = (ko + 24, ki) if back else (ki, ko)
+    g = torch.Generator().manual_seed(11)
+    codes, scales, e = matrix(g, N, K, fmt)
+    W = ref.decode(codes, scales, fmt, e)
+    W = W.t().contiguous() if back else W
+    ko = K if back else N
+    x = torch.randn((T, W.shape[1]), generator=g).to(DT[dt])
+    y = torch.empty((T, ko), dtype=DT[dt], device="cuda")
+    f = m.fp4_desc(K, N, fmt, DT[dt])
+    ws = torch.full((m.moe_fp4_workspace_bytes(f, T, back),), 0xFF, dtype=torch.uint8, device="cuda")
+    if back:
+        m.moe_fp4_backward(f, x.cuda(), N, T, codes, scales, e, None, 0, y, K, ws)
+    else:
+        m.moe_fp4_apply(f, x.cuda(), K, T, codes, scales, e, rnd, None, 0, y, N, ws)
+    rows = torch.cat([torch.arange(0, 4096, 97), torch.arange(4096, T)])
+    xs = ref.quant(x[rows], "mxfp4", "floor", False)[3] if rnd else x[rows].double()
+    want, off = ref.product(xs, W, None, DT[dt])
+    ref.close(y.cpu()[rows], want, off, (fmt, dt, rnd, back))
+
+
 @pytest.mark.parametrize("T", [3, 20, 50, 200])
 @pytest.mark.parametrize("dt", sorted(DT))
 @pytest.mark.parametrize("back", [False, True])
