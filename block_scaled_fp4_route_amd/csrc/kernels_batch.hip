@@ -72,10 +72,6 @@ int max_items(int E, int k, int T, bool shared, int per) {
     return (a < n ? a : n) + shared_items(shared, T, per);
 }
 
-__device__ __forceinline__ u4w ld_b128(rsrc_t r, uint32_t off) {
-    return __builtin_bit_cast(u4w, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
-}
-
 // The three bf16 parts of v, cut (all 24 bits down to 2^-133); those behind an
 // infinity or a NaN are 0.
 __device__ __forceinline__ void parts3(float v, uint32_t (&h)[3]) {

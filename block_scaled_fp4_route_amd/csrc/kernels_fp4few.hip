@@ -32,9 +32,6 @@ struct FewArgs {
 };
 
 __device__ __forceinline__ uint32_t ld_b16(rsrc_t r, uint32_t off) { return __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0); }
-__device__ __forceinline__ u4w ld_b128(rsrc_t r, uint32_t off) {
-    return __builtin_bit_cast(u4w, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
-}
 
 template <int DT>
 __device__ __forceinline__ float get1(const char* p, size_t i) {

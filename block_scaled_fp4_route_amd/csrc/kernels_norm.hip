@@ -401,7 +401,7 @@ hipError_t norm_types(const NormArgs& a, float* part, hipStream_t s) {
 
 }  // namespace
 
-size_t norm_ws_bytes(int H, int gate_kind, int T) { return align256((size_t)3 * norm_groups(H, T) * H * sizeof(float)); }
+size_t norm_ws_bytes(int H, int T) { return align256((size_t)3 * norm_groups(H, T) * H * sizeof(float)); }
 
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) { return norm_types(a, nullptr, s); }
 

@@ -529,6 +529,8 @@ int moe_lora_backward(const moe_lora_desc* l, const void* x, int64_t ldx, const 
 
 namespace {
 
+constexpr size_t kMaxQuant = (size_t)1 << 33;  // elements: the quantisation's pieces of 8 count in 32 bits
+
 bool act_known(int32_t dtype) { return dtype == MOE_ACT_F32 || dtype == MOE_ACT_BF16 || dtype == MOE_ACT_F16; }
 
 int fp4_checks(const moe_fp4_desc* f, int32_t T) {
@@ -617,7 +619,7 @@ int moe_fp4_quant(const void* x, int64_t ldx, int32_t rows, int32_t cols, int32_
         return fail(MOE_ERR_ARG, "scale rule %d does not go with format %d", rule, format);
     if (row_exp && format != MOE_FMT_NVFP4) return fail(MOE_ERR_ARG, "row_exp beside a format without row exponents");
     if (!codes && !scales && !values && !row_exp) return fail(MOE_ERR_ARG, "no output");
-    if ((size_t)rows * cols > ((size_t)1 << 33)) return fail(MOE_ERR_UNSUPPORTED, "rows*cols exceeds 2^33");
+    if ((size_t)rows * cols > kMaxQuant) return fail(MOE_ERR_UNSUPPORTED, "rows*cols exceeds 2^33");
     if (rows == 0) return ok();
     if ((r = check_rows(x, ldx, cols, "x"))) return r;
     if (codes && (r = check_ptr(codes, 4, "codes"))) return r;
@@ -640,6 +642,7 @@ int moe_fp4_apply(const moe_fp4_desc* f, const void* x, int64_t ldx, int32_t T, 
     int r;
     if ((r = fp4_checks(f, T))) return r;
     if (round_x && f->format != MOE_FMT_MXFP4) return fail(MOE_ERR_ARG, "round_x needs an MXFP4 matrix");
+    if (round_x && (size_t)T * f->K > kMaxQuant) return fail(MOE_ERR_UNSUPPORTED, "round_x: T*K exceeds 2^33");
     if (T == 0) return ok();
     if ((r = fp4_rows(x, ldx, f->K, "x")) || (r = fp4_matrix(f, codes, scales, row_exp)) ||
         (r = fp4_rows(y, ldy, f->N, "y")) || (base && (r = fp4_rows(base, ldbase, f->N, "base"))))
@@ -695,7 +698,7 @@ int moe_block_norm(const moe_norm_desc* n, const void* r, int64_t ldr, const voi
 }
 
 size_t moe_block_norm_workspace_bytes(const moe_norm_desc* n, int32_t T) {
-    return norm_checks(n, T) == MOE_OK ? moe::norm_ws_bytes(n->H, n->gate, T) : 0;
+    return norm_checks(n, T) == MOE_OK ? moe::norm_ws_bytes(n->H, T) : 0;
 }
 
 int moe_block_norm_backward(const moe_norm_desc* n, const void* r_out, int64_t ldr_out, const void* y, int64_t ldy,
@@ -728,7 +731,7 @@ int moe_block_norm_backward(const moe_norm_desc* n, const void* r_out, int64_t l
     } else if (shared_memory({dpost, dgate, dpre}, {post, gate, pre}, nullptr, nullptr)) {
         return fail(MOE_ERR_ARG, "an output is an input or another output");
     }
-    if ((e = check_ws(ws, ws_bytes, moe::norm_ws_bytes(n->H, n->gate, T)))) return e;
+    if ((e = check_ws(ws, ws_bytes, moe::norm_ws_bytes(n->H, T)))) return e;
     moe::NormArgs a = {};
     a.H = n->H; a.T = T; a.rt = n->r_dtype; a.yt = n->y_dtype; a.xt = n->x_dtype; a.gate_kind = n->gate;
     a.scale = n->scale; a.eps = n->eps;

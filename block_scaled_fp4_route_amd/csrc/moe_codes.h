@@ -12,6 +12,10 @@ namespace moe {
 
 constexpr uint32_t kInfBits = 0x7F800000u;
 
+__device__ __forceinline__ u4w ld_b128(rsrc_t r, uint32_t off) {
+    return __builtin_bit_cast(u4w, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
 // The E4M3 byte nearest to a / 6 (ties to even, at most 448), a >= 0 finite.
 __device__ __forceinline__ uint32_t e4m3_sixth(float a) {
     // near the result: a * fp32(1/6) is off by 2^-23 of a at most, so the byte

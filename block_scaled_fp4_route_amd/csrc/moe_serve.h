@@ -68,7 +68,7 @@ struct NormArgs {
     float *dpost, *dgate, *dpre;
     int accumulate;
 };
-size_t norm_ws_bytes(int H, int gate_kind, int T);
+size_t norm_ws_bytes(int H, int T);
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s);
 hipError_t launch_block_norm_backward(const NormArgs& a, void* ws, hipStream_t s);
 

@@ -189,9 +189,10 @@ int moe_layer_decode(const moe_desc *d, const float *x, const float *Wr, const v
 /* One layer for T tokens at once (sequences decoded side by side, a draft of
  * several tokens checked at once): for every token what moe_layer_decode
  * computes for one, in fp32 with fp32 accumulation; each chosen expert's block
- * is read once for all of its tokens. Results are bit-identical from run to
- * run, but not to moe_layer_decode's (the sums run in another order; the
- * chosen experts agree unless two logits differ by less than their rounding).
+ * is read for all of its tokens together. Results are bit-identical from run to
+ * run, but not to moe_layer_decode's, except for T = 1 without a mask, which
+ * runs its kernels (otherwise the sums run in another order; the chosen experts
+ * agree unless two logits differ by less than their rounding).
  *   x    [T][H] fp32, 16-B aligned;  Wr [E][H] fp32
  *   mask [T] uint8 or NULL: a token with mask[t] == 0 (an empty slot of a
  *        serving batch) is left out: its rows of y, idx_out and w_out stay as
@@ -488,8 +489,9 @@ typedef struct moe_fp4_desc {
 
 /* y[t] = base[t] + W x[t] with W [N][K] stored as moe_fp4_quant writes it:
  * W[n][k] = e2m1(code) * scale * 2^row_exp[n]. The activations keep all their
- * bits (fp32 ones down to 2^-133), products are exact, sums are in fp32, y is
- * rounded once. With round_x != 0 (MOE_FMT_MXFP4 only) the activations are
+ * bits (fp32 ones down to 2^-133), products are exact, sums are in fp32 (and
+ * take the row's power of two at their end, in moe_fp4_backward each product
+ * takes it), y is rounded once. With round_x != 0 (MOE_FMT_MXFP4 only) the activations are
  * first rounded to MXFP4 per 32 elements (MOE_SCALE_FLOOR) and multiplied as
  * codes on the FP4 matrix units. Results are bit-identical from run to run.
  *   x     [T] rows of K, stride ldx;  base (or NULL: zeros; may be y, with its
@@ -503,8 +505,8 @@ typedef struct moe_fp4_desc {
  * overlaps no input, but for base. Workspace:
  * moe_fp4_workspace_bytes(f, T, 0), which never falls as T grows. Errors:
  * MOE_ERR_ARG (K not a multiple of 32, N not of 8, pointers, strides, round_x
- * with NVFP4); MOE_ERR_UNSUPPORTED unless K, N <= 65536, T <= 2^20 and strides
- * <= 2^22; MOE_ERR_WORKSPACE. */
+ * with NVFP4); MOE_ERR_UNSUPPORTED unless K, N <= 65536, T <= 2^20, strides
+ * <= 2^22 and, with round_x, T * K <= 2^33; MOE_ERR_WORKSPACE. */
 size_t moe_fp4_workspace_bytes(const moe_fp4_desc *f, int32_t T, int32_t backward);
 int moe_fp4_apply(const moe_fp4_desc *f, const void *x, int64_t ldx, int32_t T, const uint8_t *codes,
                   const uint8_t *scales, const int8_t *row_exp, int32_t round_x, const void *base, int64_t ldbase,

@@ -79,6 +79,14 @@ def test_product_corner_arguments():
     assert m.moe_fp4_workspace_bytes(m.fp4_desc(48, 40, "nvfp4", BF16), 3, 0) == 0
 
 
+def test_rounded_product_of_too_many_activations():
+    """The quantisation counts its pieces in 32 bits: up to 2^33 elements."""
+    for K, want in ((8192, m.MOE_ERR_WORKSPACE), (8224, m.MOE_ERR_UNSUPPORTED), (65536, m.MOE_ERR_UNSUPPORTED)):
+        f = m.fp4_desc(K, 40, "mxfp4", BF16)
+        assert apply(f=f, ldx=65536, T=1 << 20, round_x=True, ws=None, wsb=0) == want
+        assert apply(f=f, ldx=65536, T=1 << 20, round_x=False, ws=None, wsb=0) == m.MOE_ERR_WORKSPACE
+
+
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
 @pytest.mark.parametrize("backward", [0, 1])
