@@ -20,6 +20,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "moe_codes.h"
 #include "moe_device.h"
 #include "moe_internal.h"
@@ -360,12 +362,12 @@ __device__ __forceinline__ void multiply(const u4w (&w)[4], const u4w (&x)[NG][4
 }
 
 // acc[m][i][g] += rows x columns over the whole blocks b0 .. b1 - 1 (TAIL: and
-// what lies behind them up to K): M matrices of two row blocks. The next
-// block's codes and, with one column group, its column values are on their way
-// while a block is multiplied (more groups: its own column values go out before
-// the next block's codes; loads come back in the order in which they went out,
-// and waiting for them must not wait for those).
-template <int FMT, bool AL, bool TAIL, int M, int NG>
+// what lies behind them up to K): M matrices of two row blocks. AHEAD 2: the
+// next block's codes and column values are on their way while a block is
+// multiplied. 1: its codes are (its own column values go out before the next
+// block's codes: loads come back in the order in which they went out, and
+// waiting for them must not wait for those). 0: nothing is, other waves are.
+template <int FMT, bool AL, bool TAIL, int M, int NG, int AHEAD>
 __device__ __forceinline__ void sums(rsrc_t const (&r)[M], uint32_t const (&codes)[M][2], uint32_t const (&scales)[M][2], rsrc_t rx,
                                      uint32_t const (&col)[NG], int ng, uint32_t K, int b0, int b1, f4v (&acc)[M][2][NG]) {
     const uint32_t lg = (threadIdx.x & 63) >> 4;
@@ -412,15 +414,24 @@ __device__ __forceinline__ void sums(rsrc_t const (&r)[M], uint32_t const (&code
             for (int i = 0; i < 2; i++) q1.w[m][i] = fetch_w<FMT, AL, false>(r[m], codes[m][i], scales[m][i], k, rest, K);
         fetch_x<NG, false>(rx, col, ng, k, rest, K, c1.x[0]);
         fetch_x<NG, false>(rx, c2, ng, k + 32, rest, K, c1.x[1]);
-        if (b0 < b1) fetch(b0, q0);
-        if (NG == 1 && b0 < b1) fetch_c(b0, c0);
+        if (AHEAD && b0 < b1) fetch(b0, q0);
+        if (AHEAD == 2 && b0 < b1) fetch_c(b0, c0);
         products(c1, q1);
-    } else if (b0 < b1) {
+    } else if (AHEAD && b0 < b1) {
         fetch(b0, q0);
-        if (NG == 1) fetch_c(b0, c0);
+        if (AHEAD == 2) fetch_c(b0, c0);
     }
     for (int b = b0; b < b1; b += 2) {
-        if constexpr (NG == 1) {
+        if constexpr (AHEAD == 0) {
+            fetch_c(b, c0);
+            fetch(b, q0);
+            products(c0, q0);
+            if (b + 1 < b1) {
+                fetch_c(b + 1, c0);
+                fetch(b + 1, q0);
+                products(c0, q0);
+            }
+        } else if constexpr (AHEAD == 2) {
             if (b + 1 < b1) {
                 fetch(b + 1, q1);
                 fetch_c(b + 1, c1);
@@ -485,7 +496,7 @@ __device__ __forceinline__ float token_sum(float v, int lane) {
 // ---------------------------------------------------------------------------
 // 3. gate/up: grid (row blocks of 32, items), four waves along the sum, whose
 // parts meet in LDS.
-template <int FMT, int NG>
+template <int FMT, int NG, int AHEAD>
 __global__ __launch_bounds__(256) void k_batch_gateup(BatchArgs a, const Item* __restrict__ items) {
     __shared__ f4v part[4][2][2][64];
     const Item* it = items + blockIdx.y;
@@ -521,7 +532,7 @@ __global__ __launch_bounds__(256) void k_batch_gateup(BatchArgs a, const Item* _
             }
 #pragma unroll
         for (int g = 0; g < NG; g++) cl[g] = col[g] == kOOB ? kOOB : col[g] + 128 * lg;
-        sums<FMT, true, false, 2, NG>(r, codes, scales, rx, cl, ng, H, b0, b1, acc);
+        sums<FMT, true, false, 2, NG, AHEAD>(r, codes, scales, rx, cl, ng, H, b0, b1, acc);
     } else {
         const rsrc_t r[2] = {make_rsrc(a.sg, 2 * n), make_rsrc(a.su, 2 * n)};
         const int row = r0 + (kind == kSharedHigh ? 16 : 0) + li;
@@ -598,7 +609,7 @@ __global__ __launch_bounds__(256) void k_batch_down(BatchArgs a, const Item* __r
         }
 #pragma unroll
         for (int g = 0; g < NG; g++) cl[g] = col[g] == kOOB ? kOOB : col[g] + 128 * lg;
-        sums<FMT, AL, true, 1, NG>(r, codes, scales, rx, cl, ng, I, 0, a.I / 256, acc);
+        sums<FMT, AL, true, 1, NG, NG == 1 ? 2 : 1>(r, codes, scales, rx, cl, ng, I, 0, a.I / 256, acc);
     } else {
         const rsrc_t r[1] = {make_rsrc(a.sd, 2 * n)};
         f4v one[1][NG];
@@ -649,8 +660,18 @@ template <int NG>
 hipError_t experts(int fmt, const BatchArgs& a, hipStream_t s) {
     const dim3 gu((a.I + 31) / 32, a.items_n), down(a.H / 128, a.items_n), block(256);
     const Item* items = a.items;
-    if (fmt == kFmtNvfp4) hipLaunchKernelGGL((k_batch_gateup<kFmtNvfp4, NG>), gu, block, 0, s, a, items);
-    else hipLaunchKernelGGL((k_batch_gateup<kFmtMxfp4, NG>), gu, block, 0, s, a, items);
+    // With more workgroups than two rounds of the chip (two a compute unit, of
+    // 195 registers a thread) four a compute unit without a block ahead: 48 tokens
+    // 163 -> 151 us, while 4 tokens with 800 workgroups take 30 and 32.
+    const bool crowd = (size_t)gu.x * gu.y > 1024;
+    auto gateup = [&](auto F) {
+        constexpr int FMT = decltype(F)::value;
+        if constexpr (NG > 1) hipLaunchKernelGGL((k_batch_gateup<FMT, NG, 1>), gu, block, 0, s, a, items);
+        else if (crowd) hipLaunchKernelGGL((k_batch_gateup<FMT, NG, 0>), gu, block, 0, s, a, items);
+        else hipLaunchKernelGGL((k_batch_gateup<FMT, NG, 2>), gu, block, 0, s, a, items);
+    };
+    if (fmt == kFmtNvfp4) gateup(std::integral_constant<int, kFmtNvfp4>{});
+    else gateup(std::integral_constant<int, kFmtMxfp4>{});
     const hipError_t r = hipGetLastError();
     if (r != hipSuccess) return r;
     const bool al = a.I % 64 == 0;
