@@ -362,12 +362,11 @@ __device__ __forceinline__ void multiply(const u4w (&w)[4], const u4w (&x)[NG][4
 }
 
 // acc[m][i][g] += rows x columns over the whole blocks b0 .. b1 - 1 (TAIL: and
-// what lies behind them up to K): M matrices of two row blocks. AHEAD 2: the
-// next block's codes and column values are on their way while a block is
-// multiplied. 1: its codes are (its own column values go out before the next
-// block's codes: loads come back in the order in which they went out, and
-// waiting for them must not wait for those). 0: nothing is, other waves are.
-template <int FMT, bool AL, bool TAIL, int M, int NG, int AHEAD>
+// what lies behind them up to K): M matrices of two row blocks. AHEAD: the next
+// block's codes and column values are on their way while a block is multiplied;
+// without it a block's column values go out before its codes, and other waves'
+// loads are on their way.
+template <int FMT, bool AL, bool TAIL, int M, int NG, bool AHEAD>
 __device__ __forceinline__ void sums(rsrc_t const (&r)[M], uint32_t const (&codes)[M][2], uint32_t const (&scales)[M][2], rsrc_t rx,
                                      uint32_t const (&col)[NG], int ng, uint32_t K, int b0, int b1, f4v (&acc)[M][2][NG]) {
     const uint32_t lg = (threadIdx.x & 63) >> 4;
@@ -415,14 +414,14 @@ __device__ __forceinline__ void sums(rsrc_t const (&r)[M], uint32_t const (&code
         fetch_x<NG, false>(rx, col, ng, k, rest, K, c1.x[0]);
         fetch_x<NG, false>(rx, c2, ng, k + 32, rest, K, c1.x[1]);
         if (AHEAD && b0 < b1) fetch(b0, q0);
-        if (AHEAD == 2 && b0 < b1) fetch_c(b0, c0);
+        if (AHEAD && b0 < b1) fetch_c(b0, c0);
         products(c1, q1);
     } else if (AHEAD && b0 < b1) {
         fetch(b0, q0);
-        if (AHEAD == 2) fetch_c(b0, c0);
+        if (AHEAD) fetch_c(b0, c0);
     }
     for (int b = b0; b < b1; b += 2) {
-        if constexpr (AHEAD == 0) {
+        if constexpr (!AHEAD) {
             fetch_c(b, c0);
             fetch(b, q0);
             products(c0, q0);
@@ -431,7 +430,7 @@ __device__ __forceinline__ void sums(rsrc_t const (&r)[M], uint32_t const (&code
                 fetch(b + 1, q0);
                 products(c0, q0);
             }
-        } else if constexpr (AHEAD == 2) {
+        } else {
             if (b + 1 < b1) {
                 fetch(b + 1, q1);
                 fetch_c(b + 1, c1);
@@ -442,15 +441,6 @@ __device__ __forceinline__ void sums(rsrc_t const (&r)[M], uint32_t const (&code
                 fetch_c(b + 2, c0);
             }
             if (b + 1 < b1) products(c1, q1);
-        } else {
-            fetch_c(b, c0);
-            if (b + 1 < b1) fetch(b + 1, q1);
-            products(c0, q0);
-            if (b + 1 < b1) {
-                fetch_c(b + 1, c0);
-                if (b + 2 < b1) fetch(b + 2, q0);
-                products(c0, q1);
-            }
         }
     }
 }
@@ -496,7 +486,7 @@ __device__ __forceinline__ float token_sum(float v, int lane) {
 // ---------------------------------------------------------------------------
 // 3. gate/up: grid (row blocks of 32, items), four waves along the sum, whose
 // parts meet in LDS.
-template <int FMT, int NG, int AHEAD>
+template <int FMT, int NG, bool AHEAD>
 __global__ __launch_bounds__(256) void k_batch_gateup(BatchArgs a, const Item* __restrict__ items) {
     __shared__ f4v part[4][2][2][64];
     const Item* it = items + blockIdx.y;
@@ -609,7 +599,7 @@ __global__ __launch_bounds__(256) void k_batch_down(BatchArgs a, const Item* __r
         }
 #pragma unroll
         for (int g = 0; g < NG; g++) cl[g] = col[g] == kOOB ? kOOB : col[g] + 128 * lg;
-        sums<FMT, AL, true, 1, NG, NG == 1 ? 2 : 1>(r, codes, scales, rx, cl, ng, I, 0, a.I / 256, acc);
+        sums<FMT, AL, true, 1, NG, NG == 1>(r, codes, scales, rx, cl, ng, I, 0, a.I / 256, acc);
     } else {
         const rsrc_t r[1] = {make_rsrc(a.sd, 2 * n)};
         f4v one[1][NG];
@@ -662,13 +652,18 @@ hipError_t experts(int fmt, const BatchArgs& a, hipStream_t s) {
     const Item* items = a.items;
     // With more workgroups than two rounds of the chip (two a compute unit, of
     // 195 registers a thread) four a compute unit without a block ahead: 48 tokens
-    // 163 -> 151 us, while 4 tokens with 800 workgroups take 30 and 32.
+    // 163 -> 151 us, while 4 tokens with 800 workgroups take 30 and 32. Three
+    // column groups never look ahead: one workgroup a compute unit then (64 tokens
+    // of 8 out of 128 experts of 2560 x 640: 117 us, without 81).
     const bool crowd = (size_t)gu.x * gu.y > 1024;
     auto gateup = [&](auto F) {
         constexpr int FMT = decltype(F)::value;
-        if constexpr (NG > 1) hipLaunchKernelGGL((k_batch_gateup<FMT, NG, 1>), gu, block, 0, s, a, items);
-        else if (crowd) hipLaunchKernelGGL((k_batch_gateup<FMT, NG, 0>), gu, block, 0, s, a, items);
-        else hipLaunchKernelGGL((k_batch_gateup<FMT, NG, 2>), gu, block, 0, s, a, items);
+        if constexpr (NG == 1)
+            if (!crowd) {
+                hipLaunchKernelGGL((k_batch_gateup<FMT, NG, true>), gu, block, 0, s, a, items);
+                return;
+            }
+        hipLaunchKernelGGL((k_batch_gateup<FMT, NG, false>), gu, block, 0, s, a, items);
     };
     if (fmt == kFmtNvfp4) gateup(std::integral_constant<int, kFmtNvfp4>{});
     else gateup(std::integral_constant<int, kFmtMxfp4>{});
