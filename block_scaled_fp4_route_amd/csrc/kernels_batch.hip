@@ -17,6 +17,13 @@
 //  5. combine: the weighted sum over a token's assignments, in their order.
 // An expert with more tokens than an item holds (5 or 15) is read again from the
 // caches.
+//
+// 13 tokens of 6 out of 384 MXFP4 experts of 4096 x 2880 (1.35 GB): gate/up and
+// down 304 us, 4.4 TB/s. 48 tokens of 10 out of 512 NVFP4 ones of 2560 x 640 (0.82
+// GB): 227 us, 3.6 TB/s (fp16 decoding, half the instructions, gained 2%: not the
+// arithmetic). 4 tokens: 44 of 61 us, 800 and 800 workgroups that each read for two or
+// three blocks of the sum, so that their start and end count; the other three
+// launches are chains of dependent loads.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -9,6 +9,13 @@
 // where W is fp16; fp32: 3), and one 16-bit product over P K runs on the
 // matrix units. Activations rounded to MXFP4 beside an MXFP4 matrix: both go
 // to the scaled FP4 matrix instructions as codes, never widened.
+//
+// Large products are bound by the matrix units: 8192 x 8192 x 2560 in bf16 291 us
+// beside 15 for the join and 16 for W (1.18 PFLOP/s without those). As codes 113
+// us (3.0 PFLOP/s), 35% of the matrix rate: steps of 256 codes take 2 us where the
+// products alone would take 0.85; neither bank conflicts (none) nor a longer ring
+// changed it. Products of few tiles are bound by their steps' latency: 311 tokens of
+// 640 x 2560 fp32 14 us for 30 steps.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

