@@ -460,14 +460,17 @@ __global__ __launch_bounds__(256) void k_fp4_join(MmArgs g) {
 
 constexpr int kCus = 256;                       // workgroups of a round of the large tiles
 constexpr int kLargeFrom = 192;                 // tiles of a size that is worth it
-constexpr int kSmallGroups = 512;               // workgroups of the small tiles, where the sum is split
+constexpr int kMiddleFrom = 48, kMiddleSteps = 64;  // tiles and steps from which 128 x 128 tiles have their sums split
+constexpr int kSmallGroups = 512;               // workgroups of the smaller tiles, where the sum is split
 constexpr int kMaxSplit = 8, kMaxSmallSplit = 16;
 // Bytes of parts that a product may leave: one round of large tiles, or all the
-// small ones. Neither falls as M grows.
+// smaller ones. None falls as M grows.
 size_t part_bytes(int M, int N) {
-    const size_t large = (size_t)((M + 255) / 256) * ((N + 255) / 256), small = (size_t)((M + 63) / 64) * ((N + 63) / 64) * kMaxSmallSplit;
-    const size_t a = large >= kLargeFrom ? (size_t)kCus * 256 * 256 * 4 : 0, b = (small < kSmallGroups ? small : kSmallGroups) * 64 * 64 * 4;
-    return a > b ? a : b;
+    auto tiles = [&](size_t b) { return ((size_t)M + b - 1) / b * ((N + b - 1) / b); };
+    if (tiles(256) >= kLargeFrom) return (size_t)kCus * 256 * 256 * 4;
+    if (tiles(128) >= kMiddleFrom) return (size_t)kSmallGroups * 128 * 128 * 4;
+    const size_t small = tiles(64) * kMaxSmallSplit;
+    return (small < kSmallGroups ? small : kSmallGroups) * 64 * 64 * 4;
 }
 
 template <int KIND, int DT>
@@ -502,6 +505,16 @@ hipError_t mm_tiles(MmArgs& g, hipStream_t s) {
         hipLaunchKernelGGL((k_fp4_join<DT, 256>), dim3(parts * (256 * 256 / 8 / 256)), dim3(256), 0, s, g);
     } else if (tiles(128, 128) >= kLargeFrom) {
         hipLaunchKernelGGL((k_fp4_mm<KIND, DT, 128, 128, 2, 2, 2>), dim3(g.full), dim3(256), 0, s, g);
+    } else if (const int big = tiles(128, 128); big >= kMiddleFrom && g.wide >= 128 * kMiddleSteps) {
+        // long sums: the operands are read half as often as by 64 x 64 tiles, which
+        // is worth the larger parts (300 tokens of 8192 x 2560 back to the input,
+        // fp32: 122 us in 64 x 64 tiles, 75 so; 1000 of 2560 x 2048 bf16, 40
+        // steps: 30 and 34)
+        const int split = kSmallGroups / big;
+        parts = cut(big, split, 20);
+        hipLaunchKernelGGL((k_fp4_mm<KIND, DT, 128, 128, 2, 2, 2>), dim3(g.full + parts * g.split), dim3(256), 0, s, g);
+        if ((r = hipGetLastError()) != hipSuccess || !parts) return r;
+        hipLaunchKernelGGL((k_fp4_join<DT, 128>), dim3(parts * (128 * 128 / 8 / 256)), dim3(256), 0, s, g);
     } else {
         const int all = tiles(64, 64), split = kSmallGroups / all;
         parts = cut(all, split < kMaxSmallSplit ? split : kMaxSmallSplit, 20);

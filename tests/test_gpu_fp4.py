@@ -237,7 +237,10 @@ def test_product_long(m, T, K, N, fmt, dt, rnd, back):
     (1, 256, 4104, "mxfp4", "bf16", False, True),
     (130, 5600, 72, "mxfp4", "f16", False, False),    # six tiles, a sum that ends within a step
     (200, 12320, 136, "mxfp4", "bf16", True, False),
-    (257, 3200, 200, "nvfp4", "f32", False, False)])
+    (257, 3200, 200, "nvfp4", "f32", False, False),
+    (700, 4160, 1032, "nvfp4", "f32", False, False),  # 54 tiles of 128 x 128, nine parts each
+    (700, 1056, 4104, "mxfp4", "bf16", False, True),
+    (800, 16416, 1000, "mxfp4", "bf16", True, False)])
 def test_product_split_sums(m, T, K, N, fmt, dt, rnd, back):
     check_product(m, T, K, N, fmt, dt, rnd, back)
 
