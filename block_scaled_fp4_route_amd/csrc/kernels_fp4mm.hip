@@ -128,15 +128,24 @@ __global__ __launch_bounds__(256) void k_fp4_parts(const char* __restrict__ x, s
 // bytes are one word). Blocks behind the row's end are 0.
 __host__ __device__ constexpr size_t tile_rows(size_t rows) { return (rows + 255) / 256 * 256; }
 __device__ __forceinline__ int scale_place(int b) { return (b & 1) * 4 + (b >> 1 & 3); }
-__global__ __launch_bounds__(256) void k_fp4_scale_panel(const uint8_t* __restrict__ scales, int rows, int nb,
-                                                         uint8_t* __restrict__ out) {
-    const int r = blockIdx.x * 256 + threadIdx.x, st = blockIdx.y;
+struct Panel {
+    const uint8_t* scales;
+    int rows;
+    uint8_t* out;
+};
+// The first `split` workgroups along x make a's panel, the others b's.
+__global__ __launch_bounds__(256) void k_fp4_scale_panels(Panel a, Panel b, int split, int nb) {
+    const bool first = (int)blockIdx.x < split;
+    const uint8_t* __restrict__ scales = first ? a.scales : b.scales;
+    uint8_t* __restrict__ out = first ? a.out : b.out;
+    const int rows = first ? a.rows : b.rows;
+    const int r = ((int)blockIdx.x - (first ? 0 : split)) * 256 + threadIdx.x, st = blockIdx.y;
     if (r >= rows) return;
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-        const int b = 8 * st + j;
-        if (b < nb) w[scale_place(j) / 4] |= (uint32_t)scales[(size_t)r * nb + b] << (8 * (scale_place(j) % 4));
+        const int k = 8 * st + j;
+        if (k < nb) w[scale_place(j) / 4] |= (uint32_t)scales[(size_t)r * nb + k] << (8 * (scale_place(j) % 4));
     }
     *reinterpret_cast<uint2*>(out + (st * tile_rows(rows) + r) * 8) = make_uint2(w[0], w[1]);
 }
@@ -590,9 +599,9 @@ hipError_t launch_fp4_apply(int K, int N, int fmt, int dtype, const void* x, siz
         r = launch_fp4_quant(dtype, kFmtMxfp4, kScaleFloor, x, ldx, T, K, nullptr, codes, scales, nullptr, 0, s);
         if (r != hipSuccess) return r;
         if (T <= kFewMaxT) return launch_fp4_few(K, N, fmt, dtype, codes, K / 2, scales, T, w, base, ldbase, y, ldy, s);
-        hipLaunchKernelGGL(k_fp4_scale_panel, dim3((T + 255) / 256, steps), dim3(256), 0, s, scales, T, K / 32, sa);
-        if ((r = hipGetLastError()) != hipSuccess) return r;
-        hipLaunchKernelGGL(k_fp4_scale_panel, dim3((N + 255) / 256, steps), dim3(256), 0, s, w.scales, N, K / 32, sb);
+        const int split = (T + 255) / 256;
+        hipLaunchKernelGGL(k_fp4_scale_panels, dim3(split + (N + 255) / 256, steps), dim3(256), 0, s, Panel{scales, T, sa},
+                           Panel{w.scales, N, sb}, split, K / 32);
         if ((r = hipGetLastError()) != hipSuccess) return r;
         g.a = reinterpret_cast<const char*>(codes);
         g.b = reinterpret_cast<const char*>(w.codes);
