@@ -74,7 +74,7 @@ __device__ __forceinline__ void stage(const FewArgs& a, int k0, f4v (*lds)[2][kG
                 top = max(top, (uint32_t)__shfl_xor((int)top, 2, 64));
                 const int X = mx_exponent(top, false);
                 float q[8];
-                codes8(v, exp2i(-X), 1.0f, q);
+                codes8(v, exp2i(-X), q);
                 const float s = X == -127 ? __uint_as_float(0x00400000u) : exp2i(X);
 #pragma unroll
                 for (int j = 0; j < 8; j++) v[j] = top >= kInfBits ? __uint_as_float(0x7FC00000u) : q[j] * s;

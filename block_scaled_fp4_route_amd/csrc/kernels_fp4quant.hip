@@ -7,7 +7,8 @@
 // magnitude. A magnitude m goes to code c where the borders between codes
 // (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5) times the scale s lie on the right
 // sides of m: a border has at most 3 significant bits, an E4M3 scale 4, so
-// the product is exact in fp32 and so is m times a power of two. The E4M3
+// the product is exact in fp32 and so is m times a power of two (MXFP4's scale
+// is one: the conversion instruction does the rest). The E4M3
 // scale nearest to amax / 6 is found the same way: 6 times the border between
 // two E4M3 values has 7 bits. The result is therefore the definition's, bit
 // for bit, with no case that a rounded quotient would decide.
@@ -65,7 +66,9 @@ __device__ __forceinline__ void quant_piece(const QuantArgs& a, uint32_t row, ui
         back = ue8m0_to_f32(byte);
     }
     float q[8];
-    uint32_t w = codes8(v, p, s, q);
+    uint32_t w;
+    if constexpr (FMT == kFmtNvfp4) w = codes8(v, p, s, q);
+    else w = codes8(v, p, q);
     if (bad || (FMT == kFmtNvfp4 && byte == 0u)) {  // all codes zero (under a scale of 0, every border is 0)
         w = 0;
 #pragma unroll

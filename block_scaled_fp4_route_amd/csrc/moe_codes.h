@@ -49,6 +49,21 @@ __device__ __forceinline__ uint32_t codes8(const float (&v)[8], float p, float s
     return w;
 }
 
+// The same for s = 1: times p, which is exact, the conversion instruction rounds
+// as the definition does (nearest, ties to the even code, above 6 to 6, the sign
+// kept), at a third of the comparisons' instructions.
+__device__ __forceinline__ uint32_t codes8(const float (&v)[8], float p, float (&q)[8]) {
+    uint32_t w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0] * p, v[1] * p, 1.0f, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2] * p, v[3] * p, 1.0f, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4] * p, v[5] * p, 1.0f, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6] * p, v[7] * p, 1.0f, 3);
+    const f2v d0 = fp4x2<0>(w), d1 = fp4x2<1>(w), d2 = fp4x2<2>(w), d3 = fp4x2<3>(w);
+    q[0] = d0.x; q[1] = d0.y; q[2] = d1.x; q[3] = d1.y;
+    q[4] = d2.x; q[5] = d2.y; q[6] = d3.x; q[7] = d3.y;
+    return w;
+}
+
 __device__ __forceinline__ uint32_t max_mag(const float (&v)[8]) {
     uint32_t m = 0;
 #pragma unroll

@@ -104,6 +104,22 @@ def test_quant_borders_and_extremes(m, fmt, rule, rows, dt):
 
 @pytest.mark.parametrize("dt", sorted(DT))
 @pytest.mark.parametrize("fmt,rule,rows", KINDS)
+def test_quant_random_bits(m, fmt, rule, rows, dt):
+    """Any bit patterns; then blocks of every exponent whose values lie within 2^7 of one another, with few significant
+    bits (many ties)."""
+    t = DT[dt]
+    g = torch.Generator().manual_seed(8)
+    bits = torch.int32 if t == torch.float32 else torch.int16
+    x = torch.randint(torch.iinfo(bits).min, torch.iinfo(bits).max, (300, 128), dtype=torch.int64, generator=g).to(bits).view(t)
+    check_quant(m, x.cuda(), fmt, rule, rows)
+    lo, hi = {"f32": (-149, 127), "bf16": (-133, 127), "f16": (-24, 15)}[dt]
+    e = torch.arange(lo, hi - 2).repeat_interleave(4)[:, None] + torch.randint(-5, 3, (4 * (hi - 2 - lo), 128), generator=g)
+    x = torch.randint(-15, 16, e.shape, generator=g).double() / 8 * torch.exp2(e.double())
+    check_quant(m, x.to(t).cuda(), fmt, rule, rows)
+
+
+@pytest.mark.parametrize("dt", sorted(DT))
+@pytest.mark.parametrize("fmt,rule,rows", KINDS)
 def test_quant_strides_and_in_place(m, fmt, rule, rows, dt):
     x = torch.randn((9, 640), device="cuda").to(DT[dt])
     keep = x.clone()
