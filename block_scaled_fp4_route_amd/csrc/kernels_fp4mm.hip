@@ -52,23 +52,22 @@ __device__ __forceinline__ void decode8(uint32_t w, float s, float (&v)[8]) {
     v[4] = d2.x * s; v[5] = d2.y * s; v[6] = d3.x * s; v[7] = d3.y * s;
 }
 
-// W as 16-bit values [N][K] (row exponents left out).
+// W as 16-bit values [N][K] (row exponents left out), 256 pieces of 8 a workgroup.
 template <int FMT, int KIND>
-__global__ __launch_bounds__(256) void k_fp4_widen(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                                                   size_t pieces, u4w* __restrict__ out) {
-    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= pieces) return;
+__device__ __forceinline__ void widen(const Fp4Matrix& w, int K, int N, uint32_t b, u4w* __restrict__ out) {
+    const size_t i = (size_t)b * 256 + threadIdx.x;
+    if (i >= (size_t)N * (K / 8)) return;
     float v[8];
-    decode8(codes[i], scale_to_f32<FMT>(scales[i / (Fmt<FMT>::G / 8)]), v);
+    decode8(reinterpret_cast<const uint32_t*>(w.codes)[i], scale_to_f32<FMT>(w.scales[i / (Fmt<FMT>::G / 8)]), v);
     out[i] = KIND == kF16 ? pack8<kActF16>(v).w[0] : pack8<kActBf16>(v).w[0];
 }
 
 // W^T as bf16 [K][N], row exponents included. A workgroup turns 64 rows x 64
 // columns in LDS.
 template <int FMT>
-__global__ __launch_bounds__(256) void k_fp4_widen_t(Fp4Matrix w, int K, int N, uint16_t* __restrict__ out) {
+__device__ __forceinline__ void widen_t(const Fp4Matrix& w, int K, int N, uint32_t b, uint16_t* __restrict__ out) {
     __shared__ uint16_t t[64][72];  // [k][n]; 144-byte rows
-    const int n0 = blockIdx.x * 64, k0 = blockIdx.y * 64, tid = threadIdx.x;
+    const int nt = (N + 63) / 64, n0 = (int)(b % nt) * 64, k0 = (int)(b / nt) * 64, tid = threadIdx.x;
 #pragma unroll
     for (int q = 0; q < 2; q++) {  // 64 rows of 8 pieces
         const int r = (tid >> 3) + 32 * q, c = tid & 7, n = n0 + r, k = k0 + 8 * c;
@@ -101,25 +100,50 @@ __device__ __forceinline__ uint32_t bf16_cut(float v) { return v != v ? 0x7FC0u 
 // x [T][K] as P bf16 parts [T][P][K], cut, not rounded (no part overflows, and
 // three hold 24 bits down to 2^-133). The parts behind an infinity or a NaN
 // are 0.
+struct Acts {
+    const char* x;
+    size_t ldx;  // bytes
+    int T, K;
+    u4w* out;
+};
 template <int DT>
-__global__ __launch_bounds__(256) void k_fp4_parts(const char* __restrict__ x, size_t ldx, size_t pieces, int k8,
-                                                   u4w* __restrict__ out) {
+__device__ __forceinline__ void parts(const Acts& x, uint32_t b, uint32_t groups) {
     constexpr int P = DT == kActF32 ? 3 : 2;
-    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= pieces) return;
-    const size_t t = i / (uint32_t)k8, c = i - t * k8;
-    float v[8];
-    unpack8<DT>(load8<DT>(x + t * ldx, 8 * c), v);
+    const uint32_t k8 = (uint32_t)x.K / 8;
+    const size_t pieces = (size_t)x.T * k8;
+    for (size_t i = (size_t)b * 256 + threadIdx.x; i < pieces; i += (size_t)groups * 256) {
+        const size_t t = i / k8, c = i - t * k8;
+        float v[8];
+        unpack8<DT>(load8<DT>(x.x + t * x.ldx, 8 * c), v);
 #pragma unroll
-    for (int p = 0; p < P; p++) {
-        uint32_t h[8];
+        for (int p = 0; p < P; p++) {
+            uint32_t h[8];
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            h[j] = bf16_cut(v[j]);
-            v[j] = fabsf(v[j]) < INFINITY ? v[j] - __uint_as_float(h[j] << 16) : 0.0f;
+            for (int j = 0; j < 8; j++) {
+                h[j] = bf16_cut(v[j]);
+                v[j] = fabsf(v[j]) < INFINITY ? v[j] - __uint_as_float(h[j] << 16) : 0.0f;
+            }
+            x.out[(t * P + p) * k8 + c] = u4w{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
         }
-        out[(t * P + p) * k8 + c] = u4w{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
     }
+}
+
+// Both operands in one launch (the second would cost 3 us): the first nw
+// workgroups take W, the others the activations, where those need parts (DT; -1:
+// not). TURN: W^T.
+constexpr int kNoParts = -1;
+template <int FMT, int KIND, bool TURN, int DT>
+__global__ __launch_bounds__(256) void k_fp4_operands(Fp4Matrix w, int K, int N, uint32_t nw, char* out, Acts x) {
+    if (blockIdx.x < nw) {
+        if constexpr (TURN) widen_t<FMT>(w, K, N, blockIdx.x, reinterpret_cast<uint16_t*>(out));
+        else widen<FMT, KIND>(w, K, N, blockIdx.x, reinterpret_cast<u4w*>(out));
+    } else if constexpr (DT != kNoParts) {
+        parts<DT>(x, blockIdx.x - nw, gridDim.x - nw);
+    }
+}
+template <int DT>
+__global__ __launch_bounds__(256) void k_fp4_parts(Acts x) {
+    parts<DT>(x, blockIdx.x, gridDim.x);
 }
 
 // Scale bytes for the scaled product: [K / 256 steps][rows up to a whole
@@ -540,24 +564,25 @@ hipError_t mm(int dtype, MmArgs& g, hipStream_t s) {
 }
 
 // A's operand of a 16-bit product over K: the activations themselves, or their
-// parts in the workspace.
-hipError_t activations(int dtype, int P, const void* x, size_t ldx, int T, int K, char* parts, MmArgs& g, hipStream_t s) {
-    const size_t es = dtype == kActF32 ? 4 : 2, pieces = (size_t)T * (K / 8);
+// parts in the workspace, which are still to be made (workgroups for them; 0: none).
+uint32_t activations(int dtype, int P, const void* x, size_t ldx, int T, int K, char* at, MmArgs& g, Acts& acts) {
+    const size_t es = dtype == kActF32 ? 4 : 2, groups = ((size_t)T * (K / 8) + 255) / 256;
+    acts = {static_cast<const char*>(x), ldx * es, T, K, reinterpret_cast<u4w*>(at)};
     g.wa = (uint32_t)P * K * 2u;
-    if (P == 1) {
-        g.a = static_cast<const char*>(x);
-        g.lda = ldx * es;
-        return hipSuccess;
-    }
-    const dim3 grid((unsigned)((pieces + 255) / 256));
-    if (dtype == kActF32)
-        hipLaunchKernelGGL(k_fp4_parts<kActF32>, grid, dim3(256), 0, s, static_cast<const char*>(x), ldx * es, pieces, K / 8,
-                           reinterpret_cast<u4w*>(parts));
-    else
-        hipLaunchKernelGGL(k_fp4_parts<kActF16>, grid, dim3(256), 0, s, static_cast<const char*>(x), ldx * es, pieces, K / 8,
-                           reinterpret_cast<u4w*>(parts));
-    g.a = parts;
-    g.lda = g.wa;
+    g.a = P == 1 ? acts.x : at;
+    g.lda = P == 1 ? acts.ldx : g.wa;
+    return P == 1 ? 0 : (uint32_t)(groups < (1u << 22) ? groups : 1u << 22);
+}
+
+// W (TURN: W^T) widened to `out`, and the activations' parts.
+template <int FMT, int KIND, bool TURN>
+hipError_t operands(const Fp4Matrix& w, int K, int N, char* out, int dtype, uint32_t na, const Acts& acts, hipStream_t s) {
+    const uint32_t nw = TURN ? (uint32_t)((N + 63) / 64) * ((K + 63) / 64) : (uint32_t)(((size_t)N * (K / 8) + 255) / 256);
+    const dim3 grid(nw + na), block(256);
+    if (!na) hipLaunchKernelGGL((k_fp4_operands<FMT, KIND, TURN, kNoParts>), grid, block, 0, s, w, K, N, nw, out, acts);
+    else if (dtype == kActF32) hipLaunchKernelGGL((k_fp4_operands<FMT, KIND, TURN, kActF32>), grid, block, 0, s, w, K, N, nw, out, acts);
+    else if constexpr (KIND == kBf16 && (TURN || FMT == kFmtMxfp4))
+        hipLaunchKernelGGL((k_fp4_operands<FMT, KIND, TURN, kActF16>), grid, block, 0, s, w, K, N, nw, out, acts);
     return hipGetLastError();
 }
 
@@ -612,19 +637,20 @@ hipError_t launch_fp4_apply(int K, int N, int fmt, int dtype, const void* x, siz
         return mm<kFp4>(dtype, g, s);
     }
     const int kind = act_kind(fmt, dtype, false), P = act_parts(dtype, kind);
-    if ((r = activations(dtype, P, x, ldx, T, K, p + align256((size_t)K * N * 2), g, s)) != hipSuccess) return r;
-    if (T <= kFewMaxT) return launch_fp4_few(K, N, fmt, dtype, g.a, g.lda, nullptr, T, w, base, ldbase, y, ldy, s);
-    const size_t pieces = (size_t)N * (K / 8);
-    const dim3 grid((unsigned)((pieces + 255) / 256));
-    const uint32_t* codes = reinterpret_cast<const uint32_t*>(w.codes);
-    u4w* wide = reinterpret_cast<u4w*>(p);
-    if (kind == kF16)
-        hipLaunchKernelGGL((k_fp4_widen<kFmtNvfp4, kF16>), grid, dim3(256), 0, s, codes, w.scales, pieces, wide);
-    else if (fmt == kFmtNvfp4)
-        hipLaunchKernelGGL((k_fp4_widen<kFmtNvfp4, kBf16>), grid, dim3(256), 0, s, codes, w.scales, pieces, wide);
-    else
-        hipLaunchKernelGGL((k_fp4_widen<kFmtMxfp4, kBf16>), grid, dim3(256), 0, s, codes, w.scales, pieces, wide);
-    if ((r = hipGetLastError()) != hipSuccess) return r;
+    Acts acts;
+    const uint32_t na = activations(dtype, P, x, ldx, T, K, p + align256((size_t)K * N * 2), g, acts);
+    if (T <= kFewMaxT) {
+        if (na) {
+            if (dtype == kActF32) hipLaunchKernelGGL(k_fp4_parts<kActF32>, dim3(na), dim3(256), 0, s, acts);
+            else hipLaunchKernelGGL(k_fp4_parts<kActF16>, dim3(na), dim3(256), 0, s, acts);
+            if ((r = hipGetLastError()) != hipSuccess) return r;
+        }
+        return launch_fp4_few(K, N, fmt, dtype, g.a, g.lda, nullptr, T, w, base, ldbase, y, ldy, s);
+    }
+    if (kind == kF16) r = operands<kFmtNvfp4, kF16, false>(w, K, N, p, dtype, na, acts, s);
+    else if (fmt == kFmtNvfp4) r = operands<kFmtNvfp4, kBf16, false>(w, K, N, p, dtype, na, acts, s);
+    else r = operands<kFmtMxfp4, kBf16, false>(w, K, N, p, dtype, na, acts, s);
+    if (r != hipSuccess) return r;
     g.b = p;
     g.ldb = g.wb = (uint32_t)K * 2;
     g.wide = (int)g.wa;
@@ -645,15 +671,11 @@ hipError_t launch_fp4_backward(int K, int N, int fmt, int dtype, const void* dy,
     g.y = static_cast<char*>(dx);
     g.ldbase = lddxb * es;
     g.ldy = lddx * es;
-    const dim3 grid((N + 63) / 64, (K + 63) / 64);
-    if (fmt == kFmtNvfp4)
-        hipLaunchKernelGGL(k_fp4_widen_t<kFmtNvfp4>, grid, dim3(256), 0, s, w, K, N, reinterpret_cast<uint16_t*>(p));
-    else
-        hipLaunchKernelGGL(k_fp4_widen_t<kFmtMxfp4>, grid, dim3(256), 0, s, w, K, N, reinterpret_cast<uint16_t*>(p));
-    hipError_t r = hipGetLastError();
+    Acts acts;
+    const uint32_t na = activations(dtype, act_parts(dtype, kBf16), dy, lddy, T, N, p + align256((size_t)K * N * 2), g, acts);
+    const hipError_t r = fmt == kFmtNvfp4 ? operands<kFmtNvfp4, kBf16, true>(w, K, N, p, dtype, na, acts, s)
+                                          : operands<kFmtMxfp4, kBf16, true>(w, K, N, p, dtype, na, acts, s);
     if (r != hipSuccess) return r;
-    const int P = act_parts(dtype, kBf16);
-    if ((r = activations(dtype, P, dy, lddy, T, N, p + align256((size_t)K * N * 2), g, s)) != hipSuccess) return r;
     g.b = p;
     g.ldb = g.wb = (uint32_t)N * 2;
     g.wide = (int)g.wa;
