@@ -105,6 +105,7 @@ __global__ __launch_bounds__(256) void k_fp4_quant(QuantArgs a) {
 // 256: one). The first kHeld pieces of a lane stay in registers, further ones
 // are read again (longer rows: out of the cache).
 constexpr int kHeld = 4;
+constexpr uint32_t kRowsAtOnce = 1u << 25;
 template <int DT, int NT>
 __global__ __launch_bounds__(256) void k_fp4_quant_rows(QuantArgs a) {
     __shared__ uint32_t tops[4];
@@ -157,11 +158,23 @@ __global__ __launch_bounds__(256) void k_fp4_quant_rows(QuantArgs a) {
 
 template <int DT>
 hipError_t quant(int fmt, const QuantArgs& a, hipStream_t s) {
-    if (a.row_exp) {
-        if (a.c8 <= 64 * kHeld)
-            hipLaunchKernelGGL((k_fp4_quant_rows<DT, 64>), dim3((a.rows + 3) / 4), dim3(256), 0, s, a);
-        else
-            hipLaunchKernelGGL((k_fp4_quant_rows<DT, 256>), dim3(a.rows), dim3(256), 0, s, a);
+    if (a.row_exp && a.c8 <= 64 * kHeld) {
+        // a launch has less than 2^32 threads: 64 a row, so more rows than kRowsAtOnce go out in several
+        for (uint32_t at = 0; at < a.rows; at += kRowsAtOnce) {
+            QuantArgs b = a;
+            const size_t pieces = (size_t)at * a.c8;
+            b.rows = a.rows - at < kRowsAtOnce ? a.rows - at : kRowsAtOnce;
+            b.x += at * a.ldx;
+            b.row_exp += at;
+            if (b.codes) b.codes += 4 * pieces;
+            if (b.scales) b.scales += pieces / 2;  // two pieces a block
+            if (b.values) b.values += at * a.ldv;
+            hipLaunchKernelGGL((k_fp4_quant_rows<DT, 64>), dim3((b.rows + 3) / 4), dim3(256), 0, s, b);
+            const hipError_t r = hipGetLastError();
+            if (r != hipSuccess) return r;
+        }
+    } else if (a.row_exp) {
+        hipLaunchKernelGGL((k_fp4_quant_rows<DT, 256>), dim3(a.rows), dim3(256), 0, s, a);
     } else {
         const dim3 grid((unsigned)(((size_t)a.rows * a.c8 + 255) / 256));
         if (fmt == kFmtNvfp4)
