@@ -403,13 +403,13 @@ hipError_t norm_types(const NormArgs& a, float* part, hipStream_t s) {
 
 }  // namespace
 
-size_t norm_ws_bytes(int H, int T) { return align256((size_t)3 * norm_groups(H, T) * H * sizeof(float)); }
+size_t norm_ws_bytes(int H, int T) { return kCounterBytes + align256((size_t)3 * norm_groups(H, T) * H * sizeof(float)); }
 
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) { return norm_types(a, nullptr, s); }
 
 hipError_t launch_block_norm_backward(const NormArgs& a, void* ws, hipStream_t s) {
     const int groups = norm_groups(a.H, a.T);
-    float* part = static_cast<float*>(ws);
+    float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + kCounterBytes);
     if (groups) {
         const hipError_t r = norm_types(a, part, s);
         if (r != hipSuccess) return r;

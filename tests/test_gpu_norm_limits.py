@@ -1,0 +1,38 @@
+"""The norms around a block: workspaces of exactly the size asked for, an empty
+batch."""
+import pytest
+import torch
+
+from test_gpu_norm import m  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T", [1, 700, 9001])
+def test_workspace_of_exactly_the_size(m, T):  # noqa: F811
+    """Nothing behind the size asked for is written, nor the first 4096 bytes of the workspace."""
+    H = 264
+    g = torch.Generator().manual_seed(T)
+    n = m.norm_desc(H, torch.float32, torch.float32, torch.float32, "channel", 1.0, 1e-6)
+    need = m.moe_block_norm_workspace_bytes(n, T)
+    buf = torch.randint(0, 256, (need + (1 << 20),), dtype=torch.uint8, generator=g).cuda()
+    keep = buf.clone()
+    r, y, dx = (torch.randn((T, H), generator=g).cuda() for _ in range(3))
+    w = torch.ones(H, device="cuda")
+    dr, dy = torch.empty_like(r), torch.empty_like(y)
+    out = [torch.empty(H, device="cuda") for _ in range(3)]
+    m.moe_block_norm_backward(n, r, H, y, H, T, None, w, w, w, None, 0, dx, H, dr, H, dy, H, *out, 0, buf[:need])
+    assert torch.equal(buf[need:], keep[need:])
+    assert torch.equal(buf[:4096], keep[:4096])
+
+
+def test_no_tokens_and_a_workspace_of_the_size_asked_for(m):  # noqa: F811
+    """An empty batch writes zeros with the workspace that its size asks for."""
+    H = 64
+    n = m.norm_desc(H, torch.float32, torch.float32, torch.float32, "channel", 1.0, 1e-6)
+    w = torch.ones(H, device="cuda")
+    out = [torch.full((H,), 5.0, device="cuda") for _ in range(3)]
+    e = torch.empty((0, H), device="cuda")
+    ws = torch.empty(m.moe_block_norm_workspace_bytes(n, 0), dtype=torch.uint8, device="cuda")
+    m.moe_block_norm_backward(n, e, H, e, H, 0, None, w, w, w, None, 0, e, H, None, 0, None, 0, *out, 0, ws)
+    assert all((o == 0).all() for o in out)
