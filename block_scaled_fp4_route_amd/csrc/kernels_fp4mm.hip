@@ -591,10 +591,10 @@ hipError_t operands(const Fp4Matrix& w, int K, int N, char* out, int dtype, uint
 size_t fp4_ws_bytes(int K, int N, int fmt, int dtype, int T, bool backward) {
     const int sum = backward ? N : K, P = act_parts(dtype, act_kind(fmt, dtype, backward));
     const size_t parts = T > kFewMaxT || backward ? part_bytes(T, backward ? K : N) : 0;
-    const size_t kept = parts + align256((size_t)K * N * 2) + (P > 1 ? align256((size_t)T * P * sum * 2) : 0);
+    const size_t kept = kCounterBytes + parts + align256((size_t)K * N * 2) + (P > 1 ? align256((size_t)T * P * sum * 2) : 0);
     if (backward || fmt != kFmtMxfp4) return kept;
     const size_t steps = (K + 255) / 256;
-    const size_t rounded = parts + align256((size_t)T * K / 2) + align256((size_t)T * K / 32) + steps * 8 * (tile_rows(T) + tile_rows(N));
+    const size_t rounded = kCounterBytes + parts + align256((size_t)T * K / 2) + align256((size_t)T * K / 32) + steps * 8 * (tile_rows(T) + tile_rows(N));
     return kept > rounded ? kept : rounded;
 }
 
@@ -603,7 +603,7 @@ hipError_t launch_fp4_apply(int K, int N, int fmt, int dtype, const void* x, siz
                             hipStream_t s) {
     const size_t es = dtype == kActF32 ? 4 : 2;
     if (T <= kGemvMaxT) return launch_fp4_gemv(K, N, fmt, dtype, x, ldx, T, w, round_x, base, ldbase, y, ldy, s);
-    char* p = static_cast<char*>(ws);
+    char* p = static_cast<char*>(ws) + kCounterBytes;
     MmArgs g = {};
     g.M = T;
     g.N = N;
@@ -661,7 +661,7 @@ hipError_t launch_fp4_backward(int K, int N, int fmt, int dtype, const void* dy,
                                const Fp4Matrix& w, const void* dx_base, size_t lddxb, void* dx, size_t lddx, void* ws,
                                hipStream_t s) {
     const size_t es = dtype == kActF32 ? 4 : 2;
-    char* p = static_cast<char*>(ws);
+    char* p = static_cast<char*>(ws) + kCounterBytes;
     MmArgs g = {};
     g.M = T;
     g.N = K;

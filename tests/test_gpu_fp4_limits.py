@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import serve_ref as ref
-from test_gpu_fp4 import m  # noqa: F401
+from test_gpu_fp4 import m, matrix  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +32,32 @@ def test_quant_of_many_short_rows_with_exponents(m, rows):  # noqa: F811
     codes0, scales0, e0, val = ref.quant(x[pick], "nvfp4", "nearest", True)
     for g, w in zip(got, (codes0, scales0, e0[:, None], ref.stored(val, dt))):
         assert torch.equal(g[pick].cpu(), w)
+
+
+def call(m, f, back, rnd, x, T, w, base, y, ws):  # noqa: F811
+    codes, scales, e = w
+    ldb = 0 if base is None else base.stride(0)
+    if back:
+        m.moe_fp4_backward(f, x, x.stride(0), T, codes, scales, e, base, ldb, y, y.stride(0), ws)
+    else:
+        m.moe_fp4_apply(f, x, x.stride(0), T, codes, scales, e, rnd, base, ldb, y, y.stride(0), ws)
+
+
+@pytest.mark.parametrize("T,K,N,fmt,dt,rnd,back", [
+    (1, 544, 264, "nvfp4", "f32", False, False), (4, 544, 264, "mxfp4", "bf16", True, False),
+    (20, 544, 264, "nvfp4", "bf16", False, False), (20, 544, 264, "mxfp4", "f32", False, False), (64, 544, 264, "mxfp4", "bf16", True, False),
+    (65, 544, 264, "nvfp4", "f32", False, False), (300, 544, 264, "mxfp4", "bf16", True, False), (130, 5600, 72, "mxfp4", "f16", False, False),
+    (1, 544, 264, "nvfp4", "f32", False, True), (300, 544, 264, "mxfp4", "bf16", False, True)])
+def test_workspace_of_exactly_the_size(m, T, K, N, fmt, dt, rnd, back):  # noqa: F811
+    """Nothing behind the size asked for is written, nor the first 4096 bytes of the workspace."""
+    t = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[dt]
+    g = torch.Generator().manual_seed(T)
+    f = m.fp4_desc(K, N, fmt, t)
+    need = m.moe_fp4_workspace_bytes(f, T, back)
+    buf = torch.randint(0, 256, (need + (1 << 20),), dtype=torch.uint8, generator=g).cuda()
+    keep = buf.clone()
+    x = torch.randn((T, N if back else K), generator=g).to(t).cuda()
+    y = torch.empty((T, K if back else N), dtype=t, device="cuda")
+    call(m, f, back, rnd, x, T, matrix(g, N, K, fmt), None, y, buf[:need])
+    assert torch.equal(buf[need:], keep[need:])
+    assert torch.equal(buf[:4096], keep[:4096])
