@@ -588,13 +588,18 @@ hipError_t operands(const Fp4Matrix& w, int K, int N, char* out, int dtype, uint
 
 }  // namespace
 
+// Behind the reserved bytes: nothing more for the vector kernel; the activations'
+// parts, or codes and scales, for up to kFewMaxT tokens; split sums, the widened W
+// and the parts, or codes, scales and their panels, for more tokens and backward.
 size_t fp4_ws_bytes(int K, int N, int fmt, int dtype, int T, bool backward) {
+    if (T <= kGemvMaxT && !backward) return kCounterBytes;
+    const bool few = T <= kFewMaxT && !backward;
     const int sum = backward ? N : K, P = act_parts(dtype, act_kind(fmt, dtype, backward));
-    const size_t parts = T > kFewMaxT || backward ? part_bytes(T, backward ? K : N) : 0;
-    const size_t kept = kCounterBytes + parts + align256((size_t)K * N * 2) + (P > 1 ? align256((size_t)T * P * sum * 2) : 0);
+    const size_t sums = kCounterBytes + (few ? 0 : part_bytes(T, backward ? K : N));
+    const size_t kept = sums + (few ? 0 : align256((size_t)K * N * 2)) + (P > 1 ? align256((size_t)T * P * sum * 2) : 0);
     if (backward || fmt != kFmtMxfp4) return kept;
     const size_t steps = (K + 255) / 256;
-    const size_t rounded = kCounterBytes + parts + align256((size_t)T * K / 2) + align256((size_t)T * K / 32) + steps * 8 * (tile_rows(T) + tile_rows(N));
+    const size_t rounded = sums + align256((size_t)T * K / 2) + align256((size_t)T * K / 32) + (few ? 0 : steps * 8 * (tile_rows(T) + tile_rows(N)));
     return kept > rounded ? kept : rounded;
 }
 
@@ -638,7 +643,7 @@ hipError_t launch_fp4_apply(int K, int N, int fmt, int dtype, const void* x, siz
     }
     const int kind = act_kind(fmt, dtype, false), P = act_parts(dtype, kind);
     Acts acts;
-    const uint32_t na = activations(dtype, P, x, ldx, T, K, p + align256((size_t)K * N * 2), g, acts);
+    const uint32_t na = activations(dtype, P, x, ldx, T, K, T <= kFewMaxT ? p : p + align256((size_t)K * N * 2), g, acts);
     if (T <= kFewMaxT) {
         if (na) {
             if (dtype == kActF32) hipLaunchKernelGGL(k_fp4_parts<kActF32>, dim3(na), dim3(256), 0, s, acts);
