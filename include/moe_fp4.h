@@ -500,8 +500,10 @@ typedef struct moe_fp4_desc {
  *   codes [N][K / 2], 16-B aligned; scales [N][K / G];
  *   row_exp [N] in [-100, 116], or NULL: zeros (MOE_FMT_MXFP4: must be NULL)
  * An infinity or a NaN among the activations enters the sums as in fp32
- * arithmetic; one in W (a NaN scale, a value above the largest fp32) makes
- * every output that it enters infinite or NaN. T = 0 enqueues nothing. y
+ * arithmetic. A NaN scale in W makes every output that it enters NaN; a value
+ * of W above the largest fp32 (scale bytes 253 and 254, which moe_fp4_quant
+ * does not write) makes them infinite or NaN, or, with round_x, where codes
+ * are multiplied as they are, enters as that value. T = 0 enqueues nothing. y
  * overlaps no input, but for base. Workspace:
  * moe_fp4_workspace_bytes(f, T, 0), which never falls as T grows. Errors:
  * MOE_ERR_ARG (K not a multiple of 32, N not of 8, pointers, strides, round_x

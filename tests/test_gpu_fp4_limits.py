@@ -61,3 +61,47 @@ def test_workspace_of_exactly_the_size(m, T, K, N, fmt, dt, rnd, back):  # noqa:
     call(m, f, back, rnd, x, T, matrix(g, N, K, fmt), None, y, buf[:need])
     assert torch.equal(buf[need:], keep[need:])
     assert torch.equal(buf[:4096], keep[:4096])
+
+
+def workspace(m, f, T, back):  # noqa: F811
+    return torch.full((m.moe_fp4_workspace_bytes(f, T, back),), 0xFF, dtype=torch.uint8, device="cuda")
+
+
+@pytest.mark.parametrize("T", [2, 20, 50, 200])
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+def test_nan_scale_beside_rounded_activations(m, T, dt):  # noqa: F811
+    """A NaN scale of W makes the outputs NaN that its block enters, whatever it meets (here also a block of zeros)."""
+    g = torch.Generator().manual_seed(9)
+    K, N, t = 160, 72, {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[dt]
+    codes, scales, _ = matrix(g, N, K, "mxfp4")
+    scales[5, 1] = 0xFF
+    codes[5, 16:32] = 0
+    x = torch.randn((T, K), generator=g).to(t).cuda()
+    x[1, 32:64] = 0
+    y = torch.empty((T, N), dtype=t, device="cuda")
+    f = m.fp4_desc(K, N, "mxfp4", t)
+    call(m, f, False, True, x, T, (codes, scales, None), None, y, workspace(m, f, T, False))
+    hit = torch.arange(N, device="cuda") == 5
+    assert y[:, hit].isnan().all() and y[:, ~hit].isfinite().all()
+
+
+@pytest.mark.parametrize("T", [2, 20, 50, 200])
+def test_weights_above_fp32_beside_rounded_activations(m, T):  # noqa: F811
+    """Scale byte 254 (2^127): codes of 2 and more stand for values above the largest fp32: their outputs are
+    infinite or NaN or the definition's, the others as always."""
+    g = torch.Generator().manual_seed(7)
+    K, N = 96, 40
+    codes, scales, _ = matrix(g, N, K, "mxfp4")
+    scales[5, 1] = 254
+    codes[5, 16:32] = 0x77  # 6 2^127
+    x = torch.randn((T, K), generator=g) * 2.0 ** -20
+    y = torch.empty((T, N), device="cuda")
+    f = m.fp4_desc(K, N, "mxfp4", torch.float32)
+    call(m, f, False, True, x.cuda(), T, (codes, scales, None), None, y, workspace(m, f, T, False))
+    W = ref.decode(codes, scales, "mxfp4")
+    want, off = ref.product(ref.quant(x, "mxfp4", "floor", False)[3], W, None, torch.float32)
+    y = y.cpu()
+    hit = torch.arange(N) == 5
+    as_it_is = (y[:, 5].double() - want[:, 5]).abs() <= off[:, 5]
+    assert (as_it_is | ~y[:, 5].isfinite()).all()
+    ref.close(y[:, ~hit], want[:, ~hit], off[:, ~hit], "other outputs")
