@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import serve_ref as ref
-from test_gpu_fp4 import m, matrix  # noqa: F401
+from test_gpu_fp4 import check_product, check_quant, m, matrix  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -105,3 +105,88 @@ def test_weights_above_fp32_beside_rounded_activations(m, T):  # noqa: F811
     as_it_is = (y[:, 5].double() - want[:, 5]).abs() <= off[:, 5]
     assert (as_it_is | ~y[:, 5].isfinite()).all()
     ref.close(y[:, ~hit], want[:, ~hit], off[:, ~hit], "other outputs")
+
+
+@pytest.mark.parametrize("T,K,N,fmt,dt,rnd,back", [
+    (4, 544, 264, "nvfp4", "f32", False, False), (3, 96, 40, "mxfp4", "bf16", True, False),
+    (64, 544, 264, "nvfp4", "bf16", False, False), (64, 544, 264, "mxfp4", "f32", False, False), (61, 544, 264, "mxfp4", "f16", True, False),
+    (300, 544, 264, "nvfp4", "f16", False, False), (257, 96, 40, "nvfp4", "f32", False, False), (300, 544, 264, "mxfp4", "bf16", True, False),
+    (300, 544, 264, "mxfp4", "bf16", False, True), (260, 544, 264, "nvfp4", "f32", False, True),
+    (300, 128, 24600, "mxfp4", "bf16", False, False), (300, 24608, 128, "mxfp4", "bf16", False, True)])
+def test_longest_strides(m, T, K, N, fmt, dt, rnd, back):  # noqa: F811
+    """Rows 2^22 elements apart on every side: the last row of a tile of 256 lies 2^31 bytes less 8 MiB (16-bit values)
+    behind its first, or its parts do. Bit for bit as with rows side by side."""
+    t, ld = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[dt], 1 << 22
+    ki, ko = (N, K) if back else (K, N)
+    g = torch.Generator().manual_seed(T + K + N)
+    w = matrix(g, N, K, fmt)
+    f = m.fp4_desc(K, N, fmt, t)
+    ws = workspace(m, f, T, back)
+    x, base, y = torch.randn((T, ki), generator=g).to(t).cuda(), torch.randn((T, ko), generator=g).to(t).cuda(), torch.empty((T, ko), dtype=t, device="cuda")
+    call(m, f, back, rnd, x, T, w, base, y, ws)
+    far = []
+    for v in (x, base, y):
+        buf = torch.empty((T - 1) * ld + v.shape[1], dtype=t, device="cuda")
+        far.append(buf.as_strided(v.shape, (ld, 1)))
+    far[0].copy_(x)
+    far[1].copy_(base)
+    call(m, f, back, rnd, far[0], T, w, far[1], far[2], ws)
+    assert torch.equal(far[2], y)
+
+
+@pytest.mark.parametrize("fmt,rule,rows", [("nvfp4", "nearest", True), ("nvfp4", "nearest", False), ("mxfp4", "floor", False)])
+def test_quant_of_rows_past_31_bits(m, fmt, rule, rows):  # noqa: F811
+    """Rows whose offsets pass 2^31 elements, on both sides."""
+    c, ld = 96, (1 << 30) + 8
+    buf = torch.empty(2 * ld + c, dtype=torch.bfloat16, device="cuda")
+    x = buf.as_strided((3, c), (ld, 1))
+    x.copy_(torch.randn((3, c), device="cuda"))
+    check_quant(m, x, fmt, rule, rows, inplace=True)
+
+
+@pytest.mark.parametrize("fmt,rnd,back", [("nvfp4", False, False), ("mxfp4", False, False), ("mxfp4", True, False), ("nvfp4", False, True),
+                                          ("mxfp4", False, True)])
+@pytest.mark.parametrize("T", [1, 20, 50, 200])
+def test_scales_at_odd_addresses(m, T, fmt, rnd, back):  # noqa: F811
+    """Scale bytes may lie anywhere: bit for bit as from an aligned address; and a quantisation writes them there."""
+    g = torch.Generator().manual_seed(T)
+    K, N = 544, 264
+    codes, scales, e = matrix(g, N, K, fmt)
+    odd = torch.full((scales.numel() + 2,), 0xAB, dtype=torch.uint8, device="cuda")[1:-1].view(scales.shape)
+    assert odd.data_ptr() % 2 == 1
+    odd.copy_(scales)
+    f = m.fp4_desc(K, N, fmt, torch.bfloat16)
+    ws = workspace(m, f, T, back)
+    x = torch.randn((T, N if back else K), generator=g).bfloat16().cuda()
+    y = [torch.empty((T, K if back else N), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for s, o in ((scales, y[0]), (odd, y[1])):
+        call(m, f, back, rnd, x, T, (codes, s, e), None, o, ws)
+    assert torch.equal(*y)
+    v = torch.randn((N, K), generator=g).cuda()
+    rule = m.MOE_SCALE_NEAREST if fmt == "nvfp4" else m.MOE_SCALE_FLOOR
+    for s in (scales, odd):
+        m.moe_fp4_quant(v, K, N, K, v.dtype, fmt, rule, None, None, s, None, 0)
+    assert torch.equal(odd, scales)
+
+
+@pytest.mark.parametrize("T", [2, 20, 50, 200])
+def test_far_scales_beside_rounded_activations(m, T):  # noqa: F811
+    """Scale bytes from 2^-127 up to where fp32 still holds the values."""
+    g = torch.Generator().manual_seed(5)
+    K, N = 96, 40
+    for lo, hi, p in ((0, 6, 100), (118, 137, 0), (240, 247, -10)):
+        x = torch.randn((T, K), generator=g) * 2.0 ** p
+        check_product(m, T, K, N, "mxfp4", "f32", True, w=matrix(g, N, K, "mxfp4", lo, hi), x=x, base="none")
+
+
+@pytest.mark.parametrize("base", ["none", "same", "other"])
+@pytest.mark.parametrize("fmt,dt,rnd,back", [("nvfp4", "f16", False, False), ("nvfp4", "f32", False, False), ("mxfp4", "bf16", True, False),
+                                             ("mxfp4", "f32", False, True), ("nvfp4", "bf16", False, True)])
+def test_whole_tiles_of_128(m, fmt, dt, rnd, back, base):  # noqa: F811
+    """20 x 21 tiles of 128 x 128 with ragged edges, 110 of 256 x 256: each workgroup writes its tile itself, with row
+    exponents and base."""
+    T, ki, ko = 2451, 544, 2568
+    if back:
+        check_product(m, T, ko + 24, ki, fmt, dt, back=True, base=base)
+    else:
+        check_product(m, T, ki, ko, fmt, dt, rnd, base=base)

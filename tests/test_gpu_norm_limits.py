@@ -1,11 +1,19 @@
-"""The norms around a block: workspaces of exactly the size asked for, an empty
-batch."""
+"""The norms around a block: more tokens than the backward pass has workgroups
+for short rows, workspaces of exactly the size asked for, an empty batch."""
 import pytest
 import torch
 
-from test_gpu_norm import m  # noqa: F401
+from test_gpu_norm import check, m  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T,H", [(9001, 264), (5003, 1032), (20011, 8)])
+@pytest.mark.parametrize("gate", ["channel", "token"])
+@pytest.mark.parametrize("acc", [False, True])
+def test_many_tokens(m, T, H, gate, acc):  # noqa: F811
+    """More than 512 workgroups, each with several rows."""
+    check(m, T, H, ("bf16", "f32", "f32"), gate, mask="mixed", acc=acc)
 
 
 @pytest.mark.parametrize("T", [1, 700, 9001])
