@@ -190,3 +190,35 @@ def test_whole_tiles_of_128(m, fmt, dt, rnd, back, base):  # noqa: F811
         check_product(m, T, ko + 24, ki, fmt, dt, back=True, base=base)
     else:
         check_product(m, T, ki, ko, fmt, dt, rnd, base=base)
+
+
+@pytest.mark.parametrize("T,K,N,fmt,dt,rnd,back", [
+    (1, 65536, 65536, "nvfp4", "f32", False, False), (17, 65536, 65536, "nvfp4", "bf16", False, False), (40, 65536, 65536, "mxfp4", "bf16", True, False),
+    (65, 65536, 65536, "nvfp4", "f32", False, False), (70, 65536, 65536, "mxfp4", "bf16", True, False),
+    (2, 65536, 65536, "nvfp4", "f32", False, True), (90, 65536, 65536, "mxfp4", "f16", False, True),
+    (1 << 20, 32, 8, "nvfp4", "f32", False, False), (1 << 20, 96, 40, "mxfp4", "bf16", True, False), (1 << 20, 32, 8, "mxfp4", "f16", False, True)])
+def test_largest_sizes(m, T, K, N, fmt, dt, rnd, back):  # noqa: F811
+    """The ends of every range: some tokens and outputs, the first and last among them, against the definition."""
+    t = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[dt]
+    torch.manual_seed(T)
+    codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda")
+    lo, hi = (0x18, 0x39) if fmt == "nvfp4" else (114, 123)
+    scales = torch.randint(lo, hi, (N, K // ref.GROUP[fmt]), dtype=torch.uint8, device="cuda")
+    e = torch.randint(-9, 1, (N,), dtype=torch.int8, device="cuda") if fmt == "nvfp4" else None
+    f = m.fp4_desc(K, N, fmt, t)
+    ki, ko = (N, K) if back else (K, N)
+    x, y = (torch.randn((T, ki), device="cuda") / 16).to(t), torch.empty((T, ko), dtype=t, device="cuda")
+    call(m, f, back, rnd, x, T, (codes, scales, e), None, y, workspace(m, f, T, back))
+    rows = torch.tensor(sorted({0, 1, T // 2, T - 2, T - 1} & set(range(T))), device="cuda")
+    xv = x[rows].cpu()
+    xv = ref.quant(xv, "mxfp4", "floor", False)[3] if rnd else xv.double()
+    G = ref.GROUP[fmt]
+    if back:  # whole groups of columns
+        for c in (0, K - G):
+            W = ref.decode(codes[:, c // 2:(c + G) // 2], scales[:, c // G:c // G + 1], fmt, e)
+            want, off = ref.product(xv, W.t().contiguous(), None, t)
+            ref.close(y[rows][:, c:c + G], want, off, (T, K, N, c))
+    else:
+        n = torch.tensor(sorted({0, 1, N // 2, N - 2, N - 1}), device="cuda")
+        want, off = ref.product(xv, ref.decode(codes[n], scales[n], fmt, None if e is None else e[n]), None, t)
+        ref.close(y[rows][:, n], want, off, (T, K, N))

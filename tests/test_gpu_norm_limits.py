@@ -44,3 +44,22 @@ def test_no_tokens_and_a_workspace_of_the_size_asked_for(m):  # noqa: F811
     ws = torch.empty(m.moe_block_norm_workspace_bytes(n, 0), dtype=torch.uint8, device="cuda")
     m.moe_block_norm_backward(n, e, H, e, H, 0, None, w, w, w, None, 0, e, H, None, 0, None, 0, *out, 0, ws)
     assert all((o == 0).all() for o in out)
+
+
+def test_most_tokens(m):  # noqa: F811
+    """2^20 rows of 8 channels."""
+    check(m, 1 << 20, 8, ("bf16", "f32", "f32"), "token", mask="mixed", pad=0)
+
+
+@pytest.mark.parametrize("kinds", [("bf16", "f16", "f32"), ("f32", "bf16", "bf16"), ("f16", "f32", "bf16"), ("bf16", "bf16", "bf16")])
+@pytest.mark.parametrize("H", [4104, 8192, 8200, 16384])
+@pytest.mark.parametrize("gate", ["channel", "token"])
+def test_long_rows(m, H, kinds, gate):  # noqa: F811
+    """Rows above 4096 channels in each type, masked, several to a workgroup."""
+    check(m, 601, H, kinds, gate, mask="mixed", acc=H % 512 != 0)
+
+
+@pytest.mark.parametrize("gate", ["channel", "token"])
+def test_masked_in_place(m, gate):  # noqa: F811
+    """dr over dr_out: rows left out become zeros there too."""
+    check(m, 65, 264, ("bf16", "f32", "f32"), gate, mask="mixed", inplace=True)
