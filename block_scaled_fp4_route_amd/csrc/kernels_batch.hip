@@ -20,10 +20,11 @@
 //
 // 13 tokens of 6 out of 384 MXFP4 experts of 4096 x 2880 (1.35 GB): gate/up and
 // down 304 us, 4.4 TB/s. 48 tokens of 10 out of 512 NVFP4 ones of 2560 x 640 (0.82
-// GB): 227 us, 3.6 TB/s (fp16 decoding, half the instructions, gained 2%: not the
+// GB): 227-232 us, 3.6 TB/s (fp16 decoding, half the instructions, gained 2%: not the
 // arithmetic). 4 tokens: 44 of 61 us, 800 and 800 workgroups that each read for two or
 // three blocks of the sum, so that their start and end count; the other three
-// launches are chains of dependent loads.
+// launches are chains of dependent loads. 2 tokens take 42 us in a graph, two calls of
+// the single-token layer 32; 3 take 49 and 48.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -744,7 +745,12 @@ hipError_t launch_layer_batch(int fmt, int H, int I, int E, int k, const float* 
     a.ks = T <= 32 ? kRouterParts : 2;  // workgroups for the whole chip, up to two groups of tokens
     const int et = (E + 15) / 16, nr = et * ((T + 15) / 16) * a.ks, shared = sh_gate ? 1 : 0;
     // experts with more tokens than an item are read again: few where the
-    // assignments are fewer than two an expert
+    // assignments are fewer than two an expert (items of 5 against 15: 48 tokens of 10
+    // out of 512 experts of 2560 x 640 255 and 286 us, 64 of 4 out of 128 109 and 122), while
+    // items of 15 win from 8 to 16 an expert on (64 of 4 out of 16: 73 and 68; of 8 out of
+    // 8: 120 and 104; of 2 out of 16 MXFP4 ones of 4096 x 2880: 194 and 173). In between
+    // the border is early: 64 of 8 out of 128 142 and 150, 64 of 4 out of 64 89 and 97, out
+    // of 32 77 and 79.
     const int groups = T * k <= 2 * E ? 1 : kMaxGroups;
     a.per = kTok * groups;
     a.items_n = max_items(E, k, T, shared, a.per);

@@ -11,7 +11,8 @@
 // 2560 x 8192 NVFP4 (11.8 MB): 1 token 6.5 us (launch, loads and sums over the
 // lanes are one chain, 1.8 TB/s), 4 tokens 11.4 (four times the products). 16
 // tokens of fp32 19 us, 64 35: each workgroup reads every token's parts, 250 MB
-// from L2 at 64. 64 tokens rounded to MXFP4 9 us: a sixth of those bytes.
+// from L2 at 64. 64 tokens rounded to MXFP4 9 us: an eleventh
+// of those bytes.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

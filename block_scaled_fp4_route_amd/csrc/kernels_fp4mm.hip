@@ -10,10 +10,12 @@
 // matrix units. Activations rounded to MXFP4 beside an MXFP4 matrix: both go
 // to the scaled FP4 matrix instructions as codes, never widened.
 //
-// Large products are bound by the matrix units: 8192 x 8192 x 2560 in bf16 291 us
-// beside 15 for the join and 16 for W (1.18 PFLOP/s without those). As codes 113
-// us (3.0 PFLOP/s), 35% of the matrix rate: steps of 256 codes take 2 us where the
-// products alone would take 0.85; neither bank conflicts (none) nor a longer ring
+// Large products are bound by the matrix units: 8192 x 8192 x 2560 in bf16 takes
+// 308-322 us, about 15 of them the join and 16 W (the product alone about 285, 1.2
+// PFLOP/s; 344-349 under the profiler). As codes the product takes 116-121 us under
+// the profiler (2.9 PFLOP/s), 29% of the matrix rate: steps of 256 codes take 2 us where the
+// products alone would take 0.85, and a tile has ten of them between its ring's
+// filling and its way out; neither bank conflicts (none) nor a longer ring
 // changed it. Products of few tiles are bound by their steps' latency: 311 tokens of
 // 640 x 2560 fp32 14 us for 30 steps.
 #include <hip/hip_runtime.h>
@@ -537,6 +539,10 @@ hipError_t mm_tiles(MmArgs& g, hipStream_t s) {
         if ((r = hipGetLastError()) != hipSuccess || !parts) return r;
         hipLaunchKernelGGL((k_fp4_join<DT, 256>), dim3(parts * (256 * 256 / 8 / 256)), dim3(256), 0, s, g);
     } else if (tiles(128, 128) >= kLargeFrom) {
+        // whole from 192 tiles on. For fp32 activations, three times the steps, that
+        // is too early: 192 tiles of a sum of 8192 take 285 us whole and 211 in two
+        // parts each, of 2560 98 and 77, 220 tiles 292 and 227; in bf16 192 take 87 and
+        // 92, 220 101 and 95, 256 91 and 102
         hipLaunchKernelGGL((k_fp4_mm<KIND, DT, 128, 128, 2, 2, 2>), dim3(g.full), dim3(256), 0, s, g);
     } else if (const int big = tiles(128, 128); big >= kMiddleFrom && g.wide >= 128 * kMiddleSteps) {
         // long sums: the operands are read half as often as by 64 x 64 tiles, which

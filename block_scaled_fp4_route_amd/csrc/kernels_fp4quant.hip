@@ -17,6 +17,8 @@
 // stays in registers between its two uses), codes, scales and values written
 // once: 8192 x 2560 fp32 to MXFP4 with its values 35 us, 5.1 TB/s, as fast as a
 // copy. Small matrices are a launch: 640 x 2560 bf16 with row exponents 5.5 us.
+// NVFP4 counts seven comparisons a value: 8192 x 2560 with row exponents and values
+// takes 28.6 us in bf16 where MXFP4 takes 17.1, and 37.6 in fp32 against 35.1.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
